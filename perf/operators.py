@@ -259,7 +259,10 @@ def prepare(case, seed):
         spread = 1.0 + 3.0 * (torch.rand(1, 1, dim, generator=g, device="cuda") > 0.95)
         kv = torch.cat([_rows(g, (t, heads, dim)) * spread, _rows(g, (t, heads, dim)) * 0.5], 1).to(DT[case["dtype"]])
         # K and V are the halves of one projection's rows
-        return dict(case=case, cache=cache, k=kv[:, :heads], v=kv[:, heads:], slots=slots, page=ps)
+        k, v = kv[:, :heads], kv[:, heads:]
+        return dict(case=case, cache=cache, k=k, v=v, slots=slots, page=ps,
+                    out=(torch.empty_like(k, memory_format=torch.contiguous_format),
+                         torch.empty_like(v, memory_format=torch.contiguous_format)))
     new, kv = _attn_lengths(case)
     have = [-(-n // ps) for n in kv]
     n_pages = sum(have) + 3
@@ -397,13 +400,15 @@ def run(s):
         return {"plan": _plan_plain, "append": _append_plain, "attn": _attn_plain}[op](s)
     import dequant_gemv_moe_gb300 as dq
     if op == "plan":
-        p = dq.kv_plan(s["ctx"], s["new"], s["table"], s["stack"], s["count"], page_size=s["page"], n_tokens=s["tokens"])
+        # a decode loop keeps the step's buffers
+        p = s["plan"] = dq.kv_plan(s["ctx"], s["new"], s["table"], s["stack"], s["count"], page_size=s["page"],
+                                   n_tokens=s["tokens"], out=s.get("plan"))
         return dict(table=s["table"], stack=s["stack"], kv_len=p.kv_len, q_start=p.q_start, slots=p.slots,
                     positions=p.positions, free_count=p.free_count, unserved=p.unserved)
     h = _handle(dq, s)
     if op == "append":
         dq.kv_append(h, s["k"], s["v"], s["slots"])
-        k, v = dq.kv_read(h, s["slots"], dtype=s["k"].dtype)
+        k, v = dq.kv_read(h, s["slots"], out=s["out"])
         return dict(k=k, v=v)
     out, lse = dq.kv_attention(h, s["q"], s["start"], s["kv"], s["table"], window=s["case"]["window"],
                                max_q_len=s["max_q"], out=s["out"], lse=s["lse"], ws=s["ws"])
