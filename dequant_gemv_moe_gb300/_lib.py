@@ -12,6 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdqmoe.so")
 
 Q4_K, Q6_K, Q8_0 = 1, 2, 3
+Q4_0 = 4
 F32, F16, BF16 = 0, 1, 2
 
 _P = ctypes.c_void_p
@@ -33,6 +34,22 @@ class MoeDesc(ctypes.Structure):
                 ("sh_gate", _P), ("sh_up", _P), ("sh_down", _P)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("pages", _P)]
+
+
+class KvAttn(ctypes.Structure):
+    _fields_ = [("q", _P), ("q_stride", ctypes.c_int64), ("q_dtype", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("T", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("q_start", _P), ("kv_len", _P), ("block_table", _P),
+                ("max_pages", ctypes.c_int32), ("max_q_len", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("out", _P), ("out_stride", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
+                ("lse", _P)]
+
+
 _SIGS = {
     "dq_block_geometry": [_I, _P, _P],
     "dq_dequant": [_I, _P, _I64, _P, _P],
@@ -41,6 +58,12 @@ _SIGS = {
     "dq_qgemv_ex": [_I, _P, _I64, _I64, _P, _I, _I, _P, _I, ctypes.c_uint, _P],
     "dq_device_status": [_P],
     "dq_stage": [_P, _P, _I64, _P],
+    "dq_kv_cache_size": [_P, _P],
+    "dq_kv_plan": [_P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P],
+    "dq_kv_append": [_P, _P, _I64, _P, _I64, _I, _P, _I, _P],
+    "dq_kv_read": [_P, _P, _I, _P, _P, _I, _P],
+    "dq_kv_attention_workspace_size": [_P, _I, _I, _I, _I, _P],
+    "dq_kv_attention": [_P, _P, _P, _SZ, _P],
 }
 _OPTIONAL_SIGS = {
     "dq_moe_workspace_size": [ctypes.POINTER(MoeDesc), _I, _P],

@@ -1,0 +1,183 @@
+"""torch-facing wrappers of the 4-bit paged K/V cache (marshalling only; see
+the dq_kv_* section of include/dqmoe.h for what each call computes)."""
+import collections
+import ctypes
+
+import torch
+
+from ._lib import F16, F32, BF16, Q4_0, KvAttn, KvCacheDesc
+from .ops import _call, _stream
+
+_DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+KvPlan = collections.namedtuple("KvPlan", "kv_len q_start slots positions free_count unserved")
+
+
+def _check(t, name, dtype, shape=None):
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor of %s" % (name, dtype))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+class KvCache:
+    """A paged K/V cache in Q4_0 blocks over a caller's uint8 CUDA tensor.
+
+    pages: the buffer, KvCache.size(...) bytes (its first dimension may be the
+    pages); kept by this object, never written except by kv_append.
+    """
+
+    def __init__(self, pages, page_size, n_kv_heads, head_dim, fmt=Q4_0):
+        d = KvCacheDesc(fmt, n_kv_heads, head_dim, page_size, 1, None)
+        per_page = _size(d)
+        _check(pages, "pages", torch.uint8)
+        if pages.numel() < per_page or pages.numel() % per_page:
+            raise ValueError("pages must hold a whole number of pages of %d bytes" % per_page)
+        d.n_pages = pages.numel() // per_page
+        d.pages = pages.data_ptr()
+        self.pages, self.desc = pages, d
+        self.page_size, self.n_kv_heads, self.head_dim = page_size, n_kv_heads, head_dim
+        self.n_pages = d.n_pages
+        self._ref = ctypes.byref(d)
+
+    @staticmethod
+    def size(n_pages, page_size, n_kv_heads, head_dim, fmt=Q4_0):
+        """Bytes of a cache of n_pages pages."""
+        return _size(KvCacheDesc(fmt, n_kv_heads, head_dim, page_size, n_pages, None))
+
+    @classmethod
+    def empty(cls, n_pages, page_size, n_kv_heads, head_dim, fmt=Q4_0, device="cuda"):
+        """A cache over a new buffer (its contents are whatever the memory held)."""
+        nb = cls.size(n_pages, page_size, n_kv_heads, head_dim, fmt)
+        return cls(torch.empty(nb, dtype=torch.uint8, device=device), page_size, n_kv_heads,
+                   head_dim, fmt)
+
+
+def _size(desc):
+    n = ctypes.c_size_t()
+    _call("dq_kv_cache_size", ctypes.byref(desc), ctypes.byref(n))
+    return n.value
+
+
+def kv_plan(ctx_len, new_len, block_table, free_pages, free_count, page_size, n_tokens, out=None):
+    """One step's block tables (updated in place), slots and query starts.
+
+    ctx_len, new_len: int32 [B]; block_table: int32 [B][max_pages]; free_pages:
+    int32 stack, free_count: int32 [1]; n_tokens: rows of slots and positions.
+    out: a KvPlan of an earlier step to write to (its free_count and kv_len may
+    not be this call's inputs).
+    """
+    B = ctx_len.numel()
+    _check(ctx_len, "ctx_len", torch.int32)
+    _check(new_len, "new_len", torch.int32, (B,))
+    _check(block_table, "block_table", torch.int32, (B, block_table.shape[-1]))
+    _check(free_pages, "free_pages", torch.int32)
+    _check(free_count, "free_count", torch.int32, (1,))
+    if out is None:
+        dev = ctx_len.device
+        i32 = torch.empty(2 * B + 3 + n_tokens, dtype=torch.int32, device=dev)
+        out = KvPlan(i32[:B], i32[B:2 * B + 1], torch.empty(n_tokens, dtype=torch.int64, device=dev),
+                     i32[2 * B + 3:], i32[2 * B + 1:2 * B + 2], i32[2 * B + 2:2 * B + 3])
+    else:
+        _check(out.kv_len, "kv_len", torch.int32, (B,))
+        _check(out.q_start, "q_start", torch.int32, (B + 1,))
+        _check(out.slots, "slots", torch.int64, (n_tokens,))
+        _check(out.positions, "positions", torch.int32, (n_tokens,))
+        _check(out.free_count, "free_count", torch.int32, (1,))
+        _check(out.unserved, "unserved", torch.int32, (1,))
+    _call("dq_kv_plan", ctx_len.data_ptr(), new_len.data_ptr(), B, page_size,
+          block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.numel(),
+          free_count.data_ptr(), n_tokens, out.kv_len.data_ptr(), out.q_start.data_ptr(),
+          out.slots.data_ptr(), out.positions.data_ptr(), out.free_count.data_ptr(),
+          out.unserved.data_ptr(), _stream())
+    return out
+
+
+def _rows(cache, t, name):
+    """The token stride of rows [T][n_kv_heads][head_dim] (only the first may be strided)."""
+    if t.dim() != 3 or t.shape[1] != cache.n_kv_heads or t.shape[2] != cache.head_dim:
+        raise ValueError("%s must be [T][%d][%d]" % (name, cache.n_kv_heads, cache.head_dim))
+    if not t.is_cuda or t.stride(2) != 1 or t.stride(1) != cache.head_dim:
+        raise ValueError("%s must be a CUDA tensor with consecutive heads" % name)
+    return t.stride(0) if t.shape[0] > 1 else cache.n_kv_heads * cache.head_dim
+
+
+def kv_append(cache, k, v, slots):
+    """Write K and V rows ([T][n_kv_heads][head_dim], fp32/fp16/bf16; the token
+    stride is free) into their slots (int64 [T], -1: left out)."""
+    T = k.shape[0]
+    if k.dtype != v.dtype or k.dtype not in _DT or v.shape[0] != T:
+        raise ValueError("k and v must be rows of one dtype: float32, float16 or bfloat16")
+    ks, vs = _rows(cache, k, "k"), _rows(cache, v, "v")
+    _check(slots, "slots", torch.int64, (T,))
+    if T:
+        _call("dq_kv_append", cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, _DT[k.dtype],
+              slots.data_ptr(), T, _stream())
+
+
+def kv_read(cache, slots, dtype=torch.float32, out=None):
+    """The values that slots stand for: (k, v), each [T][n_kv_heads][head_dim]."""
+    T = slots.numel()
+    _check(slots, "slots", torch.int64)
+    shape = (T, cache.n_kv_heads, cache.head_dim)
+    if out is None:
+        out = (torch.empty(shape, dtype=dtype, device=slots.device),
+               torch.empty(shape, dtype=dtype, device=slots.device))
+    k, v = out
+    if k.dtype not in _DT:
+        raise ValueError("values are float32, float16 or bfloat16")
+    _check(k, "k", k.dtype, shape)
+    _check(v, "v", k.dtype, shape)
+    if T:
+        _call("dq_kv_read", cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
+              _DT[k.dtype], _stream())
+    return k, v
+
+
+def kv_attention_workspace_size(cache, n_q_heads, B, T, max_q_len=None):
+    n = ctypes.c_size_t()
+    _call("dq_kv_attention_workspace_size", cache._ref, n_q_heads, T, B,
+          T if max_q_len is None else max_q_len, ctypes.byref(n))
+    return n.value
+
+
+def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True, window=0,
+                 max_q_len=None, out=None, out_dtype=None, lse=None, ws=None):
+    """Attention of q [T][n_q_heads][head_dim] (fp16/bf16; the row stride is
+    free) over the cache: (out, lse), lse fp32 [T][n_q_heads].
+
+    q_start int32 [B+1], kv_len int32 [B], block_table int32 [B][max_pages] as
+    kv_plan leaves them; scale: head_dim ** -0.5 unless given; max_q_len: the
+    most rows a request has (T unless given).
+    """
+    T, H, D = q.shape
+    B = kv_len.numel()
+    if q.dtype not in _DT:
+        raise TypeError("q must be float16 or bfloat16, got %s" % q.dtype)
+    if D != cache.head_dim or not q.is_cuda or q.stride(2) != 1 or (H > 1 and q.stride(1) != D):
+        raise ValueError("q must be a CUDA tensor [T][n_q_heads][%d] with consecutive heads" % cache.head_dim)
+    _check(q_start, "q_start", torch.int32, (B + 1,))
+    _check(kv_len, "kv_len", torch.int32)
+    _check(block_table, "block_table", torch.int32, (B, block_table.shape[-1]))
+    if out is None:
+        out = torch.empty((T, H, D), dtype=out_dtype or q.dtype, device=q.device)
+    elif out.dtype not in _DT or tuple(out.shape) != (T, H, D) or not out.is_cuda or \
+            out.stride(2) != 1 or (H > 1 and out.stride(1) != D):
+        raise ValueError("out must be a CUDA tensor [T][n_q_heads][head_dim] with consecutive heads")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    else:
+        _check(lse, "lse", torch.float32, (T, H))
+    if T == 0:
+        return out, lse
+    if max_q_len is None:
+        max_q_len = T
+    if ws is None:
+        ws = torch.empty(kv_attention_workspace_size(cache, H, B, T, max_q_len), dtype=torch.uint8,
+                         device=q.device)
+    a = KvAttn(q.data_ptr(), q.stride(0) if T > 1 else H * D, _DT[q.dtype], H, T, B,
+               q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+               max_q_len, D ** -0.5 if scale is None else scale, int(causal), window,
+               out.data_ptr(), out.stride(0) if T > 1 else H * D, _DT[out.dtype], lse.data_ptr())
+    _call("dq_kv_attention", cache._ref, ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream())
+    return out, lse

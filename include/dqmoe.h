@@ -425,6 +425,156 @@ int dq_expert_cache_destroy(dq_expert_cache* cache);
  *         DQ_ERR_ALIGN (pointers or size not 16-byte multiples), DQ_ERR_CUDA. */
 int dq_stage(void* dst, const void* src, int64_t bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The 4-bit K/V cache: what a decode step streams besides the weights, held */
+/* in the same blocks as they are ([KTransformers, "优化 KV 缓存大小"] shrinks  */
+/* the cache, [NTransformer, "KV cache" of its inference pipeline] keeps one; */
+/* the pages print no layout, this is the library's).                        */
+/*                                                                          */
+/* The cache is paged: page p holds page_size consecutive tokens of one      */
+/* request, and a request's pages are listed in its row of a block table.    */
+/* A token's place is its slot, page * page_size + offset in the page.       */
+/* K and V rows are Q4_0 blocks: 32 values along head_dim share an fp16       */
+/* scale d, value = d * (code - 8).  Bytes, with D = head_dim, G = D / 32     */
+/* groups and W = min(G, 4):                                                 */
+/*   pages[n_pages][n_kv_heads][page_size / 16] token blocks of 18 * D bytes, */
+/*   each 16 tokens of K and V of one head:                                  */
+/*     8D bytes  K codes [G/W][16 tokens][4 t][W]: 32-bit words; word (t, g)  */
+/*               holds values 8t..8t+7 of its group, value e in nibble        */
+/*               (e >> 1) + 4 * (e & 1)                                       */
+/*     8D bytes  V codes [2 j][G/W][8 a][4 t][2 i][W]: 16-bit units of token  */
+/*               8j + 2t + i; unit a holds values 4a..4a+3 of its group,      */
+/*               value n in nibble n                                          */
+/*      D bytes  K scales fp16 [16 tokens][G]                                 */
+/*      D bytes  V scales fp16 [4 t][G][2 j][2 i], token 8j + 2t + i          */
+/*   (the order in which a warp's lanes take them as matrix operands: the     */
+/*   loads are 16 bytes a lane, consecutive, and a nibble pair becomes an     */
+/*   operand register with one AND).  Blocks of a head in a page are          */
+/*   consecutive, so a run of tokens is one contiguous copy.                  */
+/* Bytes that no append wrote may hold anything: no result depends on them.   */
+/* ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t fmt;          /* DQ_Q4_0; other formats: DQ_ERR_UNSUPPORTED */
+  int32_t n_kv_heads;   /* 1..1024 */
+  int32_t head_dim;     /* 64, 128 or 256; others: DQ_ERR_UNSUPPORTED */
+  int32_t page_size;    /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t n_pages;      /* >= 1 */
+  void* pages;          /* device, dq_kv_cache_size bytes, 128-byte aligned */
+} dq_kv_cache;
+
+/* Bytes of the cache (host-only, no CUDA; `pages` is not looked at).
+ * Errors: DQ_ERR_ARG (null, sizes <= 0), DQ_ERR_UNSUPPORTED. */
+int dq_kv_cache_size(const dq_kv_cache* cache, size_t* bytes);
+
+#define DQ_KV_MAX_REQUESTS 8192
+
+/* dq_kv_plan — one step's block tables, slots and query rows on the GPU, from
+ * the requests' lengths (no length is read by the host, so a captured step
+ * serves any lengths).  Request r holds ctx_len[r] tokens and brings
+ * new_len[r] more; new_len[r] < 0 says that it has finished.
+ *   1. Finished requests give back their ceil(ctx_len / page_size) pages: they
+ *      are pushed on the stack of free pages in request, then page order.
+ *   2. A request needs ceil((ctx + new) / page_size) - ceil(ctx / page_size)
+ *      pages more.  It is served if its row can list them and it needs none or
+ *      the needs of the requests up to and including it (those whose rows can
+ *      list them) fit in the stack.  Pages are popped in request, then page
+ *      order, and written to the request's row behind the ones it lists.
+ *   3. kv_len[r] = ctx + new (served), ctx (not served), 0 (finished);
+ *      q_start[r] = the new tokens of the requests before r (a finished one
+ *      has none); token i of request r is row q_start[r] + i with
+ *      position ctx + i and, if r is served, the slot of that position (else -1).
+ *   ctx_len, new_len : device int32 [B]; 1 <= B <= DQ_KV_MAX_REQUESTS.
+ *   block_table      : device int32 [B][max_pages], updated in place; only the
+ *                      entries behind a served request's pages are written.
+ *   free_pages       : device int32 [n_pages], the stack; free_count: device
+ *                      int32 [1], how many it holds.  Pushes write behind them;
+ *                      nothing below is changed, so a repeated call repeats
+ *                      its results.
+ *   T                : rows of slots and positions, >= 0; rows behind the last
+ *                      new token get -1 (a captured step is sized for the most),
+ *                      new tokens behind row T are left out.
+ *   kv_len [B], q_start [B+1], slots int64 [T], positions int32 [T],
+ *   free_count_out [1], unserved [1] (how many requests were not served):
+ *                      device outputs; free_count_out may not be free_count and
+ *                      kv_len may not be ctx_len (a step swaps them).
+ * Errors: DQ_ERR_ARG (null, sizes, page_size, aliased outputs, max_pages *
+ *         page_size above 2^31 - 1), DQ_ERR_ALIGN (a pointer not aligned to its
+ *         element), DQ_ERR_UNSUPPORTED (B above the limit), DQ_ERR_CUDA. */
+int dq_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int B, int page_size,
+               int32_t* block_table, int max_pages, int32_t* free_pages, int n_pages,
+               const int32_t* free_count, int T, int32_t* kv_len, int32_t* q_start,
+               int64_t* slots, int32_t* positions, int32_t* free_count_out, int32_t* unserved,
+               void* stream);
+
+/* dq_kv_append — write T tokens' K and V rows into their slots as Q4_0 blocks.
+ * In fp32: a value is clamped to +-65504; m = the value of the largest
+ * magnitude of its 32 (the first of equal ones), d = fp16(m / -8), code =
+ * min(15, max(0, floor(x / d + 8.5))), 8 where d is 0.  NaN values are out of
+ * contract.
+ *   k, v    : device [T][n_kv_heads][head_dim] of `dtype` (F32, F16, BF16), 16-byte
+ *             aligned; k_stride, v_stride: elements between two tokens' rows
+ *             (>= n_kv_heads * head_dim, a multiple of 16 bytes), so that slices
+ *             of a fused projection are taken as they are.
+ *   slots   : device int64 [T]; a slot outside the cache (-1) is left out.  Two
+ *             tokens with one slot are out of contract.
+ * Errors: DQ_ERR_ARG, DQ_ERR_ALIGN, DQ_ERR_UNSUPPORTED, DQ_ERR_CUDA. */
+int dq_kv_append(const dq_kv_cache* cache, const void* k, int64_t k_stride, const void* v,
+                 int64_t v_stride, int dtype, const int64_t* slots, int T, void* stream);
+
+/* dq_kv_read — the values that T slots stand for, d * (code - 8) rounded once
+ * to `dtype`; zeros for a slot outside the cache.
+ *   k, v : device [T][n_kv_heads][head_dim] of `dtype`, 16-byte aligned.
+ * Errors: DQ_ERR_ARG, DQ_ERR_ALIGN, DQ_ERR_UNSUPPORTED, DQ_ERR_CUDA. */
+int dq_kv_read(const dq_kv_cache* cache, const int64_t* slots, int T, void* k, void* v, int dtype,
+               void* stream);
+
+/* dq_kv_attention — attention of a step's query rows over the cache.
+ * Row i of request r (n = q_start[r+1] - q_start[r] rows) stands at position
+ * p = kv_len[r] - n + i; query head h reads K/V head h / (n_q_heads /
+ * n_kv_heads).  It sees the positions j < kv_len[r] with j <= p (causal) and
+ * j > p - window (window > 0), and
+ *   out = sum_j e^{s_j - lse} v_j,  s_j = scale * (q . k_j),
+ *   lse = log sum_j e^{s_j}.
+ * A row that sees nothing (kv_len 0, a position below 0) gets out = 0 and
+ * lse = -inf.  The new tokens' own K/V are in the cache already (dq_kv_append).
+ * The pages are read once for up to 8 rows per K/V head; 16-bit operands with
+ * fp32 sums, so fp32 queries are refused (as dq_moe_forward). */
+typedef struct {
+  const void* q;              /* device [T][n_q_heads][head_dim], 16-byte aligned */
+  int64_t q_stride;           /* elements between two rows' first heads, a multiple of 8 */
+  int32_t q_dtype;            /* DQ_F16 or DQ_BF16 */
+  int32_t n_q_heads;          /* a multiple of n_kv_heads, <= 4096 */
+  int32_t T;                  /* rows of q, out and lse; >= 1 */
+  int32_t B;                  /* requests, 1..DQ_KV_MAX_REQUESTS */
+  const int32_t* q_start;     /* device [B+1], ascending from 0, q_start[B] <= T; rows from
+                                 q_start[B] on are not written */
+  const int32_t* kv_len;      /* device [B] */
+  const int32_t* block_table; /* device [B][max_pages]; entries of the pages below kv_len are read,
+                                 one outside the cache reads as page 0 */
+  int32_t max_pages;          /* a kv_len above max_pages * page_size reads as that many */
+  int32_t max_q_len;          /* no request has more rows, <= T; it chooses the kernels and
+                                 rows above it are not written */
+  float scale;                /* finite, > 0 */
+  int32_t causal;             /* 0 or 1 */
+  int32_t window;             /* 0: none */
+  void* out;                  /* device [T][n_q_heads][head_dim], 16-byte aligned */
+  int64_t out_stride;         /* elements between two rows, a multiple of 8 */
+  int32_t out_dtype;          /* DQ_F16, DQ_BF16 or DQ_F32 */
+  float* lse;                 /* device [T][n_q_heads] or NULL */
+} dq_kv_attn;
+
+/* Bytes of scratch dq_kv_attention needs (host-only, no CUDA): it depends on
+ * the heads, T, B and max_q_len, not on the lengths. */
+int dq_kv_attention_workspace_size(const dq_kv_cache* cache, int n_q_heads, int T, int B,
+                                   int max_q_len, size_t* bytes);
+
+/*   ws : device scratch of at least that many bytes, 256-byte aligned; contents
+ *        on entry are ignored.
+ * Errors: DQ_ERR_ARG, DQ_ERR_ALIGN, DQ_ERR_UNSUPPORTED (fp32 q, sizes above the
+ *         limits), DQ_ERR_WORKSPACE, DQ_ERR_CUDA. */
+int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* args, void* ws, size_t ws_bytes,
+                    void* stream);
+
 /* Human-readable name of a dq_status value (static string, never NULL). */
 const char* dq_status_string(int status);
 
