@@ -2,28 +2,11 @@
 // per (row, query head), every product in fp32.
 #include <algorithm>
 
-#include "kv.cuh"
+#include "kv_attn.h"
 
 namespace dqmoe {
 
 namespace {
-
-struct AttnParams {
-  KvGeom g;
-  const void* q;
-  int64_t q_stride;
-  int q_dtype, n_q_heads, group, T, B;
-  const int32_t* q_start;
-  const int32_t* kv_len;
-  const int32_t* table;
-  int max_pages, max_q_len;
-  float scale;
-  int causal, window;
-  void* out;
-  int out_dtype;
-  int64_t out_stride;
-  float* lse;
-};
 
 __device__ __forceinline__ float q_at(const AttnParams& p, int64_t i) {
   return p.q_dtype == DQ_BF16 ? __bfloat162float(((const __nv_bfloat16*)p.q)[i])
@@ -149,7 +132,7 @@ int dq_kv_attention_workspace_size(const dq_kv_cache* cache, int n_q_heads, int 
   if (rc != DQ_OK) return rc;
   rc = attn_sizes_ok(cache, n_q_heads, T, B, max_q_len);
   if (rc != DQ_OK) return rc;
-  *bytes = 256;
+  *bytes = kv_stream_workspace(cache->head_dim);
   return DQ_OK;
 }
 
@@ -201,6 +184,9 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
   p.out_dtype = a->out_dtype;
   p.out_stride = a->out_stride;
   p.lse = a->lse;
+  p.ws = (uint8_t*)ws;
+  if ((int64_t)a->max_q_len * p.group <= 64)
+    return launch_kv_stream(p, cache->head_dim, (cudaStream_t)stream);
   const dim3 grid((unsigned)a->T, (unsigned)a->n_q_heads), block(kPlainThreads);
   cudaError_t e;
   cudaStream_t s = (cudaStream_t)stream;
