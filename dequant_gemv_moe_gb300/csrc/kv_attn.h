@@ -22,11 +22,15 @@ struct AttnParams {
   int64_t out_stride;
   float* lse;
   uint8_t* ws;
+  int rows_above, rows_upto;   // the kernel looks after requests with rows_above < rows <= rows_upto
 };
 
-// streaming kernel (kv_attn_stream.cu): few rows per K/V head
-size_t kv_stream_workspace(int head_dim);
+// few rows per K/V head (kv_attn_stream.cu)
+size_t kv_stream_workspace();
 int launch_kv_stream(const AttnParams& p, int head_dim, cudaStream_t s);
+// many rows (kv_attn_tc.cu)
+size_t kv_tc_workspace();
+int launch_kv_tc(const AttnParams& p, int head_dim, cudaStream_t s);
 
 // the length of request r as the kernels read it
 __device__ __forceinline__ int kv_length(const AttnParams& p, int r) {
@@ -38,6 +42,148 @@ __device__ __forceinline__ int q_rows(const AttnParams& p, int r, int* first) {
   *first = a;
   // memory-safe whatever q_start holds
   return a < 0 ? 0 : max(0, min(min(__ldg(p.q_start + r + 1), p.T) - a, p.max_q_len));
+}
+
+
+// One row tile of a request and the tokens that its rows may see.
+struct Item {
+  int r, h, row0, rows;        // request, K/V head, first row (token * group + head), rows
+  int len, qlen, first;        // kv length, tokens of the request, its first row of q
+  int begin, end;              // tokens that some row sees
+  int t0, tiles;               // first tile, tiles (at least one)
+};
+
+// A call's work as one line of units: (request, row tile, K/V head, tile of
+// TILE tokens), the tokens fastest.
+template <int ROWS, int TILE>
+struct Walk {
+  __device__ __forceinline__ static void range(const AttnParams& p, Item& it) {
+    const int shift = it.len - it.qlen;
+    it.rows = min(ROWS, it.qlen * p.group - it.row0);
+    const int lo = shift + it.row0 / p.group, hi = shift + (it.row0 + it.rows - 1) / p.group;
+    it.end = p.causal ? min(it.len, hi + 1) : it.len;
+    it.begin = p.window > 0 ? max(0, lo - p.window + 1) : 0;
+    it.t0 = it.begin / TILE;
+    it.tiles = it.end > it.begin ? (it.end + TILE - 1) / TILE - it.t0 : 1;
+  }
+  // the request's rows of q if this kernel looks after it, else 0
+  __device__ __forceinline__ static int tokens(const AttnParams& p, int r, int* first) {
+    const int n = q_rows(p, r, first);
+    const int64_t rows = (int64_t)n * p.group;
+    return rows > p.rows_above && rows <= p.rows_upto ? n : 0;
+  }
+  __device__ __forceinline__ static int64_t units(const AttnParams& p, int r, Item& it) {
+    it.r = r;
+    it.qlen = tokens(p, r, &it.first);
+    it.len = kv_length(p, r);
+    int64_t u = 0;
+    for (it.row0 = 0; it.row0 < it.qlen * p.group; it.row0 += ROWS) {
+      range(p, it);
+      u += it.tiles;
+    }
+    return u * p.g.heads;
+  }
+  __device__ __forceinline__ static void next(const AttnParams& p, Item& it) {
+    if (++it.h < p.g.heads) return;
+    it.h = 0;
+    it.row0 += ROWS;
+    if (it.row0 >= it.qlen * p.group) {
+      it.row0 = 0;
+      do {
+        if (++it.r >= p.B) return;       // past the last unit: never read
+        it.qlen = tokens(p, it.r, &it.first);
+      } while (it.qlen == 0);
+      it.len = kv_length(p, it.r);
+    }
+    range(p, it);
+  }
+  // The units before every of the block's NTH chunks of requests, pre[NTH] in all
+  // (every thread of the block calls it).  The warps' sums lie behind them: NTH + 1 + NTH / 32
+  // entries, in the caller's dynamic shared memory (static shared memory in front of it would
+  // shift it off the alignment that swizzled operands need).
+  template <int NTH>
+  __device__ __forceinline__ static void sum_units(const AttnParams& p, int64_t* pre) {
+    int64_t* wsum = pre + NTH + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int chunk = (p.B + NTH - 1) / NTH;
+    Item it;
+    int64_t u = 0;
+    for (int i = 0; i < chunk; ++i) {
+      const int r = threadIdx.x * chunk + i;
+      if (r < p.B) u += units(p, r, it);
+    }
+    int64_t inc = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t base = 0;
+    for (int i = 0; i < warp; ++i) base += wsum[i];
+    pre[threadIdx.x] = base + inc - u;
+    if (threadIdx.x == NTH - 1) pre[NTH] = base + inc;
+    __syncthreads();
+  }
+  // the item that unit u lies in, and the unit at which it starts
+  template <int NTH>
+  __device__ __forceinline__ static int64_t seek(const AttnParams& p, const int64_t* pre, int64_t u,
+                                                 Item& it) {
+    const int chunk = (p.B + NTH - 1) / NTH;
+    int lo = 0, hi = NTH;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    int64_t iu = pre[lo];
+    for (int r = lo * chunk;; ++r) {
+      const int64_t n = units(p, r, it);
+      if (u < iu + n) break;
+      iu += n;
+    }
+    it.h = 0;
+    it.row0 = 0;
+    range(p, it);
+    while (u >= iu + it.tiles) {
+      iu += it.tiles;
+      next(p, it);
+    }
+    return iu;
+  }
+};
+
+// The line of U units is cut into N <= U equal shares: share w is [U w / N, U (w + 1) / N).
+__device__ __forceinline__ int share_of(int64_t u, int64_t N, int64_t U) {
+  return (int)(((u + 1) * N + U - 1) / U - 1);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kNone = -1e30f;           // the running maximum of a row that has seen nothing
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
+
+template <int DT>
+__device__ __forceinline__ void store_dims4(void* out, int64_t at, const float (&x)[4]) {
+  if (DT == DQ_F32) {
+    *(float4*)((float*)out + at) = make_float4(x[0], x[1], x[2], x[3]);
+  } else if (DT == DQ_F16) {
+    *(uint2*)((__half*)out + at) = make_uint2(h2_as_u32(__floats2half2_rn(x[0], x[1])),
+                                              h2_as_u32(__floats2half2_rn(x[2], x[3])));
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *(uint2*)((__nv_bfloat16*)out + at) = make_uint2(*(const uint32_t*)&a, *(const uint32_t*)&b);
+  }
+}
+__device__ __forceinline__ void store_out4(const AttnParams& p, int64_t at, const float (&x)[4]) {
+  if (p.out_dtype == DQ_BF16) store_dims4<DQ_BF16>(p.out, at, x);
+  else if (p.out_dtype == DQ_F16) store_dims4<DQ_F16>(p.out, at, x);
+  else store_dims4<DQ_F32>(p.out, at, x);
 }
 
 }  // namespace dqmoe

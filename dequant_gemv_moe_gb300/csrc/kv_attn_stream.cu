@@ -51,7 +51,7 @@ struct StreamCfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int STG = kBlks * KvBlk<D>::BYTES;
   static constexpr int OFF_PRE = 1024;                              // int64 [513]
-  static constexpr int OFF_RING = OFF_PRE + 4352;
+  static constexpr int OFF_RING = OFF_PRE + 4352;                   // (NTH + 1 + NTH / 32) * 8 at most
   static constexpr int SMEM = OFF_RING + NW * kStages * STG;
   static_assert(SMEM <= 232448, "shared memory");
 };
@@ -74,12 +74,6 @@ __device__ __forceinline__ StreamWs stream_ws(uint8_t* ws) {
   return w;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -98,62 +92,6 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
   }
 }
 
-// One row tile of a request and the tokens that its rows may see.
-struct Item {
-  int r, h, row0, rows;        // request, K/V head, first row (token * group + head), rows
-  int len, qlen, first;        // kv length, tokens of the request, its first row of q
-  int begin, end;              // tokens that some row sees
-  int t0, tiles;               // first tile, tiles (at least one)
-};
-
-template <int ROWS>
-__device__ __forceinline__ void item_range(const AttnParams& p, int len, int n, int row0, Item& it) {
-  const int rows = min(ROWS, n * p.group - row0);
-  const int lo = len - n + row0 / p.group, hi = len - n + (row0 + rows - 1) / p.group;
-  it.rows = rows;
-  it.end = p.causal ? min(len, hi + 1) : len;
-  it.begin = p.window > 0 ? max(0, lo - p.window + 1) : 0;
-  it.t0 = it.begin / kTile;
-  it.tiles = it.end > it.begin ? (it.end + kTile - 1) / kTile - it.t0 : 1;
-}
-
-// units of one request
-template <int ROWS>
-__device__ __forceinline__ int64_t request_units(const AttnParams& p, int r, int* n_out, int* len_out) {
-  int first;
-  const int n = q_rows(p, r, &first), len = kv_length(p, r);
-  *n_out = n;
-  *len_out = len;
-  int64_t u = 0;
-  Item it;
-  for (int row0 = 0; row0 < n * p.group; row0 += ROWS) {
-    item_range<ROWS>(p, len, n, row0, it);
-    u += it.tiles;
-  }
-  return u * p.g.heads;
-}
-
-template <int DT>
-__device__ __forceinline__ void store_dims4(void* out, int64_t at, const float (&x)[4]) {
-  if (DT == DQ_F32) {
-    *(float4*)((float*)out + at) = make_float4(x[0], x[1], x[2], x[3]);
-  } else if (DT == DQ_F16) {
-    *(uint2*)((__half*)out + at) = make_uint2(h2_as_u32(__floats2half2_rn(x[0], x[1])),
-                                              h2_as_u32(__floats2half2_rn(x[2], x[3])));
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *(uint2*)((__nv_bfloat16*)out + at) = make_uint2(*(const uint32_t*)&a, *(const uint32_t*)&b);
-  }
-}
-
-__device__ __forceinline__ void store_out4(const AttnParams& p, int64_t at, const float (&x)[4]) {
-  if (p.out_dtype == DQ_BF16) store_dims4<DQ_BF16>(p.out, at, x);
-  else if (p.out_dtype == DQ_F16) store_dims4<DQ_F16>(p.out, at, x);
-  else store_dims4<DQ_F32>(p.out, at, x);
-}
-
-constexpr float kNone = -1e30f;           // M of a row that has seen nothing
-
 template <int D, int NT>
 __global__ void __launch_bounds__(StreamCfg<D, NT>::NW * 32, 1)
 kv_stream_kernel(const __grid_constant__ AttnParams p) {
@@ -171,31 +109,9 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   pdl_wait();
   pdl_trigger();
 
-  // units before every chunk of requests
   constexpr int NTH = C::NW * 32;
-  const int chunk = (p.B + NTH - 1) / NTH;
-  {
-    int64_t u = 0;
-    int n, len;
-    for (int i = 0; i < chunk; ++i) {
-      const int r = threadIdx.x * chunk + i;
-      if (r < p.B) u += request_units<C::ROWS>(p, r, &n, &len);
-    }
-    int64_t inc = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    __shared__ int64_t wsum[C::NW];
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int64_t base = 0;
-    for (int i = 0; i < warp; ++i) base += wsum[i];
-    pre[threadIdx.x] = base + inc - u;
-    if (threadIdx.x == NTH - 1) pre[NTH] = base + inc;
-    __syncthreads();
-  }
+  using Wk = Walk<C::ROWS, kTile>;
+  Wk::template sum_units<NTH>(p, pre);
   const int64_t U = pre[NTH];
   // at least one unit per warp of the CTAs that take part
   const int ctas = (int)min((int64_t)gridDim.x, (U + C::NW - 1) / C::NW);
@@ -210,53 +126,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   if (lane == 0) ws.desc[gw] = make_int4(0, 0, 0, 0);
   if (gw >= N) return;
 
-  // ---- the item that u0 lies in
   Item it;
-  int64_t iu;                              // unit at which the item starts
-  {
-    int lo = 0, hi = NTH;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= u0) lo = mid;
-      else hi = mid;
-    }
-    int r = lo * chunk, n = 0, len = 0;
-    iu = pre[lo];
-    for (;; ++r) {
-      const int64_t u = request_units<C::ROWS>(p, r, &n, &len);
-      if (u0 < iu + u) break;
-      iu += u;
-    }
-    it.r = r;
-    it.h = 0;
-    it.row0 = 0;
-    it.len = len;
-    it.qlen = n;
-    q_rows(p, r, &it.first);
-    item_range<C::ROWS>(p, len, n, 0, it);
-  }
-  // to the next item: head, then row tile, then request
-  auto next_item = [&](Item& x) {
-    if (++x.h < p.g.heads) return;
-    x.h = 0;
-    x.row0 += C::ROWS;
-    if (x.row0 < x.qlen * p.group) {
-      item_range<C::ROWS>(p, x.len, x.qlen, x.row0, x);
-      return;
-    }
-    x.row0 = 0;
-    do {
-      ++x.r;
-      if (x.r >= p.B) return;              // past the last unit: never read
-      x.qlen = q_rows(p, x.r, &x.first);
-    } while (x.qlen == 0);
-    x.len = kv_length(p, x.r);
-    item_range<C::ROWS>(p, x.len, x.qlen, 0, x);
-  };
-  while (u0 >= iu + it.tiles) {
-    iu += it.tiles;
-    next_item(it);
-  }
+  int64_t iu = Wk::template seek<NTH>(p, pre, u0, it);   // the unit at which the item starts
 
   // ---- producer state: the next unit to copy, its item, and 32 entries of its table row
   Item pi = it;
@@ -292,7 +163,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     }
     if (++pu == piu + pi.tiles && pu < u1) {
       piu += pi.tiles;
-      next_item(pi);
+      Wk::next(p, pi);
       tbase = -1;
     }
   };
@@ -347,7 +218,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
       const int e = mx > 0.f ? min(14 - ex, 100) : 0;
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float c = p.scale * 1.44269504088896341f * 16777216.f *
+      const float c = p.scale * kLog2e * 16777216.f *
                       __uint_as_float((uint32_t)(127 - e) << 23);
       float sum[G];
 #pragma unroll
@@ -619,18 +490,17 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             ws.ml[((int64_t)gw * 2 + slot) * C::ROWS + col] = make_float2(M[nt][i], sum);
           else if (p.lse)
             p.lse[qrow * p.n_q_heads + head] =
-                sum > 0.f ? (M[nt][i] + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+                sum > 0.f ? (M[nt][i] + log2f(sum)) * kLn2 : -INFINITY;
         }
       }
     if (from_start && !to_end && lane == 0) {
       // the item starts here and goes on in the next warps: how many of them
       const int64_t last = iu + it.tiles - 1;
-      const int wl = (int)(((last + 1) * N + U - 1) / U - 1);
-      ws.desc[gw] = make_int4(it.r, it.h, it.row0, ((wl - gw) << 1) | slot);
+      ws.desc[gw] = make_int4(it.r, it.h, it.row0, ((share_of(last, N, U) - gw) << 1) | slot);
     }
     if (!(from_start && to_end)) slot = 1;
     iu += it.tiles;
-    if (u < u1) next_item(it);
+    if (u < u1) Wk::next(p, it);
   }
 }
 
@@ -721,7 +591,7 @@ __global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_const
         }
         if (lane == 0 && p.lse)
           p.lse[qrow * p.n_q_heads + head] =
-              lt > 0.f ? (mt + log2f(lt)) * 0.693147180559945309f : -INFINITY;
+              lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
       }
       __syncthreads();
     }
@@ -750,7 +620,7 @@ int launch_stream(const AttnParams& p, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv_stream_workspace(int) { return kStreamO + kStreamMl + kStreamDesc; }
+size_t kv_stream_workspace() { return kStreamO + kStreamMl + kStreamDesc; }
 
 int launch_kv_stream(const AttnParams& p, int head_dim, cudaStream_t s) {
   int dev = 0, sms = 0;
@@ -759,7 +629,7 @@ int launch_kv_stream(const AttnParams& p, int head_dim, cudaStream_t s) {
     return DQ_ERR_CUDA;
   const int ctas = std::min(sms, kMaxCtas);
   // more than 8 rows per K/V head: 16 at a time where the registers allow it
-  const bool two = (int64_t)p.max_q_len * p.group > 8;
+  const bool two = std::min<int64_t>((int64_t)p.max_q_len * p.group, p.rows_upto) > 8;
   if (head_dim == 64) return two ? launch_stream<64, 2>(p, ctas, s) : launch_stream<64, 1>(p, ctas, s);
   if (head_dim == 128)
     return two ? launch_stream<128, 2>(p, ctas, s) : launch_stream<128, 1>(p, ctas, s);

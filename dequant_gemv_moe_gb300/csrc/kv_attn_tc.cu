@@ -1,0 +1,711 @@
+// kv_attn_tc.cu — attention of many query rows (prompts and chunks of prompts)
+// over the 4-bit paged cache, on the 5th-generation tensor core.
+//
+// Mathematics.  A CTA holds up to 256 rows of one K/V head (two 128-row tiles;
+// one for head_dim 256) and walks tiles of 128 (64) tokens: S = Q K^T in tensor
+// memory, p = 2^(s - M) per row, O += P V with P read from tensor memory.  With
+// this many rows the codes are decoded once per tile for all of them:
+// * K and V become fp16 values (c - 8) d, one rounding, in 128-byte swizzled
+//   panels of 64 values; V's panel keeps its token rows and is read with N along
+//   the row.  The V columns stay in the order in which the codes lie in their
+//   words; the output is put in order when it is stored.
+// * Q rows are scaled by a power of two into fp16 (exact but for values 2^-28
+//   below the row's largest); the factor comes back with the softmax's scale.
+// * M is a row's maximum less 8, renewed only when a score passes it by 12: fp16
+//   weights stay between 2^8 and 2^12 at the top, and O, which lives in tensor
+//   memory, is rescaled a few times per row at most.  Rounding K, V and p to
+//   fp16 (2^-11 each) is the price of 16-bit operands; S, M, the sum of p and O
+//   are fp32.
+//
+// Roles.  Warp groups of the row tiles do the softmax (a thread per row); four
+// warps decode; one warp copies the pages' blocks (bulk copies, 32 tokens at a
+// time); one thread issues the products in the order S0 S1 | PV0 S0' PV1 S1' | ...,
+// so that one row tile's softmax runs beside the other's products.  (One row
+// tile: two score buffers take turns.)
+//
+// Work is shared as in kv_attn_stream.cu: the line of all (request, row tile,
+// head, token tile) units in equal shares, one per CTA, the partials of items
+// that cross shares joined in order by a second kernel.
+#include <algorithm>
+
+#include "kv_attn.h"
+#include "tc.cuh"
+
+namespace dqmoe {
+
+namespace {
+
+constexpr int kMaxCtas = 160;
+constexpr int kPiece = 32;                 // tokens per copy stage
+
+template <int D>
+struct TcCfg {
+  static constexpr int NQ = D == 256 ? 1 : 2;        // 128-row tiles
+  static constexpr int TT = D == 256 ? 64 : 128;     // tokens per tile
+  static constexpr int ROWS = 128 * NQ;
+  static constexpr int Q_TILE = 128 * D * 2;
+  static constexpr int KV_BUF = TT * D * 2;
+  static constexpr int PIECE_B = kPiece / kKvBlk * KvBlk<D>::BYTES;
+  static constexpr int RS = D == 64 ? 8 : D == 128 ? 6 : 3;
+  static constexpr int OFF_PRE = 1024;
+  static constexpr int OFF_Q = 5120;
+  static constexpr int OFF_K = OFF_Q + NQ * Q_TILE;
+  static constexpr int OFF_V = OFF_K + 2 * KV_BUF;
+  static constexpr int OFF_RAW = OFF_V + 2 * KV_BUF;
+  static constexpr int SMEM = OFF_RAW + RS * PIECE_B;
+  static constexpr int DEC0 = 4 * NQ;                // first decoding warp
+  static constexpr int PROD = DEC0 + 4, MMA = DEC0 + 5;
+  static constexpr int NTH = 32 * (DEC0 + 6);
+  // tensor memory columns: O of every row tile, then two score buffers
+  static constexpr int COL_S = NQ * D;
+  static_assert(COL_S + 2 * TT <= 512, "tensor memory");
+  static_assert((NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE && SMEM <= 232448, "shared memory");
+};
+
+constexpr size_t kTcO = (size_t)kMaxCtas * 2 * 256 * 128 * 4;   // ROWS * D is at most 256 * 128
+constexpr size_t kTcMl = (size_t)kMaxCtas * 2 * 256 * 8;
+constexpr size_t kTcDesc = (size_t)kMaxCtas * 16;
+
+struct TcWs {
+  float* o;
+  float2* ml;
+  int4* desc;
+};
+__device__ __forceinline__ TcWs tc_ws(uint8_t* ws) {
+  TcWs w;
+  w.o = (float*)ws;
+  w.ml = (float2*)(ws + kTcO);
+  w.desc = (int4*)(ws + kTcO + kTcMl);
+  return w;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  // the values pass through the wait: nothing that uses them can move before it
+#define DQ_R4(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : DQ_R4(0), DQ_R4(4), DQ_R4(8), DQ_R4(12), DQ_R4(16), DQ_R4(20), DQ_R4(24), DQ_R4(28)
+               :
+               : "memory");
+#undef DQ_R4
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory descriptor of an operand whose rows run along M / N (here V: the
+// row of a token holds 64 values of N): 128-byte swizzled panels of 64 values,
+// `panel` bytes apart, 8 tokens (K) every 1024 bytes.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(panel >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kBRowsAlongN = 1u << 16;
+
+// the 8 codes of a word as (c - 8) d: four pairs, in the order of the nibble pairs
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 d) {
+  const __half2 bias = u32_as_h2(0x64086408u);        // 1032
+  const __half2 sixteenth = u32_as_h2(0x2C002C00u), m72 = u32_as_h2(0xD480D480u);
+  const uint32_t w8 = w >> 8, magic = 0x64006400u;
+  uint4 r;
+  r.x = h2_as_u32(__hmul2(__hsub2(u32_as_h2(lop3_and_or(w, 0x000F000Fu, magic)), bias), d));
+  r.y = h2_as_u32(__hmul2(__hfma2(u32_as_h2(lop3_and_or(w, 0x00F000F0u, magic)), sixteenth, m72), d));
+  r.z = h2_as_u32(__hmul2(__hsub2(u32_as_h2(lop3_and_or(w8, 0x000F000Fu, magic)), bias), d));
+  r.w = h2_as_u32(__hmul2(__hfma2(u32_as_h2(lop3_and_or(w8, 0x00F000F0u, magic)), sixteenth, m72), d));
+  return r;
+}
+
+__device__ __forceinline__ void sts_u128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
+  if (W == 4) {
+    const uint4 x = lds_u128(addr);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else {
+    const uint2 x = lds_u64(addr);
+    v[0] = x.x; v[1] = x.y;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
+  using C = TcCfg<D>;
+  using B = KvBlk<D>;
+  using Wk = Walk<C::ROWS, C::TT>;
+  constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  pdl_wait();
+  pdl_trigger();
+  // the swizzle needs a window aligned to 1024 bytes: the kernel has no static shared memory,
+  // which the linker would put in front of it
+  uint64_t* raw_full = (uint64_t*)smem;
+  uint64_t* raw_empty = raw_full + C::RS;
+  uint64_t* kv_full = raw_empty + C::RS;
+  uint64_t* kv_empty = kv_full + 2;
+  uint64_t* s_full = kv_empty + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* q_full = pv_done + 2;
+  uint32_t* tmem_slot = (uint32_t*)(q_full + 2);
+  int64_t* pre = (int64_t*)(smem + C::OFF_PRE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  Wk::template sum_units<C::NTH>(p, pre);
+  const int64_t U = pre[C::NTH];
+  const int64_t N = min((int64_t)gridDim.x, U);
+  const TcWs ws = tc_ws(p.ws);
+  if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (blockIdx.x >= N) return;
+  const int64_t u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::RS; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kv_full[i], 128);
+      mbar_init(&kv_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&q_full[i], 128);
+    }
+    fence_barrier_init();
+  }
+  if (warp == C::MMA) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t qs = smem_u32(smem + C::OFF_Q), ks = smem_u32(smem + C::OFF_K),
+                 vs = smem_u32(smem + C::OFF_V);
+
+  Item it;
+  int64_t iu = Wk::template seek<C::NTH>(p, pre, u0, it);
+  bool ok = true;
+
+  if (warp < C::DEC0) {
+    // ------------------------------ softmax ------------------------------
+    const int tile = warp >> 2;            // row tile
+    const int trow = 32 * (warp & 3) + lane;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t o_addr = tmem + lane_base + (uint32_t)(tile * D);
+    const uint32_t qrow = qs + tile * C::Q_TILE;
+    int slot = 0;                          // of this CTA's partials
+    int64_t gt = 0;                        // tiles so far
+    for (int64_t u = u0; u < u1;) {
+      const int64_t ue = min(u1, iu + it.tiles);
+      const bool from_start = u == iu, to_end = ue == iu + it.tiles;
+      // the row
+      const int row = it.row0 + tile * 128 + trow;
+      const bool live = tile * 128 + trow < it.rows;
+      const int tokq = row / p.group, uq = row - tokq * p.group;
+      const int64_t q_at = it.first + tokq;
+      const int head = it.h * p.group + uq;
+      float cf;
+      {
+        const uint4* src = (const uint4*)((const uint16_t*)p.q + q_at * p.q_stride + (int64_t)head * D);
+        float mx = 0.f;
+        constexpr int CH = D / 8;
+        uint4 raw[CH < 16 ? CH : 16];
+        for (int c0 = 0; c0 < CH; c0 += 16) {
+#pragma unroll
+          for (int c = 0; c < (CH < 16 ? CH : 16); ++c) {
+            raw[c] = live ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 f;
+              if (p.q_dtype == DQ_BF16)
+                f = make_float2(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xFFFF0000u));
+              else
+                f = __half22float2(u32_as_h2(w4[i]));
+              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+        }
+        // 2^e with 2^14 <= max * 2^e < 2^15
+        const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
+        const int e = mx > 0.f ? min(14 - ex, 100) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        cf = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
+        for (int c0 = 0; c0 < CH; c0 += 16) {
+#pragma unroll
+          for (int c = 0; c < (CH < 16 ? CH : 16); ++c) {
+            if (CH > 16) raw[c] = live ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+            uint32_t r4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 f;
+              if (p.q_dtype == DQ_BF16)
+                f = make_float2(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xFFFF0000u));
+              else
+                f = __half22float2(u32_as_h2(w4[i]));
+              r4[i] = h2_as_u32(__floats2half2_rn(f.x * up, f.y * up));
+            }
+            sts_u128(qrow + (c0 + c) / 8 * 16384 + sw128_offset(trow, (c0 + c) & 7),
+                     make_uint4(r4[0], r4[1], r4[2], r4[3]));
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[tile]);
+      }
+      const int pos = it.len - it.qlen + tokq;
+      const int hi = p.causal ? min(it.len, pos + 1) : it.len;
+      const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+      int lo_all, hi_all;
+      {
+        const int pa = it.len - it.qlen + (it.row0 + tile * 128) / p.group;
+        const int pb = it.len - it.qlen + (it.row0 + min(it.rows, tile * 128 + 128) - 1) / p.group;
+        hi_all = p.causal ? min(it.len, pa + 1) : it.len;
+        lo_all = p.window > 0 ? max(0, pb - p.window + 1) : 0;
+      }
+      float M = kNone, l = 0.f;
+      for (int64_t j = u; j < ue; ++j, ++gt) {
+        const int tok0 = (it.t0 + (int)(j - iu)) * TT;
+        const int sl = NQ == 2 ? tile : (int)(gt & 1);
+        const int ph = NQ == 2 ? (int)(gt & 1) : (int)((gt >> 1) & 1);
+        ok = ok && mbar_wait(&s_full[sl], ph);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
+        const bool inner = tok0 >= lo_all && tok0 + TT <= hi_all;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < TT / 32; ++c) {
+          float v[32];
+          tmem_ld32(s_addr + 32 * c, v);
+          if (!inner) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int a = tok0 + 32 * c + i;
+              v[i] = a >= lo && a < hi ? v[i] : -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+        }
+        mx *= cf;
+        const bool over = mx > M + 12.f;
+        if (__any_sync(0xffffffffu, over)) {
+          const float mn = over ? mx - 8.f : M;
+          const float corr = ex2(M - mn);
+          M = mn;
+          l *= corr;
+          if (j > u) {
+            if (NQ == 1) {                 // the product before this one may still be running
+              const int64_t b = gt - 1;
+              ok = mbar_wait(&pv_done[b & 1], (int)((b >> 1) & 1));
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            for (int c = 0; c < D / 32; ++c) {
+              float v[32];
+              tmem_ld32(o_addr + 32 * c, v);
+              uint4 a[4], b4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a[i] = make_uint4(__float_as_uint(v[4 * i] * corr), __float_as_uint(v[4 * i + 1] * corr),
+                                  __float_as_uint(v[4 * i + 2] * corr), __float_as_uint(v[4 * i + 3] * corr));
+                b4[i] = make_uint4(
+                    __float_as_uint(v[16 + 4 * i] * corr), __float_as_uint(v[16 + 4 * i + 1] * corr),
+                    __float_as_uint(v[16 + 4 * i + 2] * corr), __float_as_uint(v[16 + 4 * i + 3] * corr));
+              }
+              tmem_st16(o_addr + 32 * c, a);
+              tmem_st16(o_addr + 32 * c + 16, b4);
+            }
+          }
+        }
+        const float2 cf2 = make_float2(cf, cf), m2 = make_float2(-M, -M);
+        float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < TT / 32; ++c) {
+          float v[32];
+          tmem_ld32(s_addr + 32 * c, v);
+          if (!inner) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int a = tok0 + 32 * c + i;
+              v[i] = a >= lo && a < hi ? v[i] : -INFINITY;
+            }
+          }
+          uint4 w[4];
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 t = ffma2(make_float2(v[2 * i], v[2 * i + 1]), cf2, m2);
+            const float2 e = make_float2(ex2(t.x), ex2(t.y));
+            l2 = fadd2(l2, e);
+            pk[i] = h2_as_u32(__floats2half2_rn(e.x, e.y));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          tmem_st16(s_addr + 16 * c, w);   // over the scores that were read already
+        }
+        l += l2.x + l2.y;
+        tc_fence_before();
+        mbar_arrive(&p_full[sl]);
+      }
+      if (!ok) break;
+      // ---- the rows: whole, or a partial
+      {
+        const int64_t b = gt - 1;
+        const int sl = NQ == 2 ? tile : (int)(b & 1);
+        ok = mbar_wait(&pv_done[sl], NQ == 2 ? (int)(b & 1) : (int)((b >> 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const bool whole = from_start && to_end;
+        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * C::ROWS + tile * 128 + trow;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          tmem_ld32(o_addr + 32 * c, v);
+          if (live) {
+            // column 8 a + 2 n + k of panel w is value 4 a + n of group 2 w + k
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int a = 0; a < 4; ++a) {
+                const float x[4] = {v[8 * a + k] * inv, v[8 * a + 2 + k] * inv, v[8 * a + 4 + k] * inv,
+                                    v[8 * a + 6 + k] * inv};
+                const int dim = ((c & ~1) + k) * 32 + (c & 1) * 16 + 4 * a;
+                if (whole)
+                  store_out4(p, q_at * p.out_stride + (int64_t)head * D + dim, x);
+                else
+                  *(float4*)(ws.o + part * D + dim) = make_float4(x[0], x[1], x[2], x[3]);
+              }
+          }
+        }
+        if (live) {
+          if (!whole)
+            ws.ml[part] = make_float2(M, l);
+          else if (p.lse)
+            p.lse[q_at * p.n_q_heads + head] = l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+        }
+        tc_fence_before();
+        if (from_start && !to_end && threadIdx.x == 0)
+          ws.desc[blockIdx.x] = make_int4(
+              it.r, it.h, it.row0,
+              ((share_of(iu + it.tiles - 1, N, U) - (int)blockIdx.x) << 1) | slot);
+        if (!whole) slot = 1;
+      }
+      u = ue;
+      iu += it.tiles;
+      if (u < u1) Wk::next(p, it);
+    }
+  } else if (warp < C::PROD) {
+    // ------------------------------ decoding ------------------------------
+    const int dw = warp - C::DEC0;
+    const int blk = dw >> 1, half = dw & 1;
+    int64_t gt = 0, piece = 0;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int64_t ue = min(u1, iu + it.tiles);
+      for (int64_t j = u; j < ue && ok; ++j, ++gt) {
+        const int tok0 = (it.t0 + (int)(j - iu)) * TT;
+        const bool inner = tok0 >= it.begin && tok0 + TT <= it.end;
+        const int buf = (int)(gt & 1);
+        if (gt >= 2) ok = mbar_wait(&kv_empty[buf], (int)(((gt >> 1) - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        const uint32_t kb = ks + buf * C::KV_BUF, vb = vs + buf * C::KV_BUF;
+        for (int pc = 0; pc < TT / kPiece && ok; ++pc, ++piece) {
+          const int st = (int)(piece % C::RS);
+          ok = mbar_wait(&raw_full[st], (int)((piece / C::RS) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t rb = smem_u32(smem + C::OFF_RAW + st * C::PIECE_B) + blk * B::BYTES;
+          const int row0 = pc * kPiece + blk * kKvBlk + half * 8;
+          {
+            // K: lane = (token, t); odd rows take their words in swapped order, so that 8 lanes'
+            // stores meet 8 different chunks
+            const int tl = lane >> 2, t = lane & 3;
+            const int tok = half * 8 + tl, row = row0 + tl;
+            const uint32_t odd = row & 1;
+#pragma unroll
+            for (int gh = 0; gh < GH; ++gh) {
+              uint32_t w[W], d[W / 2];
+              lds_words<W>(rb + ((gh * 16 + tok) * 4 + t) * W * 4, w);
+              if (W == 4) {
+                const uint2 x = lds_u64(rb + B::OFF_KD + 2 * (tok * G + gh * W));
+                d[0] = x.x;
+                d[W / 2 - 1] = x.y;
+              } else {
+                d[0] = lds_u32(rb + B::OFF_KD + 2 * tok * G);
+              }
+#pragma unroll
+              for (int i = 0; i < W; ++i) {
+                const uint32_t word = odd ? w[i ^ 1] : w[i];
+                const uint32_t hi = (i & 1) ^ odd;
+                const __half2 dd = u32_as_h2(__byte_perm(d[i / 2], 0, hi ? 0x3232 : 0x1010));
+                const int panel = (gh * W + i) / 2, chunk = hi * 4 + t;
+                sts_u128(kb + panel * (TT * 128) + sw128_offset(row, chunk), decode8(word, dd));
+              }
+            }
+          }
+          {
+            // V: lane = (a, t): tokens 2t and 2t + 1 of this half block, values 4a.. of every group
+            const int a = lane >> 2, t = lane & 3;
+            const int row = row0 + 2 * t;
+            const int at = tok0 + row;
+            uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
+            if (!inner) {
+              // a token that no row sees may hold anything: its scale becomes 0
+              keep0 = at >= it.begin && at < it.end ? 0xFFFFFFFFu : 0u;
+              keep1 = at + 1 >= it.begin && at + 1 < it.end ? 0xFFFFFFFFu : 0u;
+            }
+#pragma unroll
+            for (int gh = 0; gh < GH; ++gh) {
+              uint32_t w[W];
+              lds_words<W>(rb + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, w);
+#pragma unroll
+              for (int k = 0; k < W / 2; ++k) {
+                const int wp = gh * (W / 2) + k;
+                const uint32_t x = lds_u32(rb + B::OFF_VD + ((t * G + 2 * wp) * 4 + half * 2) * 2);
+                const uint32_t y = lds_u32(rb + B::OFF_VD + ((t * G + 2 * wp + 1) * 4 + half * 2) * 2);
+                const __half2 d0 = u32_as_h2(__byte_perm(x, y, 0x5410) & keep0);
+                const __half2 d1 = u32_as_h2(__byte_perm(x, y, 0x7632) & keep1);
+                sts_u128(vb + wp * (TT * 128) + sw128_offset(row, a), decode8(w[k], d0));
+                sts_u128(vb + wp * (TT * 128) + sw128_offset(row + 1, a), decode8(w[W / 2 + k], d1));
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_empty[st]);
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        mbar_arrive(&kv_full[buf]);
+      }
+      u = ue;
+      iu += it.tiles;
+      if (u < u1) Wk::next(p, it);
+    }
+  } else if (warp == C::PROD) {
+    // ------------------------------ copies ------------------------------
+    const uint64_t pol = l2_evict_first_policy();
+    const int shift = p.g.page_shift;
+    int64_t piece = 0;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const int64_t ue = min(u1, iu + it.tiles);
+      int tbase = -1, tent = 0;
+      for (int64_t j = u; j < ue && ok; ++j) {
+        const int tok0 = (it.t0 + (int)(j - iu)) * TT;
+        for (int pc = 0; pc < TT / kPiece && ok; ++pc, ++piece) {
+          const int st = (int)(piece % C::RS);
+          if (piece >= C::RS) ok = mbar_wait(&raw_empty[st], (int)((piece / C::RS - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], C::PIECE_B);
+          __syncwarp();
+          const int tok = tok0 + pc * kPiece;
+          int run = 0;
+          while (run < kPiece) {
+            const int pg = (tok + run) >> shift;
+            if (tbase < 0 || pg < tbase || pg >= tbase + 32) {
+              tbase = pg;
+              const int e = pg + lane;
+              tent = e < p.max_pages ? __ldg(p.table + (int64_t)it.r * p.max_pages + e) : 0;
+              if (tent < 0 || tent >= p.g.n_pages) tent = 0;
+            }
+            const int page = __shfl_sync(0xffffffffu, tent, pg - tbase);
+            const int cnt = min(p.g.page_size, kPiece - run);
+            const int off = (tok + run) & (p.g.page_size - 1);
+            if (lane == 0)
+              bulk_g2s(smem + C::OFF_RAW + st * C::PIECE_B + run / kKvBlk * B::BYTES,
+                       p.g.pages + (int64_t)page * p.g.page_bytes + it.h * p.g.head_bytes +
+                           off / kKvBlk * B::BYTES,
+                       cnt / kKvBlk * B::BYTES, &raw_full[st], pol);
+            run += cnt;
+          }
+        }
+      }
+      u = ue;
+      iu += it.tiles;
+      if (u < u1) Wk::next(p, it);
+    }
+  } else if (lane == 0) {
+    // ------------------------------ products ------------------------------
+    constexpr uint32_t id_s = idesc_f16_f32(128, TT);
+    constexpr uint32_t id_o = idesc_f16_f32(128, D) | kBRowsAlongN;
+    int64_t gt = 0;
+    int seg = 0;
+    auto slot_of = [&](int64_t g, int i) { return NQ == 2 ? i : (int)(g & 1); };
+    auto phase_of = [&](int64_t g) { return NQ == 2 ? (int)(g & 1) : (int)((g >> 1) & 1); };
+    // S of tile g and row tile i; its buffer's last weights must have been used
+    auto scores = [&](int64_t g, int i) {
+      const int sl = slot_of(g, i);
+      const int64_t before = g - (NQ == 2 ? 1 : 2);
+      if (before >= 0 && !mbar_wait(&pv_done[sl], phase_of(before))) return false;
+      if (!mbar_wait(&kv_full[g & 1], (int)((g >> 1) & 1))) return false;
+      tc_fence_after();
+      const uint32_t a = qs + i * C::Q_TILE, b = ks + (uint32_t)(g & 1) * C::KV_BUF;
+      const uint32_t d = tmem + (uint32_t)(C::COL_S + sl * TT);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc_mma_f16(d, sw128_kmajor_desc(a + (k >> 2) * 16384) + 2 * (k & 3),
+                   sw128_kmajor_desc(b + (k >> 2) * (TT * 128)) + 2 * (k & 3), id_s, k ? 1u : 0u);
+      tc_commit(&s_full[sl]);
+      return true;
+    };
+    auto weighted = [&](int64_t g, int i, bool first) {
+      const int sl = slot_of(g, i);
+      if (!mbar_wait(&p_full[sl], phase_of(g))) return false;
+      tc_fence_after();
+      const uint32_t a = tmem + (uint32_t)(C::COL_S + sl * TT);
+      const uint32_t b = vs + (uint32_t)(g & 1) * C::KV_BUF;
+#pragma unroll
+      for (int k = 0; k < TT / 16; ++k)
+        tc_mma_f16_tmem_a(tmem + (uint32_t)(i * D), a + 8 * k, sw128_mnmajor_desc(b + k * 2048, TT * 128),
+                          id_o, (first && k == 0) ? 0u : 1u);
+      tc_commit(&pv_done[sl]);
+      if (i == NQ - 1) tc_commit(&kv_empty[g & 1]);
+      return true;
+    };
+    for (int64_t u = u0; u < u1 && ok; ++seg) {
+      const int64_t ue = min(u1, iu + it.tiles);
+      const int nt = (int)(ue - u);
+      for (int i = 0; i < NQ && ok; ++i) {
+        ok = mbar_wait(&q_full[i], seg & 1);
+        ok = ok && scores(gt, i);
+      }
+      if (NQ == 1 && nt > 1) ok = ok && scores(gt + 1, 0);
+      for (int j = 0; j < nt && ok; ++j, ++gt) {
+        for (int i = 0; i < NQ && ok; ++i) {
+          ok = weighted(gt, i, j == 0);
+          const int ahead = NQ == 2 ? 1 : 2;
+          if (j + ahead < nt) ok = ok && scores(gt + ahead, i);
+        }
+      }
+      u = ue;
+      iu += it.tiles;
+      if (u < u1) Wk::next(p, it);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of the items that go over several CTAs' shares: CTA (c, y)
+// takes rows 8 y.. of the item that starts in CTA c's share and goes on behind it,
+// a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) kv_tc_join_kernel(const __grid_constant__ AttnParams p) {
+  using C = TcCfg<D>;
+  constexpr int V = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  const TcWs ws = tc_ws(p.ws);
+  const int4 d = __ldcg(ws.desc + blockIdx.x);
+  const int follow = d.w >> 1;
+  if (follow == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int first;
+  const int n = q_rows(p, d.x, &first);
+  const int col = blockIdx.y * 8 + warp;
+  if (col >= min(C::ROWS, n * p.group - d.z)) return;
+  auto part = [&](int i) -> int64_t {
+    return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? (d.w & 1) : 0)) * C::ROWS + col;
+  };
+  float m = kNone, l = 0.f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int i = lane; i <= follow; i += 32) m = fmaxf(m, __ldcg(ws.ml + part(i)).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 4
+  for (int i = 0; i <= follow; ++i) {
+    const int64_t at = part(i);
+    const float2 ml = __ldcg(ws.ml + at);
+    const float f = ex2(ml.x - m);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(__ldcg(ws.o + at * D + lane * V + v), f, acc[v]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int row = d.z + col, tokq = row / p.group, uq = row - tokq * p.group;
+  const int64_t qrow = first + tokq;
+  const int head = d.y * p.group + uq;
+  const int64_t base = qrow * p.out_stride + (int64_t)head * D;
+  // V values per lane, in fours; D = 64: two lanes' pairs make one four
+#pragma unroll
+  for (int v = 0; v < V; v += 4) {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = acc[V < 4 ? k & 1 : v + k] * inv;
+    if (V < 4) {
+      x[2] = __shfl_down_sync(0xffffffffu, x[0], 1);
+      x[3] = __shfl_down_sync(0xffffffffu, x[1], 1);
+    }
+    if (V >= 4 || (lane & 1) == 0) store_out4(p, base + lane * V + v, x);
+  }
+  if (lane == 0 && p.lse)
+    p.lse[qrow * p.n_q_heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+int launch_tc(const AttnParams& p, int ctas, cudaStream_t s) {
+  using C = TcCfg<D>;
+  static bool attr[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ERR_CUDA;
+  if (dev >= 64 || !attr[dev]) {
+    if (cudaFuncSetAttribute(kv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+      return DQ_ERR_CUDA;
+    if (dev < 64) attr[dev] = true;
+  }
+  if (launch_pdl(kv_tc_kernel<D>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) != cudaSuccess)
+    return DQ_ERR_CUDA;
+  if (launch_pdl(kv_tc_join_kernel<D>, dim3(ctas, C::ROWS / 8), dim3(256), 0, s, 0, p) != cudaSuccess)
+    return DQ_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t kv_tc_workspace() { return kTcO + kTcMl + kTcDesc; }
+
+int launch_kv_tc(const AttnParams& p, int head_dim, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DQ_ERR_CUDA;
+  const int ctas = std::min(sms, kMaxCtas);
+  if (head_dim == 64) return launch_tc<64>(p, ctas, s);
+  if (head_dim == 128) return launch_tc<128>(p, ctas, s);
+  return launch_tc<256>(p, ctas, s);
+}
+
+}  // namespace dqmoe

@@ -452,6 +452,9 @@ int dq_stage(void* dst, const void* src, int64_t bytes, void* stream);
 /*   operand register with one AND).  Blocks of a head in a page are          */
 /*   consecutive, so a run of tokens is one contiguous copy.                  */
 /* Bytes that no append wrote may hold anything: no result depends on them.   */
+/* A scale is at most 8188 in magnitude, as dq_kv_append writes it (values     */
+/* saturate at 65504 = 8 * 8188, the largest fp16): larger ones, which only a   */
+/* foreign writer could leave, are out of contract for dq_kv_attention.        */
 /* ------------------------------------------------------------------------ */
 typedef struct {
   int32_t fmt;          /* DQ_Q4_0; other formats: DQ_ERR_UNSUPPORTED */

@@ -190,7 +190,8 @@ class Case:
         ids = rng.permutation(used)
         self.table = np.full((B, width), -1, dtype=np.int32)
         cache = rng.integers(0, 256, (used, n_kv, ps // 16, 18 * D), dtype=np.uint8)
-        d = (rng.standard_normal((used, n_kv, ps // 16, D)) * 0.15 * skew).astype(np.float16)
+        # a scale that an append can write is at most 65504 / 8
+        d = np.clip(rng.standard_normal((used, n_kv, ps // 16, D)) * 0.15 * skew, -8188, 8188).astype(np.float16)
         live = np.zeros((used, ps), dtype=bool)
         at = 0
         for r in range(B):
