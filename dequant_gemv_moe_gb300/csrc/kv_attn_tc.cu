@@ -47,7 +47,7 @@ struct TcCfg {
   static constexpr int KV_BUF = TT * D * 2;
   static constexpr int PIECE_B = kPiece / kKvBlk * KvBlk<D>::BYTES;
   static constexpr int RS = D == 64 ? 8 : D == 128 ? 6 : 3;
-  static constexpr int OFF_PRE = 1024;
+  static constexpr int OFF_PRE = 512;
   static constexpr int OFF_Q = 5120;
   static constexpr int OFF_K = OFF_Q + NQ * Q_TILE;
   static constexpr int OFF_V = OFF_K + 2 * KV_BUF;
@@ -79,8 +79,8 @@ __device__ __forceinline__ TcWs tc_ws(uint8_t* ws) {
   return w;
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
+// 32 columns of this thread's lane; the values are there after tmem_wait_ld and tmem_use.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
       "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
@@ -91,17 +91,41 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
-  // the values pass through the wait: nothing that uses them can move before it
-#define DQ_R4(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : DQ_R4(0), DQ_R4(4), DQ_R4(8), DQ_R4(12), DQ_R4(16), DQ_R4(20), DQ_R4(24), DQ_R4(28)
-               :
-               : "memory");
-#undef DQ_R4
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// The values pass through here after the wait: nothing that uses them can move before it.
+__device__ __forceinline__ void tmem_use(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
+                   "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 // Shared-memory descriptor of an operand whose rows run along M / N (here V: the
 // row of a token holds 64 values of N): 128-byte swizzled panels of 64 values,
 // `panel` bytes apart, 8 tokens (K) every 1024 bytes.
@@ -295,21 +319,36 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
         const bool inner = tok0 >= lo_all && tok0 + TT <= hi_all;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < TT / 32; ++c) {
-          float v[32];
-          tmem_ld32(s_addr + 32 * c, v);
+        // The maximum, 32 columns at a time, the next ones on their way; the last ones stay for
+        // the weights, which are made from the right: those of columns 32 c.. go to columns
+        // TT / 2 + 16 c.., over scores that were read already.
+        constexpr int NC = TT / 32;
+        uint32_t r[2][32];
+        auto masked = [&](uint32_t* v, int c) {
           if (!inner) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int a = tok0 + 32 * c + i;
-              v[i] = a >= lo && a < hi ? v[i] : -INFINITY;
+              v[i] = a >= lo && a < hi ? v[i] : 0xFF800000u;
             }
           }
+        };
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld32(s_addr, r[0]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, v[i]);
+        for (int c = 0; c < NC; ++c) {
+          uint32_t* v = r[c & 1];
+          tmem_wait_ld();
+          tmem_use(v);
+          if (c + 1 < NC) tmem_ld32(s_addr + 32 * (c + 1), r[(c + 1) & 1]);
+          masked(v, c);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx4[k] = fmaxf(mx4[k], fmaxf(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1])));
         }
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         mx *= cf;
         const bool over = mx > M + 12.f;
         if (__any_sync(0xffffffffu, over)) {
@@ -325,51 +364,42 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
               if (!ok) break;
               tc_fence_after();
             }
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              float v[32];
+              uint32_t v[32];
               tmem_ld32(o_addr + 32 * c, v);
-              uint4 a[4], b4[4];
+              tmem_wait_ld();
+              tmem_use(v);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] = make_uint4(__float_as_uint(v[4 * i] * corr), __float_as_uint(v[4 * i + 1] * corr),
-                                  __float_as_uint(v[4 * i + 2] * corr), __float_as_uint(v[4 * i + 3] * corr));
-                b4[i] = make_uint4(
-                    __float_as_uint(v[16 + 4 * i] * corr), __float_as_uint(v[16 + 4 * i + 1] * corr),
-                    __float_as_uint(v[16 + 4 * i + 2] * corr), __float_as_uint(v[16 + 4 * i + 3] * corr));
-              }
-              tmem_st16(o_addr + 32 * c, a);
-              tmem_st16(o_addr + 32 * c + 16, b4);
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
+              tmem_st32(o_addr + 32 * c, v);
             }
           }
         }
         const float2 cf2 = make_float2(cf, cf), m2 = make_float2(-M, -M);
-        float2 l2 = make_float2(0.f, 0.f);
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < TT / 32; ++c) {
-          float v[32];
-          tmem_ld32(s_addr + 32 * c, v);
-          if (!inner) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int a = tok0 + 32 * c + i;
-              v[i] = a >= lo && a < hi ? v[i] : -INFINITY;
-            }
+        for (int c = NC - 1; c >= 0; --c) {
+          uint32_t* v = r[c & 1];
+          if (c < NC - 1) {
+            tmem_wait_ld();
+            tmem_use(v);
           }
-          uint4 w[4];
-          uint32_t pk[16];
+          if (c > 0) tmem_ld32(s_addr + 32 * (c - 1), r[(c - 1) & 1]);
+          if (c < NC - 1) masked(v, c);
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 t = ffma2(make_float2(v[2 * i], v[2 * i + 1]), cf2, m2);
+            const float2 t =
+                ffma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cf2, m2);
             const float2 e = make_float2(ex2(t.x), ex2(t.y));
-            l2 = fadd2(l2, e);
-            pk[i] = h2_as_u32(__floats2half2_rn(e.x, e.y));
+            l2[i & 1] = fadd2(l2[i & 1], e);
+            w[i] = h2_as_u32(__floats2half2_rn(e.x, e.y));
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-          tmem_st16(s_addr + 16 * c, w);   // over the scores that were read already
+          tmem_st16(s_addr + TT / 2 + 16 * c, w);
         }
-        l += l2.x + l2.y;
+        l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[sl]);
       }
@@ -387,8 +417,13 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * C::ROWS + tile * 128 + trow;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(o_addr + 32 * c, r);
+          tmem_wait_ld();
+          tmem_use(r);
           float v[32];
-          tmem_ld32(o_addr + 32 * c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           if (live) {
             // column 8 a + 2 n + k of panel w is value 4 a + n of group 2 w + k
 #pragma unroll
@@ -508,7 +543,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       iu += it.tiles;
       if (u < u1) Wk::next(p, it);
     }
-  } else if (warp == C::PROD) {
+  } else {
+    if (warp == C::PROD) {
     // ------------------------------ copies ------------------------------
     const uint64_t pol = l2_evict_first_policy();
     const int shift = p.g.page_shift;
@@ -551,7 +587,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       iu += it.tiles;
       if (u < u1) Wk::next(p, it);
     }
-  } else if (lane == 0) {
+    } else if (warp == C::MMA && lane == 0) {
     // ------------------------------ products ------------------------------
     constexpr uint32_t id_s = idesc_f16_f32(128, TT);
     constexpr uint32_t id_o = idesc_f16_f32(128, D) | kBRowsAlongN;
@@ -579,7 +615,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const int sl = slot_of(g, i);
       if (!mbar_wait(&p_full[sl], phase_of(g))) return false;
       tc_fence_after();
-      const uint32_t a = tmem + (uint32_t)(C::COL_S + sl * TT);
+      const uint32_t a = tmem + (uint32_t)(C::COL_S + sl * TT + TT / 2);
       const uint32_t b = vs + (uint32_t)(g & 1) * C::KV_BUF;
 #pragma unroll
       for (int k = 0; k < TT / 16; ++k)
@@ -607,6 +643,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       u = ue;
       iu += it.tiles;
       if (u < u1) Wk::next(p, it);
+    }
     }
   }
   tc_fence_before();
@@ -651,7 +688,11 @@ __global__ void __launch_bounds__(256) kv_tc_join_kernel(const __grid_constant__
     const float f = ex2(ml.x - m);
     l = fmaf(ml.y, f, l);
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(__ldcg(ws.o + at * D + lane * V + v), f, acc[v]);
+    for (int v = 0; v < V; v += 2) {
+      const float2 x = __ldcg((const float2*)(ws.o + at * D + lane * V + v));
+      acc[v] = fmaf(x.x, f, acc[v]);
+      acc[v + 1] = fmaf(x.y, f, acc[v + 1]);
+    }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int row = d.z + col, tokq = row / p.group, uq = row - tokq * p.group;
