@@ -2,7 +2,7 @@
 // over the 4-bit paged cache, on the 5th-generation tensor core.
 //
 // Mathematics.  A CTA holds up to 256 rows of one K/V head (two 128-row tiles;
-// one for head_dim 256) and walks tiles of 128 (64) tokens: S = Q K^T in tensor
+// one for head_dim 256) and walks tiles of 64 tokens: S = Q K^T in tensor
 // memory, p = 2^(s - M) per row, O += P V with P read from tensor memory.  With
 // this many rows the codes are decoded once per tile for all of them:
 // * K and V become fp16 values (c - 8) d, one rounding, in 128-byte swizzled
@@ -19,9 +19,9 @@
 //
 // Roles.  Warp groups of the row tiles do the softmax (a thread per row); four
 // warps decode; one warp copies the pages' blocks (bulk copies, 32 tokens at a
-// time); one thread issues the products in the order S0 S1 | PV0 S0' PV1 S1' | ...,
-// so that one row tile's softmax runs beside the other's products.  (One row
-// tile: two score buffers take turns.)
+// time); one thread issues the products.  Every row tile has two score buffers, which
+// take turns: while a row's thread works on one tile, the products of the one before
+// and the scores of the one after run.
 //
 // Work is shared as in kv_attn_stream.cu: the line of all (request, row tile,
 // head, token tile) units in equal shares, one per CTA, the partials of items
@@ -41,7 +41,8 @@ constexpr int kPiece = 32;                 // tokens per copy stage
 template <int D>
 struct TcCfg {
   static constexpr int NQ = D == 256 ? 1 : 2;        // 128-row tiles
-  static constexpr int TT = D == 256 ? 64 : 128;     // tokens per tile
+  static constexpr int TT = 64;                      // tokens per tile
+  static constexpr int KVS = D == 256 ? 2 : 4;       // decoded tiles
   static constexpr int ROWS = 128 * NQ;
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int KV_BUF = TT * D * 2;
@@ -50,15 +51,15 @@ struct TcCfg {
   static constexpr int OFF_PRE = 512;
   static constexpr int OFF_Q = 5120;
   static constexpr int OFF_K = OFF_Q + NQ * Q_TILE;
-  static constexpr int OFF_V = OFF_K + 2 * KV_BUF;
-  static constexpr int OFF_RAW = OFF_V + 2 * KV_BUF;
+  static constexpr int OFF_V = OFF_K + KVS * KV_BUF;
+  static constexpr int OFF_RAW = OFF_V + KVS * KV_BUF;
   static constexpr int SMEM = OFF_RAW + RS * PIECE_B;
   static constexpr int DEC0 = 4 * NQ;                // first decoding warp
   static constexpr int PROD = DEC0 + 4, MMA = DEC0 + 5;
   static constexpr int NTH = 32 * (DEC0 + 6);
-  // tensor memory columns: O of every row tile, then two score buffers
+  // tensor memory columns: O of every row tile, then two score buffers of each
   static constexpr int COL_S = NQ * D;
-  static_assert(COL_S + 2 * TT <= 512, "tensor memory");
+  static_assert(COL_S + NQ * 2 * TT <= 512, "tensor memory");
   static_assert((NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE && SMEM <= 232448, "shared memory");
 };
 
@@ -126,6 +127,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// One lane of the (converged) warp, as the compiler knows it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(v));
+  return v != 0;
+}
+// A value that is the same in every lane, in a form the compiler can see.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Shared-memory descriptor of an operand whose rows run along M / N (here V: the
 // row of a token holds 64 values of N): 128-byte swizzled panels of 64 values,
 // `panel` bytes apart, 8 tokens (K) every 1024 bytes.
@@ -184,14 +194,14 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   uint64_t* raw_full = (uint64_t*)smem;
   uint64_t* raw_empty = raw_full + C::RS;
   uint64_t* kv_full = raw_empty + C::RS;
-  uint64_t* kv_empty = kv_full + 2;
-  uint64_t* s_full = kv_empty + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* pv_done = p_full + 2;
-  uint64_t* q_full = pv_done + 2;
+  uint64_t* kv_empty = kv_full + C::KVS;
+  uint64_t* s_full = kv_empty + C::KVS;    // [row tile][tile parity], as the next two
+  uint64_t* p_full = s_full + 4;
+  uint64_t* pv_done = p_full + 4;
+  uint64_t* q_full = pv_done + 4;
   uint32_t* tmem_slot = (uint32_t*)(q_full + 2);
   int64_t* pre = (int64_t*)(smem + C::OFF_PRE);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   Wk::template sum_units<C::NTH>(p, pre);
   const int64_t U = pre[C::NTH];
@@ -206,14 +216,17 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::KVS; ++i) {
       mbar_init(&kv_full[i], 128);
       mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&q_full[i], 128);
     }
+    mbar_init(&q_full[0], 128);
+    mbar_init(&q_full[1], 128);
     fence_barrier_init();
   }
   if (warp == C::MMA) {
@@ -239,7 +252,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint32_t o_addr = tmem + lane_base + (uint32_t)(tile * D);
     const uint32_t qrow = qs + tile * C::Q_TILE;
     int slot = 0;                          // of this CTA's partials
-    int64_t gt = 0;                        // tiles so far
+    int gt = 0;                            // tiles so far
     for (int64_t u = u0; u < u1;) {
       const int64_t ue = min(u1, iu + it.tiles);
       const bool from_start = u == iu, to_end = ue == iu + it.tiles;
@@ -309,61 +322,44 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         lo_all = p.window > 0 ? max(0, pb - p.window + 1) : 0;
       }
       float M = kNone, l = 0.f;
-      for (int64_t j = u; j < ue; ++j, ++gt) {
-        const int tok0 = (it.t0 + (int)(j - iu)) * TT;
-        const int sl = NQ == 2 ? tile : (int)(gt & 1);
-        const int ph = NQ == 2 ? (int)(gt & 1) : (int)((gt >> 1) & 1);
-        ok = ok && mbar_wait(&s_full[sl], ph);
+      const int nt = (int)(ue - u);
+      int tok0 = (it.t0 + (int)(u - iu)) * TT;
+      for (int j = 0; j < nt; ++j, ++gt, tok0 += TT) {
+        const int sl = tile * 2 + (gt & 1);
+        ok = ok && mbar_wait(&s_full[sl], (gt >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
-        const bool inner = tok0 >= lo_all && tok0 + TT <= hi_all;
-        // The maximum, 32 columns at a time, the next ones on their way; the last ones stay for
-        // the weights, which are made from the right: those of columns 32 c.. go to columns
-        // TT / 2 + 16 c.., over scores that were read already.
-        constexpr int NC = TT / 32;
-        uint32_t r[2][32];
-        auto masked = [&](uint32_t* v, int c) {
-          if (!inner) {
+        uint32_t r[TT];
+        tmem_ld32(s_addr, r);
+        tmem_ld32(s_addr + 32, r + 32);
+        tmem_wait_ld();
+        tmem_use(r);
+        tmem_use(r + 32);
+        if (!(tok0 >= lo_all && tok0 + TT <= hi_all)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int a = tok0 + 32 * c + i;
-              v[i] = a >= lo && a < hi ? v[i] : 0xFF800000u;
-            }
-          }
-        };
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld32(s_addr, r[0]);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          uint32_t* v = r[c & 1];
-          tmem_wait_ld();
-          tmem_use(v);
-          if (c + 1 < NC) tmem_ld32(s_addr + 32 * (c + 1), r[(c + 1) & 1]);
-          masked(v, c);
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx4[k] = fmaxf(mx4[k], fmaxf(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1])));
+          for (int i = 0; i < TT; ++i) r[i] = tok0 + i >= lo && tok0 + i < hi ? r[i] : 0xFF800000u;
         }
-        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        mx *= cf;
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < TT; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx4[k] = fmaxf(mx4[k], fmaxf(__uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1])));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * cf;
         const bool over = mx > M + 12.f;
         if (__any_sync(0xffffffffu, over)) {
           const float mn = over ? mx - 8.f : M;
           const float corr = ex2(M - mn);
           M = mn;
           l *= corr;
-          if (j > u) {
-            if (NQ == 1) {                 // the product before this one may still be running
-              const int64_t b = gt - 1;
-              ok = mbar_wait(&pv_done[b & 1], (int)((b >> 1) & 1));
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              tc_fence_after();
-            }
+          if (j > 0) {
+            // the product of the tile before may still be running
+            ok = mbar_wait(&pv_done[tile * 2 + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t v[32];
@@ -378,25 +374,19 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         }
         const float2 cf2 = make_float2(cf, cf), m2 = make_float2(-M, -M);
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // the weights go over the scores, two to a column
 #pragma unroll
-        for (int c = NC - 1; c >= 0; --c) {
-          uint32_t* v = r[c & 1];
-          if (c < NC - 1) {
-            tmem_wait_ld();
-            tmem_use(v);
-          }
-          if (c > 0) tmem_ld32(s_addr + 32 * (c - 1), r[(c - 1) & 1]);
-          if (c < NC - 1) masked(v, c);
+        for (int c = 0; c < 2; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 t =
-                ffma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), cf2, m2);
+            const int k = 32 * c + 2 * i;
+            const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), cf2, m2);
             const float2 e = make_float2(ex2(t.x), ex2(t.y));
             l2[i & 1] = fadd2(l2[i & 1], e);
             w[i] = h2_as_u32(__floats2half2_rn(e.x, e.y));
           }
-          tmem_st16(s_addr + TT / 2 + 16 * c, w);
+          tmem_st16(s_addr + 16 * c, w);
         }
         l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         tmem_wait_st();
@@ -406,9 +396,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       if (!ok) break;
       // ---- the rows: whole, or a partial
       {
-        const int64_t b = gt - 1;
-        const int sl = NQ == 2 ? tile : (int)(b & 1);
-        ok = mbar_wait(&pv_done[sl], NQ == 2 ? (int)(b & 1) : (int)((b >> 1) & 1));
+        ok = mbar_wait(&pv_done[tile * 2 + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -461,79 +449,81 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     // ------------------------------ decoding ------------------------------
     const int dw = warp - C::DEC0;
     const int blk = dw >> 1, half = dw & 1;
-    int64_t gt = 0, piece = 0;
+    // K: lane = (token, t); odd rows take their words in swapped order, so that 8 lanes' stores meet
+    // 8 different chunks.  V: lane = (a, t): tokens 2t and 2t + 1 of the half block.
+    const int r4 = lane >> 2, t = lane & 3;
+    const int ktok = half * 8 + r4, krow = blk * kKvBlk + ktok, vrow = blk * kKvBlk + half * 8 + 2 * t;
+    const uint32_t odd = r4 & 1;
+    const uint32_t k_at[2] = {sw128_offset(krow, (int)odd * 4 + t), sw128_offset(krow, (int)(odd ^ 1) * 4 + t)};
+    const uint32_t k_sel[2] = {odd ? 0x3232u : 0x1010u, odd ? 0x1010u : 0x3232u};
+    const uint32_t v_at[2] = {sw128_offset(vrow, r4), sw128_offset(vrow + 1, r4)};
+    const uint32_t raw0 = smem_u32(smem + C::OFF_RAW) + blk * B::BYTES;
+    int gt = 0, st = 0, st_phase = 0;
     for (int64_t u = u0; u < u1 && ok;) {
       const int64_t ue = min(u1, iu + it.tiles);
-      for (int64_t j = u; j < ue && ok; ++j, ++gt) {
-        const int tok0 = (it.t0 + (int)(j - iu)) * TT;
+      const int nt = (int)(ue - u);
+      int tok0 = (it.t0 + (int)(u - iu)) * TT;
+      for (int j = 0; j < nt && ok; ++j, ++gt, tok0 += TT) {
         const bool inner = tok0 >= it.begin && tok0 + TT <= it.end;
-        const int buf = (int)(gt & 1);
-        if (gt >= 2) ok = mbar_wait(&kv_empty[buf], (int)(((gt >> 1) - 1) & 1));
+        const int buf = gt % C::KVS;
+        if (gt >= C::KVS) ok = mbar_wait(&kv_empty[buf], (gt / C::KVS - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         const uint32_t kb = ks + buf * C::KV_BUF, vb = vs + buf * C::KV_BUF;
-        for (int pc = 0; pc < TT / kPiece && ok; ++pc, ++piece) {
-          const int st = (int)(piece % C::RS);
-          ok = mbar_wait(&raw_full[st], (int)((piece / C::RS) & 1));
+#pragma unroll 1
+        for (int pc = 0; pc < TT / kPiece; ++pc) {
+          ok = mbar_wait(&raw_full[st], st_phase);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint32_t rb = smem_u32(smem + C::OFF_RAW + st * C::PIECE_B) + blk * B::BYTES;
-          const int row0 = pc * kPiece + blk * kKvBlk + half * 8;
-          {
-            // K: lane = (token, t); odd rows take their words in swapped order, so that 8 lanes'
-            // stores meet 8 different chunks
-            const int tl = lane >> 2, t = lane & 3;
-            const int tok = half * 8 + tl, row = row0 + tl;
-            const uint32_t odd = row & 1;
-#pragma unroll
-            for (int gh = 0; gh < GH; ++gh) {
-              uint32_t w[W], d[W / 2];
-              lds_words<W>(rb + ((gh * 16 + tok) * 4 + t) * W * 4, w);
-              if (W == 4) {
-                const uint2 x = lds_u64(rb + B::OFF_KD + 2 * (tok * G + gh * W));
-                d[0] = x.x;
-                d[W / 2 - 1] = x.y;
-              } else {
-                d[0] = lds_u32(rb + B::OFF_KD + 2 * tok * G);
-              }
-#pragma unroll
-              for (int i = 0; i < W; ++i) {
-                const uint32_t word = odd ? w[i ^ 1] : w[i];
-                const uint32_t hi = (i & 1) ^ odd;
-                const __half2 dd = u32_as_h2(__byte_perm(d[i / 2], 0, hi ? 0x3232 : 0x1010));
-                const int panel = (gh * W + i) / 2, chunk = hi * 4 + t;
-                sts_u128(kb + panel * (TT * 128) + sw128_offset(row, chunk), decode8(word, dd));
-              }
-            }
+          const uint32_t rb = raw0 + st * C::PIECE_B;
+          const uint32_t row_b = pc * kPiece * 128;      // 32 rows of 128 bytes
+          uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
+          if (!inner) {
+            // a token that no row sees may hold anything: its V scale becomes 0
+            const int at = tok0 + pc * kPiece + vrow;
+            keep0 = at >= it.begin && at < it.end ? 0xFFFFFFFFu : 0u;
+            keep1 = at + 1 >= it.begin && at + 1 < it.end ? 0xFFFFFFFFu : 0u;
           }
-          {
-            // V: lane = (a, t): tokens 2t and 2t + 1 of this half block, values 4a.. of every group
-            const int a = lane >> 2, t = lane & 3;
-            const int row = row0 + 2 * t;
-            const int at = tok0 + row;
-            uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
-            if (!inner) {
-              // a token that no row sees may hold anything: its scale becomes 0
-              keep0 = at >= it.begin && at < it.end ? 0xFFFFFFFFu : 0u;
-              keep1 = at + 1 >= it.begin && at + 1 < it.end ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+          for (int gh = 0; gh < GH; ++gh) {
+            // every load of this part before the first store
+            uint32_t kw[W], kd[W / 2], vw[W], vx[W / 2], vy[W / 2];
+            lds_words<W>(rb + ((gh * 16 + ktok) * 4 + t) * W * 4, kw);
+            if (W == 4) {
+              const uint2 x = lds_u64(rb + B::OFF_KD + 2 * (ktok * G + gh * W));
+              kd[0] = x.x;
+              kd[W / 2 - 1] = x.y;
+            } else {
+              kd[0] = lds_u32(rb + B::OFF_KD + 2 * ktok * G);
+            }
+            lds_words<W>(rb + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, vw);
+#pragma unroll
+            for (int k = 0; k < W / 2; ++k) {
+              const int g = gh * W + 2 * k;
+              vx[k] = lds_u32(rb + B::OFF_VD + ((t * G + g) * 4 + half * 2) * 2);
+              vy[k] = lds_u32(rb + B::OFF_VD + ((t * G + g + 1) * 4 + half * 2) * 2);
             }
 #pragma unroll
-            for (int gh = 0; gh < GH; ++gh) {
-              uint32_t w[W];
-              lds_words<W>(rb + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, w);
+            for (int i = 0; i < W; ++i) {
+              const uint32_t word = odd ? kw[i ^ 1] : kw[i];
+              const __half2 dd = u32_as_h2(__byte_perm(kd[i / 2], 0, k_sel[i & 1]));
+              sts_u128(kb + row_b + (gh * W + i) / 2 * (TT * 128) + k_at[i & 1], decode8(word, dd));
+            }
 #pragma unroll
-              for (int k = 0; k < W / 2; ++k) {
-                const int wp = gh * (W / 2) + k;
-                const uint32_t x = lds_u32(rb + B::OFF_VD + ((t * G + 2 * wp) * 4 + half * 2) * 2);
-                const uint32_t y = lds_u32(rb + B::OFF_VD + ((t * G + 2 * wp + 1) * 4 + half * 2) * 2);
-                const __half2 d0 = u32_as_h2(__byte_perm(x, y, 0x5410) & keep0);
-                const __half2 d1 = u32_as_h2(__byte_perm(x, y, 0x7632) & keep1);
-                sts_u128(vb + wp * (TT * 128) + sw128_offset(row, a), decode8(w[k], d0));
-                sts_u128(vb + wp * (TT * 128) + sw128_offset(row + 1, a), decode8(w[W / 2 + k], d1));
-              }
+            for (int k = 0; k < W / 2; ++k) {
+              const __half2 d0 = u32_as_h2(__byte_perm(vx[k], vy[k], 0x5410) & keep0);
+              const __half2 d1 = u32_as_h2(__byte_perm(vx[k], vy[k], 0x7632) & keep1);
+              const uint32_t at = vb + row_b + (gh * (W / 2) + k) * (TT * 128);
+              sts_u128(at + v_at[0], decode8(vw[k], d0));
+              sts_u128(at + v_at[1], decode8(vw[W / 2 + k], d1));
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&raw_empty[st]);
+          if (++st == C::RS) {
+            st = 0;
+            st_phase ^= 1;
+          }
         }
         if (!ok) break;
         fence_proxy_async_smem();
@@ -587,63 +577,78 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       iu += it.tiles;
       if (u < u1) Wk::next(p, it);
     }
-    } else if (warp == C::MMA && lane == 0) {
-    // ------------------------------ products ------------------------------
-    constexpr uint32_t id_s = idesc_f16_f32(128, TT);
-    constexpr uint32_t id_o = idesc_f16_f32(128, D) | kBRowsAlongN;
-    int64_t gt = 0;
-    int seg = 0;
-    auto slot_of = [&](int64_t g, int i) { return NQ == 2 ? i : (int)(g & 1); };
-    auto phase_of = [&](int64_t g) { return NQ == 2 ? (int)(g & 1) : (int)((g >> 1) & 1); };
-    // S of tile g and row tile i; its buffer's last weights must have been used
-    auto scores = [&](int64_t g, int i) {
-      const int sl = slot_of(g, i);
-      const int64_t before = g - (NQ == 2 ? 1 : 2);
-      if (before >= 0 && !mbar_wait(&pv_done[sl], phase_of(before))) return false;
-      if (!mbar_wait(&kv_full[g & 1], (int)((g >> 1) & 1))) return false;
-      tc_fence_after();
-      const uint32_t a = qs + i * C::Q_TILE, b = ks + (uint32_t)(g & 1) * C::KV_BUF;
-      const uint32_t d = tmem + (uint32_t)(C::COL_S + sl * TT);
+    } else {
+      // ------------------------------ products ------------------------------
+      // The whole warp walks the loop, so that descriptors and addresses are uniform values (the
+      // instruction takes them from uniform registers: from one lane's own registers each of its
+      // operands is moved first, which took 70 cycles a product); one lane issues.
+      constexpr uint32_t id_s = idesc_f16_f32(128, TT);
+      constexpr uint32_t id_o = idesc_f16_f32(128, D) | kBRowsAlongN;
+      const uint32_t tm = (uint32_t)uniform((int)tmem);
+      const uint64_t q_desc = sw128_kmajor_desc(qs), k_desc = sw128_kmajor_desc(ks),
+                     v_desc = sw128_mnmajor_desc(vs, TT * 128);
+      int gt = 0, seg = 0;
+      // S of tile g and row tile i; its buffer's last weights must have been used
+      auto scores = [&](int g, int i) {
+        const int sl = i * 2 + (g & 1), buf = g % C::KVS;
+        bool good = g < 2 || mbar_wait(&pv_done[sl], ((g - 2) >> 1) & 1);
+        good = good && mbar_wait(&kv_full[buf], (g / C::KVS) & 1);
+        if (!__all_sync(0xffffffffu, good)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = q_desc + (uint32_t)(i * (C::Q_TILE >> 4));
+          const uint64_t b = k_desc + (uint32_t)(buf * (C::KV_BUF >> 4));
+          const uint32_t d = tm + (uint32_t)(C::COL_S + sl * TT);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc_mma_f16(d, sw128_kmajor_desc(a + (k >> 2) * 16384) + 2 * (k & 3),
-                   sw128_kmajor_desc(b + (k >> 2) * (TT * 128)) + 2 * (k & 3), id_s, k ? 1u : 0u);
-      tc_commit(&s_full[sl]);
-      return true;
-    };
-    auto weighted = [&](int64_t g, int i, bool first) {
-      const int sl = slot_of(g, i);
-      if (!mbar_wait(&p_full[sl], phase_of(g))) return false;
-      tc_fence_after();
-      const uint32_t a = tmem + (uint32_t)(C::COL_S + sl * TT + TT / 2);
-      const uint32_t b = vs + (uint32_t)(g & 1) * C::KV_BUF;
-#pragma unroll
-      for (int k = 0; k < TT / 16; ++k)
-        tc_mma_f16_tmem_a(tmem + (uint32_t)(i * D), a + 8 * k, sw128_mnmajor_desc(b + k * 2048, TT * 128),
-                          id_o, (first && k == 0) ? 0u : 1u);
-      tc_commit(&pv_done[sl]);
-      if (i == NQ - 1) tc_commit(&kv_empty[g & 1]);
-      return true;
-    };
-    for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const int64_t ue = min(u1, iu + it.tiles);
-      const int nt = (int)(ue - u);
-      for (int i = 0; i < NQ && ok; ++i) {
-        ok = mbar_wait(&q_full[i], seg & 1);
-        ok = ok && scores(gt, i);
-      }
-      if (NQ == 1 && nt > 1) ok = ok && scores(gt + 1, 0);
-      for (int j = 0; j < nt && ok; ++j, ++gt) {
-        for (int i = 0; i < NQ && ok; ++i) {
-          ok = weighted(gt, i, j == 0);
-          const int ahead = NQ == 2 ? 1 : 2;
-          if (j + ahead < nt) ok = ok && scores(gt + ahead, i);
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma_f16(d, a + (k >> 2) * (16384 >> 4) + 2 * (k & 3),
+                       b + (k >> 2) * (TT * 128 >> 4) + 2 * (k & 3), id_s, k ? 1u : 0u);
+          tc_commit(&s_full[sl]);
         }
+        __syncwarp();
+        return true;
+      };
+      auto weighted = [&](int g, int i, bool first) {
+        const int sl = i * 2 + (g & 1), buf = g % C::KVS;
+        if (!__all_sync(0xffffffffu, mbar_wait(&p_full[sl], (g >> 1) & 1))) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t a = tm + (uint32_t)(C::COL_S + sl * TT);
+          const uint64_t b = v_desc + (uint32_t)(buf * (C::KV_BUF >> 4));
+#pragma unroll
+          for (int k = 0; k < TT / 16; ++k)
+            tc_mma_f16_tmem_a(tm + (uint32_t)(i * D), a + 8 * k, b + k * (2048 >> 4), id_o,
+                              (first && k == 0) ? 0u : 1u);
+          tc_commit(&pv_done[sl]);
+          if (i == NQ - 1) tc_commit(&kv_empty[buf]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int64_t u = u0; u < u1 && ok; ++seg) {
+        const int64_t ue = min(u1, iu + it.tiles);
+        const int nt = uniform((int)(ue - u)), end = gt + nt;
+        for (int i = 0; i < NQ && ok; ++i) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
+          ok = ok && scores(gt, i);
+        }
+        for (int i = 0; i < NQ && ok && nt > 1; ++i) ok = scores(gt + 1, i);
+        const int g0 = gt;
+        for (; gt < end && ok; ++gt) {
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            ok = ok && weighted(gt, i, gt == g0);
+            // the scores two tiles after the step before this one, whose product is done by now
+            const int gp = i > 0 ? gt : gt - 1, ip = i > 0 ? i - 1 : NQ - 1;
+            if (gp >= g0 && gp + 2 < end) ok = ok && scores(gp + 2, ip);
+          }
+        }
+        u = ue;
+        iu += it.tiles;
+        if (u < u1) Wk::next(p, it);
       }
-      u = ue;
-      iu += it.tiles;
-      if (u < u1) Wk::next(p, it);
-    }
+      // no arrival is under way when the CTA ends
+      if (ok) mbar_wait(&kv_empty[(gt - 1) % C::KVS], ((gt - 1) / C::KVS) & 1);
     }
   }
   tc_fence_before();
