@@ -55,8 +55,8 @@ struct TcCfg {
   static constexpr int OFF_RAW = OFF_V + KVS * KV_BUF;
   static constexpr int SMEM = OFF_RAW + RS * PIECE_B;
   static constexpr int DEC0 = 4 * NQ;                // first decoding warp
-  static constexpr int PROD = DEC0 + 4, MMA = DEC0 + 5;
-  static constexpr int NTH = 32 * (DEC0 + 6);
+  static constexpr int PROD = DEC0 + 4, MMA = DEC0 + 5;   // one warp of products per row tile
+  static constexpr int NTH = 32 * (MMA + NQ);
   // tensor memory columns: O of every row tile, then two score buffers of each
   static constexpr int COL_S = NQ * D;
   static_assert(COL_S + NQ * 2 * TT <= 512, "tensor memory");
@@ -127,6 +127,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// tcgen05.mma with descriptors as their 32-bit halves: only the low one (the address) changes from
+// product to product, one addition each.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // One lane of the (converged) warp, as the compiler knows it.
 __device__ __forceinline__ bool elect_one() {
   uint32_t v;
@@ -218,7 +241,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     }
     for (int i = 0; i < C::KVS; ++i) {
       mbar_init(&kv_full[i], 128);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], NQ);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -579,7 +602,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     }
     } else {
       // ------------------------------ products ------------------------------
-      // The whole warp walks the loop, so that descriptors and addresses are uniform values (the
+      // A warp per row tile, so that neither waits for the other's softmax.  The whole warp walks the loop, so that descriptors and addresses are uniform values (the
       // instruction takes them from uniform registers: from one lane's own registers each of its
       // operands is moved first, which took 70 cycles a product); one lane issues.
       constexpr uint32_t id_s = idesc_f16_f32(128, TT);
@@ -587,61 +610,57 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const uint32_t tm = (uint32_t)uniform((int)tmem);
       const uint64_t q_desc = sw128_kmajor_desc(qs), k_desc = sw128_kmajor_desc(ks),
                      v_desc = sw128_mnmajor_desc(vs, TT * 128);
+      const uint32_t q_lo = (uint32_t)uniform((int)(uint32_t)q_desc), k_lo = (uint32_t)uniform((int)(uint32_t)k_desc),
+                     v_lo = (uint32_t)uniform((int)(uint32_t)v_desc);
+      const uint32_t hi = (uint32_t)(k_desc >> 32);      // the same for all three: stride, version, swizzle
+      const int i = warp - C::MMA;
+      const uint32_t q_i = q_lo + (uint32_t)(i * (C::Q_TILE >> 4)), o_i = tm + (uint32_t)(i * D);
+      const uint32_t s_i = tm + (uint32_t)(C::COL_S + i * 2 * TT);
       int gt = 0, seg = 0;
-      // S of tile g and row tile i; its buffer's last weights must have been used
-      auto scores = [&](int g, int i) {
-        const int sl = i * 2 + (g & 1), buf = g % C::KVS;
-        bool good = g < 2 || mbar_wait(&pv_done[sl], ((g - 2) >> 1) & 1);
+      // S of tile g; its buffer's last weights must have been used
+      auto scores = [&](int g) {
+        const int par = g & 1, buf = g % C::KVS;
+        bool good = g < 2 || mbar_wait(&pv_done[i * 2 + par], ((g - 2) >> 1) & 1);
         good = good && mbar_wait(&kv_full[buf], (g / C::KVS) & 1);
         if (!__all_sync(0xffffffffu, good)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t a = q_desc + (uint32_t)(i * (C::Q_TILE >> 4));
-          const uint64_t b = k_desc + (uint32_t)(buf * (C::KV_BUF >> 4));
-          const uint32_t d = tm + (uint32_t)(C::COL_S + sl * TT);
+          const uint32_t b = k_lo + (uint32_t)(buf * (C::KV_BUF >> 4));
+          const uint32_t d = s_i + (uint32_t)(par * TT);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            tc_mma_f16(d, a + (k >> 2) * (16384 >> 4) + 2 * (k & 3),
-                       b + (k >> 2) * (TT * 128 >> 4) + 2 * (k & 3), id_s, k ? 1u : 0u);
-          tc_commit(&s_full[sl]);
+            mma_ss(d, q_i + (k >> 2) * (16384 >> 4) + 2 * (k & 3), b + (k >> 2) * (TT * 128 >> 4) + 2 * (k & 3),
+                   hi, id_s, k ? 1u : 0u);
+          tc_commit(&s_full[i * 2 + par]);
         }
         __syncwarp();
         return true;
       };
-      auto weighted = [&](int g, int i, bool first) {
-        const int sl = i * 2 + (g & 1), buf = g % C::KVS;
-        if (!__all_sync(0xffffffffu, mbar_wait(&p_full[sl], (g >> 1) & 1))) return false;
+      auto weighted = [&](int g, bool first) {
+        const int par = g & 1, buf = g % C::KVS;
+        if (!__all_sync(0xffffffffu, mbar_wait(&p_full[i * 2 + par], (g >> 1) & 1))) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a = tm + (uint32_t)(C::COL_S + sl * TT);
-          const uint64_t b = v_desc + (uint32_t)(buf * (C::KV_BUF >> 4));
+          const uint32_t a = s_i + (uint32_t)(par * TT);
+          const uint32_t b = v_lo + (uint32_t)(buf * (C::KV_BUF >> 4));
 #pragma unroll
           for (int k = 0; k < TT / 16; ++k)
-            tc_mma_f16_tmem_a(tm + (uint32_t)(i * D), a + 8 * k, b + k * (2048 >> 4), id_o,
-                              (first && k == 0) ? 0u : 1u);
-          tc_commit(&pv_done[sl]);
-          if (i == NQ - 1) tc_commit(&kv_empty[buf]);
+            mma_ts(o_i, a + 8 * k, b + k * (2048 >> 4), hi, id_o, (first && k == 0) ? 0u : 1u);
+          tc_commit(&pv_done[i * 2 + par]);
+          tc_commit(&kv_empty[buf]);
         }
         __syncwarp();
         return true;
       };
       for (int64_t u = u0; u < u1 && ok; ++seg) {
         const int64_t ue = min(u1, iu + it.tiles);
-        const int nt = uniform((int)(ue - u)), end = gt + nt;
-        for (int i = 0; i < NQ && ok; ++i) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
-          ok = ok && scores(gt, i);
-        }
-        for (int i = 0; i < NQ && ok && nt > 1; ++i) ok = scores(gt + 1, i);
-        const int g0 = gt;
+        const int nt = uniform((int)(ue - u)), end = gt + nt, g0 = gt;
+        ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
+        ok = ok && scores(gt);
+        if (nt > 1) ok = ok && scores(gt + 1);
         for (; gt < end && ok; ++gt) {
-#pragma unroll
-          for (int i = 0; i < NQ; ++i) {
-            ok = ok && weighted(gt, i, gt == g0);
-            // the scores two tiles after the step before this one, whose product is done by now
-            const int gp = i > 0 ? gt : gt - 1, ip = i > 0 ? i - 1 : NQ - 1;
-            if (gp >= g0 && gp + 2 < end) ok = ok && scores(gp + 2, ip);
-          }
+          ok = weighted(gt, gt == g0);
+          if (gt + 2 < end) ok = ok && scores(gt + 2);
         }
         u = ue;
         iu += it.tiles;
