@@ -54,8 +54,9 @@ struct Item {
 };
 
 // A call's work as one line of units: (request, row tile, K/V head, tile of
-// TILE tokens), the tokens fastest.
-template <int ROWS, int TILE>
+// TILE tokens), the tokens fastest.  An item (all of them but the tokens) takes
+// OV units before its tiles: what starting and ending one costs.
+template <int ROWS, int TILE, int OV>
 struct Walk {
   __device__ __forceinline__ static void range(const AttnParams& p, Item& it) {
     const int shift = it.len - it.qlen;
@@ -79,7 +80,7 @@ struct Walk {
     int64_t u = 0;
     for (it.row0 = 0; it.row0 < it.qlen * p.group; it.row0 += ROWS) {
       range(p, it);
-      u += it.tiles;
+      u += it.tiles + OV;
     }
     return u * p.g.heads;
   }
@@ -146,18 +147,40 @@ struct Walk {
     it.h = 0;
     it.row0 = 0;
     range(p, it);
-    while (u >= iu + it.tiles) {
-      iu += it.tiles;
+    while (u >= iu + it.tiles + OV) {
+      iu += it.tiles + OV;
       next(p, it);
     }
     return iu;
   }
+  // The tiles [a, b) of the item at unit iu that lie in the share [u0, u1); none: on to the next
+  // item that has some.  False: the share holds no more.
+  __device__ __forceinline__ static bool here(const AttnParams& p, Item& it, int64_t& iu, int64_t u0,
+                                              int64_t u1, int& a, int& b) {
+    for (;;) {
+      a = (int)max(u0 - iu - OV, (int64_t)0);
+      b = (int)min(u1 - iu - OV, (int64_t)it.tiles);
+      if (b > a) return true;
+      iu += it.tiles + OV;
+      if (iu >= u1) return false;
+      next(p, it);
+    }
+  }
+  __device__ __forceinline__ static bool after(const AttnParams& p, Item& it, int64_t& iu, int64_t u0,
+                                               int64_t u1, int& a, int& b) {
+    iu += it.tiles + OV;
+    if (iu >= u1) return false;
+    next(p, it);
+    return here(p, it, iu, u0, u1, a, b);
+  }
+  // the share in which the last tile of the item at unit iu lies
+  __device__ __forceinline__ static int last_share(const Item& it, int64_t iu, int64_t N, int64_t U) {
+    return (int)(((iu + OV + it.tiles) * N + U - 1) / U - 1);
+  }
 };
 
-// The line of U units is cut into N <= U equal shares: share w is [U w / N, U (w + 1) / N).
-__device__ __forceinline__ int share_of(int64_t u, int64_t N, int64_t U) {
-  return (int)(((u + 1) * N + U - 1) / U - 1);
-}
+// The line of U units is cut into N <= U equal shares: share w is [U w / N, U (w + 1) / N), and
+// unit u lies in share ceil((u + 1) N / U) - 1.
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -184,6 +207,32 @@ __device__ __forceinline__ void store_out4(const AttnParams& p, int64_t at, cons
   if (p.out_dtype == DQ_BF16) store_dims4<DQ_BF16>(p.out, at, x);
   else if (p.out_dtype == DQ_F16) store_dims4<DQ_F16>(p.out, at, x);
   else store_dims4<DQ_F32>(p.out, at, x);
+}
+
+// A joined row: a warp's lane holds values D / 32 * lane.. of the weighted sum, all lanes the maximum
+// and the sum of the weights.  `row` is the row (token * group + head) of request r and K/V head h.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnParams& p, int r, int h, int row, int lane,
+                                          const float (&acc)[D / 32], float m, float l) {
+  constexpr int V = D / 32;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int tokq = row / p.group, uq = row - tokq * p.group;
+  const int64_t qrow = __ldg(p.q_start + r) + tokq;
+  const int head = h * p.group + uq;
+  const int64_t base = qrow * p.out_stride + (int64_t)head * D + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 4) {
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = acc[V < 4 ? k & 1 : v + k] * inv;
+    if (V < 4) {                           // 64 values: two lanes' pairs make one four
+      x[2] = __shfl_down_sync(0xffffffffu, x[0], 1);
+      x[3] = __shfl_down_sync(0xffffffffu, x[1], 1);
+    }
+    if (V >= 4 || (lane & 1) == 0) store_out4(p, base + v, x);
+  }
+  if (lane == 0 && p.lse)
+    p.lse[qrow * p.n_q_heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace dqmoe

@@ -26,11 +26,13 @@
 // one line, cut into equal contiguous shares, one per warp: any mix of lengths
 // fills the GPU, and no warp waits for another.  The host never sees a length:
 // every CTA sums the requests' units itself.  A warp that holds a whole item
-// writes its rows; otherwise it leaves a partial (at most two per warp), which
-// kv_stream_join_kernel adds up in order, so that results do not depend on timing.
+// writes its rows; otherwise it leaves a partial (at most two per warp) in shared
+// memory, and the CTA's warps join them in order when all have ended.  What goes on
+// in another CTA (again at most two partials) is left to kv_stream_join_kernel.  The
+// order of every sum is fixed, so results do not depend on timing.
 //
-// Each warp has a ring of three tiles filled by its own bulk copies (a tile of a page
-// is one contiguous run), two in flight while one is computed.
+// Each warp has a ring of tiles filled by its own bulk copies (a tile of a page
+// is one contiguous run), all but one in flight while one is computed.
 #include <algorithm>
 
 #include "kv_attn.h"
@@ -41,8 +43,14 @@ namespace {
 
 constexpr int kTile = 32;                 // tokens per unit
 constexpr int kBlks = kTile / kKvBlk;
-constexpr int kStages = 3;
+constexpr int kItemCost = 1;              // tiles' worth of starting and ending an item
 constexpr int kMaxCtas = 160;
+
+// what a warp did not finish: bit 0 of `open`: the item goes on behind this share
+struct Left {
+  int r, h, row0, rows;
+  int has, open, follow;                  // follow: the share in which the item ends
+};
 
 template <int D, int NT>
 struct StreamCfg {
@@ -50,21 +58,27 @@ struct StreamCfg {
   static constexpr int NW = D * NT <= 64 ? 16 : D * NT <= 128 ? 12 : 8;
   static constexpr int ROWS = 8 * NT;
   static constexpr int STG = kBlks * KvBlk<D>::BYTES;
-  static constexpr int OFF_PRE = 1024;                              // int64 [513]
-  static constexpr int OFF_RING = OFF_PRE + 4352;                   // (NTH + 1 + NTH / 32) * 8 at most
-  static constexpr int SMEM = OFF_RING + NW * kStages * STG;
-  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int STAGES = D == 256 ? 2 : 3;
+  static constexpr int NTH = NW * 32;
+  static constexpr int PART = ROWS * D * 4 + ROWS * 8;              // rows of O, then (M, l)
+  static constexpr int OFF_LEFT = 512;                              // Left [NW][2]
+  static constexpr int OFF_PRE = 1536;                              // int64 [NTH + 1 + NW]
+  static constexpr int OFF_RING = OFF_PRE + 4352;
+  static constexpr int OFF_HEAD = OFF_RING + NW * STAGES * STG;     // the warps' first partials
+  static constexpr int SMEM = OFF_HEAD + NW * PART;                 // (the second ones lie in the rings)
+  static_assert(SMEM <= 232448 && STAGES * STG >= PART && (NTH + 1 + NW) * 8 <= 4352 &&
+                    NW * STAGES * 8 <= OFF_LEFT && NW * 2 * sizeof(Left) <= 1024, "shared memory");
 };
 
-// workspace: partial O [warps][2][ROWS][D] fp32, (M, l) [warps][2][ROWS], descriptors [warps]
+// workspace: partial O [ctas][2][ROWS][D] fp32, (M, l) [ctas][2][ROWS], descriptors [ctas]
 struct StreamWs {
   float* o;
   float2* ml;
   int4* desc;
 };
-constexpr size_t kStreamO = (size_t)kMaxCtas * 16 * 2 * 8 * 128 * 4;   // NW * ROWS * D is the same for every D >= 128
-constexpr size_t kStreamMl = (size_t)kMaxCtas * 16 * 2 * 16 * 8;
-constexpr size_t kStreamDesc = (size_t)kMaxCtas * 16 * 16;
+constexpr size_t kStreamO = (size_t)kMaxCtas * 2 * 16 * 128 * 4;    // ROWS * D is at most 16 * 128
+constexpr size_t kStreamMl = (size_t)kMaxCtas * 2 * 16 * 8;
+constexpr size_t kStreamDesc = (size_t)kMaxCtas * 16;
 
 __device__ __forceinline__ StreamWs stream_ws(uint8_t* ws) {
   StreamWs w;
@@ -93,7 +107,7 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(StreamCfg<D, NT>::NW * 32, 1)
+__global__ void __launch_bounds__(StreamCfg<D, NT>::NTH, 1)
 kv_stream_kernel(const __grid_constant__ AttnParams p) {
   using B = KvBlk<D>;
   using C = StreamCfg<D, NT>;
@@ -101,43 +115,49 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lr = lane >> 2, lt = lane & 3;
-  uint64_t* bars = (uint64_t*)smem + warp * kStages;
+  uint64_t* bars = (uint64_t*)smem + warp * C::STAGES;
+  Left* left = (Left*)(smem + C::OFF_LEFT);
   int64_t* pre = (int64_t*)(smem + C::OFF_PRE);
-  uint8_t* ring = smem + C::OFF_RING + warp * kStages * C::STG;
-  if (lane < kStages) mbar_init(&bars[lane], 1);
+  uint8_t* ring = smem + C::OFF_RING + warp * C::STAGES * C::STG;
+  if (lane < C::STAGES) mbar_init(&bars[lane], 1);
+  if (lane < 2) left[warp * 2 + lane].has = 0;
   fence_barrier_init();
   pdl_wait();
   pdl_trigger();
 
-  constexpr int NTH = C::NW * 32;
-  using Wk = Walk<C::ROWS, kTile>;
-  Wk::template sum_units<NTH>(p, pre);
-  const int64_t U = pre[NTH];
+  using Wk = Walk<C::ROWS, kTile, kItemCost>;
+  Wk::template sum_units<C::NTH>(p, pre);
+  const int64_t U = pre[C::NTH];
+  const StreamWs ws = stream_ws(p.ws);
   // at least one unit per warp of the CTAs that take part
   const int ctas = (int)min((int64_t)gridDim.x, (U + C::NW - 1) / C::NW);
+  if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (blockIdx.x >= ctas) return;
   const int gw = blockIdx.x * C::NW + warp;
-  const StreamWs ws = stream_ws(p.ws);
-  if (blockIdx.x >= ctas) {
-    if (lane == 0) ws.desc[gw] = make_int4(0, 0, 0, 0);
-    return;
-  }
   const int64_t N = min((int64_t)ctas * C::NW, U);      // every one of the N shares holds a unit
-  const int64_t u0 = U * gw / N, u1 = U * (gw + 1) / N;
-  if (lane == 0) ws.desc[gw] = make_int4(0, 0, 0, 0);
-  if (gw >= N) return;
+  const int64_t u0 = U * min((int64_t)gw, N) / N, u1 = U * min((int64_t)gw + 1, N) / N;
 
+  // ---- the first item of the share, and its tiles [ta, tb) that lie in it
   Item it;
-  int64_t iu = Wk::template seek<NTH>(p, pre, u0, it);   // the unit at which the item starts
+  int64_t iu = 0;
+  int ta = 0, tb = 0;
+  bool more = u0 < u1;
+  if (more) {
+    iu = Wk::template seek<C::NTH>(p, pre, u0, it);
+    more = Wk::here(p, it, iu, u0, u1, ta, tb);
+  }
 
-  // ---- producer state: the next unit to copy, its item, and 32 entries of its table row
+  // ---- producer state: the next tile to copy, its item, and 32 entries of its table row
   Item pi = it;
-  int64_t pu = u0, piu = iu;
+  int64_t piu = iu;
+  int pt = ta, pta = ta, ptb = tb;
+  bool pmore = more;
   int tbase = -1, tent = 0;
   const uint64_t pol = l2_evict_first_policy();
   const int tshift = p.g.page_shift;
   auto produce = [&](int stage) {
-    if (pu >= u1) return;
-    const int tile = pi.t0 + (int)(pu - piu);
+    if (!pmore) return;
+    const int tile = pi.t0 + pt;
     uint8_t* dst = ring + stage * C::STG;
     const int tok = tile * kTile;
     if (lane == 0) mbar_arrive_expect_tx(&bars[stage], C::STG);
@@ -161,15 +181,15 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
                  cnt / kKvBlk * B::BYTES, &bars[stage], pol);
       run += cnt;
     }
-    if (++pu == piu + pi.tiles && pu < u1) {
-      piu += pi.tiles;
-      Wk::next(p, pi);
+    if (++pt == ptb) {
+      pmore = Wk::after(p, pi, piu, u0, u1, pta, ptb);
+      pt = pta;
       tbase = -1;
     }
   };
   __syncwarp();
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) produce(s);
+  for (int s = 0; s < C::STAGES; ++s) produce(s);
 
   // ---- consumer state
   uint32_t qf[G][4][NT];
@@ -179,10 +199,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   float b = 10.f;
   bool ok = true;
 
-  int64_t u = u0;
-  int slot = 0;
   int stage = 0, phase = 0;
-  while (u < u1) {
+  for (; more; more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
     // ---- rows of the item: column lr of each 8-row tile, values 8 lt.. of every group
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -266,10 +284,9 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         }
     }
 
-    const int64_t ue = min(u1, iu + it.tiles);
-    const bool from_start = u == iu, to_end = ue == iu + it.tiles;
-    for (; u < ue; ++u) {
-      const int tok0 = (it.t0 + (int)(u - iu)) * kTile;
+    const bool from_start = ta == 0, to_end = tb == it.tiles;
+    for (int tl = ta; tl < tb; ++tl) {
+      const int tok0 = (it.t0 + tl) * kTile;
       ok = ok && mbar_wait(&bars[stage], phase);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -449,14 +466,18 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         }
       __syncwarp();
       produce(stage);
-      if (++stage == kStages) {
+      if (++stage == C::STAGES) {
         stage = 0;
         phase ^= 1;
       }
     }
     if (!ok) break;
 
-    // ---- the segment's rows: whole, or a partial
+    // ---- the item's rows: whole, or a partial (the second one over the ring, whose copies have all
+    // been used: the share ends here)
+    const bool whole = from_start && to_end;
+    float* part = (float*)(from_start ? ring : smem + C::OFF_HEAD + warp * C::PART);
+    __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -467,7 +488,6 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int col = nt * 8 + 2 * lt + i;
         if (col >= it.rows) continue;
-        const bool whole = from_start && to_end;
         const float k24 = 16777216.f, k20 = 1048576.f;
         const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
         const int row = it.row0 + col, tokq = row / p.group, uq = row - tokq * p.group;
@@ -482,119 +502,154 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
           if (whole)
             store_out4(p, qrow * p.out_stride + (int64_t)head * D + 32 * g + 4 * lr, x);
           else
-            *(float4*)(ws.o + (((int64_t)gw * 2 + slot) * C::ROWS + col) * D + 32 * g + 4 * lr) =
-                make_float4(x[0], x[1], x[2], x[3]);
+            *(float4*)(part + col * D + 32 * g + 4 * lr) = make_float4(x[0], x[1], x[2], x[3]);
         }
         if (lr == 0) {
           if (!whole)
-            ws.ml[((int64_t)gw * 2 + slot) * C::ROWS + col] = make_float2(M[nt][i], sum);
+            ((float2*)(part + C::ROWS * D))[col] = make_float2(M[nt][i], sum);
           else if (p.lse)
-            p.lse[qrow * p.n_q_heads + head] =
-                sum > 0.f ? (M[nt][i] + log2f(sum)) * kLn2 : -INFINITY;
+            p.lse[qrow * p.n_q_heads + head] = sum > 0.f ? (M[nt][i] + log2f(sum)) * kLn2 : -INFINITY;
         }
       }
-    if (from_start && !to_end && lane == 0) {
-      // the item starts here and goes on in the next warps: how many of them
-      const int64_t last = iu + it.tiles - 1;
-      ws.desc[gw] = make_int4(it.r, it.h, it.row0, ((share_of(last, N, U) - gw) << 1) | slot);
+    if (!whole && lane == 0) {
+      Left& x = left[warp * 2 + (from_start ? 1 : 0)];
+      x.r = it.r;
+      x.h = it.h;
+      x.row0 = it.row0;
+      x.rows = it.rows;
+      x.has = 1;
+      x.open = to_end ? 0 : 1;
+      x.follow = Wk::last_share(it, iu, N, U);
     }
-    if (!(from_start && to_end)) slot = 1;
-    iu += it.tiles;
-    if (u < u1) Wk::next(p, it);
+  }
+  __syncthreads();
+
+  // ---- the CTA's partials.  An item starts with a warp's second partial (or with the first warp's
+  // first one, if it comes from the CTA before) and goes on in the next warps' first ones.
+  int job = 0;
+  for (int w = -1; w < C::NW; ++w) {
+    const Left& x = w < 0 ? left[0] : left[w * 2 + 1];
+    if (!x.has) continue;
+    int n = 1, open = x.open;              // partials of the item in this CTA
+    const int w0 = w < 0 ? 0 : w;
+    while (open && w0 + n < C::NW && left[(w0 + n) * 2].has) {
+      open = left[(w0 + n) * 2].open;
+      ++n;
+    }
+    const bool whole = w >= 0 && !open;
+    auto part = [&](int i) -> const float* {
+      return (const float*)(i == 0 && w >= 0 ? smem + C::OFF_RING + w * C::STAGES * C::STG
+                                             : smem + C::OFF_HEAD + (w0 + i) * C::PART);
+    };
+    if (open && w >= 0 && threadIdx.x == 0)
+      ws.desc[blockIdx.x] = make_int4(x.r, x.h, x.row0, x.follow / C::NW - (int)blockIdx.x);
+    for (int col = 0; col < x.rows; ++col, ++job) {
+      if (job % C::NW != warp) continue;
+      float m = kNone;
+      for (int i = 0; i < n; ++i) m = fmaxf(m, ((const float2*)(part(i) + C::ROWS * D))[col].x);
+      float sum = 0.f, acc[G];
+#pragma unroll
+      for (int v = 0; v < G; ++v) acc[v] = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float* src = part(i);
+        const float2 ml = ((const float2*)(src + C::ROWS * D))[col];
+        const float f = ex2(ml.x - m);
+        sum = fmaf(ml.y, f, sum);
+#pragma unroll
+        for (int v = 0; v < G; v += 2) {
+          const float2 y = *(const float2*)(src + col * D + lane * G + v);
+          acc[v] = fmaf(y.x, f, acc[v]);
+          acc[v + 1] = fmaf(y.y, f, acc[v + 1]);
+        }
+      }
+      if (whole) {
+        store_row<D>(p, x.r, x.h, x.row0 + col, lane, acc, m, sum);
+      } else {
+        const int64_t at = ((int64_t)blockIdx.x * 2 + (w < 0 ? 0 : 1)) * C::ROWS + col;
+#pragma unroll
+        for (int v = 0; v < G; v += 2)
+          *(float2*)(ws.o + at * D + lane * G + v) = make_float2(acc[v], acc[v + 1]);
+        if (lane == 0) ws.ml[at] = make_float2(m, sum);
+      }
+    }
   }
 }
 
-// Joins the partials of the items that go over several warps' shares.  CTA c
-// looks after the items that start in CTA c of the kernel above; a warp takes a
-// row of an item and one of SUB interleaved shares of its partials.
+// Joins the partials of the items that go over several CTAs' shares.  CTA c
+// looks after the item that starts in CTA c of the kernel above and goes on behind
+// it; a warp takes a row and one of kSub interleaved shares of its partials.
 constexpr int kSub = 4;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_constant__ AttnParams p) {
   using C = StreamCfg<D, NT>;
-  constexpr int V = D / 32;                // values of a row per lane
+  constexpr int G = D / 32;                // values of a row per lane
   __shared__ float acc_s[8][kSub][D];
   __shared__ float2 ml_s[8][kSub];
   pdl_wait();
   pdl_trigger();
   const StreamWs ws = stream_ws(p.ws);
+  const int4 d = __ldcg(ws.desc + blockIdx.x);
+  const int follow = d.w;                  // CTAs behind this one that the item goes on in
+  if (follow == 0) return;                 // uniform for the CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp >> 3, rw = warp & 7;
-  for (int w = 0; w < C::NW; ++w) {
-    const int gw = blockIdx.x * C::NW + w;
-    const int4 d = __ldcg(ws.desc + gw);
-    const int follow = d.w >> 1;
-    if (follow == 0) continue;             // uniform for the CTA
-    int first;
-    const int n = q_rows(p, d.x, &first);
-    const int rows = min(C::ROWS, n * p.group - d.z);
+  int first;
+  const int rows = min(C::ROWS, q_rows(p, d.x, &first) * p.group - d.z);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int col = nt * 8 + rw;
-      const bool live = col < rows;
-      // partial i: warp gw's slot (i = 0), then the first slot of the warps after it
-      auto part = [&](int i) -> int64_t {
-        return (((int64_t)(gw + i) * 2 + (i == 0 ? (d.w & 1) : 0)) * C::ROWS + col);
-      };
-      float m = kNone, l = 0.f, acc[V];
+  for (int nt = 0; nt < NT; ++nt) {
+    const int col = nt * 8 + rw;
+    const bool live = col < rows;
+    // partial 0 is this CTA's second one, the others the first ones of the CTAs after it
+    auto part = [&](int i) -> int64_t {
+      return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::ROWS + col;
+    };
+    float m = kNone, l = 0.f, acc[G];
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = 0.f;
-      if (live) {
-        for (int i = sub + kSub * lane; i <= follow; i += kSub * 32) m = fmaxf(m, __ldcg(ws.ml + part(i)).x);
+    for (int v = 0; v < G; ++v) acc[v] = 0.f;
+    if (live) {
+      for (int i = sub + kSub * lane; i <= follow; i += kSub * 32) m = fmaxf(m, __ldcg(ws.ml + part(i)).x);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll 4
-        for (int i = sub; i <= follow; i += kSub) {
-          const int64_t at = part(i);
-          const float2 ml = __ldcg(ws.ml + at);
-          const float f = ex2(ml.x - m);
-          l = fmaf(ml.y, f, l);
+      for (int i = sub; i <= follow; i += kSub) {
+        const int64_t at = part(i);
+        const float2 ml = __ldcg(ws.ml + at);
+        const float f = ex2(ml.x - m);
+        l = fmaf(ml.y, f, l);
 #pragma unroll
-          for (int v = 0; v < V; v += 2) {
-            const float2 x = __ldcg((const float2*)(ws.o + at * D + v * 32 + 2 * lane));
-            acc[v] = fmaf(x.x, f, acc[v]);
-            acc[v + 1] = fmaf(x.y, f, acc[v + 1]);
-          }
+        for (int v = 0; v < G; v += 2) {
+          const float2 x = __ldcg((const float2*)(ws.o + at * D + lane * G + v));
+          acc[v] = fmaf(x.x, f, acc[v]);
+          acc[v + 1] = fmaf(x.y, f, acc[v + 1]);
         }
       }
-#pragma unroll
-      for (int v = 0; v < V; v += 2)
-        *(float2*)&acc_s[rw][sub][v * 32 + 2 * lane] = make_float2(acc[v], acc[v + 1]);
-      if (lane == 0) ml_s[rw][sub] = make_float2(m, l);
-      __syncthreads();
-      if (sub == 0 && live) {
-        float mt = kNone;
-        for (int k = 0; k < kSub; ++k) mt = fmaxf(mt, ml_s[rw][k].x);
-        float f[kSub], lt = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSub; ++k) {
-          f[k] = ex2(ml_s[rw][k].x - mt);
-          lt = fmaf(ml_s[rw][k].y, f[k], lt);
-        }
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
-        const int row = d.z + col, tokq = row / p.group, uq = row - tokq * p.group;
-        const int64_t qrow = first + tokq;
-        const int head = d.y * p.group + uq;
-        for (int c = lane; c < D / 4; c += 32) {
-          float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < kSub; ++k) {
-            const float4 a = *(const float4*)&acc_s[rw][k][4 * c];
-            x[0] = fmaf(a.x, f[k], x[0]);
-            x[1] = fmaf(a.y, f[k], x[1]);
-            x[2] = fmaf(a.z, f[k], x[2]);
-            x[3] = fmaf(a.w, f[k], x[3]);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] *= inv;
-          store_out4(p, qrow * p.out_stride + (int64_t)head * D + 4 * c, x);
-        }
-        if (lane == 0 && p.lse)
-          p.lse[qrow * p.n_q_heads + head] =
-              lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
-      }
-      __syncthreads();
     }
+#pragma unroll
+    for (int v = 0; v < G; v += 2)
+      *(float2*)&acc_s[rw][sub][lane * G + v] = make_float2(acc[v], acc[v + 1]);
+    if (lane == 0) ml_s[rw][sub] = make_float2(m, l);
+    __syncthreads();
+    if (sub == 0 && live) {
+      float mt = kNone, lt = 0.f, x[G];
+      for (int k = 0; k < kSub; ++k) mt = fmaxf(mt, ml_s[rw][k].x);
+#pragma unroll
+      for (int v = 0; v < G; ++v) x[v] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSub; ++k) {
+        const float f = ex2(ml_s[rw][k].x - mt);
+        lt = fmaf(ml_s[rw][k].y, f, lt);
+#pragma unroll
+        for (int v = 0; v < G; v += 2) {
+          const float2 y = *(const float2*)&acc_s[rw][k][lane * G + v];
+          x[v] = fmaf(y.x, f, x[v]);
+          x[v + 1] = fmaf(y.y, f, x[v + 1]);
+        }
+      }
+      store_row<D>(p, d.x, d.y, d.z + col, lane, x, mt, lt);
+    }
+    __syncthreads();
   }
 }
 
@@ -610,7 +665,7 @@ int launch_stream(const AttnParams& p, int ctas, cudaStream_t s) {
       return DQ_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
   }
-  if (launch_pdl(kv_stream_kernel<D, NT>, dim3(ctas), dim3(C::NW * 32), C::SMEM, s, 0, p) !=
+  if (launch_pdl(kv_stream_kernel<D, NT>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) !=
       cudaSuccess)
     return DQ_ERR_CUDA;
   if (launch_pdl(kv_stream_join_kernel<D, NT>, dim3(ctas), dim3(1024), 0, s, 0, p) != cudaSuccess)

@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kMaxCtas = 160;
 constexpr int kPiece = 32;                 // tokens per copy stage
+constexpr int kItemCost = 4;               // tiles' worth of starting and ending an item
 
 template <int D>
 struct TcCfg {
@@ -60,6 +61,7 @@ struct TcCfg {
   // tensor memory columns: O of every row tile, then two score buffers of each
   static constexpr int COL_S = NQ * D;
   static_assert(COL_S + NQ * 2 * TT <= 512, "tensor memory");
+  static_assert(TT == 2 * kPiece && RS >= 3, "a tile is two pieces");
   static_assert((NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE && SMEM <= 232448, "shared memory");
 };
 
@@ -150,6 +152,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // One lane of the (converged) warp, as the compiler knows it.
 __device__ __forceinline__ bool elect_one() {
   uint32_t v;
@@ -207,7 +215,7 @@ template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
   using B = KvBlk<D>;
-  using Wk = Walk<C::ROWS, C::TT>;
+  using Wk = Walk<C::ROWS, C::TT, kItemCost>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
   extern __shared__ __align__(1024) uint8_t smem[];
   pdl_wait();
@@ -265,6 +273,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 
   Item it;
   int64_t iu = Wk::template seek<C::NTH>(p, pre, u0, it);
+  int ta, tb;                              // the tiles of the item that this share holds
   bool ok = true;
 
   if (warp < C::DEC0) {
@@ -276,9 +285,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint32_t qrow = qs + tile * C::Q_TILE;
     int slot = 0;                          // of this CTA's partials
     int gt = 0;                            // tiles so far
-    for (int64_t u = u0; u < u1;) {
-      const int64_t ue = min(u1, iu + it.tiles);
-      const bool from_start = u == iu, to_end = ue == iu + it.tiles;
+    for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more;
+         more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+      const bool from_start = ta == 0, to_end = tb == it.tiles;
       // the row
       const int row = it.row0 + tile * 128 + trow;
       const bool live = tile * 128 + trow < it.rows;
@@ -345,8 +354,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         lo_all = p.window > 0 ? max(0, pb - p.window + 1) : 0;
       }
       float M = kNone, l = 0.f;
-      const int nt = (int)(ue - u);
-      int tok0 = (it.t0 + (int)(u - iu)) * TT;
+      const int nt = tb - ta;
+      int tok0 = (it.t0 + ta) * TT;
       for (int j = 0; j < nt; ++j, ++gt, tok0 += TT) {
         const int sl = tile * 2 + (gt & 1);
         ok = ok && mbar_wait(&s_full[sl], (gt >> 1) & 1);
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         for (int i = 0; i < TT; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mx4[k] = fmaxf(mx4[k], fmaxf(__uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1])));
+            mx4[k] = max3(mx4[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * cf;
         const bool over = mx > M + 12.f;
         if (__any_sync(0xffffffffu, over)) {
@@ -461,12 +470,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         if (from_start && !to_end && threadIdx.x == 0)
           ws.desc[blockIdx.x] = make_int4(
               it.r, it.h, it.row0,
-              ((share_of(iu + it.tiles - 1, N, U) - (int)blockIdx.x) << 1) | slot);
+              ((Wk::last_share(it, iu, N, U) - (int)blockIdx.x) << 1) | slot);
         if (!whole) slot = 1;
       }
-      u = ue;
-      iu += it.tiles;
-      if (u < u1) Wk::next(p, it);
     }
   } else if (warp < C::PROD) {
     // ------------------------------ decoding ------------------------------
@@ -482,94 +488,103 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint32_t v_at[2] = {sw128_offset(vrow, r4), sw128_offset(vrow + 1, r4)};
     const uint32_t raw0 = smem_u32(smem + C::OFF_RAW) + blk * B::BYTES;
     int gt = 0, st = 0, st_phase = 0;
-    for (int64_t u = u0; u < u1 && ok;) {
-      const int64_t ue = min(u1, iu + it.tiles);
-      const int nt = (int)(ue - u);
-      int tok0 = (it.t0 + (int)(u - iu)) * TT;
-      for (int j = 0; j < nt && ok; ++j, ++gt, tok0 += TT) {
+    for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
+         more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+      int tok0 = (it.t0 + ta) * TT;
+      for (int j = ta; j < tb && ok; ++j, ++gt, tok0 += TT) {
         const bool inner = tok0 >= it.begin && tok0 + TT <= it.end;
         const int buf = gt % C::KVS;
         if (gt >= C::KVS) ok = mbar_wait(&kv_empty[buf], (gt / C::KVS - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t kb = ks + buf * C::KV_BUF, vb = vs + buf * C::KV_BUF;
-#pragma unroll 1
-        for (int pc = 0; pc < TT / kPiece; ++pc) {
-          ok = mbar_wait(&raw_full[st], st_phase);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint32_t rb = raw0 + st * C::PIECE_B;
-          const uint32_t row_b = pc * kPiece * 128;      // 32 rows of 128 bytes
-          uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
-          if (!inner) {
-            // a token that no row sees may hold anything: its V scale becomes 0
-            const int at = tok0 + pc * kPiece + vrow;
-            keep0 = at >= it.begin && at < it.end ? 0xFFFFFFFFu : 0u;
-            keep1 = at + 1 >= it.begin && at + 1 < it.end ? 0xFFFFFFFFu : 0u;
-          }
+        // every load of the tile's two pieces before the first store: one warp per scheduler decodes, so
+        // its latencies have to overlap
+        int sn = st + 1, sn_phase = st_phase;
+        if (sn == C::RS) {
+          sn = 0;
+          sn_phase ^= 1;
+        }
+        ok = mbar_wait(&raw_full[st], st_phase) && mbar_wait(&raw_full[sn], sn_phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t rb[2] = {raw0 + st * C::PIECE_B, raw0 + sn * C::PIECE_B};
+        uint32_t keep[2][2];
 #pragma unroll
-          for (int gh = 0; gh < GH; ++gh) {
-            // every load of this part before the first store
-            uint32_t kw[W], kd[W / 2], vw[W], vx[W / 2], vy[W / 2];
-            lds_words<W>(rb + ((gh * 16 + ktok) * 4 + t) * W * 4, kw);
+        for (int pc = 0; pc < 2; ++pc) {
+          // a token that no row sees may hold anything: its V scale becomes 0
+          const int at = tok0 + pc * kPiece + vrow;
+          keep[pc][0] = inner || (at >= it.begin && at < it.end) ? 0xFFFFFFFFu : 0u;
+          keep[pc][1] = inner || (at + 1 >= it.begin && at + 1 < it.end) ? 0xFFFFFFFFu : 0u;
+        }
+#pragma unroll
+        for (int gh = 0; gh < GH; ++gh) {
+          uint32_t kw[2][W], kd[2][W / 2], vw[2][W], vx[2][W / 2], vy[2][W / 2];
+#pragma unroll
+          for (int pc = 0; pc < 2; ++pc) {
+            lds_words<W>(rb[pc] + ((gh * 16 + ktok) * 4 + t) * W * 4, kw[pc]);
             if (W == 4) {
-              const uint2 x = lds_u64(rb + B::OFF_KD + 2 * (ktok * G + gh * W));
-              kd[0] = x.x;
-              kd[W / 2 - 1] = x.y;
+              const uint2 x = lds_u64(rb[pc] + B::OFF_KD + 2 * (ktok * G + gh * W));
+              kd[pc][0] = x.x;
+              kd[pc][W / 2 - 1] = x.y;
             } else {
-              kd[0] = lds_u32(rb + B::OFF_KD + 2 * ktok * G);
+              kd[pc][0] = lds_u32(rb[pc] + B::OFF_KD + 2 * ktok * G);
             }
-            lds_words<W>(rb + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, vw);
+            lds_words<W>(rb[pc] + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, vw[pc]);
 #pragma unroll
             for (int k = 0; k < W / 2; ++k) {
               const int g = gh * W + 2 * k;
-              vx[k] = lds_u32(rb + B::OFF_VD + ((t * G + g) * 4 + half * 2) * 2);
-              vy[k] = lds_u32(rb + B::OFF_VD + ((t * G + g + 1) * 4 + half * 2) * 2);
+              vx[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g) * 4 + half * 2) * 2);
+              vy[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g + 1) * 4 + half * 2) * 2);
             }
+          }
+#pragma unroll
+          for (int pc = 0; pc < 2; ++pc) {
+            const uint32_t row_b = pc * kPiece * 128;      // 32 rows of 128 bytes
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-              const uint32_t word = odd ? kw[i ^ 1] : kw[i];
-              const __half2 dd = u32_as_h2(__byte_perm(kd[i / 2], 0, k_sel[i & 1]));
+              const uint32_t word = odd ? kw[pc][i ^ 1] : kw[pc][i];
+              const __half2 dd = u32_as_h2(__byte_perm(kd[pc][i / 2], 0, k_sel[i & 1]));
               sts_u128(kb + row_b + (gh * W + i) / 2 * (TT * 128) + k_at[i & 1], decode8(word, dd));
             }
 #pragma unroll
             for (int k = 0; k < W / 2; ++k) {
-              const __half2 d0 = u32_as_h2(__byte_perm(vx[k], vy[k], 0x5410) & keep0);
-              const __half2 d1 = u32_as_h2(__byte_perm(vx[k], vy[k], 0x7632) & keep1);
+              const __half2 d0 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x5410) & keep[pc][0]);
+              const __half2 d1 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x7632) & keep[pc][1]);
               const uint32_t at = vb + row_b + (gh * (W / 2) + k) * (TT * 128);
-              sts_u128(at + v_at[0], decode8(vw[k], d0));
-              sts_u128(at + v_at[1], decode8(vw[W / 2 + k], d1));
+              sts_u128(at + v_at[0], decode8(vw[pc][k], d0));
+              sts_u128(at + v_at[1], decode8(vw[pc][W / 2 + k], d1));
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_empty[st]);
-          if (++st == C::RS) {
-            st = 0;
-            st_phase ^= 1;
-          }
         }
-        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[st]);
+          mbar_arrive(&raw_empty[sn]);
+        }
+        st = sn + 1;
+        st_phase = sn_phase;
+        if (st == C::RS) {
+          st = 0;
+          st_phase ^= 1;
+        }
         fence_proxy_async_smem();
         mbar_arrive(&kv_full[buf]);
       }
-      u = ue;
-      iu += it.tiles;
-      if (u < u1) Wk::next(p, it);
     }
   } else {
     if (warp == C::PROD) {
     // ------------------------------ copies ------------------------------
     const uint64_t pol = l2_evict_first_policy();
     const int shift = p.g.page_shift;
-    int64_t piece = 0;
-    for (int64_t u = u0; u < u1 && ok;) {
-      const int64_t ue = min(u1, iu + it.tiles);
+    int piece = 0, st = 0, st_phase = 0;
+    for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
+         more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
       int tbase = -1, tent = 0;
-      for (int64_t j = u; j < ue && ok; ++j) {
-        const int tok0 = (it.t0 + (int)(j - iu)) * TT;
-        for (int pc = 0; pc < TT / kPiece && ok; ++pc, ++piece) {
-          const int st = (int)(piece % C::RS);
-          if (piece >= C::RS) ok = mbar_wait(&raw_empty[st], (int)((piece / C::RS - 1) & 1));
+      for (int j = ta; j < tb && ok; ++j) {
+        const int tok0 = (it.t0 + j) * TT;
+        for (int pc = 0; pc < TT / kPiece && ok; ++pc) {
+          if (piece >= C::RS) ok = mbar_wait(&raw_empty[st], st_phase ^ 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], C::PIECE_B);
@@ -594,11 +609,13 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
                        cnt / kKvBlk * B::BYTES, &raw_full[st], pol);
             run += cnt;
           }
+          if (piece < C::RS) ++piece;
+          if (++st == C::RS) {
+            st = 0;
+            st_phase ^= 1;
+          }
         }
       }
-      u = ue;
-      iu += it.tiles;
-      if (u < u1) Wk::next(p, it);
     }
     } else {
       // ------------------------------ products ------------------------------
@@ -652,9 +669,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         __syncwarp();
         return true;
       };
-      for (int64_t u = u0; u < u1 && ok; ++seg) {
-        const int64_t ue = min(u1, iu + it.tiles);
-        const int nt = uniform((int)(ue - u)), end = gt + nt, g0 = gt;
+      for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
+           more = Wk::after(p, it, iu, u0, u1, ta, tb), ++seg) {
+        const int nt = uniform(tb - ta), end = gt + nt, g0 = gt;
         ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
         ok = ok && scores(gt);
         if (nt > 1) ok = ok && scores(gt + 1);
@@ -662,12 +679,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           ok = weighted(gt, gt == g0);
           if (gt + 2 < end) ok = ok && scores(gt + 2);
         }
-        u = ue;
-        iu += it.tiles;
-        if (u < u1) Wk::next(p, it);
       }
       // no arrival is under way when the CTA ends
-      if (ok) mbar_wait(&kv_empty[(gt - 1) % C::KVS], ((gt - 1) / C::KVS) & 1);
+      if (ok && gt > 0) mbar_wait(&kv_empty[(gt - 1) % C::KVS], ((gt - 1) / C::KVS) & 1);
     }
   }
   tc_fence_before();
@@ -678,9 +692,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   }
 }
 
-// Joins the partials of the items that go over several CTAs' shares: CTA (c, y)
-// takes rows 8 y.. of the item that starts in CTA c's share and goes on behind it,
-// a warp per row.
+// Joins the partials of the items that go over several CTAs' shares: the CTAs (c, y)
+// take the rows of the item that starts in CTA c's share and goes on behind it.
+constexpr int kJoinRows = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) kv_tc_join_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
@@ -693,50 +708,43 @@ __global__ void __launch_bounds__(256) kv_tc_join_kernel(const __grid_constant__
   if (follow == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int first;
-  const int n = q_rows(p, d.x, &first);
-  const int col = blockIdx.y * 8 + warp;
-  if (col >= min(C::ROWS, n * p.group - d.z)) return;
-  auto part = [&](int i) -> int64_t {
-    return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? (d.w & 1) : 0)) * C::ROWS + col;
-  };
-  float m = kNone, l = 0.f, acc[V];
+  const int rows = min(C::ROWS, q_rows(p, d.x, &first) * p.group - d.z);
+  // kJoinRows rows at a time, so that their loads overlap
+  for (int c0 = (blockIdx.y * 8 + warp) * kJoinRows; c0 < rows; c0 += gridDim.y * 8 * kJoinRows) {
+    float m[kJoinRows], l[kJoinRows], acc[kJoinRows][V];
+    auto part = [&](int i, int k) -> int64_t {
+      return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? (d.w & 1) : 0)) * C::ROWS + min(c0 + k, rows - 1);
+    };
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int i = lane; i <= follow; i += 32) m = fmaxf(m, __ldcg(ws.ml + part(i)).x);
+    for (int k = 0; k < kJoinRows; ++k) {
+      m[k] = kNone;
+      l[k] = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll 4
-  for (int i = 0; i <= follow; ++i) {
-    const int64_t at = part(i);
-    const float2 ml = __ldcg(ws.ml + at);
-    const float f = ex2(ml.x - m);
-    l = fmaf(ml.y, f, l);
-#pragma unroll
-    for (int v = 0; v < V; v += 2) {
-      const float2 x = __ldcg((const float2*)(ws.o + at * D + lane * V + v));
-      acc[v] = fmaf(x.x, f, acc[v]);
-      acc[v + 1] = fmaf(x.y, f, acc[v + 1]);
+      for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
     }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int row = d.z + col, tokq = row / p.group, uq = row - tokq * p.group;
-  const int64_t qrow = first + tokq;
-  const int head = d.y * p.group + uq;
-  const int64_t base = qrow * p.out_stride + (int64_t)head * D;
-  // V values per lane, in fours; D = 64: two lanes' pairs make one four
+    for (int i = 0; i <= follow; ++i) {
 #pragma unroll
-  for (int v = 0; v < V; v += 4) {
-    float x[4];
+      for (int k = 0; k < kJoinRows; ++k) {
+        const int64_t at = part(i, k);
+        const float2 ml = __ldcg(ws.ml + at);
+        float x[V];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = acc[V < 4 ? k & 1 : v + k] * inv;
-    if (V < 4) {
-      x[2] = __shfl_down_sync(0xffffffffu, x[0], 1);
-      x[3] = __shfl_down_sync(0xffffffffu, x[1], 1);
+        for (int v = 0; v < V; v += 2) {
+          const float2 y = __ldcg((const float2*)(ws.o + at * D + lane * V + v));
+          x[v] = y.x;
+          x[v + 1] = y.y;
+        }
+        const float mn = fmaxf(m[k], ml.x), f0 = ex2(m[k] - mn), f1 = ex2(ml.x - mn);
+        m[k] = mn;
+        l[k] = l[k] * f0 + ml.y * f1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[k][v] = acc[k][v] * f0 + x[v] * f1;
+      }
     }
-    if (V >= 4 || (lane & 1) == 0) store_out4(p, base + lane * V + v, x);
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k)
+      if (c0 + k < rows) store_row<D>(p, d.x, d.y, d.z + c0 + k, lane, acc[k], m[k], l[k]);
   }
-  if (lane == 0 && p.lse)
-    p.lse[qrow * p.n_q_heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <int D>
@@ -753,7 +761,7 @@ int launch_tc(const AttnParams& p, int ctas, cudaStream_t s) {
   }
   if (launch_pdl(kv_tc_kernel<D>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
-  if (launch_pdl(kv_tc_join_kernel<D>, dim3(ctas, C::ROWS / 8), dim3(256), 0, s, 0, p) != cudaSuccess)
+  if (launch_pdl(kv_tc_join_kernel<D>, dim3(ctas, C::ROWS / (8 * kJoinRows)), dim3(256), 0, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }
