@@ -94,6 +94,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
+// D = A B + C with C the same for both rows of a lane
+__device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
 // W consecutive words (2 or 4) from shared memory
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
@@ -147,44 +156,38 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     more = Wk::here(p, it, iu, u0, u1, ta, tb);
   }
 
-  // ---- producer state: the next tile to copy, its item, and 32 entries of its table row
+  // ---- producer state: the next tile to copy and its item.  A tile is one contiguous run of a page,
+  // or two of 16-token pages; each lane holds the address of one of the next 32 runs and issues its
+  // copy, so that page numbers are looked up once in 32 runs.
   Item pi = it;
   int64_t piu = iu;
   int pt = ta, pta = ta, ptb = tb;
   bool pmore = more;
-  int tbase = -1, tent = 0;
   const uint64_t pol = l2_evict_first_policy();
-  const int tshift = p.g.page_shift;
+  const int runs = p.g.page_size < kTile ? kTile / kKvBlk : 1;      // page_size is 16 or at least kTile
+  const uint32_t run_bytes = C::STG / runs;
+  int used = 32;                           // runs of the 32 that were issued
+  const uint8_t* src = nullptr;
   auto produce = [&](int stage) {
     if (!pmore) return;
-    const int tile = pi.t0 + pt;
-    uint8_t* dst = ring + stage * C::STG;
-    const int tok = tile * kTile;
+    if (used == 32) {
+      used = 0;
+      const int tok = (pi.t0 + pt) * kTile + lane * (kTile / runs);
+      const int pg = tok >> p.g.page_shift;
+      int page = pg < p.max_pages ? __ldg(p.table + (int64_t)pi.r * p.max_pages + pg) : 0;
+      if (page < 0 || page >= p.g.n_pages) page = 0;
+      src = p.g.pages + (int64_t)page * p.g.page_bytes + pi.h * p.g.head_bytes +
+            (tok & (p.g.page_size - 1)) / kKvBlk * B::BYTES;
+    }
     if (lane == 0) mbar_arrive_expect_tx(&bars[stage], C::STG);
     __syncwarp();
-    int run = 0;
-    while (run < kTile) {
-      const int pg = (tok + run) >> tshift;
-      if (tbase < 0 || pg < tbase || pg >= tbase + 32) {
-        tbase = pg;
-        const int e = pg + lane;
-        tent = e < p.max_pages ? __ldg(p.table + (int64_t)pi.r * p.max_pages + e) : 0;
-        if (tent < 0 || tent >= p.g.n_pages) tent = 0;
-      }
-      const int page = __shfl_sync(0xffffffffu, tent, pg - tbase);
-      const int cnt = min(p.g.page_size, kTile - run);
-      const int off = (tok + run) & (p.g.page_size - 1);
-      if (lane == 0)
-        bulk_g2s(dst + run / kKvBlk * B::BYTES,
-                 p.g.pages + (int64_t)page * p.g.page_bytes + pi.h * p.g.head_bytes +
-                     off / kKvBlk * B::BYTES,
-                 cnt / kKvBlk * B::BYTES, &bars[stage], pol);
-      run += cnt;
-    }
+    const uint32_t mine = lane - used;
+    if (mine < runs) bulk_g2s(ring + stage * C::STG + mine * run_bytes, src, run_bytes, &bars[stage], pol);
+    used += runs;
     if (++pt == ptb) {
       pmore = Wk::after(p, pi, piu, u0, u1, pta, ptb);
       pt = pta;
-      tbase = -1;
+      used = 32;
     }
   };
   __syncwarp();
@@ -195,7 +198,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   uint32_t qf[G][4][NT];
   float qi[G][NT][2], cf[NT][2];
   float o[G][2][NT][4], ofs[G][NT][4];
-  float M[NT][2], l[NT][2];
+  float M[NT][2], lim[NT][2];
+  float2 l[NT];
   float b = 10.f;
   bool ok = true;
 
@@ -207,12 +211,12 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       const int row = it.row0 + nt * 8 + lr;
       const bool live = nt * 8 + lr < it.rows;
       const int tokq = row / p.group, uq = row - tokq * p.group;
-      const uint16_t* src = (const uint16_t*)p.q + (int64_t)(it.first + tokq) * p.q_stride +
+      const uint16_t* qsrc = (const uint16_t*)p.q + (int64_t)(it.first + tokq) * p.q_stride +
                             ((int64_t)it.h * p.group + uq) * D + 8 * lt;
       uint4 raw[G];
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        raw[g] = live ? __ldg((const uint4*)(src + 32 * g)) : make_uint4(0, 0, 0, 0);
+        raw[g] = live ? __ldg((const uint4*)(qsrc + 32 * g)) : make_uint4(0, 0, 0, 0);
       float x[G][8], mx = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -259,7 +263,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       cf[nt][0] = __shfl_sync(0xffffffffu, c, 8 * lt);
       cf[nt][1] = __shfl_sync(0xffffffffu, c, 8 * lt + 4);
       M[nt][0] = M[nt][1] = kNone;
-      l[nt][0] = l[nt][1] = 0.f;
+      lim[nt][0] = lim[nt][1] = kNone;
+      l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -299,10 +304,6 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       for (int k = 0; k < kBlks; ++k) {
         const uint32_t kb = base + k * B::BYTES;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[k][nt][i] = 0.f;
-#pragma unroll
         for (int gh = 0; gh < GH; ++gh) {
           uint32_t wa[W], wb[W];
           lds_words<W>(kb + (((gh * 16 + lr) * 4 + lt) * W) * 4, wa);
@@ -326,29 +327,26 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             const float sa = (gw2 & 1) ? fa.y : fa.x, sb = (gw2 & 1) ? fb.y : fb.x;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float acc[4] = {qi[g][nt][0], qi[g][nt][1], qi[g][nt][0], qi[g][nt][1]};
-              mma_16816_nv(acc, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
-                           qf[g][0][nt], qf[g][1][nt]);
+              float acc[4];
+              mma_16816_c(acc, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
+                          qf[g][0][nt], qf[g][1][nt], qi[g][nt][0], qi[g][nt][1]);
               mma_16816_nv(acc, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u,
                            y8 & 0x00F000F0u, qf[g][2][nt], qf[g][3][nt]);
-              s[k][nt][0] = fmaf(sa, acc[0], s[k][nt][0]);
-              s[k][nt][1] = fmaf(sa, acc[1], s[k][nt][1]);
-              s[k][nt][2] = fmaf(sb, acc[2], s[k][nt][2]);
-              s[k][nt][3] = fmaf(sb, acc[3], s[k][nt][3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                s[k][nt][i] = g == 0 ? (i < 2 ? sa : sb) * acc[i] : fmaf(i < 2 ? sa : sb, acc[i], s[k][nt][i]);
             }
           }
         }
       }
-      // ---- V scales (and their exponents' top bit)
-      uint32_t dv[kBlks][G][2], big = 0;
-#pragma unroll
-      for (int k = 0; k < kBlks; ++k) {
+      // the V scales of block k for this lane's tokens, pairs (2t, 2t + 1) and (2t + 8, 2t + 9)
+      auto v_scales = [&](int k, uint32_t (&dv)[G][2]) {
         const uint32_t va = base + k * B::BYTES + B::OFF_VD + 8 * lt * G;
 #pragma unroll
         for (int g = 0; g < G; g += 2) {
           const uint4 x = lds_u128(va + 8 * g);
-          dv[k][g][0] = x.x; dv[k][g][1] = x.y;
-          dv[k][g + 1][0] = x.z; dv[k][g + 1][1] = x.w;
+          dv[g][0] = x.x; dv[g][1] = x.y;
+          dv[g + 1][0] = x.z; dv[g + 1][1] = x.w;
         }
         if (!inner) {
           // tokens that no row sees may hold anything: their scales become 0
@@ -358,39 +356,51 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             const uint32_t keep = ((a >= it.begin && a < it.end) ? 0x0000FFFFu : 0u) |
                                   ((a + 1 >= it.begin && a + 1 < it.end) ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int g = 0; g < G; ++g) dv[k][g][j] &= keep;
+            for (int g = 0; g < G; ++g) dv[g][j] &= keep;
           }
         }
+      };
+      uint32_t big = 0;                    // has bit 14 of either half set: some V scale is 2 or more
+      if (inner) {
+        // the tile's scales once over the lanes
+        const uint32_t va = base + (lane >> 4) * B::BYTES + B::OFF_VD + (lane & 15) * (D / 16);
+        if (D == 64) {
+          big = lds_u32(va);
+        } else if (D == 128) {
+          const uint2 x = lds_u64(va);
+          big = x.x | x.y;
+        } else {
+          const uint4 x = lds_u128(va);
+          big = x.x | x.y | x.z | x.w;
+        }
+      } else {
 #pragma unroll
-        for (int g = 0; g < G; ++g) big |= dv[k][g][0] | dv[k][g][1];
+        for (int k = 0; k < kBlks; ++k) {
+          uint32_t dv[G][2];
+          v_scales(k, dv);
+#pragma unroll
+          for (int g = 0; g < G; ++g) big |= dv[g][0] | dv[g][1];
+        }
+#pragma unroll
+        for (int k = 0; k < kBlks; ++k)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int a = tok0 + k * 16 + 8 * (i >> 1) + lr;
+              if (a < lo_c[nt][i & 1] || a >= hi_c[nt][i & 1]) s[k][nt][i] = -INFINITY;
+            }
       }
       // ---- weights
       float top[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float m = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < kBlks; ++k)
-#pragma unroll
-            for (int hrow = 0; hrow < 2; ++hrow) {
-              float v = s[k][nt][2 * hrow + i] * cf[nt][i];
-              if (!inner) {
-                const int a = tok0 + k * 16 + 8 * hrow + lr;
-                v = a >= lo_c[nt][i] && a < hi_c[nt][i] ? v : -INFINITY;
-              }
-              s[k][nt][2 * hrow + i] = v;
-              m = fmaxf(m, v);
-            }
-          top[nt][i] = m;
-        }
-      }
-      const float lim = b + 4.f;
       bool over = b > 0.f && (big & 0x40004000u) != 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        over = over || top[nt][0] > M[nt][0] + lim || top[nt][1] > M[nt][1] + lim;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]), fmaxf(s[1][nt][i], s[1][nt][2 + i])) * cf[nt][i];
+          over = over || top[nt][i] > lim[nt][i];
+        }
       if (__any_sync(0xffffffffu, over)) {
         const float bn = __any_sync(0xffffffffu, (big & 0x40004000u) != 0) ? -2.f : b;
 #pragma unroll
@@ -403,7 +413,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
             const float mo = M[nt][i], mn = fmaxf(mo + (b - bn), m - bn), corr = ex2(mo - mn);
             M[nt][i] = mn;
-            l[nt][i] *= corr;
+            lim[nt][i] = mn + bn + 4.f;
+            (i == 0 ? l[nt].x : l[nt].y) *= corr;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -423,12 +434,13 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int hrow = 0; hrow < 2; ++hrow) {
-            const float p0 = ex2(s[k][nt][2 * hrow] - M[nt][0]);
-            const float p1 = ex2(s[k][nt][2 * hrow + 1] - M[nt][1]);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            pt[nt][hrow] = transpose8x8(h2_as_u32(__floats2half2_rn(p0, p1)));
+            const float2 w = make_float2(ex2(fmaf(s[k][nt][2 * hrow], cf[nt][0], -M[nt][0])),
+                                         ex2(fmaf(s[k][nt][2 * hrow + 1], cf[nt][1], -M[nt][1])));
+            l[nt] = fadd2(l[nt], w);
+            pt[nt][hrow] = transpose8x8(h2_as_u32(__floats2half2_rn(w.x, w.y)));
           }
+        uint32_t dv[G][2];
+        v_scales(k, dv);
         const uint32_t vb = base + k * B::BYTES + B::OFF_V;
 #pragma unroll
         for (int gh = 0; gh < GH; ++gh) {
@@ -444,8 +456,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(pt[nt][0]), u32_as_h2(dv[k][g][0])));
-              const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(pt[nt][1]), u32_as_h2(dv[k][g][1])));
+              const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(pt[nt][0]), u32_as_h2(dv[g][0])));
+              const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(pt[nt][1]), u32_as_h2(dv[g][1])));
               mma_16816_nv(o[g][0][nt], z0 & 0x000F000Fu, z0 & 0x00F000F0u, z1 & 0x000F000Fu,
                            z1 & 0x00F000F0u, b0, b1);
               mma_16816_nv(o[g][1][nt], y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu,
@@ -482,7 +494,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float sum = l[nt][i];
+        float sum = i == 0 ? l[nt].x : l[nt].y;
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
