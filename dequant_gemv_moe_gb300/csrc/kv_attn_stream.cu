@@ -52,9 +52,23 @@ struct Left {
   int has, open, follow;                  // follow: the share in which the item ends
 };
 
+// Where a warp is in its share, kept in shared memory: the tile loop needs its registers.  [0] is the
+// item that is computed, [1] the one that is copied; lo, hi: the positions that each row sees.
+struct Place {
+  Item it;
+  int64_t iu;
+  int a, b;
+};
+struct WarpState {
+  Place at[2];
+  int64_t u0, u1;
+  int lo[16], hi[16];
+};
+
 template <int D, int NT>
 struct StreamCfg {
-  // O (D NT / 4 registers), the offsets, Q and the scores: 16 warps of 128 registers, 12 of 168 or 8 of 255
+  // O (D NT / 4 registers), Q, its sums and the scores: 16 warps of 128 registers, 12 of 168 or 8 of 255.
+  // (attn of 64 requests, 576 MB, heads of 128: 12 warps with three tiles each 111.9 us, 16 with two 113.5.)
   static constexpr int NW = D * NT <= 64 ? 16 : D * NT <= 128 ? 12 : 8;
   static constexpr int ROWS = 8 * NT;
   static constexpr int STG = kBlks * KvBlk<D>::BYTES;
@@ -63,7 +77,8 @@ struct StreamCfg {
   static constexpr int PART = ROWS * D * 4 + ROWS * 8;              // rows of O, then (M, l)
   static constexpr int OFF_LEFT = 512;                              // Left [NW][2]
   static constexpr int OFF_PRE = 1536;                              // int64 [NTH + 1 + NW]
-  static constexpr int OFF_RING = OFF_PRE + 4352;
+  static constexpr int OFF_STATE = OFF_PRE + 4352;
+  static constexpr int OFF_RING = OFF_STATE + (NW * (int)sizeof(WarpState) + 127) / 128 * 128;
   static constexpr int OFF_HEAD = OFF_RING + NW * STAGES * STG;     // the warps' first partials
   static constexpr int SMEM = OFF_HEAD + NW * PART;                 // (the second ones lie in the rings)
   static_assert(SMEM <= 232448 && STAGES * STG >= PART && (NTH + 1 + NW) * 8 <= 4352 &&
@@ -146,22 +161,34 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   const int64_t N = min((int64_t)ctas * C::NW, U);      // every one of the N shares holds a unit
   const int64_t u0 = U * min((int64_t)gw, N) / N, u1 = U * min((int64_t)gw + 1, N) / N;
 
-  // ---- the first item of the share, and its tiles [ta, tb) that lie in it
-  Item it;
-  int64_t iu = 0;
-  int ta = 0, tb = 0;
+  // ---- the first item of the share, and its tiles [a, b) that lie in it
+  WarpState& S = ((WarpState*)(smem + C::OFF_STATE))[warp];
   bool more = u0 < u1;
   if (more) {
-    iu = Wk::template seek<C::NTH>(p, pre, u0, it);
-    more = Wk::here(p, it, iu, u0, u1, ta, tb);
+    Place x;
+    x.iu = Wk::template seek<C::NTH>(p, pre, u0, x.it);
+    more = Wk::here(p, x.it, x.iu, u0, u1, x.a, x.b);
+    if (lane == 0) {
+      S.at[0] = S.at[1] = x;
+      S.u0 = u0;
+      S.u1 = u1;
+    }
   }
+  __syncwarp();
+  // on to the next item of the share; every lane computes it
+  auto advance = [&](Place& at) {
+    Place x = at;
+    const bool m = Wk::after(p, x.it, x.iu, S.u0, S.u1, x.a, x.b);
+    __syncwarp();
+    if (lane == 0) at = x;
+    __syncwarp();
+    return m;
+  };
 
-  // ---- producer state: the next tile to copy and its item.  A tile is one contiguous run of a page,
+  // ---- the next tile to copy.  A tile is one contiguous run of a page,
   // or two of 16-token pages; each lane holds the address of one of the next 32 runs and issues its
   // copy, so that page numbers are looked up once in 32 runs.
-  Item pi = it;
-  int64_t piu = iu;
-  int pt = ta, pta = ta, ptb = tb;
+  int pt = more ? S.at[1].a : 0, ptb = more ? S.at[1].b : 0;
   bool pmore = more;
   const uint64_t pol = l2_evict_first_policy();
   const int runs = p.g.page_size < kTile ? kTile / kKvBlk : 1;      // page_size is 16 or at least kTile
@@ -172,11 +199,12 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     if (!pmore) return;
     if (used == 32) {
       used = 0;
-      const int tok = (pi.t0 + pt) * kTile + lane * (kTile / runs);
+      const Item& x = S.at[1].it;
+      const int tok = (x.t0 + pt) * kTile + lane * (kTile / runs);
       const int pg = tok >> p.g.page_shift;
-      int page = pg < p.max_pages ? __ldg(p.table + (int64_t)pi.r * p.max_pages + pg) : 0;
+      int page = pg < p.max_pages ? __ldg(p.table + (int64_t)x.r * p.max_pages + pg) : 0;
       if (page < 0 || page >= p.g.n_pages) page = 0;
-      src = p.g.pages + (int64_t)page * p.g.page_bytes + pi.h * p.g.head_bytes +
+      src = p.g.pages + (int64_t)page * p.g.page_bytes + x.h * p.g.head_bytes +
             (tok & (p.g.page_size - 1)) / kKvBlk * B::BYTES;
     }
     if (lane == 0) mbar_arrive_expect_tx(&bars[stage], C::STG);
@@ -185,8 +213,9 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     if (mine < runs) bulk_g2s(ring + stage * C::STG + mine * run_bytes, src, run_bytes, &bars[stage], pol);
     used += runs;
     if (++pt == ptb) {
-      pmore = Wk::after(p, pi, piu, u0, u1, pta, ptb);
-      pt = pta;
+      pmore = advance(S.at[1]);
+      pt = S.at[1].a;
+      ptb = S.at[1].b;
       used = 32;
     }
   };
@@ -197,14 +226,15 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   // ---- consumer state
   uint32_t qf[G][4][NT];
   float qi[G][NT][2], cf[NT][2];
-  float o[G][2][NT][4], ofs[G][NT][4];
+  float o[G][2][NT][4];
   float M[NT][2], lim[NT][2];
   float2 l[NT];
   float b = 10.f;
   bool ok = true;
 
   int stage = 0, phase = 0;
-  for (; more; more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+  for (; more; more = advance(S.at[0])) {
+    const Item it = S.at[0].it;
     // ---- rows of the item: column lr of each 8-row tile, values 8 lt.. of every group
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -268,30 +298,27 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[g][0][nt][k] = o[g][1][nt][k] = ofs[g][nt][k] = 0.f;
+        for (int k = 0; k < 4; ++k) o[g][0][nt][k] = o[g][1][nt][k] = 0.f;
     }
     b = 10.f;
-    // the positions that every row of the item sees, and each column's own limits
-    int lo_c[NT][2], hi_c[NT][2];
+    // the positions that every row of the item sees, and each row's own limits
     int lo_all, hi_all;
     {
       const int lo_pos = it.len - it.qlen + it.row0 / p.group;
       const int hi_pos = it.len - it.qlen + (it.row0 + it.rows - 1) / p.group;
       hi_all = p.causal ? min(it.len, lo_pos + 1) : it.len;
       lo_all = p.window > 0 ? max(0, hi_pos - p.window + 1) : 0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int pos = it.len - it.qlen + (it.row0 + nt * 8 + 2 * lt + k) / p.group;
-          hi_c[nt][k] = p.causal ? min(it.len, pos + 1) : it.len;
-          lo_c[nt][k] = p.window > 0 ? pos - p.window + 1 : 0;
-        }
+      if (lane < C::ROWS) {
+        const int pos = it.len - it.qlen + (it.row0 + lane) / p.group;
+        S.hi[lane] = p.causal ? min(it.len, pos + 1) : it.len;
+        S.lo[lane] = p.window > 0 ? pos - p.window + 1 : 0;
+      }
+      __syncwarp();
     }
 
-    const bool from_start = ta == 0, to_end = tb == it.tiles;
-    for (int tl = ta; tl < tb; ++tl) {
-      const int tok0 = (it.t0 + tl) * kTile;
+    const int tb = S.at[0].b;
+    int tok0 = (it.t0 + S.at[0].a) * kTile;
+    for (int tl = S.at[0].a; tl < tb; ++tl, tok0 += kTile) {
       ok = ok && mbar_wait(&bars[stage], phase);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -353,8 +380,9 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int a = tok0 + k * 16 + 8 * j + 2 * lt;
-            const uint32_t keep = ((a >= it.begin && a < it.end) ? 0x0000FFFFu : 0u) |
-                                  ((a + 1 >= it.begin && a + 1 < it.end) ? 0xFFFF0000u : 0u);
+            const int from = S.at[0].it.begin, to = S.at[0].it.end;
+            const uint32_t keep = ((a >= from && a < to) ? 0x0000FFFFu : 0u) |
+                                  ((a + 1 >= from && a + 1 < to) ? 0xFFFF0000u : 0u);
 #pragma unroll
             for (int g = 0; g < G; ++g) dv[g][j] &= keep;
           }
@@ -382,14 +410,18 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
           for (int g = 0; g < G; ++g) big |= dv[g][0] | dv[g][1];
         }
 #pragma unroll
-        for (int k = 0; k < kBlks; ++k)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int i = 0; i < 2; ++i) {
+            const int lo = S.lo[nt * 8 + 2 * lt + i], hi = S.hi[nt * 8 + 2 * lt + i];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int a = tok0 + k * 16 + 8 * (i >> 1) + lr;
-              if (a < lo_c[nt][i & 1] || a >= hi_c[nt][i & 1]) s[k][nt][i] = -INFINITY;
-            }
+            for (int k = 0; k < kBlks; ++k)
+#pragma unroll
+              for (int hrow = 0; hrow < 2; ++hrow) {
+                const int a = tok0 + k * 16 + 8 * hrow + lr;
+                if (a < lo || a >= hi) s[k][nt][2 * hrow + i] = -INFINITY;
+              }
+          }
       }
       // ---- weights
       float top[NT][2];
@@ -421,7 +453,6 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
               for (int k = i; k < 4; k += 2) {
                 o[g][0][nt][k] *= corr;
                 o[g][1][nt][k] *= corr;
-                ofs[g][nt][k] *= corr;
               }
           }
         b = bn;
@@ -463,7 +494,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
               mma_16816_nv(o[g][1][nt], y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu,
                            y1 & 0x00F000F0u, b0, b1);
               // the offset: -8 in each row's unit
-              mma_16816_nv(ofs[g][nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+              mma_16816_nv(o[g][0][nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+              mma_16816_nv(o[g][1][nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
             }
           }
         }
@@ -487,6 +519,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
 
     // ---- the item's rows: whole, or a partial (the second one over the ring, whose copies have all
     // been used: the share ends here)
+    const Item done = S.at[0].it;
+    const bool from_start = S.at[0].a == 0, to_end = S.at[0].b == done.tiles;
     const bool whole = from_start && to_end;
     float* part = (float*)(from_start ? ring : smem + C::OFF_HEAD + warp * C::PART);
     __syncwarp();
@@ -499,18 +533,18 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int col = nt * 8 + 2 * lt + i;
-        if (col >= it.rows) continue;
+        if (col >= done.rows) continue;
         const float k24 = 16777216.f, k20 = 1048576.f;
         const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-        const int row = it.row0 + col, tokq = row / p.group, uq = row - tokq * p.group;
-        const int64_t qrow = it.first + tokq;
-        const int head = it.h * p.group + uq;
+        const int row = done.row0 + col, tokq = row / p.group, uq = row - tokq * p.group;
+        const int64_t qrow = done.first + tokq;
+        const int head = done.h * p.group + uq;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const float x[4] = {(o[g][0][nt][i] + ofs[g][nt][i]) * (k24 * inv),
-                              (o[g][0][nt][2 + i] + ofs[g][nt][2 + i]) * (k20 * inv),
-                              (o[g][1][nt][i] + ofs[g][nt][i]) * (k24 * inv),
-                              (o[g][1][nt][2 + i] + ofs[g][nt][2 + i]) * (k20 * inv)};
+          const float x[4] = {(o[g][0][nt][i]) * (k24 * inv),
+                              (o[g][0][nt][2 + i]) * (k20 * inv),
+                              (o[g][1][nt][i]) * (k24 * inv),
+                              (o[g][1][nt][2 + i]) * (k20 * inv)};
           if (whole)
             store_out4(p, qrow * p.out_stride + (int64_t)head * D + 32 * g + 4 * lr, x);
           else
@@ -525,13 +559,13 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       }
     if (!whole && lane == 0) {
       Left& x = left[warp * 2 + (from_start ? 1 : 0)];
-      x.r = it.r;
-      x.h = it.h;
-      x.row0 = it.row0;
-      x.rows = it.rows;
+      x.r = done.r;
+      x.h = done.h;
+      x.row0 = done.row0;
+      x.rows = done.rows;
       x.has = 1;
       x.open = to_end ? 0 : 1;
-      x.follow = Wk::last_share(it, iu, N, U);
+      x.follow = Wk::last_share(done, S.at[0].iu, N, U);
     }
   }
   __syncthreads();
