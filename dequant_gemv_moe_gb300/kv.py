@@ -1,23 +1,53 @@
 """torch-facing wrappers of the 4-bit paged K/V cache (marshalling only; see
 the dq_kv_* section of include/dqmoe.h for what each call computes)."""
-import collections
 import ctypes
 
 import torch
 
-from ._lib import F16, F32, BF16, Q4_0, KvAttn, KvCacheDesc
-from .ops import _call, _stream
+from ._lib import F16, F32, BF16, Q4_0, DqError, KvAttn, KvCacheDesc, lib
 
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_plan, _append, _read, _attention = (lib.dq_kv_plan, lib.dq_kv_append, lib.dq_kv_read,
+                                     lib.dq_kv_attention)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-KvPlan = collections.namedtuple("KvPlan", "kv_len q_start slots positions free_count unserved")
+# A decode step's calls take a few microseconds on the GPU, so the wrappers keep to few Python
+# operations: bound functions, plain integers, the stream's handle without a Stream object.
+
+
+def _stream(t):
+    """The handle of the current stream of t's device."""
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _raise(name, rc):
+    raise DqError(name, rc)
 
 
 def _check(t, name, dtype, shape=None):
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor of %s" % (name, dtype))
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+class KvPlan:
+    """A step's outputs of kv_plan: kv_len, q_start, positions, free_count, unserved (int32) and
+    slots (int64), for B requests and n_tokens rows; a step may write to an earlier one's."""
+
+    __slots__ = ("kv_len", "q_start", "slots", "positions", "free_count", "unserved", "size", "_ptrs")
+
+    def __init__(self, B, n_tokens, device="cuda"):
+        i32 = torch.empty(2 * B + 3 + n_tokens, dtype=torch.int32, device=device)
+        self.kv_len, self.q_start = i32[:B], i32[B:2 * B + 1]
+        self.free_count, self.unserved = i32[2 * B + 1:2 * B + 2], i32[2 * B + 2:2 * B + 3]
+        self.positions = i32[2 * B + 3:]
+        self.slots = torch.empty(n_tokens, dtype=torch.int64, device=device)
+        self.size = (B, n_tokens)
+        self._ptrs = tuple(t.data_ptr() for t in (self.kv_len, self.q_start, self.slots, self.positions,
+                                                  self.free_count, self.unserved))
 
 
 class KvCache:
@@ -55,8 +85,8 @@ class KvCache:
 
 def _size(desc):
     n = ctypes.c_size_t()
-    _call("dq_kv_cache_size", ctypes.byref(desc), ctypes.byref(n))
-    return n.value
+    rc = lib.dq_kv_cache_size(ctypes.byref(desc), ctypes.byref(n))
+    return n.value if rc == 0 else _raise("dq_kv_cache_size", rc)
 
 
 def kv_plan(ctx_len, new_len, block_table, free_pages, free_count, page_size, n_tokens, out=None):
@@ -70,36 +100,29 @@ def kv_plan(ctx_len, new_len, block_table, free_pages, free_count, page_size, n_
     B = ctx_len.numel()
     _check(ctx_len, "ctx_len", torch.int32)
     _check(new_len, "new_len", torch.int32, (B,))
-    _check(block_table, "block_table", torch.int32, (B, block_table.shape[-1]))
+    _check(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B][max_pages]")
     _check(free_pages, "free_pages", torch.int32)
     _check(free_count, "free_count", torch.int32, (1,))
     if out is None:
-        dev = ctx_len.device
-        i32 = torch.empty(2 * B + 3 + n_tokens, dtype=torch.int32, device=dev)
-        out = KvPlan(i32[:B], i32[B:2 * B + 1], torch.empty(n_tokens, dtype=torch.int64, device=dev),
-                     i32[2 * B + 3:], i32[2 * B + 1:2 * B + 2], i32[2 * B + 2:2 * B + 3])
-    else:
-        _check(out.kv_len, "kv_len", torch.int32, (B,))
-        _check(out.q_start, "q_start", torch.int32, (B + 1,))
-        _check(out.slots, "slots", torch.int64, (n_tokens,))
-        _check(out.positions, "positions", torch.int32, (n_tokens,))
-        _check(out.free_count, "free_count", torch.int32, (1,))
-        _check(out.unserved, "unserved", torch.int32, (1,))
-    _call("dq_kv_plan", ctx_len.data_ptr(), new_len.data_ptr(), B, page_size,
-          block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.numel(),
-          free_count.data_ptr(), n_tokens, out.kv_len.data_ptr(), out.q_start.data_ptr(),
-          out.slots.data_ptr(), out.positions.data_ptr(), out.free_count.data_ptr(),
-          out.unserved.data_ptr(), _stream())
-    return out
+        out = KvPlan(B, n_tokens, ctx_len.device)
+    elif out.size != (B, n_tokens):
+        raise ValueError("out holds %d requests and %d rows, not %d and %d" % (*out.size, B, n_tokens))
+    rc = _plan(ctx_len.data_ptr(), new_len.data_ptr(), B, page_size, block_table.data_ptr(),
+               block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
+               n_tokens, *out._ptrs, _stream(ctx_len))
+    return out if rc == 0 else _raise("dq_kv_plan", rc)
 
 
 def _rows(cache, t, name):
     """The token stride of rows [T][n_kv_heads][head_dim] (only the first may be strided)."""
-    if t.dim() != 3 or t.shape[1] != cache.n_kv_heads or t.shape[2] != cache.head_dim:
-        raise ValueError("%s must be [T][%d][%d]" % (name, cache.n_kv_heads, cache.head_dim))
-    if not t.is_cuda or t.stride(2) != 1 or t.stride(1) != cache.head_dim:
-        raise ValueError("%s must be a CUDA tensor with consecutive heads" % name)
-    return t.stride(0) if t.shape[0] > 1 else cache.n_kv_heads * cache.head_dim
+    T, H, D = t.shape
+    a, b, c = t.stride()
+    if H != cache.n_kv_heads or D != cache.head_dim or not t.is_cuda or c != 1 or (b != D and H > 1):
+        raise ValueError("%s must be a CUDA tensor [T][%d][%d] with consecutive heads" %
+                         (name, cache.n_kv_heads, cache.head_dim))
+    return a if T > 1 else H * D
 
 
 def kv_append(cache, k, v, slots):
@@ -111,8 +134,10 @@ def kv_append(cache, k, v, slots):
     ks, vs = _rows(cache, k, "k"), _rows(cache, v, "v")
     _check(slots, "slots", torch.int64, (T,))
     if T:
-        _call("dq_kv_append", cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, _DT[k.dtype],
-              slots.data_ptr(), T, _stream())
+        rc = _append(cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, _DT[k.dtype], slots.data_ptr(), T,
+                     _stream(k))
+        if rc != 0:
+            _raise("dq_kv_append", rc)
 
 
 def kv_read(cache, slots, dtype=torch.float32, out=None):
@@ -129,16 +154,17 @@ def kv_read(cache, slots, dtype=torch.float32, out=None):
     _check(k, "k", k.dtype, shape)
     _check(v, "v", k.dtype, shape)
     if T:
-        _call("dq_kv_read", cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(),
-              _DT[k.dtype], _stream())
+        rc = _read(cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _DT[k.dtype], _stream(k))
+        if rc != 0:
+            _raise("dq_kv_read", rc)
     return k, v
 
 
 def kv_attention_workspace_size(cache, n_q_heads, B, T, max_q_len=None):
     n = ctypes.c_size_t()
-    _call("dq_kv_attention_workspace_size", cache._ref, n_q_heads, T, B,
-          T if max_q_len is None else max_q_len, ctypes.byref(n))
-    return n.value
+    rc = lib.dq_kv_attention_workspace_size(cache._ref, n_q_heads, T, B,
+                                            T if max_q_len is None else max_q_len, ctypes.byref(n))
+    return n.value if rc == 0 else _raise("dq_kv_attention_workspace_size", rc)
 
 
 def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True, window=0,
@@ -151,18 +177,21 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
     most rows a request has (T unless given).
     """
     T, H, D = q.shape
+    qs, qh, qd = q.stride()
     B = kv_len.numel()
     if q.dtype not in _DT:
         raise TypeError("q must be float16 or bfloat16, got %s" % q.dtype)
-    if D != cache.head_dim or not q.is_cuda or q.stride(2) != 1 or (H > 1 and q.stride(1) != D):
+    if D != cache.head_dim or not q.is_cuda or qd != 1 or (qh != D and H > 1):
         raise ValueError("q must be a CUDA tensor [T][n_q_heads][%d] with consecutive heads" % cache.head_dim)
     _check(q_start, "q_start", torch.int32, (B + 1,))
     _check(kv_len, "kv_len", torch.int32)
-    _check(block_table, "block_table", torch.int32, (B, block_table.shape[-1]))
+    _check(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B][max_pages]")
     if out is None:
         out = torch.empty((T, H, D), dtype=out_dtype or q.dtype, device=q.device)
-    elif out.dtype not in _DT or tuple(out.shape) != (T, H, D) or not out.is_cuda or \
-            out.stride(2) != 1 or (H > 1 and out.stride(1) != D):
+    os, oh, od = out.stride()
+    if out.dtype not in _DT or out.shape != (T, H, D) or not out.is_cuda or od != 1 or (oh != D and H > 1):
         raise ValueError("out must be a CUDA tensor [T][n_q_heads][head_dim] with consecutive heads")
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
@@ -175,9 +204,9 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
     if ws is None:
         ws = torch.empty(kv_attention_workspace_size(cache, H, B, T, max_q_len), dtype=torch.uint8,
                          device=q.device)
-    a = KvAttn(q.data_ptr(), q.stride(0) if T > 1 else H * D, _DT[q.dtype], H, T, B,
-               q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-               max_q_len, D ** -0.5 if scale is None else scale, int(causal), window,
-               out.data_ptr(), out.stride(0) if T > 1 else H * D, _DT[out.dtype], lse.data_ptr())
-    _call("dq_kv_attention", cache._ref, ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream())
-    return out, lse
+    a = KvAttn(q.data_ptr(), qs if T > 1 else H * D, _DT[q.dtype], H, T, B, q_start.data_ptr(),
+               kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1], max_q_len,
+               D ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
+               os if T > 1 else H * D, _DT[out.dtype], lse.data_ptr())
+    rc = _attention(cache._ref, ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream(q))
+    return (out, lse) if rc == 0 else _raise("dq_kv_attention", rc)
