@@ -11,6 +11,7 @@ struct AttnParams {
   const void* q;
   int64_t q_stride;
   int q_dtype, n_q_heads, group, T, B;
+  uint32_t group_inv;          // floor(2^32 / group), 2^32 - 1 for 1
   const int32_t* q_start;
   const int32_t* kv_len;
   const int32_t* table;
@@ -31,6 +32,12 @@ int launch_kv_stream(const AttnParams& p, int head_dim, cudaStream_t s);
 // many rows (kv_attn_tc.cu)
 size_t kv_tc_workspace();
 int launch_kv_tc(const AttnParams& p, int head_dim, cudaStream_t s);
+
+// The token of row (token * group + head).  floor(row * floor(2^32 / g) / 2^32) is row / g or one less.
+__device__ __forceinline__ int row_token(const AttnParams& p, int row) {
+  const int t = (int)__umulhi((uint32_t)row, p.group_inv);
+  return row - t * p.group >= p.group ? t + 1 : t;
+}
 
 // the length of request r as the kernels read it
 __device__ __forceinline__ int kv_length(const AttnParams& p, int r) {
@@ -61,7 +68,7 @@ struct Walk {
   __device__ __forceinline__ static void range(const AttnParams& p, Item& it) {
     const int shift = it.len - it.qlen;
     it.rows = min(ROWS, it.qlen * p.group - it.row0);
-    const int lo = shift + it.row0 / p.group, hi = shift + (it.row0 + it.rows - 1) / p.group;
+    const int lo = shift + row_token(p, it.row0), hi = shift + row_token(p, it.row0 + it.rows - 1);
     it.end = p.causal ? min(it.len, hi + 1) : it.len;
     it.begin = p.window > 0 ? max(0, lo - p.window + 1) : 0;
     it.t0 = it.begin / TILE;
@@ -73,10 +80,18 @@ struct Walk {
     const int64_t rows = (int64_t)n * p.group;
     return rows > p.rows_above && rows <= p.rows_upto ? n : 0;
   }
-  __device__ __forceinline__ static int64_t units(const AttnParams& p, int r, Item& it) {
+  // `known`: rows, length and first row of q of every request, in shared memory, or null
+  __device__ __forceinline__ static int64_t units(const AttnParams& p, int r, Item& it,
+                                                  const int* known = nullptr) {
     it.r = r;
-    it.qlen = tokens(p, r, &it.first);
-    it.len = kv_length(p, r);
+    if (known) {
+      it.qlen = known[3 * r];
+      it.len = known[3 * r + 1];
+      it.first = known[3 * r + 2];
+    } else {
+      it.qlen = tokens(p, r, &it.first);
+      it.len = kv_length(p, r);
+    }
     int64_t u = 0;
     for (it.row0 = 0; it.row0 < it.qlen * p.group; it.row0 += ROWS) {
       range(p, it);
@@ -102,8 +117,9 @@ struct Walk {
   // (every thread of the block calls it).  The warps' sums lie behind them: NTH + 1 + NTH / 32
   // entries, in the caller's dynamic shared memory (static shared memory in front of it would
   // shift it off the alignment that swizzled operands need).
+  // `known` (3 NTH ints, may be null) is filled where every thread has one request at most.
   template <int NTH>
-  __device__ __forceinline__ static void sum_units(const AttnParams& p, int64_t* pre) {
+  __device__ __forceinline__ static void sum_units(const AttnParams& p, int64_t* pre, int* known = nullptr) {
     int64_t* wsum = pre + NTH + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int chunk = (p.B + NTH - 1) / NTH;
@@ -112,6 +128,11 @@ struct Walk {
     for (int i = 0; i < chunk; ++i) {
       const int r = threadIdx.x * chunk + i;
       if (r < p.B) u += units(p, r, it);
+    }
+    if (known && chunk == 1 && (int)threadIdx.x < p.B) {
+      known[3 * threadIdx.x] = it.qlen;
+      known[3 * threadIdx.x + 1] = it.len;
+      known[3 * threadIdx.x + 2] = it.first;
     }
     int64_t inc = u;
 #pragma unroll
@@ -127,20 +148,21 @@ struct Walk {
     if (threadIdx.x == NTH - 1) pre[NTH] = base + inc;
     __syncthreads();
   }
-  // the item that unit u lies in, and the unit at which it starts
+  // The item that unit u lies in, and the unit at which it starts (a whole warp calls it).
   template <int NTH>
   __device__ __forceinline__ static int64_t seek(const AttnParams& p, const int64_t* pre, int64_t u,
-                                                 Item& it) {
+                                                 Item& it, const int* known = nullptr) {
     const int chunk = (p.B + NTH - 1) / NTH;
-    int lo = 0, hi = NTH;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    int64_t iu = pre[lo];
-    for (int r = lo * chunk;; ++r) {
-      const int64_t n = units(p, r, it);
+    // the last chunk with pre <= u: 32 at a time, then among 32
+    constexpr int STEP = (NTH + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    const int big = 31 - __clz(__ballot_sync(0xffffffffu, pre[min(lane * STEP, NTH)] <= u));
+    const int at = big * STEP + lane;
+    const int small = 31 - __clz(__ballot_sync(0xffffffffu, lane < STEP && at < NTH && pre[min(at, NTH)] <= u));
+    const int c = big * STEP + small;
+    int64_t iu = pre[c];
+    for (int r = c * chunk;; ++r) {
+      const int64_t n = units(p, r, it, chunk == 1 ? known : nullptr);
       if (u < iu + n) break;
       iu += n;
     }
@@ -173,14 +195,24 @@ struct Walk {
     next(p, it);
     return here(p, it, iu, u0, u1, a, b);
   }
-  // the share in which the last tile of the item at unit iu lies
-  __device__ __forceinline__ static int last_share(const Item& it, int64_t iu, int64_t N, int64_t U) {
-    return (int)(((iu + OV + it.tiles) * N + U - 1) / U - 1);
+  // the unit of the item's last tile
+  __device__ __forceinline__ static int64_t last_unit(const Item& it, int64_t iu) {
+    return iu + OV + it.tiles - 1;
   }
 };
 
-// The line of U units is cut into N <= U equal shares: share w is [U w / N, U (w + 1) / N), and
-// unit u lies in share ceil((u + 1) N / U) - 1.
+// The line of U units is cut into N <= U equal shares: share w is [floor(U w / N), floor(U (w + 1) / N)),
+// and unit u lies in share ceil((u + 1) N / U) - 1.
+__device__ __forceinline__ int64_t share_start(int64_t U, int N, int w) {
+  if (U < (1LL << 31)) {                   // 32-bit divisions: U w / N = (U / N) w + (U mod N) w / N
+    const uint32_t q = (uint32_t)U / (uint32_t)N, r = (uint32_t)U - q * (uint32_t)N;
+    return (int64_t)q * w + r * (uint32_t)w / (uint32_t)N;
+  }
+  return U * w / N;
+}
+__device__ __forceinline__ int share_of(int64_t u, int N, int64_t U) {
+  return (int)(((u + 1) * N + U - 1) / U - 1);
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -216,7 +248,7 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int r, int h, int
                                           const float (&acc)[D / 32], float m, float l) {
   constexpr int V = D / 32;
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int tokq = row / p.group, uq = row - tokq * p.group;
+  const int tokq = row_token(p, row), uq = row - tokq * p.group;
   const int64_t qrow = __ldg(p.q_start + r) + tokq;
   const int head = h * p.group + uq;
   const int64_t base = qrow * p.out_stride + (int64_t)head * D + lane * V;

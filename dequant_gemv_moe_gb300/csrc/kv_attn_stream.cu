@@ -46,10 +46,11 @@ constexpr int kBlks = kTile / kKvBlk;
 constexpr int kItemCost = 1;              // tiles' worth of starting and ending an item
 constexpr int kMaxCtas = 160;
 
-// what a warp did not finish: bit 0 of `open`: the item goes on behind this share
+// what a warp did not finish
 struct Left {
   int r, h, row0, rows;
-  int has, open, follow;                  // follow: the share in which the item ends
+  int has, open;                          // open: the item goes on behind this share
+  int64_t last;                           // the unit of its last tile
 };
 
 // Where a warp is in its share, kept in shared memory: the tile loop needs its registers.  [0] is the
@@ -76,13 +77,14 @@ struct StreamCfg {
   static constexpr int NTH = NW * 32;
   static constexpr int PART = ROWS * D * 4 + ROWS * 8;              // rows of O, then (M, l)
   static constexpr int OFF_LEFT = 512;                              // Left [NW][2]
-  static constexpr int OFF_PRE = 1536;                              // int64 [NTH + 1 + NW]
-  static constexpr int OFF_STATE = OFF_PRE + 4352;
-  static constexpr int OFF_RING = OFF_STATE + (NW * (int)sizeof(WarpState) + 127) / 128 * 128;
+  static constexpr int OFF_PRE = 1792;                              // int64 [NTH + 1 + NW]
+  static constexpr int OFF_KNOWN = OFF_PRE + (NTH + 1 + NW) * 8;   // int [3 NTH]
+  static constexpr int OFF_STATE = (OFF_KNOWN + NTH * 12 + 15) / 16 * 16;
+  static constexpr int OFF_RING = (OFF_STATE + NW * (int)sizeof(WarpState) + 127) / 128 * 128;
   static constexpr int OFF_HEAD = OFF_RING + NW * STAGES * STG;     // the warps' first partials
   static constexpr int SMEM = OFF_HEAD + NW * PART;                 // (the second ones lie in the rings)
-  static_assert(SMEM <= 232448 && STAGES * STG >= PART && (NTH + 1 + NW) * 8 <= 4352 &&
-                    NW * STAGES * 8 <= OFF_LEFT && NW * 2 * sizeof(Left) <= 1024, "shared memory");
+  static_assert(NW <= 16 && SMEM <= 232448 && STAGES * STG >= PART &&
+                    NW * STAGES * 8 <= OFF_LEFT && NW * 2 * sizeof(Left) <= OFF_PRE - OFF_LEFT, "shared memory");
 };
 
 // workspace: partial O [ctas][2][ROWS][D] fp32, (M, l) [ctas][2][ROWS], descriptors [ctas]
@@ -150,7 +152,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   pdl_trigger();
 
   using Wk = Walk<C::ROWS, kTile, kItemCost>;
-  Wk::template sum_units<C::NTH>(p, pre);
+  int* known = (int*)(smem + C::OFF_KNOWN);
+  Wk::template sum_units<C::NTH>(p, pre, known);
   const int64_t U = pre[C::NTH];
   const StreamWs ws = stream_ws(p.ws);
   // at least one unit per warp of the CTAs that take part
@@ -158,15 +161,15 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x >= ctas) return;
   const int gw = blockIdx.x * C::NW + warp;
-  const int64_t N = min((int64_t)ctas * C::NW, U);      // every one of the N shares holds a unit
-  const int64_t u0 = U * min((int64_t)gw, N) / N, u1 = U * min((int64_t)gw + 1, N) / N;
+  const int N = (int)min((int64_t)ctas * C::NW, U);     // every one of the N shares holds a unit
+  const int64_t u0 = share_start(U, N, min(gw, N)), u1 = share_start(U, N, min(gw + 1, N));
 
   // ---- the first item of the share, and its tiles [a, b) that lie in it
   WarpState& S = ((WarpState*)(smem + C::OFF_STATE))[warp];
   bool more = u0 < u1;
   if (more) {
     Place x;
-    x.iu = Wk::template seek<C::NTH>(p, pre, u0, x.it);
+    x.iu = Wk::template seek<C::NTH>(p, pre, u0, x.it, known);
     more = Wk::here(p, x.it, x.iu, u0, u1, x.a, x.b);
     if (lane == 0) {
       S.at[0] = S.at[1] = x;
@@ -219,6 +222,23 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       used = 32;
     }
   };
+  // The rows of item x: column lr of each 8-row tile, values 8 lt.. of every group.  Loaded before the
+  // copies are issued, or before the item in front is written, and used after.
+  uint4 raw[NT][G];
+  auto load_rows = [&](const Item& x) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = x.row0 + nt * 8 + lr;
+      const bool live = nt * 8 + lr < x.rows;
+      const int tokq = row_token(p, row), uq = row - tokq * p.group;
+      const uint16_t* q = (const uint16_t*)p.q + (int64_t)(x.first + tokq) * p.q_stride +
+                          ((int64_t)x.h * p.group + uq) * D + 8 * lt;
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        raw[nt][g] = live ? __ldg((const uint4*)(q + 32 * g)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (more) load_rows(S.at[0].it);
   __syncwarp();
 #pragma unroll
   for (int s = 0; s < C::STAGES; ++s) produce(s);
@@ -233,24 +253,14 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   bool ok = true;
 
   int stage = 0, phase = 0;
-  for (; more; more = advance(S.at[0])) {
+  while (more) {
     const Item it = S.at[0].it;
-    // ---- rows of the item: column lr of each 8-row tile, values 8 lt.. of every group
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = it.row0 + nt * 8 + lr;
-      const bool live = nt * 8 + lr < it.rows;
-      const int tokq = row / p.group, uq = row - tokq * p.group;
-      const uint16_t* qsrc = (const uint16_t*)p.q + (int64_t)(it.first + tokq) * p.q_stride +
-                            ((int64_t)it.h * p.group + uq) * D + 8 * lt;
-      uint4 raw[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        raw[g] = live ? __ldg((const uint4*)(qsrc + 32 * g)) : make_uint4(0, 0, 0, 0);
       float x[G][8], mx = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const uint32_t w4[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+        const uint32_t w4[4] = {raw[nt][g].x, raw[nt][g].y, raw[nt][g].z, raw[nt][g].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (p.q_dtype == DQ_BF16) {
@@ -304,12 +314,12 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     // the positions that every row of the item sees, and each row's own limits
     int lo_all, hi_all;
     {
-      const int lo_pos = it.len - it.qlen + it.row0 / p.group;
-      const int hi_pos = it.len - it.qlen + (it.row0 + it.rows - 1) / p.group;
+      const int lo_pos = it.len - it.qlen + row_token(p, it.row0);
+      const int hi_pos = it.len - it.qlen + row_token(p, it.row0 + it.rows - 1);
       hi_all = p.causal ? min(it.len, lo_pos + 1) : it.len;
       lo_all = p.window > 0 ? max(0, hi_pos - p.window + 1) : 0;
       if (lane < C::ROWS) {
-        const int pos = it.len - it.qlen + (it.row0 + lane) / p.group;
+        const int pos = it.len - it.qlen + row_token(p, it.row0 + lane);
         S.hi[lane] = p.causal ? min(it.len, pos + 1) : it.len;
         S.lo[lane] = p.window > 0 ? pos - p.window + 1 : 0;
       }
@@ -520,10 +530,12 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     // ---- the item's rows: whole, or a partial (the second one over the ring, whose copies have all
     // been used: the share ends here)
     const Item done = S.at[0].it;
+    const int64_t done_last = Wk::last_unit(done, S.at[0].iu);
     const bool from_start = S.at[0].a == 0, to_end = S.at[0].b == done.tiles;
     const bool whole = from_start && to_end;
     float* part = (float*)(from_start ? ring : smem + C::OFF_HEAD + warp * C::PART);
-    __syncwarp();
+    more = advance(S.at[0]);
+    if (more) load_rows(S.at[0].it);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -536,7 +548,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         if (col >= done.rows) continue;
         const float k24 = 16777216.f, k20 = 1048576.f;
         const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-        const int row = done.row0 + col, tokq = row / p.group, uq = row - tokq * p.group;
+        const int row = done.row0 + col, tokq = row_token(p, row), uq = row - tokq * p.group;
         const int64_t qrow = done.first + tokq;
         const int head = done.h * p.group + uq;
 #pragma unroll
@@ -565,7 +577,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       x.rows = done.rows;
       x.has = 1;
       x.open = to_end ? 0 : 1;
-      x.follow = Wk::last_share(done, S.at[0].iu, N, U);
+      x.last = done_last;
     }
   }
   __syncthreads();
@@ -588,25 +600,31 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
                                              : smem + C::OFF_HEAD + (w0 + i) * C::PART);
     };
     if (open && w >= 0 && threadIdx.x == 0)
-      ws.desc[blockIdx.x] = make_int4(x.r, x.h, x.row0, x.follow / C::NW - (int)blockIdx.x);
+      ws.desc[blockIdx.x] = make_int4(x.r, x.h, x.row0, share_of(x.last, N, U) / C::NW - (int)blockIdx.x);
     for (int col = 0; col < x.rows; ++col, ++job) {
       if (job % C::NW != warp) continue;
-      float m = kNone;
-      for (int i = 0; i < n; ++i) m = fmaxf(m, ((const float2*)(part(i) + C::ROWS * D))[col].x);
-      float sum = 0.f, acc[G];
+      // a lane weighs a partial, then all lanes add them up
+      const float2 ml = lane < n ? ((const float2*)(part(lane) + C::ROWS * D))[col] : make_float2(kNone, 0.f);
+      float m = ml.x;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float f = ex2(ml.x - m);
+      float sum = ml.y * f, acc[G];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      m = __shfl_sync(0xffffffffu, m, 0);  // lanes 16.. hold none
+      sum = __shfl_sync(0xffffffffu, sum, 0);
 #pragma unroll
       for (int v = 0; v < G; ++v) acc[v] = 0.f;
 #pragma unroll 4
       for (int i = 0; i < n; ++i) {
-        const float* src = part(i);
-        const float2 ml = ((const float2*)(src + C::ROWS * D))[col];
-        const float f = ex2(ml.x - m);
-        sum = fmaf(ml.y, f, sum);
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* src = part(i) + col * D + lane * G;
 #pragma unroll
         for (int v = 0; v < G; v += 2) {
-          const float2 y = *(const float2*)(src + col * D + lane * G + v);
-          acc[v] = fmaf(y.x, f, acc[v]);
-          acc[v + 1] = fmaf(y.y, f, acc[v + 1]);
+          const float2 y = *(const float2*)(src + v);
+          acc[v] = fmaf(y.x, fi, acc[v]);
+          acc[v + 1] = fmaf(y.y, fi, acc[v + 1]);
         }
       }
       if (whole) {

@@ -211,6 +211,22 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
   }
 }
 
+// The tiles [a, b) of the item's [ta, tb) that row tile i sees anything of: a causal item's first row
+// tile is done before its last one, and rows behind the item's end see nothing.
+template <int TT>
+__device__ __forceinline__ void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, int tb,
+                                               int& a, int& b) {
+  a = b = ta;
+  const int last = min(it.rows, 128 * i + 128) - 1;
+  if (last < 128 * i) return;
+  const int shift = it.len - it.qlen;
+  const int end = p.causal ? min(it.len, shift + row_token(p, it.row0 + last) + 1) : it.len;
+  const int begin = p.window > 0 ? max(0, shift + row_token(p, it.row0 + 128 * i) - p.window + 1) : 0;
+  if (end <= begin) return;
+  a = max(ta, begin / TT - it.t0);
+  b = max(a, min(tb, (end + TT - 1) / TT - it.t0));
+}
+
 template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
@@ -236,11 +252,11 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 
   Wk::template sum_units<C::NTH>(p, pre);
   const int64_t U = pre[C::NTH];
-  const int64_t N = min((int64_t)gridDim.x, U);
+  const int N = (int)min((int64_t)gridDim.x, U);
   const TcWs ws = tc_ws(p.ws);
   if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x >= N) return;
-  const int64_t u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
+  const int64_t u0 = share_start(U, N, blockIdx.x), u1 = share_start(U, N, blockIdx.x + 1);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::RS; ++i) {
@@ -288,14 +304,17 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more;
          more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
       const bool from_start = ta == 0, to_end = tb == it.tiles;
+      int ra, rb;
+      row_tile_range<TT>(p, it, tile, ta, tb, ra, rb);
+      const int nt = rb - ra;              // tiles of this row tile
       // the row
       const int row = it.row0 + tile * 128 + trow;
       const bool live = tile * 128 + trow < it.rows;
-      const int tokq = row / p.group, uq = row - tokq * p.group;
+      const int tokq = row_token(p, row), uq = row - tokq * p.group;
       const int64_t q_at = it.first + tokq;
       const int head = it.h * p.group + uq;
-      float cf;
-      {
+      float cf = 0.f;
+      if (nt > 0) {
         const uint4* src = (const uint4*)((const uint16_t*)p.q + q_at * p.q_stride + (int64_t)head * D);
         float mx = 0.f;
         constexpr int CH = D / 8;
@@ -348,14 +367,13 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const int lo = p.window > 0 ? pos - p.window + 1 : 0;
       int lo_all, hi_all;
       {
-        const int pa = it.len - it.qlen + (it.row0 + tile * 128) / p.group;
-        const int pb = it.len - it.qlen + (it.row0 + min(it.rows, tile * 128 + 128) - 1) / p.group;
+        const int pa = it.len - it.qlen + row_token(p, it.row0 + tile * 128);
+        const int pb = it.len - it.qlen + row_token(p, it.row0 + min(it.rows, tile * 128 + 128) - 1);
         hi_all = p.causal ? min(it.len, pa + 1) : it.len;
         lo_all = p.window > 0 ? max(0, pb - p.window + 1) : 0;
       }
       float M = kNone, l = 0.f;
-      const int nt = tb - ta;
-      int tok0 = (it.t0 + ta) * TT;
+      int tok0 = (it.t0 + ra) * TT;
       for (int j = 0; j < nt; ++j, ++gt, tok0 += TT) {
         const int sl = tile * 2 + (gt & 1);
         ok = ok && mbar_wait(&s_full[sl], (gt >> 1) & 1);
@@ -370,8 +388,14 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         tmem_use(r);
         tmem_use(r + 32);
         if (!(tok0 >= lo_all && tok0 + TT <= hi_all)) {
+          const int n = hi - tok0;
 #pragma unroll
-          for (int i = 0; i < TT; ++i) r[i] = tok0 + i >= lo && tok0 + i < hi ? r[i] : 0xFF800000u;
+          for (int i = 0; i < TT; ++i) r[i] = i < n ? r[i] : 0xFF800000u;
+          if (p.window > 0) {
+            const int f = lo - tok0;
+#pragma unroll
+            for (int i = 0; i < TT; ++i) r[i] = i >= f ? r[i] : 0xFF800000u;
+          }
         }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -428,10 +452,12 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       if (!ok) break;
       // ---- the rows: whole, or a partial
       {
-        ok = mbar_wait(&pv_done[tile * 2 + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
+        if (nt > 0) {
+          ok = mbar_wait(&pv_done[tile * 2 + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
         const bool whole = from_start && to_end;
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
         const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * C::ROWS + tile * 128 + trow;
@@ -443,7 +469,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           tmem_use(r);
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          for (int i = 0; i < 32; ++i) v[i] = nt > 0 ? __uint_as_float(r[i]) : 0.f;
           if (live) {
             // column 8 a + 2 n + k of panel w is value 4 a + n of group 2 w + k
 #pragma unroll
@@ -470,7 +496,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         if (from_start && !to_end && threadIdx.x == 0)
           ws.desc[blockIdx.x] = make_int4(
               it.r, it.h, it.row0,
-              ((Wk::last_share(it, iu, N, U) - (int)blockIdx.x) << 1) | slot);
+              ((share_of(Wk::last_unit(it, iu), N, U) - (int)blockIdx.x) << 1) | slot);
         if (!whole) slot = 1;
       }
     }
@@ -633,12 +659,12 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const int i = warp - C::MMA;
       const uint32_t q_i = q_lo + (uint32_t)(i * (C::Q_TILE >> 4)), o_i = tm + (uint32_t)(i * D);
       const uint32_t s_i = tm + (uint32_t)(C::COL_S + i * 2 * TT);
-      int gt = 0, seg = 0;
-      // S of tile g; its buffer's last weights must have been used
-      auto scores = [&](int g) {
-        const int par = g & 1, buf = g % C::KVS;
+      int gt = 0, ring = 0, seg = 0;         // tiles of this row tile, of the CTA; items
+      // S of this row tile's tile g, which is the CTA's tile r; its buffer's last weights must have been used
+      auto scores = [&](int g, int r) {
+        const int par = g & 1, buf = r % C::KVS;
         bool good = g < 2 || mbar_wait(&pv_done[i * 2 + par], ((g - 2) >> 1) & 1);
-        good = good && mbar_wait(&kv_full[buf], (g / C::KVS) & 1);
+        good = good && mbar_wait(&kv_full[buf], (r / C::KVS) & 1);
         if (!__all_sync(0xffffffffu, good)) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -653,8 +679,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         __syncwarp();
         return true;
       };
-      auto weighted = [&](int g, bool first) {
-        const int par = g & 1, buf = g % C::KVS;
+      auto weighted = [&](int g, int r, bool first) {
+        const int par = g & 1, buf = r % C::KVS;
         if (!__all_sync(0xffffffffu, mbar_wait(&p_full[i * 2 + par], (g >> 1) & 1))) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -669,19 +695,33 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         __syncwarp();
         return true;
       };
+      // a tile that this row tile has no part in
+      auto pass = [&](int r) {
+        const int buf = r % C::KVS;
+        if (!__all_sync(0xffffffffu, mbar_wait(&kv_full[buf], (r / C::KVS) & 1))) return false;
+        if (lane == 0) mbar_arrive(&kv_empty[buf]);
+        return true;
+      };
       for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
-           more = Wk::after(p, it, iu, u0, u1, ta, tb), ++seg) {
-        const int nt = uniform(tb - ta), end = gt + nt, g0 = gt;
-        ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
-        ok = ok && scores(gt);
-        if (nt > 1) ok = ok && scores(gt + 1);
-        for (; gt < end && ok; ++gt) {
-          ok = weighted(gt, gt == g0);
-          if (gt + 2 < end) ok = ok && scores(gt + 2);
+           more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+        int ra, rb;
+        row_tile_range<TT>(p, it, i, ta, tb, ra, rb);
+        const int before = uniform(ra - ta), nt = uniform(rb - ra), behind = uniform(tb - rb);
+        for (int k = 0; k < before && ok; ++k) ok = pass(ring++);
+        if (nt > 0 && ok) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
+          ++seg;
+          ok = ok && scores(gt, ring);
+          if (nt > 1) ok = ok && scores(gt + 1, ring + 1);
+          for (int k = 0; k < nt && ok; ++k, ++gt, ++ring) {
+            ok = weighted(gt, ring, k == 0);
+            if (k + 2 < nt) ok = ok && scores(gt + 2, ring + 2);
+          }
         }
+        for (int k = 0; k < behind && ok; ++k) ok = pass(ring++);
       }
       // no arrival is under way when the CTA ends
-      if (ok && gt > 0) mbar_wait(&kv_empty[(gt - 1) % C::KVS], ((gt - 1) / C::KVS) & 1);
+      if (ok && ring > 0) mbar_wait(&kv_empty[(ring - 1) % C::KVS], ((ring - 1) / C::KVS) & 1);
     }
   }
   tc_fence_before();
