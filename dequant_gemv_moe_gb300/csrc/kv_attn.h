@@ -166,14 +166,16 @@ struct Walk {
       if (u < iu + n) break;
       iu += n;
     }
-    it.h = 0;
-    it.row0 = 0;
-    range(p, it);
-    while (u >= iu + it.tiles + OV) {
-      iu += it.tiles + OV;
-      next(p, it);
+    // the row tile, then the head: all heads of a row tile cost the same
+    for (it.row0 = 0;; it.row0 += ROWS) {
+      range(p, it);
+      const int cost = it.tiles + OV;
+      if (u < iu + (int64_t)cost * p.g.heads) {
+        it.h = (int)((uint32_t)(u - iu) / (uint32_t)cost);
+        return iu + (int64_t)it.h * cost;
+      }
+      iu += (int64_t)cost * p.g.heads;
     }
-    return iu;
   }
   // The tiles [a, b) of the item at unit iu that lie in the share [u0, u1); none: on to the next
   // item that has some.  False: the share holds no more.

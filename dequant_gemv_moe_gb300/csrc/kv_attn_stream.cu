@@ -583,17 +583,23 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   __syncthreads();
 
   // ---- the CTA's partials.  An item starts with a warp's second partial (or with the first warp's
-  // first one, if it comes from the CTA before) and goes on in the next warps' first ones.
+  // first one, if it comes from the CTA before) and goes on in the next warps' first ones.  Bit w of
+  // head / tail: warp w has a first / second partial; of on: its first one goes on in warp w + 1's.
+  const int fl = lane < C::NW ? left[lane * 2].has | (left[lane * 2].open & 1) << 1 | left[lane * 2 + 1].has << 2 : 0;
+  const uint32_t head = __ballot_sync(0xffffffffu, fl & 1), open_head = __ballot_sync(0xffffffffu, (fl & 3) == 3),
+                 tail = __ballot_sync(0xffffffffu, fl & 4);
+  const uint32_t on = open_head & (head >> 1);
   int job = 0;
-  for (int w = -1; w < C::NW; ++w) {
+  for (uint32_t todo = (head & 1) | tail << 1; todo; todo &= todo - 1) {
+    const int w = __ffs(todo) - 2;         // -1: the first warp's first partial, else warp w's second
     const Left& x = w < 0 ? left[0] : left[w * 2 + 1];
-    if (!x.has) continue;
-    int n = 1, open = x.open;              // partials of the item in this CTA
     const int w0 = w < 0 ? 0 : w;
-    while (open && w0 + n < C::NW && left[(w0 + n) * 2].has) {
-      open = left[(w0 + n) * 2].open;
-      ++n;
-    }
+    const int s0 = w < 0 ? 0 : w + 1;      // the first of the item's first partials
+    // a second partial always goes on; where the next warp has none, in the next CTA
+    const bool more_here = w < 0 || (head >> s0 & 1);
+    const int run = more_here ? __ffs(~(on >> s0)) : 0;               // first partials: s0 .. s0 + run - 1
+    const int n = run + (w < 0 ? 0 : 1);   // partials of the item in this CTA
+    const bool open = more_here ? open_head >> (s0 + run - 1) & 1 : true;
     const bool whole = w >= 0 && !open;
     auto part = [&](int i) -> const float* {
       return (const float*)(i == 0 && w >= 0 ? smem + C::OFF_RING + w * C::STAGES * C::STG
