@@ -9,71 +9,87 @@ namespace dqmoe {
 
 namespace {
 
+// eight consecutive values as fp32
 template <int DT>
-struct Elem;
-template <> struct Elem<DQ_F32> { using T = float; };
-template <> struct Elem<DQ_F16> { using T = __half; };
-template <> struct Elem<DQ_BF16> { using T = __nv_bfloat16; };
-
-// four consecutive values as fp32
-template <int DT>
-__device__ __forceinline__ void load4(const void* p, int64_t i, float (&x)[4]) {
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
   if (DT == DQ_F32) {
-    const float4 v = __ldg((const float4*)((const float*)p + i));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    const float4 a = __ldg((const float4*)((const float*)p + i)), b = __ldg((const float4*)((const float*)p + i) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   } else {
-    const uint2 v = __ldg((const uint2*)((const unsigned short*)p + i));
-    if (DT == DQ_BF16) {
-      x[0] = __uint_as_float(v.x << 16);
-      x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(v.y << 16);
-      x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    } else {
-      const float2 a = __half22float2(u32_as_h2(v.x)), b = __half22float2(u32_as_h2(v.y));
-      x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+    const uint4 v = __ldg((const uint4*)((const unsigned short*)p + i));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (DT == DQ_BF16) {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(u32_as_h2(w[k]));
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+      }
     }
   }
 }
 
 template <int DT>
-__device__ __forceinline__ void store4(void* p, int64_t i, const float (&x)[4]) {
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8]) {
   if (DT == DQ_F32) {
-    *(float4*)((float*)p + i) = make_float4(x[0], x[1], x[2], x[3]);
-  } else if (DT == DQ_BF16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *(uint2*)((__nv_bfloat16*)p + i) = make_uint2(*(const uint32_t*)&a, *(const uint32_t*)&b);
+    float4* q = (float4*)((float*)p + i);
+    q[0] = make_float4(x[0], x[1], x[2], x[3]);
+    q[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-    const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
-    *(uint2*)((__half*)p + i) = make_uint2(h2_as_u32(a), h2_as_u32(b));
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (DT == DQ_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *(const uint32_t*)&v;
+      } else {
+        w[k] = h2_as_u32(__floats2half2_rn(x[2 * k], x[2 * k + 1]));
+      }
+    }
+    *(uint4*)((unsigned short*)p + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// The Q4_0 codes and scale of the 32 values that 8 consecutive lanes hold four
+// The Q4_0 codes and scale of the 32 values that 4 consecutive lanes hold eight
 // of each.  The scale takes the first value of the largest magnitude, so a tie
-// between lanes goes to the lower one.  x / d is the correctly rounded
-// quotient: for 16-bit x the code then equals that of exact arithmetic (x and d
-// have at most 11 bits, so a quotient that is not itself half-way between two
-// codes differs from half-way by at least 2^-14, and the sum with 8.5 rounds by
-// less than 2^-20).
-__device__ __forceinline__ __half quantise4(const float (&xin)[4], int lane, uint32_t (&c)[4]) {
-  float x[4], m = 0.f;
+// between lanes goes to the lower one.
+//
+// code = floor(x / d + 8.5) in exact arithmetic for 16-bit x: x and d have at most 11 bits, so a
+// quotient that is not half-way between two codes is at least 2^-14 from it (for x = X 2^a, d = D 2^b
+// the distance is |2 X 2^(a-b) - (2k+1) D| / 2D, and 2^(a-b) >= D / 4X wherever the quotient is not
+// below 1/4).  x * (1 / d) + 8.5 in one FMA is off by less than 2^-18, so adding 2^-16 decides every
+// half-way case upwards and no other case differently; no division.  fp32 x has no such margin and
+// is divided (one correctly rounded quotient).
+template <int DT>
+__device__ __forceinline__ __half quantise8(float (&x)[8], int lane, uint32_t (&c)[8]) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = fminf(fmaxf(xin[i], -65504.f), 65504.f);
+  for (int i = 0; i < 8; ++i) {
+    x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
     if (fabsf(x[i]) > fabsf(m)) m = x[i];
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
+  for (int o = 1; o < 4; o <<= 1) {
     const float p = __shfl_xor_sync(0xffffffffu, m, o);
     const bool mine = fabsf(m) > fabsf(p) || (fabsf(m) == fabsf(p) && (lane & o) == 0);
     m = mine ? m : p;
   }
   const __half d = __float2half_rn(m * -0.125f);
   const float df = __half2float(d);
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(df));
+  if (df == 0.f) inv = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float q = floorf(__fadd_rn(__fdiv_rn(x[i], df), 8.5f));
-    c[i] = df == 0.f ? 8u : (uint32_t)fminf(fmaxf(q, 0.f), 15.f);
+  for (int i = 0; i < 8; ++i) {
+    float q;
+    if (DT == DQ_F32) q = df == 0.f ? 8.5f : __fadd_rn(__fdiv_rn(x[i], df), 8.5f);
+    else q = fmaf(x[i], inv, 8.5f + 0x1p-16f);
+    // truncation of a value in [0, 15.5] by adding 2^23 towards zero
+    c[i] = __float_as_uint(__fadd_rz(fminf(fmaxf(q, 0.f), 15.5f), 8388608.f)) & 15u;
   }
   return d;
 }
@@ -88,86 +104,110 @@ struct KvRows {
   const int64_t* slots;
   int64_t n_slots;
   int T;
+  int64_t items;               // of one head: T * 2 * D / 8
 };
 
-// One warp per (token, head); a lane holds four consecutive values of each 128.
+constexpr int kRowsThreads = 256;
+constexpr int kRowsUnroll = 2;   // chunks per thread, their loads all in flight
+
+// Eight values per thread, a head's (token, K or V, chunk of 8) in one line, the
+// chunks fastest: a group of 32 values is four lanes.  In the block both K and V
+// take one 32-bit word per lane: K's eight values are a word of its layout, and
+// two lanes whose groups are neighbours exchange halves of their V units.
 template <int D, int DT>
-__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvRows p) {
+__global__ void __launch_bounds__(kRowsThreads) kv_append_kernel(const __grid_constant__ KvRows p) {
   using B = KvBlk<D>;
+  constexpr int C = D / 8;
   pdl_wait();
   pdl_trigger();
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int64_t tok = w / p.g.heads;
-  const int h = (int)(w - tok * p.g.heads);
-  if (tok >= p.T) return;
-  const int64_t slot = __ldg(p.slots + tok);
-  if (slot < 0 || slot >= p.n_slots) return;
-  const int off = (int)(slot & (p.g.page_size - 1));
-  uint8_t* blk = p.g.pages + (slot >> p.g.page_shift) * p.g.page_bytes + h * p.g.head_bytes +
-                 (off / kKvBlk) * B::BYTES;
-  const int i = off % kKvBlk;
-  constexpr int LANES = D < 128 ? D / 4 : 32;
+  const int lane = threadIdx.x & 31, h = blockIdx.y;
+  const int64_t base = (int64_t)blockIdx.x * (kRowsThreads * kRowsUnroll) + threadIdx.x;
+  float x[kRowsUnroll][8];
+  int64_t slot[kRowsUnroll];
 #pragma unroll
-  for (int r = 0; r < (D + 127) / 128; ++r) {
-    // lanes without values of their own (D = 64) repeat the last ones and store nothing
-    const int l = lane < LANES ? lane : LANES - 8 + (lane & 7);
-    const int grp = r * 4 + l / 8, a = l & 7;
-    float x[4], y[4];
-    load4<DT>(p.k, tok * p.k_stride + (int64_t)h * D + grp * 32 + 4 * a, x);
-    load4<DT>(p.v, tok * p.v_stride + (int64_t)h * D + grp * 32 + 4 * a, y);
-    uint32_t c[4], e[4];
-    const __half dk = quantise4(x, lane, c), dv = quantise4(y, lane, e);
-    uint32_t kw = (c[0] | c[1] << 16 | c[2] << 4 | c[3] << 20) << (8 * (a & 1));
-    kw |= __shfl_xor_sync(0xffffffffu, kw, 1);
-    if (lane < LANES) {
-      if (!(a & 1)) *(uint32_t*)(blk + B::k_word(i, grp, a >> 1)) = kw;
-      *(uint16_t*)(blk + B::v_unit(i, grp, a)) =
-          (uint16_t)(e[0] | e[1] << 4 | e[2] << 8 | e[3] << 12);
-      if (a == 0) {
-        *(__half*)(blk + B::k_scale(i, grp)) = dk;
-        *(__half*)(blk + B::v_scale(i, grp)) = dv;
-      }
+  for (int j = 0; j < kRowsUnroll; ++j) {
+    const int64_t id = base + j * kRowsThreads;
+    const bool in = id < p.items;          // (the shuffles below take whole warps)
+    const int64_t tok = in ? id / (2 * C) : 0;
+    const int c = (int)(id % C);
+    const bool isv = id / C & 1;
+    slot[j] = in ? __ldg(p.slots + tok) : -1;
+    if (slot[j] >= p.n_slots) slot[j] = -1;
+    load8<DT>(isv ? p.v : p.k, tok * (isv ? p.v_stride : p.k_stride) + (int64_t)h * D + 8 * c, x[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kRowsUnroll; ++j) {
+    const int64_t id = base + j * kRowsThreads;
+    const int c = (int)(id % C);
+    const bool isv = id / C & 1;
+    const int g = c / 4, t = c & 3;
+    uint32_t q[8];
+    const __half d = quantise8<DT>(x[j], lane, q);
+    // V: units 2t (values 0-3) and 2t + 1 of group g; lane of the neighbouring group: lane ^ 4
+    const uint32_t u0 = q[0] | q[1] << 4 | q[2] << 8 | q[3] << 12, u1 = q[4] | q[5] << 4 | q[6] << 8 | q[7] << 12;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, (g & 1) ? u0 : u1, 4);
+    if (slot[j] < 0) continue;
+    const int off = (int)(slot[j] & (p.g.page_size - 1)), i = off % kKvBlk;
+    uint8_t* blk = p.g.pages + (slot[j] >> p.g.page_shift) * p.g.page_bytes + h * p.g.head_bytes +
+                   (off / kKvBlk) * B::BYTES;
+    uint32_t word;
+    int at;
+    if (isv) {
+      word = (g & 1) ? other | u1 << 16 : u0 | other << 16;
+      at = B::v_unit(i, g & ~1, 2 * t + (g & 1));
+    } else {
+      word = q[0] | q[1] << 16 | q[2] << 4 | q[3] << 20 | q[4] << 8 | q[5] << 24 | q[6] << 12 | q[7] << 28;
+      at = B::k_word(i, g, t);
     }
+    *(uint32_t*)(blk + at) = word;
+    if (t == 0) *(__half*)(blk + (isv ? B::v_scale(i, g) : B::k_scale(i, g))) = d;
   }
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRows p) {
+__global__ void __launch_bounds__(kRowsThreads) kv_read_kernel(const __grid_constant__ KvRows p) {
   using B = KvBlk<D>;
+  constexpr int C = D / 8;
   pdl_wait();
   pdl_trigger();
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int64_t tok = w / p.g.heads;
-  const int h = (int)(w - tok * p.g.heads);
-  if (tok >= p.T) return;
-  const int64_t slot = __ldg(p.slots + tok);
-  const bool in = slot >= 0 && slot < p.n_slots;
-  const int off = in ? (int)(slot & (p.g.page_size - 1)) : 0;
-  const uint8_t* blk = p.g.pages + (in ? slot >> p.g.page_shift : 0) * p.g.page_bytes +
-                       h * p.g.head_bytes + (off / kKvBlk) * B::BYTES;
-  const int i = off % kKvBlk;
+  const int h = blockIdx.y;
+  const int64_t base = (int64_t)blockIdx.x * (kRowsThreads * kRowsUnroll) + threadIdx.x;
+  uint32_t word[kRowsUnroll];
+  float d[kRowsUnroll];
 #pragma unroll
-  for (int r = 0; r < (D + 127) / 128; ++r) {
-    const int grp = r * 4 + lane / 8, a = lane & 7;
-    if (grp >= B::G) return;
-    float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      const uint32_t kw = *(const uint32_t*)(blk + B::k_word(i, grp, a >> 1)) >> (8 * (a & 1));
-      const uint32_t vw = *(const uint16_t*)(blk + B::v_unit(i, grp, a));
-      const float dk = __half2float(*(const __half*)(blk + B::k_scale(i, grp)));
-      const float dv = __half2float(*(const __half*)(blk + B::v_scale(i, grp)));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // value e sits in nibble (e >> 1) + 4 * (e & 1) of the half of the word
-        x[e] = dk * (float)((int)(kw >> (4 * (e >> 1) + 16 * (e & 1)) & 15u) - 8);
-        y[e] = dv * (float)((int)(vw >> (4 * e) & 15u) - 8);
-      }
+  for (int j = 0; j < kRowsUnroll; ++j) {
+    const int64_t id = base + j * kRowsThreads;
+    const bool isv = id / C & 1;
+    const int c = (int)(id % C), g = c / 4, t = c & 3;
+    const int64_t slot = __ldg(p.slots + (id < p.items ? id / (2 * C) : 0));
+    const bool in = slot >= 0 && slot < p.n_slots;
+    const int off = in ? (int)(slot & (p.g.page_size - 1)) : 0, i = off % kKvBlk;
+    const uint8_t* blk = p.g.pages + (in ? slot >> p.g.page_shift : 0) * p.g.page_bytes +
+                         h * p.g.head_bytes + (off / kKvBlk) * B::BYTES;
+    if (isv)
+      word[j] = *(const uint16_t*)(blk + B::v_unit(i, g, 2 * t)) |
+                (uint32_t)*(const uint16_t*)(blk + B::v_unit(i, g, 2 * t + 1)) << 16;
+    else
+      word[j] = *(const uint32_t*)(blk + B::k_word(i, g, t));
+    d[j] = __half2float(*(const __half*)(blk + (isv ? B::v_scale(i, g) : B::k_scale(i, g))));
+    if (!in) {
+      d[j] = 0.f;
+      word[j] = 0x88888888u;
     }
-    const int64_t at = (tok * p.g.heads + h) * D + grp * 32 + 4 * a;
-    store4<DT>(p.ko, at, x);
-    store4<DT>(p.vo, at, y);
+  }
+#pragma unroll
+  for (int j = 0; j < kRowsUnroll; ++j) {
+    const int64_t id = base + j * kRowsThreads;
+    if (id >= p.items) continue;
+    const bool isv = id / C & 1;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // K: value e in nibble (e >> 1) + 4 (e & 1); V: value e in nibble e
+      const int sh = isv ? 4 * e : 4 * (e >> 1) + 16 * (e & 1);
+      x[e] = d[j] * (float)((int)(word[j] >> sh & 15u) - 8);
+    }
+    store8<DT>(isv ? p.vo : p.ko, (id / (2 * C) * p.g.heads + h) * D + 8 * (id % C), x);
   }
 }
 
@@ -369,10 +409,11 @@ int launched(cudaError_t e) {
 }
 
 template <int D>
-int launch_rows(const KvRows& p, int dtype, bool append, cudaStream_t s) {
-  const int64_t ctas = ((int64_t)p.T * p.g.heads + 7) / 8;
+int launch_rows(KvRows p, int dtype, bool append, cudaStream_t s) {
+  p.items = (int64_t)p.T * 2 * (D / 8);
+  const int64_t ctas = (p.items + kRowsThreads * kRowsUnroll - 1) / (kRowsThreads * kRowsUnroll);
   if (ctas > 2147483647) return DQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)ctas), block(256);
+  const dim3 grid((unsigned)ctas, (unsigned)p.g.heads), block(kRowsThreads);
 #define DQ_KV_ROWS(DT)                                                                        \
   if (dtype == DT)                                                                            \
     return launched(append ? launch_pdl(kv_append_kernel<D, DT>, grid, block, 0, s, 0, p)     \
