@@ -54,44 +54,66 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8]) 
   }
 }
 
-// The Q4_0 codes and scale of the 32 values that 4 consecutive lanes hold eight
-// of each.  The scale takes the first value of the largest magnitude, so a tie
-// between lanes goes to the lower one.
-//
-// code = floor(x / d + 8.5) in exact arithmetic for 16-bit x: x and d have at most 11 bits, so a
-// quotient that is not half-way between two codes is at least 2^-14 from it (for x = X 2^a, d = D 2^b
-// the distance is |2 X 2^(a-b) - (2k+1) D| / 2D, and 2^(a-b) >= D / 4X wherever the quotient is not
-// below 1/4).  x * (1 / d) + 8.5 in one FMA is off by less than 2^-18, so adding 2^-16 decides every
-// half-way case upwards and no other case differently; no division.  fp32 x has no such margin and
-// is divided (one correctly rounded quotient).
-template <int DT>
-__device__ __forceinline__ __half quantise8(float (&x)[8], int lane, uint32_t (&c)[8]) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
-    if (fabsf(x[i]) > fabsf(m)) m = x[i];
-  }
+// The value of the largest magnitude of the 32 that 4 consecutive lanes hold eight of each, the first of
+// equal ones; values beyond +-65504 count as that.  The largest and the smallest value tell it, unless they
+// are equal in magnitude (or beyond): then, for the whole warp, the values are gone through in order.
+__device__ __forceinline__ float first_largest(const float (&x)[8], int lane) {
+  float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    const float p = __shfl_xor_sync(0xffffffffu, m, o);
-    const bool mine = fabsf(m) > fabsf(p) || (fabsf(m) == fabsf(p) && (lane & o) == 0);
-    m = mine ? m : p;
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
   }
-  const __half d = __float2half_rn(m * -0.125f);
+  float m = hi > -lo ? hi : lo;
+  if (__any_sync(0xffffffffu, hi == -lo || fmaxf(hi, -lo) > 65504.f)) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = fminf(fmaxf(x[i], -65504.f), 65504.f);
+      if (fabsf(v) > fabsf(m)) m = v;
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float p = __shfl_xor_sync(0xffffffffu, m, o);
+      const bool mine = fabsf(m) > fabsf(p) || (fabsf(m) == fabsf(p) && (lane & o) == 0);
+      m = mine ? m : p;
+    }
+  }
+  return m;
+}
+
+// The Q4_0 word of eight values with scale d, value e in nibble NIB(e): floor(x / d + 8.5), in [0, 15].
+//
+// For 16-bit x this is exact without a division.  x and d have at most 11 bits, so a quotient that is not
+// half-way between two codes is at least 2^-14 from it (for x = X 2^a, d = D 2^b the distance is
+// |2 X 2^(a-b) - (2k+1) D| / 2D, and 2^(a-b) >= D / 4X wherever the quotient is not below 1/4).  With 1 / d
+// within 2^-22 of itself the sum below is off by less than 2^-17, so adding 2^-16 decides every half-way
+// case upwards and no other case differently.  The sum is taken in units of 15.5, where the saturating FMA
+// clamps it, and brought back by one that rounds towards zero at 2^23: the code is its lowest bits, and eight
+// of them are packed by multiplications whose surplus is subtracted once.  fp32 x has no such margin: one
+// correctly rounded quotient each.
+template <int DT, bool V>
+__device__ __forceinline__ uint32_t q4_word(const float (&x)[8], __half d) {
   const float df = __half2float(d);
   float inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(df));
-  if (df == 0.f) inv = 0.f;
+  inv = df == 0.f ? 0.f : inv * (1.f / 15.5f);
+  uint32_t word = 0, surplus = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float q;
-    if (DT == DQ_F32) q = df == 0.f ? 8.5f : __fadd_rn(__fdiv_rn(x[i], df), 8.5f);
-    else q = fmaf(x[i], inv, 8.5f + 0x1p-16f);
-    // truncation of a value in [0, 15.5] by adding 2^23 towards zero
-    c[i] = __float_as_uint(__fadd_rz(fminf(fmaxf(q, 0.f), 15.5f), 8388608.f)) & 15u;
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t unit = 1u << (V ? 4 * e : 4 * (e >> 1) + 16 * (e & 1));
+    float t;
+    if (DT == DQ_F32) {
+      const float q = df == 0.f ? 8.5f : __fadd_rn(__fdiv_rn(fminf(fmaxf(x[e], -65504.f), 65504.f), df), 8.5f);
+      t = __fadd_rz(fminf(fmaxf(q, 0.f), 15.5f), 8388608.f);
+    } else {
+      t = __fmaf_rz(__saturatef(fmaf(x[e], inv, (8.5f + 0x1p-16f) / 15.5f)), 15.5f, 8388608.f);
+    }
+    word += __float_as_uint(t) * unit;
+    surplus += 0x4B000000u * unit;
   }
-  return d;
+  return word - surplus;
 }
 
 struct KvRows {
@@ -103,94 +125,87 @@ struct KvRows {
   int64_t k_stride, v_stride;
   const int64_t* slots;
   int64_t n_slots;
-  int T;
-  int64_t items;               // of one head: T * 2 * D / 8
+  int64_t items;               // of one head's K or V: T * D / 8
 };
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsUnroll = 2;   // chunks per thread, their loads all in flight
 
-// Eight values per thread, a head's (token, K or V, chunk of 8) in one line, the
-// chunks fastest: a group of 32 values is four lanes.  In the block both K and V
-// take one 32-bit word per lane: K's eight values are a word of its layout, and
-// two lanes whose groups are neighbours exchange halves of their V units.
-template <int D, int DT>
-__global__ void __launch_bounds__(kRowsThreads) kv_append_kernel(const __grid_constant__ KvRows p) {
+// Eight values per thread, a head's (token, chunk of 8) in one line, the chunks
+// fastest: a group of 32 values is four lanes.  K's eight values are a word of its
+// layout; for V two lanes whose groups are neighbours exchange halves of their
+// units, so that each stores one word too.
+template <int D, int DT, bool V>
+__device__ __forceinline__ void append_rows(const KvRows& p) {
   using B = KvBlk<D>;
   constexpr int C = D / 8;
-  pdl_wait();
-  pdl_trigger();
   const int lane = threadIdx.x & 31, h = blockIdx.y;
+  const void* src = V ? p.v : p.k;
+  const int64_t stride = V ? p.v_stride : p.k_stride;
   const int64_t base = (int64_t)blockIdx.x * (kRowsThreads * kRowsUnroll) + threadIdx.x;
+  const int c = threadIdx.x % C, g = c / 4, t = c & 3;   // kRowsThreads is a multiple of C
   float x[kRowsUnroll][8];
   int64_t slot[kRowsUnroll];
 #pragma unroll
   for (int j = 0; j < kRowsUnroll; ++j) {
     const int64_t id = base + j * kRowsThreads;
     const bool in = id < p.items;          // (the shuffles below take whole warps)
-    const int64_t tok = in ? id / (2 * C) : 0;
-    const int c = (int)(id % C);
-    const bool isv = id / C & 1;
+    const int64_t tok = in ? id / C : 0;
     slot[j] = in ? __ldg(p.slots + tok) : -1;
     if (slot[j] >= p.n_slots) slot[j] = -1;
-    load8<DT>(isv ? p.v : p.k, tok * (isv ? p.v_stride : p.k_stride) + (int64_t)h * D + 8 * c, x[j]);
+    load8<DT>(src, tok * stride + h * D + 8 * c, x[j]);
   }
 #pragma unroll
   for (int j = 0; j < kRowsUnroll; ++j) {
-    const int64_t id = base + j * kRowsThreads;
-    const int c = (int)(id % C);
-    const bool isv = id / C & 1;
-    const int g = c / 4, t = c & 3;
-    uint32_t q[8];
-    const __half d = quantise8<DT>(x[j], lane, q);
-    // V: units 2t (values 0-3) and 2t + 1 of group g; lane of the neighbouring group: lane ^ 4
-    const uint32_t u0 = q[0] | q[1] << 4 | q[2] << 8 | q[3] << 12, u1 = q[4] | q[5] << 4 | q[6] << 8 | q[7] << 12;
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, (g & 1) ? u0 : u1, 4);
+    const __half d = __float2half_rn(first_largest(x[j], lane) * -0.125f);
+    uint32_t word = q4_word<DT, V>(x[j], d);
+    if (V) {
+      // units 2t and 2t + 1 of group g are the halves of `word`; the even group stores both groups' first
+      // units, the odd one their second
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
+      word = (g & 1) ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+    }
     if (slot[j] < 0) continue;
     const int off = (int)(slot[j] & (p.g.page_size - 1)), i = off % kKvBlk;
     uint8_t* blk = p.g.pages + (slot[j] >> p.g.page_shift) * p.g.page_bytes + h * p.g.head_bytes +
                    (off / kKvBlk) * B::BYTES;
-    uint32_t word;
-    int at;
-    if (isv) {
-      word = (g & 1) ? other | u1 << 16 : u0 | other << 16;
-      at = B::v_unit(i, g & ~1, 2 * t + (g & 1));
-    } else {
-      word = q[0] | q[1] << 16 | q[2] << 4 | q[3] << 20 | q[4] << 8 | q[5] << 24 | q[6] << 12 | q[7] << 28;
-      at = B::k_word(i, g, t);
-    }
-    *(uint32_t*)(blk + at) = word;
-    if (t == 0) *(__half*)(blk + (isv ? B::v_scale(i, g) : B::k_scale(i, g))) = d;
+    *(uint32_t*)(blk + (V ? B::v_unit(i, g & ~1, 2 * t + (g & 1)) : B::k_word(i, g, t))) = word;
+    if (t == 0) *(__half*)(blk + (V ? B::v_scale(i, g) : B::k_scale(i, g))) = d;
   }
 }
 
 template <int D, int DT>
-__global__ void __launch_bounds__(kRowsThreads) kv_read_kernel(const __grid_constant__ KvRows p) {
-  using B = KvBlk<D>;
-  constexpr int C = D / 8;
+__global__ void __launch_bounds__(kRowsThreads) kv_append_kernel(const __grid_constant__ KvRows p) {
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.z) append_rows<D, DT, true>(p);
+  else append_rows<D, DT, false>(p);
+}
+
+template <int D, int DT, bool V>
+__device__ __forceinline__ void read_rows(const KvRows& p) {
+  using B = KvBlk<D>;
+  constexpr int C = D / 8;
   const int h = blockIdx.y;
   const int64_t base = (int64_t)blockIdx.x * (kRowsThreads * kRowsUnroll) + threadIdx.x;
+  const int c = threadIdx.x % C, g = c / 4, t = c & 3;
   uint32_t word[kRowsUnroll];
   float d[kRowsUnroll];
 #pragma unroll
   for (int j = 0; j < kRowsUnroll; ++j) {
     const int64_t id = base + j * kRowsThreads;
-    const bool isv = id / C & 1;
-    const int c = (int)(id % C), g = c / 4, t = c & 3;
-    const int64_t slot = __ldg(p.slots + (id < p.items ? id / (2 * C) : 0));
+    const int64_t slot = __ldg(p.slots + (id < p.items ? id / C : 0));
     const bool in = slot >= 0 && slot < p.n_slots;
     const int off = in ? (int)(slot & (p.g.page_size - 1)) : 0, i = off % kKvBlk;
     const uint8_t* blk = p.g.pages + (in ? slot >> p.g.page_shift : 0) * p.g.page_bytes +
                          h * p.g.head_bytes + (off / kKvBlk) * B::BYTES;
-    if (isv)
+    if (V)
       word[j] = *(const uint16_t*)(blk + B::v_unit(i, g, 2 * t)) |
                 (uint32_t)*(const uint16_t*)(blk + B::v_unit(i, g, 2 * t + 1)) << 16;
     else
       word[j] = *(const uint32_t*)(blk + B::k_word(i, g, t));
-    d[j] = __half2float(*(const __half*)(blk + (isv ? B::v_scale(i, g) : B::k_scale(i, g))));
-    if (!in) {
+    d[j] = __half2float(*(const __half*)(blk + (V ? B::v_scale(i, g) : B::k_scale(i, g))));
+    if (!in) {                             // zeros, whatever the block in front holds
       d[j] = 0.f;
       word[j] = 0x88888888u;
     }
@@ -199,16 +214,25 @@ __global__ void __launch_bounds__(kRowsThreads) kv_read_kernel(const __grid_cons
   for (int j = 0; j < kRowsUnroll; ++j) {
     const int64_t id = base + j * kRowsThreads;
     if (id >= p.items) continue;
-    const bool isv = id / C & 1;
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      // K: value e in nibble (e >> 1) + 4 (e & 1); V: value e in nibble e
-      const int sh = isv ? 4 * e : 4 * (e >> 1) + 16 * (e & 1);
-      x[e] = d[j] * (float)((int)(word[j] >> sh & 15u) - 8);
+      // nibble n, read where it stands: 2^23 + c 2^s is a float for s <= 19, and loses its 2^23 and 8 2^s exactly
+      const int n = V ? e : (e >> 1) + 4 * (e & 1);
+      const int s = n < 5 ? 4 * n : 4 * n - 20;
+      const float y = __uint_as_float(lop3_and_or(n < 5 ? word[j] : word[j] >> 20, 15u << s, 0x4B000000u));
+      x[e] = (y - (8388608.f + 8.f * (float)(1 << s))) * (d[j] * (1.f / (float)(1 << s)));
     }
-    store8<DT>(isv ? p.vo : p.ko, (id / (2 * C) * p.g.heads + h) * D + 8 * (id % C), x);
+    store8<DT>(V ? p.vo : p.ko, (id / C * p.g.heads + h) * D + 8 * c, x);
   }
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kRowsThreads) kv_read_kernel(const __grid_constant__ KvRows p) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.z) read_rows<D, DT, true>(p);
+  else read_rows<D, DT, false>(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -409,11 +433,11 @@ int launched(cudaError_t e) {
 }
 
 template <int D>
-int launch_rows(KvRows p, int dtype, bool append, cudaStream_t s) {
-  p.items = (int64_t)p.T * 2 * (D / 8);
+int launch_rows(KvRows p, int T, int dtype, bool append, cudaStream_t s) {
+  p.items = (int64_t)T * (D / 8);
   const int64_t ctas = (p.items + kRowsThreads * kRowsUnroll - 1) / (kRowsThreads * kRowsUnroll);
   if (ctas > 2147483647) return DQ_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)ctas, (unsigned)p.g.heads), block(kRowsThreads);
+  const dim3 grid((unsigned)ctas, (unsigned)p.g.heads, 2), block(kRowsThreads);
 #define DQ_KV_ROWS(DT)                                                                        \
   if (dtype == DT)                                                                            \
     return launched(append ? launch_pdl(kv_append_kernel<D, DT>, grid, block, 0, s, 0, p)     \
@@ -515,9 +539,8 @@ int dq_kv_append(const dq_kv_cache* cache, const void* k, int64_t k_stride, cons
   p.v_stride = v_stride;
   p.slots = slots;
   p.n_slots = (int64_t)cache->n_pages * cache->page_size;
-  p.T = T;
   return by_dim(cache->head_dim, [&](auto d) {
-    return launch_rows<decltype(d)::value>(p, dtype, true, (cudaStream_t)stream);
+    return launch_rows<decltype(d)::value>(p, T, dtype, true, (cudaStream_t)stream);
   });
 }
 
@@ -535,9 +558,8 @@ int dq_kv_read(const dq_kv_cache* cache, const int64_t* slots, int T, void* k, v
   p.k_stride = p.v_stride = 0;
   p.slots = slots;
   p.n_slots = (int64_t)cache->n_pages * cache->page_size;
-  p.T = T;
   return by_dim(cache->head_dim, [&](auto d) {
-    return launch_rows<decltype(d)::value>(p, dtype, false, (cudaStream_t)stream);
+    return launch_rows<decltype(d)::value>(p, T, dtype, false, (cudaStream_t)stream);
   });
 }
 
