@@ -80,9 +80,9 @@ struct Walk {
     const int64_t rows = (int64_t)n * p.group;
     return rows > p.rows_above && rows <= p.rows_upto ? n : 0;
   }
-  // `known`: rows, length and first row of q of every request, in shared memory, or null
-  __device__ __forceinline__ static int64_t units(const AttnParams& p, int r, Item& it,
-                                                  const int* known = nullptr) {
+  // Request r.  `known`: rows, length and first row of q of every request, in shared memory, or null.
+  __device__ __forceinline__ static void request(const AttnParams& p, int r, Item& it,
+                                                 const int* known = nullptr) {
     it.r = r;
     if (known) {
       it.qlen = known[3 * r];
@@ -92,12 +92,15 @@ struct Walk {
       it.qlen = tokens(p, r, &it.first);
       it.len = kv_length(p, r);
     }
+  }
+  // Units of the row tiles k, k + step, .. of the request in `it` (one head's).
+  __device__ __forceinline__ static int64_t row_tile_units(const AttnParams& p, Item& it, int k, int step) {
     int64_t u = 0;
-    for (it.row0 = 0; it.row0 < it.qlen * p.group; it.row0 += ROWS) {
+    for (it.row0 = k * ROWS; it.row0 < it.qlen * p.group; it.row0 += step * ROWS) {
       range(p, it);
       u += it.tiles + OV;
     }
-    return u * p.g.heads;
+    return u;
   }
   __device__ __forceinline__ static void next(const AttnParams& p, Item& it) {
     if (++it.h < p.g.heads) return;
@@ -127,7 +130,21 @@ struct Walk {
     int64_t u = 0;
     for (int i = 0; i < chunk; ++i) {
       const int r = threadIdx.x * chunk + i;
-      if (r < p.B) u += units(p, r, it);
+      if (r < p.B) request(p, r, it);
+      else it.qlen = it.len = it.first = 0;
+      // a request of few row tiles by its thread, one of many by the warp
+      const bool few = (int64_t)it.qlen * p.group <= 4 * ROWS;
+      if (few) u += row_tile_units(p, it, 0, 1) * p.g.heads;
+      for (uint32_t m = __ballot_sync(0xffffffffu, !few); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        Item x;
+        x.qlen = __shfl_sync(0xffffffffu, it.qlen, src);
+        x.len = __shfl_sync(0xffffffffu, it.len, src);
+        int64_t n = row_tile_units(p, x, lane, 32);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (lane == src) u += n * p.g.heads;
+      }
     }
     if (known && chunk == 1 && (int)threadIdx.x < p.B) {
       known[3 * threadIdx.x] = it.qlen;
@@ -161,20 +178,34 @@ struct Walk {
     const int small = 31 - __clz(__ballot_sync(0xffffffffu, lane < STEP && at < NTH && pre[min(at, NTH)] <= u));
     const int c = big * STEP + small;
     int64_t iu = pre[c];
+    // the request, 32 row tiles at a time; then the row tile and the head (a row tile's heads cost the same)
     for (int r = c * chunk;; ++r) {
-      const int64_t n = units(p, r, it, chunk == 1 ? known : nullptr);
-      if (u < iu + n) break;
-      iu += n;
-    }
-    // the row tile, then the head: all heads of a row tile cost the same
-    for (it.row0 = 0;; it.row0 += ROWS) {
-      range(p, it);
-      const int cost = it.tiles + OV;
-      if (u < iu + (int64_t)cost * p.g.heads) {
-        it.h = (int)((uint32_t)(u - iu) / (uint32_t)cost);
-        return iu + (int64_t)it.h * cost;
+      request(p, r, it, chunk == 1 ? known : nullptr);
+      for (int row0 = 0; row0 < it.qlen * p.group; row0 += 32 * ROWS) {
+        it.row0 = row0 + lane * ROWS;
+        int64_t n = 0;
+        if (it.row0 < it.qlen * p.group) {
+          range(p, it);
+          n = (int64_t)(it.tiles + OV) * p.g.heads;
+        }
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, u < iu + inc);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          iu += __shfl_sync(0xffffffffu, inc - n, l);
+          it.row0 = row0 + l * ROWS;
+          range(p, it);
+          const int cost = it.tiles + OV;
+          it.h = (int)((uint32_t)(u - iu) / (uint32_t)cost);
+          return iu + (int64_t)it.h * cost;
+        }
+        iu += __shfl_sync(0xffffffffu, inc, 31);
       }
-      iu += (int64_t)cost * p.g.heads;
     }
   }
   // The tiles [a, b) of the item at unit iu that lie in the share [u0, u1); none: on to the next

@@ -227,12 +227,19 @@ __device__ __forceinline__ void row_tile_range(const AttnParams& p, const Item& 
   b = max(a, min(tb, (end + TT - 1) / TT - it.t0));
 }
 
+// The power of two that brings a row's largest magnitude into [2^14, 2^15) (1 for a row of zeros).
+__device__ __forceinline__ float row_up(float mx) {
+  const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
+  return mx > 0.f ? __uint_as_float((uint32_t)(127 + min(14 - ex, 100)) << 23) : 1.f;
+}
+
 template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
   using B = KvBlk<D>;
   using Wk = Walk<C::ROWS, C::TT, kItemCost>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
+  constexpr int LPR = D / 8, RPI = 32 / LPR, QB = D == 64 ? 8 : 4;   // rows to and from the warps
   extern __shared__ __align__(1024) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
@@ -315,50 +322,45 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const int head = it.h * p.group + uq;
       float cf = 0.f;
       if (nt > 0) {
-        const uint4* src = (const uint4*)((const uint16_t*)p.q + q_at * p.q_stride + (int64_t)head * D);
-        float mx = 0.f;
-        constexpr int CH = D / 8;
-        uint4 raw[CH < 16 ? CH : 16];
-        for (int c0 = 0; c0 < CH; c0 += 16) {
+        // The warp loads its 32 rows, LPR lanes a row: 16 bytes a lane, whole rows at a time.
+        float own = 0.f;                   // the largest magnitude of this thread's row
 #pragma unroll
-          for (int c = 0; c < (CH < 16 ? CH : 16); ++c) {
-            raw[c] = live ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+        for (int i0 = 0; i0 < 32 / RPI; i0 += QB) {
+          uint4 raw[QB];
+#pragma unroll
+          for (int k = 0; k < QB; ++k) {
+            const int lr = tile * 128 + 32 * (warp & 3) + (i0 + k) * RPI + lane / LPR;
+            const int rw = it.row0 + lr, tq = row_token(p, rw), u = rw - tq * p.group;
+            const uint16_t* src = (const uint16_t*)p.q + (int64_t)(it.first + tq) * p.q_stride +
+                                  ((int64_t)it.h * p.group + u) * D + 8 * (lane % LPR);
+            raw[k] = lr < it.rows ? __ldg((const uint4*)src) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < QB; ++k) {
+            const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+            float2 f[4];
+            float mx = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float2 f;
               if (p.q_dtype == DQ_BF16)
-                f = make_float2(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xFFFF0000u));
+                f[i] = make_float2(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xFFFF0000u));
               else
-                f = __half22float2(u32_as_h2(w4[i]));
-              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                f[i] = __half22float2(u32_as_h2(w4[i]));
+              mx = fmaxf(mx, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
             }
-          }
-        }
-        // 2^e with 2^14 <= max * 2^e < 2^15
-        const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
-        const int e = mx > 0.f ? min(14 - ex, 100) : 0;
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        cf = p.scale * kLog2e * __uint_as_float((uint32_t)(127 - e) << 23);
-        for (int c0 = 0; c0 < CH; c0 += 16) {
 #pragma unroll
-          for (int c = 0; c < (CH < 16 ? CH : 16); ++c) {
-            if (CH > 16) raw[c] = live ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+            for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float got = __shfl_sync(0xffffffffu, mx, (lane % RPI) * LPR);
+            if (lane / RPI == i0 + k) own = got;
+            const float up = row_up(mx);
             uint32_t r4[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float2 f;
-              if (p.q_dtype == DQ_BF16)
-                f = make_float2(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xFFFF0000u));
-              else
-                f = __half22float2(u32_as_h2(w4[i]));
-              r4[i] = h2_as_u32(__floats2half2_rn(f.x * up, f.y * up));
-            }
-            sts_u128(qrow + (c0 + c) / 8 * 16384 + sw128_offset(trow, (c0 + c) & 7),
-                     make_uint4(r4[0], r4[1], r4[2], r4[3]));
+            for (int i = 0; i < 4; ++i) r4[i] = h2_as_u32(__floats2half2_rn(f[i].x * up, f[i].y * up));
+            const int tr = 32 * (warp & 3) + (i0 + k) * RPI + lane / LPR, ch = lane % LPR;
+            sts_u128(qrow + ch / 8 * 16384 + sw128_offset(tr, ch & 7), make_uint4(r4[0], r4[1], r4[2], r4[3]));
           }
         }
+        cf = p.scale * kLog2e / row_up(own);
         fence_proxy_async_smem();
         mbar_arrive(&q_full[tile]);
       }
@@ -461,30 +463,70 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         const bool whole = from_start && to_end;
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
         const int64_t part = ((int64_t)blockIdx.x * 2 + slot) * C::ROWS + tile * 128 + trow;
+        // The rows go through the row tile's place in shared memory (its last scores are done): a thread
+        // puts its own there, the warp takes them out row by row.  16-bit outputs in one round, fp32 in
+        // two of half a row.
+        const bool f32 = !whole || p.out_dtype == DQ_F32;
+        for (int round = 0; round < (f32 ? 2 : 1); ++round) {
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(o_addr + 32 * c, r);
-          tmem_wait_ld();
-          tmem_use(r);
-          float v[32];
+          for (int c = 0; c < D / 32; ++c) {
+            if (f32 && D > 64 && c / (D / 64) != round) continue;
+            uint32_t r[32];
+            tmem_ld32(o_addr + 32 * c, r);
+            tmem_wait_ld();
+            tmem_use(r);
+            float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = nt > 0 ? __uint_as_float(r[i]) : 0.f;
-          if (live) {
+            for (int i = 0; i < 32; ++i) v[i] = nt > 0 ? __uint_as_float(r[i]) * inv : 0.f;
             // column 8 a + 2 n + k of panel w is value 4 a + n of group 2 w + k
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k) {
+              const int dim = ((c & ~1) + k) * 32 + (c & 1) * 16;    // 16 values from here
+              if (f32) {
+                if (D == 64 && k != round) continue;
 #pragma unroll
-              for (int a = 0; a < 4; ++a) {
-                const float x[4] = {v[8 * a + k] * inv, v[8 * a + 2 + k] * inv, v[8 * a + 4 + k] * inv,
-                                    v[8 * a + 6 + k] * inv};
-                const int dim = ((c & ~1) + k) * 32 + (c & 1) * 16 + 4 * a;
-                if (whole)
-                  store_out4(p, q_at * p.out_stride + (int64_t)head * D + dim, x);
-                else
-                  *(float4*)(ws.o + part * D + dim) = make_float4(x[0], x[1], x[2], x[3]);
+                for (int a = 0; a < 4; ++a) {
+                  const int ch = (dim - round * (D / 2)) / 4 + a;
+                  sts_u128(qrow + ch / 8 * 16384 + sw128_offset(trow, ch & 7),
+                           make_uint4(__float_as_uint(v[8 * a + k]), __float_as_uint(v[8 * a + 2 + k]),
+                                      __float_as_uint(v[8 * a + 4 + k]), __float_as_uint(v[8 * a + 6 + k])));
+                }
+              } else {
+#pragma unroll
+                for (int a = 0; a < 4; a += 2) {
+                  uint32_t h[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int j = 8 * (a + i / 2) + 4 * (i & 1) + k;
+                    if (p.out_dtype == DQ_BF16) {
+                      const __nv_bfloat162 t = __floats2bfloat162_rn(v[j], v[j + 2]);
+                      h[i] = *(const uint32_t*)&t;
+                    } else {
+                      h[i] = h2_as_u32(__floats2half2_rn(v[j], v[j + 2]));
+                    }
+                  }
+                  const int ch = dim / 8 + a / 2;
+                  sts_u128(qrow + ch / 8 * 16384 + sw128_offset(trow, ch & 7), make_uint4(h[0], h[1], h[2], h[3]));
+                }
               }
+            }
           }
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int tr = 32 * (warp & 3) + i * RPI + lane / LPR, lr = tile * 128 + tr, ch = lane % LPR;
+            const uint4 v = lds_u128(qrow + ch / 8 * 16384 + sw128_offset(tr, ch & 7));
+            if (lr >= it.rows) continue;
+            const int rw = it.row0 + lr, tq = row_token(p, rw), u = rw - tq * p.group;
+            const int64_t at = (int64_t)(it.first + tq) * p.out_stride + ((int64_t)it.h * p.group + u) * D;
+            if (!whole)
+              *(uint4*)(ws.o + (((int64_t)blockIdx.x * 2 + slot) * C::ROWS + lr) * D + round * (D / 2) + 4 * ch) = v;
+            else if (f32)
+              *(uint4*)((float*)p.out + at + round * (D / 2) + 4 * ch) = v;
+            else
+              *(uint4*)((uint16_t*)p.out + at + 8 * ch) = v;
+          }
+          __syncwarp();
         }
         if (live) {
           if (!whole)
