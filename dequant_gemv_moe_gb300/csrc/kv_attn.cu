@@ -5,8 +5,9 @@ namespace dqmoe {
 
 namespace {
 
-// 64 rows: 20 requests of 7 to 42 rows (heads of 128, 6000 tokens) take 44.8 us in the streaming kernel
-// and 63.5 us in the tensor-core one from 32 rows on.
+// The streaming kernel decodes a page once for every 8 rows, the tensor-core kernel once for 256, at the
+// price of a tile of 128 rows whatever their number.  32 requests of up to 32 rows (8 K/V heads of 128,
+// 16000 tokens): 134 us streaming, 257 us on the tensor core; they meet at about 64 rows.
 constexpr int kStreamRows = 64;
 
 int attn_sizes_ok(const dq_kv_cache* cache, int n_q_heads, int T, int B, int max_q_len) {
@@ -88,12 +89,12 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
   p.out_stride = a->out_stride;
   p.lse = a->lse;
   p.ws = (uint8_t*)ws;
-  // Requests with at most kStreamRows rows per K/V head stream their pages once for every 16 rows;
-  // if one may have more, those with more than 16 go to the tensor-core kernel (which is launched
-  // anyway: a request of 45 rows on its own in the streaming kernel cost 11 us more there).
+  // Requests with at most kStreamRows rows per K/V head stream.  If one may have more, so that the
+  // tensor-core kernel is launched anyway, those with more than half as many go there: what streams is
+  // then a launch of its own beside it (one request of 45 rows among prompts: 11 us more as a stream).
   const bool many = (int64_t)a->max_q_len * p.group > kStreamRows;
   p.rows_above = 0;
-  p.rows_upto = many ? 16 : kStreamRows;
+  p.rows_upto = many ? kStreamRows / 2 : kStreamRows;
   p.ws = (uint8_t*)ws;
   rc = launch_kv_stream(p, cache->head_dim, (cudaStream_t)stream);
   if (rc != DQ_OK || !many) return rc;

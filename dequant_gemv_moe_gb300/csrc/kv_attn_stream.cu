@@ -1,7 +1,7 @@
 // kv_attn_stream.cu — attention of few query rows over the 4-bit paged cache:
 // a decode step, or a handful of drafted tokens per request.
 //
-// Mathematics.  For one K/V head and up to 8 NT query rows (the query heads that
+// Mathematics.  For one K/V head and up to 8 query rows (the query heads that
 // share it, and the step's tokens) a warp walks tiles of 32 tokens and keeps
 // the running maximum, sum and weighted V sum of the softmax.  Both products
 // run on the tensor core with the tokens' codes as the A operand and the rows
@@ -63,15 +63,15 @@ struct Place {
 struct WarpState {
   Place at[2];
   int64_t u0, u1;
-  int lo[16], hi[16];
+  int lo[8], hi[8];
 };
 
-template <int D, int NT>
+template <int D>
 struct StreamCfg {
-  // O (D NT / 4 registers), Q, its sums and the scores: 16 warps of 128 registers, 12 of 168 or 8 of 255.
+  // O (D / 4 registers), Q, its sums and the scores: 16 warps of 128 registers, 12 of 168 or 8 of 255.
   // (attn of 64 requests, 576 MB, heads of 128: 12 warps with three tiles each 111.9 us, 16 with two 113.5.)
-  static constexpr int NW = D * NT <= 64 ? 16 : D * NT <= 128 ? 12 : 8;
-  static constexpr int ROWS = 8 * NT;
+  static constexpr int NW = D <= 64 ? 16 : D <= 128 ? 12 : 8;
+  static constexpr int ROWS = 8;
   static constexpr int STG = kBlks * KvBlk<D>::BYTES;
   static constexpr int STAGES = D == 256 ? 2 : 3;
   static constexpr int NTH = NW * 32;
@@ -93,8 +93,8 @@ struct StreamWs {
   float2* ml;
   int4* desc;
 };
-constexpr size_t kStreamO = (size_t)kMaxCtas * 2 * 16 * 128 * 4;    // ROWS * D is at most 16 * 128
-constexpr size_t kStreamMl = (size_t)kMaxCtas * 2 * 16 * 8;
+constexpr size_t kStreamO = (size_t)kMaxCtas * 2 * 8 * 256 * 4;     // ROWS * D is at most 8 * 256
+constexpr size_t kStreamMl = (size_t)kMaxCtas * 2 * 8 * 8;
 constexpr size_t kStreamDesc = (size_t)kMaxCtas * 16;
 
 __device__ __forceinline__ StreamWs stream_ws(uint8_t* ws) {
@@ -132,11 +132,11 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
   }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(StreamCfg<D, NT>::NTH, 1)
+template <int D>
+__global__ void __launch_bounds__(StreamCfg<D>::NTH, 1)
 kv_stream_kernel(const __grid_constant__ AttnParams p) {
   using B = KvBlk<D>;
-  using C = StreamCfg<D, NT>;
+  using C = StreamCfg<D>;
   constexpr int G = B::G, W = B::W, GH = G / W;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,19 +224,16 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   };
   // The rows of item x: column lr of each 8-row tile, values 8 lt.. of every group.  Loaded before the
   // copies are issued, or before the item in front is written, and used after.
-  uint4 raw[NT][G];
+  uint4 raw[G];
   auto load_rows = [&](const Item& x) {
+    const int row = x.row0 + lr;
+    const bool live = lr < x.rows;
+    const int tokq = row_token(p, row), uq = row - tokq * p.group;
+    const uint16_t* q = (const uint16_t*)p.q + (int64_t)(x.first + tokq) * p.q_stride +
+                        ((int64_t)x.h * p.group + uq) * D + 8 * lt;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = x.row0 + nt * 8 + lr;
-      const bool live = nt * 8 + lr < x.rows;
-      const int tokq = row_token(p, row), uq = row - tokq * p.group;
-      const uint16_t* q = (const uint16_t*)p.q + (int64_t)(x.first + tokq) * p.q_stride +
-                          ((int64_t)x.h * p.group + uq) * D + 8 * lt;
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        raw[nt][g] = live ? __ldg((const uint4*)(q + 32 * g)) : make_uint4(0, 0, 0, 0);
-    }
+    for (int g = 0; g < G; ++g)
+      raw[g] = live ? __ldg((const uint4*)(q + 32 * g)) : make_uint4(0, 0, 0, 0);
   };
   if (more) load_rows(S.at[0].it);
   __syncwarp();
@@ -244,72 +241,69 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   for (int s = 0; s < C::STAGES; ++s) produce(s);
 
   // ---- consumer state
-  uint32_t qf[G][4][NT];
-  float qi[G][NT][2], cf[NT][2];
-  float o[G][2][NT][4];
-  float M[NT][2], lim[NT][2];
-  float2 l[NT];
+  uint32_t qf[G][4];
+  float qi[G][2], cf[2];
+  float o[G][2][4];
+  float M[2], lim[2];
+  float2 l;
   float b = 10.f;
   bool ok = true;
 
   int stage = 0, phase = 0;
   while (more) {
     const Item it = S.at[0].it;
+    float x[G][8], mx = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float x[G][8], mx = 0.f;
+    for (int g = 0; g < G; ++g) {
+      const uint32_t w4[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint32_t w4[4] = {raw[nt][g].x, raw[nt][g].y, raw[nt][g].z, raw[nt][g].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (p.q_dtype == DQ_BF16) {
-            x[g][2 * i] = __uint_as_float(w4[i] << 16);
-            x[g][2 * i + 1] = __uint_as_float(w4[i] & 0xFFFF0000u);
-          } else {
-            const float2 f = __half22float2(u32_as_h2(w4[i]));
-            x[g][2 * i] = f.x;
-            x[g][2 * i + 1] = f.y;
-          }
-          mx = fmaxf(mx, fmaxf(fabsf(x[g][2 * i]), fabsf(x[g][2 * i + 1])));
+      for (int i = 0; i < 4; ++i) {
+        if (p.q_dtype == DQ_BF16) {
+          x[g][2 * i] = __uint_as_float(w4[i] << 16);
+          x[g][2 * i + 1] = __uint_as_float(w4[i] & 0xFFFF0000u);
+        } else {
+          const float2 f = __half22float2(u32_as_h2(w4[i]));
+          x[g][2 * i] = f.x;
+          x[g][2 * i + 1] = f.y;
         }
+        mx = fmaxf(mx, fmaxf(fabsf(x[g][2 * i]), fabsf(x[g][2 * i + 1])));
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // 2^e with 2^14 <= max * 2^e < 2^15
-      const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
-      const int e = mx > 0.f ? min(14 - ex, 100) : 0;
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float c = p.scale * kLog2e * 16777216.f *
-                      __uint_as_float((uint32_t)(127 - e) << 23);
-      float sum[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        sum[g] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = (i & 1) ? up * 0.0625f : up;
-          const __half2 hv = __floats2half2_rn(x[g][2 * i] * f, x[g][2 * i + 1] * f);
-          qf[g][i][nt] = h2_as_u32(hv);
-          const float2 back = __half22float2(hv);
-          sum[g] += (back.x + back.y) * ((i & 1) ? 16.f : 1.f);
-        }
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-        const float s8 = sum[g] * (-8.f / 16777216.f);
-        qi[g][nt][0] = __shfl_sync(0xffffffffu, s8, 8 * lt);
-        qi[g][nt][1] = __shfl_sync(0xffffffffu, s8, 8 * lt + 4);
-      }
-      cf[nt][0] = __shfl_sync(0xffffffffu, c, 8 * lt);
-      cf[nt][1] = __shfl_sync(0xffffffffu, c, 8 * lt + 4);
-      M[nt][0] = M[nt][1] = kNone;
-      lim[nt][0] = lim[nt][1] = kNone;
-      l[nt] = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[g][0][nt][k] = o[g][1][nt][k] = 0.f;
     }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // 2^e with 2^14 <= max * 2^e < 2^15
+    const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
+    const int e = mx > 0.f ? min(14 - ex, 100) : 0;
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    const float c = p.scale * kLog2e * 16777216.f *
+                    __uint_as_float((uint32_t)(127 - e) << 23);
+    float sum[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      sum[g] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = (i & 1) ? up * 0.0625f : up;
+        const __half2 hv = __floats2half2_rn(x[g][2 * i] * f, x[g][2 * i + 1] * f);
+        qf[g][i] = h2_as_u32(hv);
+        const float2 back = __half22float2(hv);
+        sum[g] += (back.x + back.y) * ((i & 1) ? 16.f : 1.f);
+      }
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+      const float s8 = sum[g] * (-8.f / 16777216.f);
+      qi[g][0] = __shfl_sync(0xffffffffu, s8, 8 * lt);
+      qi[g][1] = __shfl_sync(0xffffffffu, s8, 8 * lt + 4);
+    }
+    cf[0] = __shfl_sync(0xffffffffu, c, 8 * lt);
+    cf[1] = __shfl_sync(0xffffffffu, c, 8 * lt + 4);
+    M[0] = M[1] = kNone;
+    lim[0] = lim[1] = kNone;
+    l = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[g][0][k] = o[g][1][k] = 0.f;
     b = 10.f;
     // the positions that every row of the item sees, and each row's own limits
     int lo_all, hi_all;
@@ -336,7 +330,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       const bool inner = tok0 >= lo_all && tok0 + kTile <= hi_all;
 
       // ---- scores
-      float s[kBlks][NT][4];
+      float s[kBlks][4];
 #pragma unroll
       for (int k = 0; k < kBlks; ++k) {
         const uint32_t kb = base + k * B::BYTES;
@@ -362,17 +356,14 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             const float2 fa = __half22float2(u32_as_h2(da[gw2 / 2])),
                          fb = __half22float2(u32_as_h2(db[gw2 / 2]));
             const float sa = (gw2 & 1) ? fa.y : fa.x, sb = (gw2 & 1) ? fb.y : fb.x;
+            float acc[4];
+            mma_16816_c(acc, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
+                        qf[g][0], qf[g][1], qi[g][0], qi[g][1]);
+            mma_16816_nv(acc, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u,
+                         y8 & 0x00F000F0u, qf[g][2], qf[g][3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float acc[4];
-              mma_16816_c(acc, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
-                          qf[g][0][nt], qf[g][1][nt], qi[g][nt][0], qi[g][nt][1]);
-              mma_16816_nv(acc, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u,
-                           y8 & 0x00F000F0u, qf[g][2][nt], qf[g][3][nt]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                s[k][nt][i] = g == 0 ? (i < 2 ? sa : sb) * acc[i] : fmaf(i < 2 ? sa : sb, acc[i], s[k][nt][i]);
-            }
+            for (int i = 0; i < 4; ++i)
+              s[k][i] = g == 0 ? (i < 2 ? sa : sb) * acc[i] : fmaf(i < 2 ? sa : sb, acc[i], s[k][i]);
           }
         }
       }
@@ -420,66 +411,58 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
           for (int g = 0; g < G; ++g) big |= dv[g][0] | dv[g][1];
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 2; ++i) {
+          const int lo = S.lo[2 * lt + i], hi = S.hi[2 * lt + i];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int lo = S.lo[nt * 8 + 2 * lt + i], hi = S.hi[nt * 8 + 2 * lt + i];
+          for (int k = 0; k < kBlks; ++k)
 #pragma unroll
-            for (int k = 0; k < kBlks; ++k)
-#pragma unroll
-              for (int hrow = 0; hrow < 2; ++hrow) {
-                const int a = tok0 + k * 16 + 8 * hrow + lr;
-                if (a < lo || a >= hi) s[k][nt][2 * hrow + i] = -INFINITY;
-              }
-          }
+            for (int hrow = 0; hrow < 2; ++hrow) {
+              const int a = tok0 + k * 16 + 8 * hrow + lr;
+              if (a < lo || a >= hi) s[k][2 * hrow + i] = -INFINITY;
+            }
+        }
       }
       // ---- weights
-      float top[NT][2];
+      float top[2];
       bool over = b > 0.f && (big & 0x40004000u) != 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          top[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]), fmaxf(s[1][nt][i], s[1][nt][2 + i])) * cf[nt][i];
-          over = over || top[nt][i] > lim[nt][i];
-        }
+      for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i])) * cf[i];
+        over = over || top[i] > lim[i];
+      }
       if (__any_sync(0xffffffffu, over)) {
         const float bn = __any_sync(0xffffffffu, (big & 0x40004000u) != 0) ? -2.f : b;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 2; ++i) {
+          float m = top[i];
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          const float mo = M[i], mn = fmaxf(mo + (b - bn), m - bn), corr = ex2(mo - mn);
+          M[i] = mn;
+          lim[i] = mn + bn + 4.f;
+          (i == 0 ? l.x : l.y) *= corr;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float m = top[nt][i];
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float mo = M[nt][i], mn = fmaxf(mo + (b - bn), m - bn), corr = ex2(mo - mn);
-            M[nt][i] = mn;
-            lim[nt][i] = mn + bn + 4.f;
-            (i == 0 ? l[nt].x : l[nt].y) *= corr;
+          for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-              for (int k = i; k < 4; k += 2) {
-                o[g][0][nt][k] *= corr;
-                o[g][1][nt][k] *= corr;
-              }
-          }
+            for (int k = i; k < 4; k += 2) {
+              o[g][0][k] *= corr;
+              o[g][1][k] *= corr;
+            }
+        }
         b = bn;
       }
       // ---- p and P V
 #pragma unroll
       for (int k = 0; k < kBlks; ++k) {
-        uint32_t pt[NT][2];
+        uint32_t pt[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int hrow = 0; hrow < 2; ++hrow) {
-            const float2 w = make_float2(ex2(fmaf(s[k][nt][2 * hrow], cf[nt][0], -M[nt][0])),
-                                         ex2(fmaf(s[k][nt][2 * hrow + 1], cf[nt][1], -M[nt][1])));
-            l[nt] = fadd2(l[nt], w);
-            pt[nt][hrow] = transpose8x8(h2_as_u32(__floats2half2_rn(w.x, w.y)));
-          }
+        for (int hrow = 0; hrow < 2; ++hrow) {
+          const float2 w = make_float2(ex2(fmaf(s[k][2 * hrow], cf[0], -M[0])),
+                                       ex2(fmaf(s[k][2 * hrow + 1], cf[1], -M[1])));
+          l = fadd2(l, w);
+          pt[hrow] = transpose8x8(h2_as_u32(__floats2half2_rn(w.x, w.y)));
+        }
         uint32_t dv[G][2];
         v_scales(k, dv);
         const uint32_t vb = base + k * B::BYTES + B::OFF_V;
@@ -495,29 +478,24 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             const uint32_t z0 = __byte_perm(v0[gw2 / 2], v0[W / 2 + gw2 / 2], sel);
             const uint32_t z1 = __byte_perm(v1[gw2 / 2], v1[W / 2 + gw2 / 2], sel);
             const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(pt[nt][0]), u32_as_h2(dv[g][0])));
-              const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(pt[nt][1]), u32_as_h2(dv[g][1])));
-              mma_16816_nv(o[g][0][nt], z0 & 0x000F000Fu, z0 & 0x00F000F0u, z1 & 0x000F000Fu,
-                           z1 & 0x00F000F0u, b0, b1);
-              mma_16816_nv(o[g][1][nt], y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu,
-                           y1 & 0x00F000F0u, b0, b1);
-              // the offset: -8 in each row's unit
-              mma_16816_nv(o[g][0][nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
-              mma_16816_nv(o[g][1][nt], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
-            }
+            const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(pt[0]), u32_as_h2(dv[g][0])));
+            const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(pt[1]), u32_as_h2(dv[g][1])));
+            mma_16816_nv(o[g][0], z0 & 0x000F000Fu, z0 & 0x00F000F0u, z1 & 0x000F000Fu,
+                         z1 & 0x00F000F0u, b0, b1);
+            mma_16816_nv(o[g][1], y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu,
+                         y1 & 0x00F000F0u, b0, b1);
+            // the offset: -8 in each row's unit
+            mma_16816_nv(o[g][0], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+            mma_16816_nv(o[g][1], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
           }
         }
       }
       // every load of the stage has fed an instruction before its next copy is issued
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          keep_before_release<4>(o[g][0][nt]);
-          keep_before_release<4>(o[g][1][nt]);
-        }
+      for (int g = 0; g < G; ++g) {
+        keep_before_release<4>(o[g][0]);
+        keep_before_release<4>(o[g][1]);
+      }
       __syncwarp();
       produce(stage);
       if (++stage == C::STAGES) {
@@ -537,38 +515,36 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     more = advance(S.at[0]);
     if (more) load_rows(S.at[0].it);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < 2; ++i) {
+      float sum = i == 0 ? l.x : l.y;
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int col = 2 * lt + i;
+      if (col >= done.rows) continue;
+      const float k24 = 16777216.f, k20 = 1048576.f;
+      const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+      const int row = done.row0 + col, tokq = row_token(p, row), uq = row - tokq * p.group;
+      const int64_t qrow = done.first + tokq;
+      const int head = done.h * p.group + uq;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float sum = i == 0 ? l[nt].x : l[nt].y;
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int col = nt * 8 + 2 * lt + i;
-        if (col >= done.rows) continue;
-        const float k24 = 16777216.f, k20 = 1048576.f;
-        const float inv = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-        const int row = done.row0 + col, tokq = row_token(p, row), uq = row - tokq * p.group;
-        const int64_t qrow = done.first + tokq;
-        const int head = done.h * p.group + uq;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float x[4] = {(o[g][0][nt][i]) * (k24 * inv),
-                              (o[g][0][nt][2 + i]) * (k20 * inv),
-                              (o[g][1][nt][i]) * (k24 * inv),
-                              (o[g][1][nt][2 + i]) * (k20 * inv)};
-          if (whole)
-            store_out4(p, qrow * p.out_stride + (int64_t)head * D + 32 * g + 4 * lr, x);
-          else
-            *(float4*)(part + col * D + 32 * g + 4 * lr) = make_float4(x[0], x[1], x[2], x[3]);
-        }
-        if (lr == 0) {
-          if (!whole)
-            ((float2*)(part + C::ROWS * D))[col] = make_float2(M[nt][i], sum);
-          else if (p.lse)
-            p.lse[qrow * p.n_q_heads + head] = sum > 0.f ? (M[nt][i] + log2f(sum)) * kLn2 : -INFINITY;
-        }
+      for (int g = 0; g < G; ++g) {
+        const float x[4] = {(o[g][0][i]) * (k24 * inv),
+                            (o[g][0][2 + i]) * (k20 * inv),
+                            (o[g][1][i]) * (k24 * inv),
+                            (o[g][1][2 + i]) * (k20 * inv)};
+        if (whole)
+          store_out4(p, qrow * p.out_stride + (int64_t)head * D + 32 * g + 4 * lr, x);
+        else
+          *(float4*)(part + col * D + 32 * g + 4 * lr) = make_float4(x[0], x[1], x[2], x[3]);
       }
+      if (lr == 0) {
+        if (!whole)
+          ((float2*)(part + C::ROWS * D))[col] = make_float2(M[i], sum);
+        else if (p.lse)
+          p.lse[qrow * p.n_q_heads + head] = sum > 0.f ? (M[i] + log2f(sum)) * kLn2 : -INFINITY;
+      }
+    }
     if (!whole && lane == 0) {
       Left& x = left[warp * 2 + (from_start ? 1 : 0)];
       x.r = done.r;
@@ -651,9 +627,9 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
 // it; a warp takes a row and one of kSub interleaved shares of its partials.
 constexpr int kSub = 4;
 
-template <int D, int NT>
+template <int D>
 __global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_constant__ AttnParams p) {
-  using C = StreamCfg<D, NT>;
+  using C = StreamCfg<D>;
   constexpr int G = D / 32;                // values of a row per lane
   __shared__ float acc_s[8][kSub][D];
   __shared__ float2 ml_s[8][kSub];
@@ -664,81 +640,76 @@ __global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_const
   const int follow = d.w;                  // CTAs behind this one that the item goes on in
   if (follow == 0) return;                 // uniform for the CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp >> 3, rw = warp & 7;
+  const int sub = warp >> 3, col = warp & 7;
   int first;
   const int rows = min(C::ROWS, q_rows(p, d.x, &first) * p.group - d.z);
+  const bool live = col < rows;
+  // partial 0 is this CTA's second one, the others the first ones of the CTAs after it
+  auto part = [&](int i) -> int64_t {
+    return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::ROWS + col;
+  };
+  float m = kNone, l = 0.f, acc[G];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int col = nt * 8 + rw;
-    const bool live = col < rows;
-    // partial 0 is this CTA's second one, the others the first ones of the CTAs after it
-    auto part = [&](int i) -> int64_t {
-      return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::ROWS + col;
-    };
-    float m = kNone, l = 0.f, acc[G];
+  for (int v = 0; v < G; ++v) acc[v] = 0.f;
+  if (live) {
+    for (int i = sub + kSub * lane; i <= follow; i += kSub * 32) m = fmaxf(m, __ldcg(ws.ml + part(i)).x);
 #pragma unroll
-    for (int v = 0; v < G; ++v) acc[v] = 0.f;
-    if (live) {
-      for (int i = sub + kSub * lane; i <= follow; i += kSub * 32) m = fmaxf(m, __ldcg(ws.ml + part(i)).x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll 4
-      for (int i = sub; i <= follow; i += kSub) {
-        const int64_t at = part(i);
-        const float2 ml = __ldcg(ws.ml + at);
-        const float f = ex2(ml.x - m);
-        l = fmaf(ml.y, f, l);
+    for (int i = sub; i <= follow; i += kSub) {
+      const int64_t at = part(i);
+      const float2 ml = __ldcg(ws.ml + at);
+      const float f = ex2(ml.x - m);
+      l = fmaf(ml.y, f, l);
 #pragma unroll
-        for (int v = 0; v < G; v += 2) {
-          const float2 x = __ldcg((const float2*)(ws.o + at * D + lane * G + v));
-          acc[v] = fmaf(x.x, f, acc[v]);
-          acc[v + 1] = fmaf(x.y, f, acc[v + 1]);
-        }
+      for (int v = 0; v < G; v += 2) {
+        const float2 x = __ldcg((const float2*)(ws.o + at * D + lane * G + v));
+        acc[v] = fmaf(x.x, f, acc[v]);
+        acc[v + 1] = fmaf(x.y, f, acc[v + 1]);
       }
     }
+  }
 #pragma unroll
-    for (int v = 0; v < G; v += 2)
-      *(float2*)&acc_s[rw][sub][lane * G + v] = make_float2(acc[v], acc[v + 1]);
-    if (lane == 0) ml_s[rw][sub] = make_float2(m, l);
-    __syncthreads();
-    if (sub == 0 && live) {
-      float mt = kNone, lt = 0.f, x[G];
-      for (int k = 0; k < kSub; ++k) mt = fmaxf(mt, ml_s[rw][k].x);
+  for (int v = 0; v < G; v += 2)
+    *(float2*)&acc_s[col][sub][lane * G + v] = make_float2(acc[v], acc[v + 1]);
+  if (lane == 0) ml_s[col][sub] = make_float2(m, l);
+  __syncthreads();
+  if (sub == 0 && live) {
+    float mt = kNone, lt = 0.f, x[G];
+    for (int k = 0; k < kSub; ++k) mt = fmaxf(mt, ml_s[col][k].x);
 #pragma unroll
-      for (int v = 0; v < G; ++v) x[v] = 0.f;
+    for (int v = 0; v < G; ++v) x[v] = 0.f;
 #pragma unroll
-      for (int k = 0; k < kSub; ++k) {
-        const float f = ex2(ml_s[rw][k].x - mt);
-        lt = fmaf(ml_s[rw][k].y, f, lt);
+    for (int k = 0; k < kSub; ++k) {
+      const float f = ex2(ml_s[col][k].x - mt);
+      lt = fmaf(ml_s[col][k].y, f, lt);
 #pragma unroll
-        for (int v = 0; v < G; v += 2) {
-          const float2 y = *(const float2*)&acc_s[rw][k][lane * G + v];
-          x[v] = fmaf(y.x, f, x[v]);
-          x[v + 1] = fmaf(y.y, f, x[v + 1]);
-        }
+      for (int v = 0; v < G; v += 2) {
+        const float2 y = *(const float2*)&acc_s[col][k][lane * G + v];
+        x[v] = fmaf(y.x, f, x[v]);
+        x[v + 1] = fmaf(y.y, f, x[v + 1]);
       }
-      store_row<D>(p, d.x, d.y, d.z + col, lane, x, mt, lt);
     }
-    __syncthreads();
+    store_row<D>(p, d.x, d.y, d.z + col, lane, x, mt, lt);
   }
 }
 
-template <int D, int NT>
+template <int D>
 int launch_stream(const AttnParams& p, int ctas, cudaStream_t s) {
-  using C = StreamCfg<D, NT>;
+  using C = StreamCfg<D>;
   static bool attr[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cudaFuncSetAttribute(kv_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(kv_stream_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM) != cudaSuccess)
       return DQ_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
   }
-  if (launch_pdl(kv_stream_kernel<D, NT>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) !=
+  if (launch_pdl(kv_stream_kernel<D>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) !=
       cudaSuccess)
     return DQ_ERR_CUDA;
-  if (launch_pdl(kv_stream_join_kernel<D, NT>, dim3(ctas), dim3(1024), 0, s, 0, p) != cudaSuccess)
+  if (launch_pdl(kv_stream_join_kernel<D>, dim3(ctas), dim3(1024), 0, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }
@@ -753,12 +724,9 @@ int launch_kv_stream(const AttnParams& p, int head_dim, cudaStream_t s) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DQ_ERR_CUDA;
   const int ctas = std::min(sms, kMaxCtas);
-  // more than 8 rows per K/V head: 16 at a time where the registers allow it
-  const bool two = std::min<int64_t>((int64_t)p.max_q_len * p.group, p.rows_upto) > 8;
-  if (head_dim == 64) return two ? launch_stream<64, 2>(p, ctas, s) : launch_stream<64, 1>(p, ctas, s);
-  if (head_dim == 128)
-    return two ? launch_stream<128, 2>(p, ctas, s) : launch_stream<128, 1>(p, ctas, s);
-  return launch_stream<256, 1>(p, ctas, s);
+  if (head_dim == 64) return launch_stream<64>(p, ctas, s);
+  if (head_dim == 128) return launch_stream<128>(p, ctas, s);
+  return launch_stream<256>(p, ctas, s);
 }
 
 }  // namespace dqmoe
