@@ -62,9 +62,16 @@ struct Item {
 
 // A call's work as one line of units: (request, row tile, K/V head, tile of
 // TILE tokens), the tokens fastest.  An item (all of them but the tokens) takes
-// OV units before its tiles: what starting and ending one costs.
-template <int ROWS, int TILE, int OV>
+// OV units before its tiles: what starting and ending one costs.  A tile takes one
+// unit, or WEIGHT::of(item).
+struct UnitWeight {
+  __device__ __forceinline__ static int of(const AttnParams&, const Item&) { return 1; }
+};
+template <int ROWS, int TILE, int OV, typename WEIGHT = UnitWeight>
 struct Walk {
+  __device__ __forceinline__ static int cost(const AttnParams& p, const Item& it) {
+    return it.tiles * WEIGHT::of(p, it) + OV;
+  }
   __device__ __forceinline__ static void range(const AttnParams& p, Item& it) {
     const int shift = it.len - it.qlen;
     it.rows = min(ROWS, it.qlen * p.group - it.row0);
@@ -98,7 +105,7 @@ struct Walk {
     int64_t u = 0;
     for (it.row0 = k * ROWS; it.row0 < it.qlen * p.group; it.row0 += step * ROWS) {
       range(p, it);
-      u += it.tiles + OV;
+      u += cost(p, it);
     }
     return u;
   }
@@ -186,7 +193,7 @@ struct Walk {
         int64_t n = 0;
         if (it.row0 < it.qlen * p.group) {
           range(p, it);
-          n = (int64_t)(it.tiles + OV) * p.g.heads;
+          n = (int64_t)cost(p, it) * p.g.heads;
         }
         int64_t inc = n;
 #pragma unroll
@@ -200,9 +207,9 @@ struct Walk {
           iu += __shfl_sync(0xffffffffu, inc - n, l);
           it.row0 = row0 + l * ROWS;
           range(p, it);
-          const int cost = it.tiles + OV;
-          it.h = (int)((uint32_t)(u - iu) / (uint32_t)cost);
-          return iu + (int64_t)it.h * cost;
+          const int each = cost(p, it);
+          it.h = (int)((uint32_t)(u - iu) / (uint32_t)each);
+          return iu + (int64_t)it.h * each;
         }
         iu += __shfl_sync(0xffffffffu, inc, 31);
       }
@@ -213,24 +220,31 @@ struct Walk {
   __device__ __forceinline__ static bool here(const AttnParams& p, Item& it, int64_t& iu, int64_t u0,
                                               int64_t u1, int& a, int& b) {
     for (;;) {
-      a = (int)max(u0 - iu - OV, (int64_t)0);
-      b = (int)min(u1 - iu - OV, (int64_t)it.tiles);
+      // tile t lies in the share that its first unit lies in
+      const int w = WEIGHT::of(p, it);
+      const int64_t lo = max(u0 - iu - OV, (int64_t)0), hi = min(u1 - iu - OV, (int64_t)it.tiles * w);
+      a = (int)lo;
+      b = (int)hi;
+      if (w > 1) {
+        a = (a + w - 1) / w;
+        b = b > 0 ? (b + w - 1) / w : 0;
+      }
       if (b > a) return true;
-      iu += it.tiles + OV;
+      iu += cost(p, it);
       if (iu >= u1) return false;
       next(p, it);
     }
   }
   __device__ __forceinline__ static bool after(const AttnParams& p, Item& it, int64_t& iu, int64_t u0,
                                                int64_t u1, int& a, int& b) {
-    iu += it.tiles + OV;
+    iu += cost(p, it);
     if (iu >= u1) return false;
     next(p, it);
     return here(p, it, iu, u0, u1, a, b);
   }
-  // the unit of the item's last tile
-  __device__ __forceinline__ static int64_t last_unit(const Item& it, int64_t iu) {
-    return iu + OV + it.tiles - 1;
+  // the first unit of the item's last tile
+  __device__ __forceinline__ static int64_t last_unit(const AttnParams& p, const Item& it, int64_t iu) {
+    return iu + OV + (int64_t)(it.tiles - 1) * WEIGHT::of(p, it);
   }
 };
 

@@ -508,7 +508,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     // ---- the item's rows: whole, or a partial (the second one over the ring, whose copies have all
     // been used: the share ends here)
     const Item done = S.at[0].it;
-    const int64_t done_last = Wk::last_unit(done, S.at[0].iu);
+    const int64_t done_last = Wk::last_unit(p, done, S.at[0].iu);
     const bool from_start = S.at[0].a == 0, to_end = S.at[0].b == done.tiles;
     const bool whole = from_start && to_end;
     float* part = (float*)(from_start ? ring : smem + C::OFF_HEAD + warp * C::PART);

@@ -27,6 +27,7 @@
 // head, token tile) units in equal shares, one per CTA, the partials of items
 // that cross shares joined in order by a second kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_attn.h"
 #include "tc.cuh"
@@ -43,7 +44,7 @@ template <int D>
 struct TcCfg {
   static constexpr int NQ = D == 256 ? 1 : 2;        // 128-row tiles
   static constexpr int TT = 64;                      // tokens per tile
-  static constexpr int KVS = D == 256 ? 2 : 4;       // decoded tiles
+  static constexpr int KVS = D == 256 ? 2 : 4;   // decoded tiles
   static constexpr int ROWS = 128 * NQ;
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int KV_BUF = TT * D * 2;
@@ -181,18 +182,23 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t p
 }
 constexpr uint32_t kBRowsAlongN = 1u << 16;
 
-// the 8 codes of a word as (c - 8) d: four pairs, in the order of the nibble pairs
-__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 d) {
+// the 8 codes of a word as c - 8: four pairs, in the order of the nibble pairs
+__device__ __forceinline__ void decode8(uint32_t w, __half2 (&c)[4]) {
   const __half2 bias = u32_as_h2(0x64086408u);        // 1032
   const __half2 sixteenth = u32_as_h2(0x2C002C00u), m72 = u32_as_h2(0xD480D480u);
   const uint32_t w8 = w >> 8, magic = 0x64006400u;
-  uint4 r;
-  r.x = h2_as_u32(__hmul2(__hsub2(u32_as_h2(lop3_and_or(w, 0x000F000Fu, magic)), bias), d));
-  r.y = h2_as_u32(__hmul2(__hfma2(u32_as_h2(lop3_and_or(w, 0x00F000F0u, magic)), sixteenth, m72), d));
-  r.z = h2_as_u32(__hmul2(__hsub2(u32_as_h2(lop3_and_or(w8, 0x000F000Fu, magic)), bias), d));
-  r.w = h2_as_u32(__hmul2(__hfma2(u32_as_h2(lop3_and_or(w8, 0x00F000F0u, magic)), sixteenth, m72), d));
-  return r;
+  c[0] = __hsub2(u32_as_h2(lop3_and_or(w, 0x000F000Fu, magic)), bias);
+  c[1] = __hfma2(u32_as_h2(lop3_and_or(w, 0x00F000F0u, magic)), sixteenth, m72);
+  c[2] = __hsub2(u32_as_h2(lop3_and_or(w8, 0x000F000Fu, magic)), bias);
+  c[3] = __hfma2(u32_as_h2(lop3_and_or(w8, 0x00F000F0u, magic)), sixteenth, m72);
 }
+__device__ __forceinline__ uint4 times(const __half2 (&c)[4], __half2 d) {
+  return make_uint4(h2_as_u32(__hmul2(c[0], d)), h2_as_u32(__hmul2(c[1], d)), h2_as_u32(__hmul2(c[2], d)),
+                    h2_as_u32(__hmul2(c[3], d)));
+}
+// The first 8 significant bits of a scale: (c - 8) times them is exact in fp16, and so is (c - 8) times the
+// rest.  (Cut, not rounded: 8 * 8188 must not pass the largest fp16.)
+__device__ __forceinline__ __half2 scale_top(__half2 d) { return u32_as_h2(h2_as_u32(d) & 0xFFF8FFF8u); }
 
 __device__ __forceinline__ void sts_u128(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -210,6 +216,21 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
     v[0] = x.x; v[1] = x.y;
   }
 }
+
+// Rounding K to fp16 moves a score by about 2^-12 of itself.  Over many tokens that averages out, but where
+// a row sees few of them its lse and weights carry it (rel. 4e-5 in the lse of a 17-token prompt).  There K is
+// taken as two exact fp16 products, with the scale's top 8 bits and with the rest, and Q K^T as two sums; the
+// second one takes the K half of a second decoded buffer.
+// (7 prompts up to 3001 tokens, 12 heads of 64: 160 us with it, 143 us without.)
+constexpr int kFineTokens = 1024;
+__device__ __forceinline__ bool is_fine(const AttnParams& p, const Item& it) {
+  return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;
+}
+
+// Two sums for a score, and half the decoded buffers: such a tile takes about twice as long.
+struct TcWeight {
+  __device__ __forceinline__ static int of(const AttnParams& p, const Item& it) { return is_fine(p, it) ? 2 : 1; }
+};
 
 // The tiles [a, b) of the item's [ta, tb) that row tile i sees anything of: a causal item's first row
 // tile is done before its last one, and rows behind the item's end see nothing.
@@ -237,7 +258,7 @@ template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
   using B = KvBlk<D>;
-  using Wk = Walk<C::ROWS, C::TT, kItemCost>;
+  using Wk = Walk<C::ROWS, C::TT, kItemCost, TcWeight>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
   constexpr int LPR = D / 8, RPI = 32 / LPR, QB = D == 64 ? 8 : 4;   // rows to and from the warps
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -259,7 +280,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 
   Wk::template sum_units<C::NTH>(p, pre);
   const int64_t U = pre[C::NTH];
-  const int N = (int)min((int64_t)gridDim.x, U);
+  // shares of two units at least: none inside an item is without a tile
+  const int N = (int)min((int64_t)gridDim.x, U / 2);
   const TcWs ws = tc_ws(p.ws);
   if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x >= N) return;
@@ -538,7 +560,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         if (from_start && !to_end && threadIdx.x == 0)
           ws.desc[blockIdx.x] = make_int4(
               it.r, it.h, it.row0,
-              ((share_of(Wk::last_unit(it, iu), N, U) - (int)blockIdx.x) << 1) | slot);
+              ((share_of(Wk::last_unit(p, it, iu), N, U) - (int)blockIdx.x) << 1) | slot);
         if (!whole) slot = 1;
       }
     }
@@ -559,13 +581,15 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
          more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
       int tok0 = (it.t0 + ta) * TT;
-      for (int j = ta; j < tb && ok; ++j, ++gt, tok0 += TT) {
+      const bool fine = is_fine(p, it);
+      for (int j = ta; j < tb && ok; ++j, tok0 += TT) {
         const bool inner = tok0 >= it.begin && tok0 + TT <= it.end;
-        const int buf = gt % C::KVS;
+        const int buf = gt % C::KVS, buf2 = (gt + 1) % C::KVS;
         if (gt >= C::KVS) ok = mbar_wait(&kv_empty[buf], (gt / C::KVS - 1) & 1);
+        if (fine && ok && gt + 1 >= C::KVS) ok = mbar_wait(&kv_empty[buf2], ((gt + 1) / C::KVS - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t kb = ks + buf * C::KV_BUF, vb = vs + buf * C::KV_BUF;
+        const uint32_t kb = ks + buf * C::KV_BUF, kb2 = ks + buf2 * C::KV_BUF, vb = vs + buf * C::KV_BUF;
         // every load of the tile's two pieces before the first store: one warp per scheduler decodes, so
         // its latencies have to overlap
         int sn = st + 1, sn_phase = st_phase;
@@ -585,46 +609,63 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           keep[pc][0] = inner || (at >= it.begin && at < it.end) ? 0xFFFFFFFFu : 0u;
           keep[pc][1] = inner || (at + 1 >= it.begin && at + 1 < it.end) ? 0xFFFFFFFFu : 0u;
         }
+        auto decode = [&](auto fine_c) {
+          constexpr bool FINE = decltype(fine_c)::value;
 #pragma unroll
-        for (int gh = 0; gh < GH; ++gh) {
-          uint32_t kw[2][W], kd[2][W / 2], vw[2][W], vx[2][W / 2], vy[2][W / 2];
+          for (int gh = 0; gh < GH; ++gh) {
+            uint32_t kw[2][W], kd[2][W / 2], vw[2][W], vx[2][W / 2], vy[2][W / 2];
 #pragma unroll
-          for (int pc = 0; pc < 2; ++pc) {
-            lds_words<W>(rb[pc] + ((gh * 16 + ktok) * 4 + t) * W * 4, kw[pc]);
-            if (W == 4) {
-              const uint2 x = lds_u64(rb[pc] + B::OFF_KD + 2 * (ktok * G + gh * W));
-              kd[pc][0] = x.x;
-              kd[pc][W / 2 - 1] = x.y;
-            } else {
-              kd[pc][0] = lds_u32(rb[pc] + B::OFF_KD + 2 * ktok * G);
+            for (int pc = 0; pc < 2; ++pc) {
+              lds_words<W>(rb[pc] + ((gh * 16 + ktok) * 4 + t) * W * 4, kw[pc]);
+              if (W == 4) {
+                const uint2 x = lds_u64(rb[pc] + B::OFF_KD + 2 * (ktok * G + gh * W));
+                kd[pc][0] = x.x;
+                kd[pc][W / 2 - 1] = x.y;
+              } else {
+                kd[pc][0] = lds_u32(rb[pc] + B::OFF_KD + 2 * ktok * G);
+              }
+              lds_words<W>(rb[pc] + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, vw[pc]);
+#pragma unroll
+              for (int k = 0; k < W / 2; ++k) {
+                const int g = gh * W + 2 * k;
+                vx[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g) * 4 + half * 2) * 2);
+                vy[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g + 1) * 4 + half * 2) * 2);
+              }
             }
-            lds_words<W>(rb[pc] + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, vw[pc]);
 #pragma unroll
-            for (int k = 0; k < W / 2; ++k) {
-              const int g = gh * W + 2 * k;
-              vx[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g) * 4 + half * 2) * 2);
-              vy[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g + 1) * 4 + half * 2) * 2);
+            for (int pc = 0; pc < 2; ++pc) {
+              const uint32_t row_b = pc * kPiece * 128;      // 32 rows of 128 bytes
+#pragma unroll
+              for (int i = 0; i < W; ++i) {
+                const uint32_t word = odd ? kw[pc][i ^ 1] : kw[pc][i];
+                const __half2 dd = u32_as_h2(__byte_perm(kd[pc][i / 2], 0, k_sel[i & 1]));
+                const uint32_t at = row_b + (gh * W + i) / 2 * (TT * 128) + k_at[i & 1];
+                __half2 c[4];
+                decode8(word, c);
+                if (FINE) {
+                  const __half2 top = scale_top(dd);
+                  sts_u128(kb + at, times(c, top));
+                  sts_u128(kb2 + at, times(c, __hsub2(dd, top)));
+                } else {
+                  sts_u128(kb + at, times(c, dd));
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < W / 2; ++k) {
+                const __half2 d0 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x5410) & keep[pc][0]);
+                const __half2 d1 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x7632) & keep[pc][1]);
+                const uint32_t at = vb + row_b + (gh * (W / 2) + k) * (TT * 128);
+                __half2 c[4];
+                decode8(vw[pc][k], c);
+                sts_u128(at + v_at[0], times(c, d0));
+                decode8(vw[pc][W / 2 + k], c);
+                sts_u128(at + v_at[1], times(c, d1));
+              }
             }
           }
-#pragma unroll
-          for (int pc = 0; pc < 2; ++pc) {
-            const uint32_t row_b = pc * kPiece * 128;      // 32 rows of 128 bytes
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const uint32_t word = odd ? kw[pc][i ^ 1] : kw[pc][i];
-              const __half2 dd = u32_as_h2(__byte_perm(kd[pc][i / 2], 0, k_sel[i & 1]));
-              sts_u128(kb + row_b + (gh * W + i) / 2 * (TT * 128) + k_at[i & 1], decode8(word, dd));
-            }
-#pragma unroll
-            for (int k = 0; k < W / 2; ++k) {
-              const __half2 d0 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x5410) & keep[pc][0]);
-              const __half2 d1 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x7632) & keep[pc][1]);
-              const uint32_t at = vb + row_b + (gh * (W / 2) + k) * (TT * 128);
-              sts_u128(at + v_at[0], decode8(vw[pc][k], d0));
-              sts_u128(at + v_at[1], decode8(vw[pc][W / 2 + k], d1));
-            }
-          }
-        }
+        };
+        if (fine) decode(std::true_type());
+        else decode(std::false_type());
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&raw_empty[st]);
@@ -638,6 +679,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         }
         fence_proxy_async_smem();
         mbar_arrive(&kv_full[buf]);
+        if (fine) mbar_arrive(&kv_full[buf2]);
+        gt += fine ? 2 : 1;
       }
     }
   } else {
@@ -703,10 +746,12 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const uint32_t s_i = tm + (uint32_t)(C::COL_S + i * 2 * TT);
       int gt = 0, ring = 0, seg = 0;         // tiles of this row tile, of the CTA; items
       // S of this row tile's tile g, which is the CTA's tile r; its buffer's last weights must have been used
-      auto scores = [&](int g, int r) {
-        const int par = g & 1, buf = r % C::KVS;
+      auto scores = [&](int g, int r, auto fine_c) {
+        constexpr bool FINE = decltype(fine_c)::value;
+        const int par = g & 1, buf = r % C::KVS, buf2 = (r + 1) % C::KVS;
         bool good = g < 2 || mbar_wait(&pv_done[i * 2 + par], ((g - 2) >> 1) & 1);
         good = good && mbar_wait(&kv_full[buf], (r / C::KVS) & 1);
+        if (FINE) good = good && mbar_wait(&kv_full[buf2], ((r + 1) / C::KVS) & 1);
         if (!__all_sync(0xffffffffu, good)) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -716,12 +761,20 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           for (int k = 0; k < D / 16; ++k)
             mma_ss(d, q_i + (k >> 2) * (16384 >> 4) + 2 * (k & 3), b + (k >> 2) * (TT * 128 >> 4) + 2 * (k & 3),
                    hi, id_s, k ? 1u : 0u);
+          if (FINE) {
+            const uint32_t b2 = k_lo + (uint32_t)(buf2 * (C::KV_BUF >> 4));
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(d, q_i + (k >> 2) * (16384 >> 4) + 2 * (k & 3), b2 + (k >> 2) * (TT * 128 >> 4) + 2 * (k & 3),
+                     hi, id_s, 1u);
+          }
           tc_commit(&s_full[i * 2 + par]);
         }
         __syncwarp();
         return true;
       };
-      auto weighted = [&](int g, int r, bool first) {
+      auto weighted = [&](int g, int r, bool first, auto fine_c) {
+        constexpr bool FINE = decltype(fine_c)::value;
         const int par = g & 1, buf = r % C::KVS;
         if (!__all_sync(0xffffffffu, mbar_wait(&p_full[i * 2 + par], (g >> 1) & 1))) return false;
         tc_fence_after();
@@ -733,6 +786,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
             mma_ts(o_i, a + 8 * k, b + k * (2048 >> 4), hi, id_o, (first && k == 0) ? 0u : 1u);
           tc_commit(&pv_done[i * 2 + par]);
           tc_commit(&kv_empty[buf]);
+          if (FINE) tc_commit(&kv_empty[(r + 1) % C::KVS]);
         }
         __syncwarp();
         return true;
@@ -748,19 +802,26 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
            more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
         int ra, rb;
         row_tile_range<TT>(p, it, i, ta, tb, ra, rb);
-        const int before = uniform(ra - ta), nt = uniform(rb - ra), behind = uniform(tb - rb);
-        for (int k = 0; k < before && ok; ++k) ok = pass(ring++);
-        if (nt > 0 && ok) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
-          ++seg;
-          ok = ok && scores(gt, ring);
-          if (nt > 1) ok = ok && scores(gt + 1, ring + 1);
-          for (int k = 0; k < nt && ok; ++k, ++gt, ++ring) {
-            ok = weighted(gt, ring, k == 0);
-            if (k + 2 < nt) ok = ok && scores(gt + 2, ring + 2);
+        auto item = [&](auto fine_c) {
+          constexpr int STEP = decltype(fine_c)::value ? 2 : 1;     // decoded buffers a tile takes
+          // scores run two tiles ahead of the weights, or one where two tiles' buffers are not there
+          constexpr int AHEAD = C::KVS >= 2 * STEP ? 2 : 1;
+          const int before = uniform(ra - ta) * STEP, nt = uniform(rb - ra), behind = uniform(tb - rb) * STEP;
+          for (int k = 0; k < before && ok; ++k) ok = pass(ring++);
+          if (nt > 0 && ok) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
+            ++seg;
+            ok = ok && scores(gt, ring, fine_c);
+            if (nt > 1 && AHEAD == 2) ok = ok && scores(gt + 1, ring + STEP, fine_c);
+            for (int k = 0; k < nt && ok; ++k, ++gt, ring += STEP) {
+              ok = weighted(gt, ring, k == 0, fine_c);
+              if (k + AHEAD < nt) ok = ok && scores(gt + AHEAD, ring + AHEAD * STEP, fine_c);
+            }
           }
-        }
-        for (int k = 0; k < behind && ok; ++k) ok = pass(ring++);
+          for (int k = 0; k < behind && ok; ++k) ok = pass(ring++);
+        };
+        if (is_fine(p, it)) item(std::true_type());
+        else item(std::false_type());
       }
       // no arrival is under way when the CTA ends
       if (ok && ring > 0) mbar_wait(&kv_empty[(ring - 1) % C::KVS], ((ring - 1) / C::KVS) & 1);
