@@ -14,8 +14,9 @@
 //   nibble by 2^-4 less; each 32-value group sums in its own accumulator, which starts
 //   at -8 sum(q) (the codes' offset) and is scaled by the group's d in fp32.
 //   V: d is a factor of the token, so it goes into the weights: per group
-//   P' = fp16(p) * d (one HMUL2 for two tokens), and the offset is one more product, of
-//   a constant -8 with P'.  O's even and odd values carry 2^-24 and 2^-20 to the end.
+//   P' = fp16(p) * d (one HMUL2 for two tokens).  The codes lose their offset before the product (one
+//   more addition per register: taking 8 sum(p') off the sums instead left 1e-7 of the largest scale in
+//   values whose own scales are small).  O's even and odd values carry 2^-24 and 2^-20 to the end.
 // * fp16 weights: p = 2^(s - M) with M = max - b, renewed only when a score passes
 //   M + b + 4, so p <= 2^(b + 4).  b = 10 while every V scale is below 2 (p' < 2^15), and
 //   -2 for good once one is not (p' <= 2^2 * 8188): no overflow, and weights down to
@@ -69,7 +70,7 @@ struct WarpState {
 template <int D>
 struct StreamCfg {
   // O (D / 4 registers), Q, its sums and the scores: 16 warps of 128 registers, 12 of 168 or 8 of 255.
-  // (attn of 64 requests, 576 MB, heads of 128: 12 warps with three tiles each 111.9 us, 16 with two 113.5.)
+  // (64 requests, 576 MB, heads of 128: 12 warps with three tiles each 111.9 us, 16 with two 113.5.)
   static constexpr int NW = D <= 64 ? 16 : D <= 128 ? 12 : 8;
   static constexpr int ROWS = 8;
   static constexpr int STG = kBlks * KvBlk<D>::BYTES;
@@ -109,6 +110,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+
+// Nibble n (0 or 1) of each half less 8, as fp16 subnormals in units of 2^-24 or 2^-20.
+__device__ __forceinline__ uint32_t less8(uint32_t w, int n) {
+  return n == 0 ? h2_as_u32(__hadd2(u32_as_h2(w & 0x000F000Fu), u32_as_h2(0x80088008u)))
+                : h2_as_u32(__hadd2(u32_as_h2(w & 0x00F000F0u), u32_as_h2(0x80808080u)));
 }
 
 // D = A B + C with C the same for both rows of a lane
@@ -480,13 +487,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
             const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(pt[0]), u32_as_h2(dv[g][0])));
             const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(pt[1]), u32_as_h2(dv[g][1])));
-            mma_16816_nv(o[g][0], z0 & 0x000F000Fu, z0 & 0x00F000F0u, z1 & 0x000F000Fu,
-                         z1 & 0x00F000F0u, b0, b1);
-            mma_16816_nv(o[g][1], y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu,
-                         y1 & 0x00F000F0u, b0, b1);
-            // the offset: -8 in each row's unit
-            mma_16816_nv(o[g][0], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
-            mma_16816_nv(o[g][1], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+            mma_16816_nv(o[g][0], less8(z0, 0), less8(z0, 1), less8(z1, 0), less8(z1, 1), b0, b1);
+            mma_16816_nv(o[g][1], less8(y0, 0), less8(y0, 1), less8(y1, 0), less8(y1, 1), b0, b1);
           }
         }
       }

@@ -328,6 +328,61 @@ def test_attention_v_scales_that_grow_along_the_row(dq, new, kv):
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("new,kv,H,n_kv,D", [
+    ([1], [40000], 4, 1, 128),                     # one item over every CTA of the streaming kernel
+    ([2, 1], [30011, 9000], 3, 1, 64),
+    ([1], [20000], 8, 1, 256),
+    ([70], [30000], 1, 1, 128),                    # and of the tensor-core kernel
+    ([300, 20], [6000, 9000], 1, 1, 64),
+    ([66], [9000], 2, 2, 256),
+])
+def test_attention_one_item_over_many_shares(dq, new, kv, H, n_kv, D):
+    c = Case(dq, 20, new, kv, H, n_kv, D, 64, "fp16")
+    out, lse = c.run(max_q_len=max(new))
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("B,rows,most", [(1000, 1, 40), (600, 2, 300), (3000, 1, 20), (8192, 1, 3), (700, 70, 75)])
+def test_attention_many_requests(dq, B, rows, most):
+    # many short requests, more of them than a CTA has threads: shares hold many items, warps none or several
+    rng = np.random.default_rng(B)
+    new = [int(n) for n in rng.integers(0, rows + 1, B)]
+    new[B // 2] = rows
+    kv = [int(n) for n in rng.integers(0, most + 1, B)]
+    c = Case(dq, 21, new, kv, 2, 1, 64, 16, "bf16")
+    out, lse = c.run(max_q_len=rows)
+    c.check(out, lse)
+    again, _ = c.run(max_q_len=rows)
+    assert torch.equal(out, again)
+
+
+def test_attention_rows_above_max_q_len_are_not_written(dq):
+    for most, new in ((2, [3, 2]), (70, [90, 65])):
+        c = Case(dq, 22, new, [200, 300], 2, 2, 64, 16, "fp16")
+        out = torch.full_like(c.q, 7.0)
+        lse = torch.full((sum(new), 2), 7.0, device="cuda")
+        c.run(max_q_len=most, out=out, lse=lse)
+        torch.cuda.synchronize()
+        rest = torch.arange(sum(new), device="cuda")
+        keep = (rest < new[0]) & (rest >= most)
+        assert (out[keep] == 7).all() and (lse[keep] == 7).all()
+        assert not (out[~keep] == 7).all(-1).any()
+        # request 1 has no row too many: its rows are right
+        full, fl = c.run(max_q_len=max(new))
+        assert torch.allclose(out[new[0]:].float(), full[new[0]:].float(), atol=2e-2)
+        assert torch.allclose(lse[new[0]:], fl[new[0]:], atol=1e-3)
+
+
+def test_attention_lse_of_few_tokens(dq):
+    # where rows see few tokens their lse carries no rounding of K: within 2^-18 (1 + |lse|), as fp32 sums give it
+    for new, kv, window in (([17] * 9, [17] * 9, 0), ([300], [300], 0), ([200], [4000], 100)):
+        c = Case(dq, 23, new, kv, 10, 2, 128, 16, "bf16")
+        out, lse = c.run(max_q_len=max(new), window=window)
+        _, rl, _, _ = kv_ref.attention(c.host, 16, 128, c.q64, c.start, kv, c.table, 128 ** -0.5, True, window, 2)
+        off = np.abs(lse.double().cpu().numpy() - rl)
+        assert (off <= 2.0 ** -18 * (1 + np.abs(rl))).all(), off.max()
+
+
 def test_attention_rows_outside_are_not_written(dq):
     c = Case(dq, 11, [2, 3], [50, 70], 8, 2, 128, 16, "fp16")
     q = torch.cat([c.q, torch.full((4, 8, 128), float("nan"), dtype=c.q.dtype, device="cuda")])
