@@ -94,6 +94,7 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
   // then a launch of its own beside it (one request of 45 rows among prompts: 11 us more as a stream).
   const bool many = (int64_t)a->max_q_len * p.group > kStreamRows;
   p.rows_above = 0;
+  p.alone = 0;
   p.rows_upto = many ? kStreamRows / 2 : kStreamRows;
   p.ws = (uint8_t*)ws;
   rc = launch_kv_stream(p, cache->head_dim, (cudaStream_t)stream);

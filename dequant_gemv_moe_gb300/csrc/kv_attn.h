@@ -24,6 +24,7 @@ struct AttnParams {
   float* lse;
   uint8_t* ws;
   int rows_above, rows_upto;   // the kernel looks after requests with rows_above < rows <= rows_upto
+  int alone;                   // streaming: 0, or every row tile has a CTA of its own, and a request this many
 };
 
 // few rows per K/V head (kv_attn_stream.cu)
@@ -122,6 +123,17 @@ struct Walk {
       it.len = kv_length(p, it.r);
     }
     range(p, it);
+  }
+  // Row tile i of all (request, row tile, K/V head) where every request takes the place of `per` row tiles.
+  __device__ __forceinline__ static bool nth(const AttnParams& p, int i, int per, Item& it) {
+    const int k = i / p.g.heads;
+    it.h = i - k * p.g.heads;
+    const int r = k / per;
+    it.row0 = (k - r * per) * ROWS;
+    request(p, r, it);
+    if (it.row0 >= it.qlen * p.group) return false;
+    range(p, it);
+    return true;
   }
   // The units before every of the block's NTH chunks of requests, pre[NTH] in all
   // (every thread of the block calls it).  The warps' sums lie behind them: NTH + 1 + NTH / 32

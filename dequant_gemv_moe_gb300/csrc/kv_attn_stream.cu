@@ -46,6 +46,15 @@ constexpr int kTile = 32;                 // tokens per unit
 constexpr int kBlks = kTile / kKvBlk;
 constexpr int kItemCost = 1;              // tiles' worth of starting and ending an item
 constexpr int kMaxCtas = 160;
+// Where the row tiles fit the GPU a CTA each, they may be left whole: no walk to find the shares and no
+// second launch, which take 4 to 5 us, but a warp has more tiles, at 1.2 us each (heads of 64), 1.3 (128) or
+// 1.8 (256).  Whole if it has at most this many more than equal shares would give it.  (Heads of 128, 8
+// row tiles: 977 tokens 9.2 us whole, 11.0 shared; 1500 tokens 11.0, 10.8; 4000 tokens 19.9, 11.9.  128 row tiles:
+// 977 tokens 9.6, 13.3; 2500 tokens 14.8, 16.6; 4000 tokens 20.1, 20.0.  Heads of 256, 64 row tiles: a window of 256
+// tokens 9.2, 12.0; of 1024 14.6, 13.9.)
+template <int D>
+constexpr int kAloneTiles = D == 256 ? 2 : 4;
+constexpr int kAloneMost = 10;             // and this many in all
 
 // what a warp did not finish
 struct Left {
@@ -160,23 +169,32 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
 
   using Wk = Walk<C::ROWS, kTile, kItemCost>;
   int* known = (int*)(smem + C::OFF_KNOWN);
-  Wk::template sum_units<C::NTH>(p, pre, known);
-  const int64_t U = pre[C::NTH];
   const StreamWs ws = stream_ws(p.ws);
-  // at least one unit per warp of the CTAs that take part
-  const int ctas = (int)min((int64_t)gridDim.x, (U + C::NW - 1) / C::NW);
-  if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (blockIdx.x >= ctas) return;
-  const int gw = blockIdx.x * C::NW + warp;
-  const int N = (int)min((int64_t)ctas * C::NW, U);     // every one of the N shares holds a unit
+  int64_t U;
+  int w0 = blockIdx.x * C::NW, N;          // the CTA's first share of N
+  Place x;
+  if (p.alone) {
+    if (!Wk::nth(p, blockIdx.x, p.alone, x.it)) return;
+    U = Wk::cost(p, x.it);
+    N = (int)min((int64_t)C::NW, U);
+    w0 = 0;
+  } else {
+    Wk::template sum_units<C::NTH>(p, pre, known);
+    U = pre[C::NTH];
+    // at least one unit per warp of the CTAs that take part
+    const int ctas = (int)min((int64_t)gridDim.x, (U + C::NW - 1) / C::NW);
+    if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (blockIdx.x >= ctas) return;
+    N = (int)min((int64_t)ctas * C::NW, U);             // every one of the N shares holds a unit
+  }
+  const int gw = w0 + warp;
   const int64_t u0 = share_start(U, N, min(gw, N)), u1 = share_start(U, N, min(gw + 1, N));
 
   // ---- the first item of the share, and its tiles [a, b) that lie in it
   WarpState& S = ((WarpState*)(smem + C::OFF_STATE))[warp];
   bool more = u0 < u1;
   if (more) {
-    Place x;
-    x.iu = Wk::template seek<C::NTH>(p, pre, u0, x.it, known);
+    x.iu = p.alone ? 0 : Wk::template seek<C::NTH>(p, pre, u0, x.it, known);
     more = Wk::here(p, x.it, x.iu, u0, u1, x.a, x.b);
     if (lane == 0) {
       S.at[0] = S.at[1] = x;
@@ -697,7 +715,7 @@ __global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_const
 }
 
 template <int D>
-int launch_stream(const AttnParams& p, int ctas, cudaStream_t s) {
+int launch_stream(AttnParams p, int ctas, cudaStream_t s) {
   using C = StreamCfg<D>;
   static bool attr[64] = {false};
   int dev = 0;
@@ -708,9 +726,19 @@ int launch_stream(const AttnParams& p, int ctas, cudaStream_t s) {
       return DQ_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
   }
-  if (launch_pdl(kv_stream_kernel<D>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) !=
+  // what a row tile sees: the table's tokens, or a window and the tokens of 8 rows
+  const int64_t tokens = std::min<int64_t>((int64_t)p.max_pages << p.g.page_shift,
+                                           p.window > 0 ? (int64_t)p.window + 7 : INT64_MAX);
+  const int64_t per = (std::min<int64_t>((int64_t)p.max_q_len * p.group, p.rows_upto) + C::ROWS - 1) / C::ROWS;
+  const int64_t items = per * p.B * p.g.heads;
+  const int64_t tiles = tokens / kTile + 2;
+  const bool alone = items <= ctas && tiles * (ctas - items) <= (int64_t)kAloneTiles<D> * C::NW * ctas &&
+                     tiles <= kAloneMost * C::NW;
+  p.alone = alone ? (int)per : 0;
+  if (launch_pdl(kv_stream_kernel<D>, dim3(alone ? (int)items : ctas), dim3(C::NTH), C::SMEM, s, 0, p) !=
       cudaSuccess)
     return DQ_ERR_CUDA;
+  if (alone) return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
   if (launch_pdl(kv_stream_join_kernel<D>, dim3(ctas), dim3(1024), 0, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
