@@ -11,21 +11,29 @@
 //   words; the output is put in order when it is stored.
 // * Q rows are scaled by a power of two into fp16 (exact but for values 2^-28
 //   below the row's largest); the factor comes back with the softmax's scale.
-// * M is a row's maximum less 8, renewed only when a score passes it by 12: fp16
-//   weights stay between 2^8 and 2^12 at the top, and O, which lives in tensor
-//   memory, is rescaled a few times per row at most.  Rounding K, V and p to
-//   fp16 (2^-11 each) is the price of 16-bit operands; S, M, the sum of p and O
-//   are fp32.
+// * M is a row's maximum less 8 when it is set, and set again only when the sum of
+//   a tile's weights passes 2^15: fp16 weights stay between 2^8 and 2^15 at the top, no
+//   maximum is taken of most tiles, and O, which lives in tensor memory, is rescaled a
+//   few times per row at most.  Rounding K, V and p to fp16 (2^-11 each) is the price of
+//   16-bit operands; S, M, the sum of p and O are fp32.
 //
-// Roles.  Warp groups of the row tiles do the softmax (a thread per row); four
+// Roles.  Warp groups of the row tiles do the softmax (a thread per row); eight
 // warps decode; one warp copies the pages' blocks (bulk copies, 32 tokens at a
-// time); one thread issues the products.  Every row tile has two score buffers, which
+// time); one warp per row tile issues its products.  Every row tile has two score buffers, which
 // take turns: while a row's thread works on one tile, the products of the one before
 // and the scores of the one after run.
 //
 // Work is shared as in kv_attn_stream.cu: the line of all (request, row tile,
 // head, token tile) units in equal shares, one per CTA, the partials of items
 // that cross shares joined in order by a second kernel.
+//
+// What bounds it: the instructions of the softmax (160 for 64 scores) and of the
+// decoding (13 for 8 values) beside each other on four schedulers that issue in 0.61 of
+// all cycles; the tensor pipe is busy in half of them.  2 requests' chunks of 2048 tokens
+// over up to 16384, 32 query heads on 8 of 128: 943 us, 1.24 PFLOP/s.  Left out for a
+// measurement, the decoding's arithmetic takes 15 % of the time, the exponentials none,
+// three quarters of the products 6 %.  Four warps decoding and 64 scores a thread at a time
+// take 966 us, two warps to a row 1088 (registers).
 #include <algorithm>
 #include <type_traits>
 
@@ -51,13 +59,13 @@ struct TcCfg {
   static constexpr int PIECE_B = kPiece / kKvBlk * KvBlk<D>::BYTES;
   static constexpr int RS = D == 64 ? 8 : D == 128 ? 6 : 3;
   static constexpr int OFF_PRE = 512;
-  static constexpr int OFF_Q = 5120;
+  static constexpr int OFF_Q = 6144;
   static constexpr int OFF_K = OFF_Q + NQ * Q_TILE;
   static constexpr int OFF_V = OFF_K + KVS * KV_BUF;
   static constexpr int OFF_RAW = OFF_V + KVS * KV_BUF;
   static constexpr int SMEM = OFF_RAW + RS * PIECE_B;
   static constexpr int DEC0 = 4 * NQ;                // first decoding warp
-  static constexpr int PROD = DEC0 + 4, MMA = DEC0 + 5;   // one warp of products per row tile
+  static constexpr int PROD = DEC0 + 8, MMA = DEC0 + 9;   // one warp of products per row tile
   static constexpr int NTH = 32 * (MMA + NQ);
   // tensor memory columns: O of every row tile, then two score buffers of each
   static constexpr int COL_S = NQ * D;
@@ -117,14 +125,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -221,7 +221,7 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
 // a row sees few of them its lse and weights carry it (rel. 4e-5 in the lse of a 17-token prompt).  There K is
 // taken as two exact fp16 products, with the scale's top 8 bits and with the rest, and Q K^T as two sums; the
 // second one takes the K half of a second decoded buffer.
-// (7 prompts up to 3001 tokens, 12 heads of 64: 160 us with it, 143 us without.)
+// (7 prompts up to 3001 tokens, 12 heads of 64: 160 us with it, 143 us without, the kernel of that time.)
 constexpr int kFineTokens = 1024;
 __device__ __forceinline__ bool is_fine(const AttnParams& p, const Item& it) {
   return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;
@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   int64_t* pre = (int64_t*)(smem + C::OFF_PRE);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
-  Wk::template sum_units<C::NTH>(p, pre);
+  int* known = (int*)(smem + C::OFF_Q);    // (Q comes after the walk's start)
+  static_assert(C::NTH * 12 <= NQ * C::Q_TILE, "shared memory");
+  Wk::template sum_units<C::NTH>(p, pre, known);
   const int64_t U = pre[C::NTH];
   // shares of two units at least: none inside an item is without a tile
   const int N = (int)min((int64_t)gridDim.x, U / 2);
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < C::KVS; ++i) {
-      mbar_init(&kv_full[i], 128);
+      mbar_init(&kv_full[i], 256);
       mbar_init(&kv_empty[i], NQ);
     }
     for (int i = 0; i < 4; ++i) {
@@ -317,9 +319,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
                  vs = smem_u32(smem + C::OFF_V);
 
   Item it;
-  int64_t iu = Wk::template seek<C::NTH>(p, pre, u0, it);
+  int64_t iu = Wk::template seek<C::NTH>(p, pre, u0, it, known);
   int ta, tb;                              // the tiles of the item that this share holds
   bool ok = true;
+  __syncthreads();
 
   if (warp < C::DEC0) {
     // ------------------------------ softmax ------------------------------
@@ -405,70 +408,94 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
-        uint32_t r[TT];
-        tmem_ld32(s_addr, r);
-        tmem_ld32(s_addr + 32, r + 32);
-        tmem_wait_ld();
-        tmem_use(r);
-        tmem_use(r + 32);
-        if (!(tok0 >= lo_all && tok0 + TT <= hi_all)) {
-          const int n = hi - tok0;
+        const bool inner = tok0 >= lo_all && tok0 + TT <= hi_all;
+        // 32 scores of this thread's row, those that it does not see as -inf
+        auto load = [&](int c, uint32_t (&r)[32]) {
+          tmem_ld32(s_addr + c, r);
+          tmem_wait_ld();
+          tmem_use(r);
+          if (!inner) {
+            const int n = hi - tok0 - c;
 #pragma unroll
-          for (int i = 0; i < TT; ++i) r[i] = i < n ? r[i] : 0xFF800000u;
-          if (p.window > 0) {
-            const int f = lo - tok0;
+            for (int i = 0; i < 32; ++i) r[i] = i < n ? r[i] : 0xFF800000u;
+            if (p.window > 0) {
+              const int f = lo - tok0 - c;
 #pragma unroll
-            for (int i = 0; i < TT; ++i) r[i] = i >= f ? r[i] : 0xFF800000u;
-          }
-        }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < TT; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx4[k] = max3(mx4[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * cf;
-        const bool over = mx > M + 12.f;
-        if (__any_sync(0xffffffffu, over)) {
-          const float mn = over ? mx - 8.f : M;
-          const float corr = ex2(M - mn);
-          M = mn;
-          l *= corr;
-          if (j > 0) {
-            // the product of the tile before may still be running
-            ok = mbar_wait(&pv_done[tile * 2 + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(o_addr + 32 * c, v);
-              tmem_wait_ld();
-              tmem_use(v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
-              tmem_st32(o_addr + 32 * c, v);
+              for (int i = 0; i < 32; ++i) r[i] = i >= f ? r[i] : 0xFF800000u;
             }
           }
-        }
-        const float2 cf2 = make_float2(cf, cf), m2 = make_float2(-M, -M);
-        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // the weights go over the scores, two to a column
+        };
+        uint32_t w[TT / 2];
+        float sum;
+        // The first tile sets M.  After that the sum of the weights tells whether M has to follow: while it
+        // is at most 2^15, so is every weight.  If it is not, the tile is done again with a new M.
+        for (bool renew = j == 0;; renew = true) {
+          if (renew) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < TT; c += 32) {
+              uint32_t r[32];
+              load(c, r);
+              float mx4[4] = {mx, mx, mx, mx};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[16];
+              for (int i = 0; i < 32; i += 8)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int k = 32 * c + 2 * i;
-            const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), cf2, m2);
-            const float2 e = make_float2(ex2(t.x), ex2(t.y));
-            l2[i & 1] = fadd2(l2[i & 1], e);
-            w[i] = h2_as_u32(__floats2half2_rn(e.x, e.y));
+                for (int k = 0; k < 4; ++k)
+                  mx4[k] = max3(mx4[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
+              mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            }
+            mx *= cf;
+            const float mn = mx > M + 9.f ? mx - 8.f : M;     // (at most M + 9: a sum of 64 2^9 at most)
+            const float corr = ex2(M - mn);
+            M = mn;
+            l *= corr;
+            if (j > 0) {
+              // the product of the tile before may still be running
+              ok = mbar_wait(&pv_done[tile * 2 + ((gt - 1) & 1)], ((gt - 1) >> 1) & 1);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32(o_addr + 32 * c, v);
+                tmem_wait_ld();
+                tmem_use(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
+                tmem_st32(o_addr + 32 * c, v);
+              }
+            }
           }
-          tmem_st16(s_addr + 16 * c, w);
+          const float2 cf2 = make_float2(cf, cf), m2 = make_float2(-M, -M);
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < TT; h += 32) {
+            uint32_t r[32];
+            load(h, r);
+            // in three passes over the registers: the exponentials' latencies overlap
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), cf2, m2);
+              r[k] = __float_as_uint(t.x);
+              r[k + 1] = __float_as_uint(t.y);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+r"(r[k]));
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 e = make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+              l2[(k >> 1) & 1] = fadd2(l2[(k >> 1) & 1], e);
+              w[(h + k) >> 1] = h2_as_u32(__floats2half2_rn(e.x, e.y));
+            }
+          }
+          sum = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+          if (renew || !__any_sync(0xffffffffu, sum > 32768.f)) break;
         }
-        l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+        if (!ok) break;
+        // the weights go over the scores, two to a column
+        tmem_st32(s_addr, w);
+        l += sum;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[sl]);
@@ -567,7 +594,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   } else if (warp < C::PROD) {
     // ------------------------------ decoding ------------------------------
     const int dw = warp - C::DEC0;
-    const int blk = dw >> 1, half = dw & 1;
+    const int pc = dw >> 2, blk = (dw >> 1) & 1, half = dw & 1;      // piece of the tile, block, its half
     // K: lane = (token, t); odd rows take their words in swapped order, so that 8 lanes' stores meet
     // 8 different chunks.  V: lane = (a, t): tokens 2t and 2t + 1 of the half block.
     const int r4 = lane >> 2, t = lane & 3;
@@ -577,7 +604,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint32_t k_sel[2] = {odd ? 0x3232u : 0x1010u, odd ? 0x1010u : 0x3232u};
     const uint32_t v_at[2] = {sw128_offset(vrow, r4), sw128_offset(vrow + 1, r4)};
     const uint32_t raw0 = smem_u32(smem + C::OFF_RAW) + blk * B::BYTES;
-    int gt = 0, st = 0, st_phase = 0;
+    int gt = 0, st = pc, st_phase = 0;     // every other stage is this warp's
     for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
          more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
       int tok0 = (it.t0 + ta) * TT;
@@ -590,91 +617,77 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t kb = ks + buf * C::KV_BUF, kb2 = ks + buf2 * C::KV_BUF, vb = vs + buf * C::KV_BUF;
-        // every load of the tile's two pieces before the first store: one warp per scheduler decodes, so
-        // its latencies have to overlap
-        int sn = st + 1, sn_phase = st_phase;
-        if (sn == C::RS) {
-          sn = 0;
-          sn_phase ^= 1;
-        }
-        ok = mbar_wait(&raw_full[st], st_phase) && mbar_wait(&raw_full[sn], sn_phase);
+        ok = mbar_wait(&raw_full[st], st_phase);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t rb[2] = {raw0 + st * C::PIECE_B, raw0 + sn * C::PIECE_B};
-        uint32_t keep[2][2];
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-          // a token that no row sees may hold anything: its V scale becomes 0
-          const int at = tok0 + pc * kPiece + vrow;
-          keep[pc][0] = inner || (at >= it.begin && at < it.end) ? 0xFFFFFFFFu : 0u;
-          keep[pc][1] = inner || (at + 1 >= it.begin && at + 1 < it.end) ? 0xFFFFFFFFu : 0u;
-        }
+        const uint32_t rb = raw0 + st * C::PIECE_B;
+        // a token that no row sees may hold anything: its V scale becomes 0
+        const int at0 = tok0 + pc * kPiece + vrow;
+        const uint32_t keep = (at0 >= it.begin && at0 < it.end ? 0x0000FFFFu : 0u) |
+                              (at0 + 1 >= it.begin && at0 + 1 < it.end ? 0xFFFF0000u : 0u);
+        const uint32_t row_b = pc * kPiece * 128;          // 32 rows of 128 bytes
         auto decode = [&](auto fine_c) {
           constexpr bool FINE = decltype(fine_c)::value;
 #pragma unroll
           for (int gh = 0; gh < GH; ++gh) {
-            uint32_t kw[2][W], kd[2][W / 2], vw[2][W], vx[2][W / 2], vy[2][W / 2];
+            uint32_t kw[W], kd[W / 2], vw[W], vx[W / 2], vy[W / 2];
+            lds_words<W>(rb + ((gh * 16 + ktok) * 4 + t) * W * 4, kw);
+            if (W == 4) {
+              const uint2 x = lds_u64(rb + B::OFF_KD + 2 * (ktok * G + gh * W));
+              kd[0] = x.x;
+              kd[W / 2 - 1] = x.y;
+            } else {
+              kd[0] = lds_u32(rb + B::OFF_KD + 2 * ktok * G);
+            }
+            lds_words<W>(rb + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, vw);
 #pragma unroll
-            for (int pc = 0; pc < 2; ++pc) {
-              lds_words<W>(rb[pc] + ((gh * 16 + ktok) * 4 + t) * W * 4, kw[pc]);
-              if (W == 4) {
-                const uint2 x = lds_u64(rb[pc] + B::OFF_KD + 2 * (ktok * G + gh * W));
-                kd[pc][0] = x.x;
-                kd[pc][W / 2 - 1] = x.y;
-              } else {
-                kd[pc][0] = lds_u32(rb[pc] + B::OFF_KD + 2 * ktok * G);
-              }
-              lds_words<W>(rb[pc] + B::OFF_V + ((half * GH + gh) * 32 + lane) * 4 * W, vw[pc]);
+            for (int k = 0; k < W / 2; ++k) {
+              const int g = gh * W + 2 * k;
+              vx[k] = lds_u32(rb + B::OFF_VD + ((t * G + g) * 4 + half * 2) * 2);
+              vy[k] = lds_u32(rb + B::OFF_VD + ((t * G + g + 1) * 4 + half * 2) * 2);
+            }
+            if (!inner) {
 #pragma unroll
               for (int k = 0; k < W / 2; ++k) {
-                const int g = gh * W + 2 * k;
-                vx[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g) * 4 + half * 2) * 2);
-                vy[pc][k] = lds_u32(rb[pc] + B::OFF_VD + ((t * G + g + 1) * 4 + half * 2) * 2);
+                vx[k] &= keep;
+                vy[k] &= keep;
               }
             }
 #pragma unroll
-            for (int pc = 0; pc < 2; ++pc) {
-              const uint32_t row_b = pc * kPiece * 128;      // 32 rows of 128 bytes
-#pragma unroll
-              for (int i = 0; i < W; ++i) {
-                const uint32_t word = odd ? kw[pc][i ^ 1] : kw[pc][i];
-                const __half2 dd = u32_as_h2(__byte_perm(kd[pc][i / 2], 0, k_sel[i & 1]));
-                const uint32_t at = row_b + (gh * W + i) / 2 * (TT * 128) + k_at[i & 1];
-                __half2 c[4];
-                decode8(word, c);
-                if (FINE) {
-                  const __half2 top = scale_top(dd);
-                  sts_u128(kb + at, times(c, top));
-                  sts_u128(kb2 + at, times(c, __hsub2(dd, top)));
-                } else {
-                  sts_u128(kb + at, times(c, dd));
-                }
+            for (int i = 0; i < W; ++i) {
+              const uint32_t word = odd ? kw[i ^ 1] : kw[i];
+              const __half2 dd = u32_as_h2(__byte_perm(kd[i / 2], 0, k_sel[i & 1]));
+              const uint32_t at = row_b + (gh * W + i) / 2 * (TT * 128) + k_at[i & 1];
+              __half2 c[4];
+              decode8(word, c);
+              if (FINE) {
+                const __half2 top = scale_top(dd);
+                sts_u128(kb + at, times(c, top));
+                sts_u128(kb2 + at, times(c, __hsub2(dd, top)));
+              } else {
+                sts_u128(kb + at, times(c, dd));
               }
+            }
 #pragma unroll
-              for (int k = 0; k < W / 2; ++k) {
-                const __half2 d0 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x5410) & keep[pc][0]);
-                const __half2 d1 = u32_as_h2(__byte_perm(vx[pc][k], vy[pc][k], 0x7632) & keep[pc][1]);
-                const uint32_t at = vb + row_b + (gh * (W / 2) + k) * (TT * 128);
-                __half2 c[4];
-                decode8(vw[pc][k], c);
-                sts_u128(at + v_at[0], times(c, d0));
-                decode8(vw[pc][W / 2 + k], c);
-                sts_u128(at + v_at[1], times(c, d1));
-              }
+            for (int k = 0; k < W / 2; ++k) {
+              const __half2 d0 = u32_as_h2(__byte_perm(vx[k], vy[k], 0x5410));
+              const __half2 d1 = u32_as_h2(__byte_perm(vx[k], vy[k], 0x7632));
+              const uint32_t at = vb + row_b + (gh * (W / 2) + k) * (TT * 128);
+              __half2 c[4];
+              decode8(vw[k], c);
+              sts_u128(at + v_at[0], times(c, d0));
+              decode8(vw[W / 2 + k], c);
+              sts_u128(at + v_at[1], times(c, d1));
             }
           }
         };
         if (fine) decode(std::true_type());
         else decode(std::false_type());
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&raw_empty[st]);
-          mbar_arrive(&raw_empty[sn]);
-        }
-        st = sn + 1;
-        st_phase = sn_phase;
-        if (st == C::RS) {
-          st = 0;
+        if (lane == 0) mbar_arrive(&raw_empty[st]);
+        st += 2;
+        if (st >= C::RS) {
+          st -= C::RS;
           st_phase ^= 1;
         }
         fence_proxy_async_smem();
@@ -730,9 +743,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     }
     } else {
       // ------------------------------ products ------------------------------
-      // A warp per row tile, so that neither waits for the other's softmax.  The whole warp walks the loop, so that descriptors and addresses are uniform values (the
-      // instruction takes them from uniform registers: from one lane's own registers each of its
-      // operands is moved first, which took 70 cycles a product); one lane issues.
+      // A warp per row tile, so that neither waits for the other's softmax.  The whole warp walks the loop,
+      // so that descriptors and addresses are uniform values (the instruction takes them from uniform
+      // registers: from one lane's own registers each of its operands is moved first, which took 70 cycles a
+      // product); one lane issues.
       constexpr uint32_t id_s = idesc_f16_f32(128, TT);
       constexpr uint32_t id_o = idesc_f16_f32(128, D) | kBRowsAlongN;
       const uint32_t tm = (uint32_t)uniform((int)tmem);
@@ -836,57 +850,62 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 }
 
 // Joins the partials of the items that go over several CTAs' shares: the CTAs (c, y)
-// take the rows of the item that starts in CTA c's share and goes on behind it.
-constexpr int kJoinRows = 4;
+// take the rows of the item that starts in CTA c's share and goes on behind it, four
+// values of a row per thread.  Bound by latency (partials are in L2), so all of it runs at
+// once: kJoinRows rows a thread whose loads overlap, and few registers.  (7 prompts, 12
+// heads of 64: 12.5 us with a warp to a row and 87 registers, 6.6 us so.)
+constexpr int kJoinRows = 2;
+template <int D>
+constexpr int kJoinPass = 256 / (D / 4);   // rows a CTA takes at once
 
 template <int D>
-__global__ void __launch_bounds__(256) kv_tc_join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(256, 6) kv_tc_join_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
-  constexpr int V = D / 32;
   pdl_wait();
   pdl_trigger();
   const TcWs ws = tc_ws(p.ws);
   const int4 d = __ldcg(ws.desc + blockIdx.x);
   const int follow = d.w >> 1;
   if (follow == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int first;
   const int rows = min(C::ROWS, q_rows(p, d.x, &first) * p.group - d.z);
-  // kJoinRows rows at a time, so that their loads overlap
-  for (int c0 = (blockIdx.y * 8 + warp) * kJoinRows; c0 < rows; c0 += gridDim.y * 8 * kJoinRows) {
-    float m[kJoinRows], l[kJoinRows], acc[kJoinRows][V];
-    auto part = [&](int i, int k) -> int64_t {
-      return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? (d.w & 1) : 0)) * C::ROWS + min(c0 + k, rows - 1);
-    };
+  const int c = threadIdx.x % (D / 4), row0 = blockIdx.y * (kJoinPass<D> * kJoinRows) + threadIdx.x / (D / 4);
+  float m[kJoinRows], l[kJoinRows];
+  float4 acc[kJoinRows];
+#pragma unroll
+  for (int k = 0; k < kJoinRows; ++k) {
+    m[k] = kNone;
+    l[k] = 0.f;
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int i = 0; i <= follow; ++i) {
+    const int64_t part = ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? (d.w & 1) : 0)) * C::ROWS + row0;
 #pragma unroll
     for (int k = 0; k < kJoinRows; ++k) {
-      m[k] = kNone;
-      l[k] = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
+      const int64_t at = part + k * kJoinPass<D>;        // (a row behind the item's last is read and not used)
+      const float2 ml = __ldcg(ws.ml + at);
+      const float4 x = __ldcg((const float4*)(ws.o + at * D) + c);
+      const float mn = fmaxf(m[k], ml.x), f0 = ex2(m[k] - mn), f1 = ex2(ml.x - mn);
+      m[k] = mn;
+      l[k] = l[k] * f0 + ml.y * f1;
+      acc[k].x = acc[k].x * f0 + x.x * f1;
+      acc[k].y = acc[k].y * f0 + x.y * f1;
+      acc[k].z = acc[k].z * f0 + x.z * f1;
+      acc[k].w = acc[k].w * f0 + x.w * f1;
     }
-    for (int i = 0; i <= follow; ++i) {
+  }
 #pragma unroll
-      for (int k = 0; k < kJoinRows; ++k) {
-        const int64_t at = part(i, k);
-        const float2 ml = __ldcg(ws.ml + at);
-        float x[V];
-#pragma unroll
-        for (int v = 0; v < V; v += 2) {
-          const float2 y = __ldcg((const float2*)(ws.o + at * D + lane * V + v));
-          x[v] = y.x;
-          x[v + 1] = y.y;
-        }
-        const float mn = fmaxf(m[k], ml.x), f0 = ex2(m[k] - mn), f1 = ex2(ml.x - mn);
-        m[k] = mn;
-        l[k] = l[k] * f0 + ml.y * f1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[k][v] = acc[k][v] * f0 + x[v] * f1;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kJoinRows; ++k)
-      if (c0 + k < rows) store_row<D>(p, d.x, d.y, d.z + c0 + k, lane, acc[k], m[k], l[k]);
+  for (int k = 0; k < kJoinRows; ++k) {
+    const int in = row0 + k * kJoinPass<D>;
+    if (in >= rows) continue;
+    const int row = d.z + in, tokq = row_token(p, row), uq = row - tokq * p.group;
+    const int64_t qrow = first + tokq;
+    const int head = d.y * p.group + uq;
+    const float inv = l[k] > 0.f ? 1.f / l[k] : 0.f;
+    const float x[4] = {acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv};
+    store_out4(p, qrow * p.out_stride + (int64_t)head * D + 4 * c, x);
+    if (c == 0 && p.lse) p.lse[qrow * p.n_q_heads + head] = l[k] > 0.f ? (m[k] + log2f(l[k])) * kLn2 : -INFINITY;
   }
 }
 
@@ -904,7 +923,7 @@ int launch_tc(const AttnParams& p, int ctas, cudaStream_t s) {
   }
   if (launch_pdl(kv_tc_kernel<D>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
-  if (launch_pdl(kv_tc_join_kernel<D>, dim3(ctas, C::ROWS / (8 * kJoinRows)), dim3(256), 0, s, 0, p) != cudaSuccess)
+  if (launch_pdl(kv_tc_join_kernel<D>, dim3(ctas, C::ROWS / (kJoinPass<D> * kJoinRows)), dim3(256), 0, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }
