@@ -135,6 +135,11 @@ constexpr int kRowsUnroll = 2;   // chunks per thread, their loads all in flight
 // fastest: a group of 32 values is four lanes.  K's eight values are a word of its
 // layout; for V two lanes whose groups are neighbours exchange halves of their
 // units, so that each stores one word too.
+//
+// Bound by latency for a step (64 tokens, 8 heads of 128: 2.7 us) and by issue for a
+// prompt (8191 tokens, bf16: 13 us, 43 MB at 3.3 TB/s; issue slots 61 % busy, ALU most).  1, 2
+// and 4 chunks a thread take 25.4, 23.1 and 22.5 us with the reading back, and four leave a
+// step on too few CTAs.  K and V are different CTAs: with both in one thread it was 31 us.
 template <int D, int DT, bool V>
 __device__ __forceinline__ void append_rows(const KvRows& p) {
   using B = KvBlk<D>;
@@ -182,6 +187,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv_append_kernel(const __grid_co
   else append_rows<D, DT, false>(p);
 }
 
+// The way back, by the same chunks: the codes' words are gathered, whole rows are written.
+// (8191 tokens, 8 heads of 128, bf16: 10.5 us, 43 MB at 4.1 TB/s.)
 template <int D, int DT, bool V>
 __device__ __forceinline__ void read_rows(const KvRows& p) {
   using B = KvBlk<D>;
@@ -308,6 +315,9 @@ __device__ __forceinline__ int find_last(const int* first, int n, int x) {
 // then share the tokens, the popped and the pushed pages among them.  A page
 // that is pushed and popped by one call is found through the request that
 // returns it, never through the stack: no CTA reads what another writes.
+//
+// Bound by the latency of one launch and a few dependent loads: 48 requests of one token
+// each 3.9 us in a graph, 1000 requests with prompts and finished ones 7.0 us.
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_constant__ PlanParams p) {
   extern __shared__ int sm[];
   __shared__ int part[32][3];
