@@ -152,7 +152,7 @@ struct Walk {
       if (r < p.B) request(p, r, it);
       else it.qlen = it.len = it.first = 0;
       // a request of few row tiles by its thread, one of many by the warp
-      const bool few = (int64_t)it.qlen * p.group <= 4 * ROWS;
+      const bool few = (int64_t)it.qlen * p.group <= 8 * ROWS;
       if (few) u += row_tile_units(p, it, 0, 1) * p.g.heads;
       for (uint32_t m = __ballot_sync(0xffffffffu, !few); m; m &= m - 1) {
         const int src = __ffs(m) - 1;

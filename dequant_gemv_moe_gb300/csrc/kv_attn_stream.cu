@@ -651,15 +651,18 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
 // Joins the partials of the items that go over several CTAs' shares.  CTA c
 // looks after the item that starts in CTA c of the kernel above and goes on behind
 // it; a warp takes a row and one of kSub interleaved shares of its partials.  Bound by latency:
-// 3 to 4 us behind the kernel above.
-constexpr int kSub = 4;
+// about 3 us behind the kernel above, whose CTAs leave no room for these before they end, so small CTAs
+// start sooner: a kernel behind an empty join waits 3.6 us less for 2 shares than for 4.
+// (Heads of 256, with four values more per lane, are joined 0.5 us sooner by 4.)
+template <int D>
+constexpr int kSub = D == 256 ? 4 : 2;
 
 template <int D>
-__global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(256 * kSub<D>) kv_stream_join_kernel(const __grid_constant__ AttnParams p) {
   using C = StreamCfg<D>;
   constexpr int G = D / 32;                // values of a row per lane
-  __shared__ float acc_s[8][kSub][D];
-  __shared__ float2 ml_s[8][kSub];
+  __shared__ float acc_s[8][kSub<D>][D];
+  __shared__ float2 ml_s[8][kSub<D>];
   pdl_wait();
   pdl_trigger();
   const StreamWs ws = stream_ws(p.ws);
@@ -675,25 +678,24 @@ __global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_const
   auto part = [&](int i) -> int64_t {
     return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::ROWS + col;
   };
+  // The loads wait for nothing but the descriptor (a row behind the item's last is read and not used).
   float m = kNone, l = 0.f, acc[G];
 #pragma unroll
   for (int v = 0; v < G; ++v) acc[v] = 0.f;
-  if (live) {
-    for (int i = sub + kSub * lane; i <= follow; i += kSub * 32) m = fmaxf(m, __ldcg(ws.ml + part(i)).x);
+#pragma unroll (G > 4 ? 2 : 4)
+  for (int i = sub; i <= follow; i += kSub<D>) {
+    const int64_t at = part(i);
+    const float2 ml = __ldcg(ws.ml + at);
+    float2 x[G / 2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll 4
-    for (int i = sub; i <= follow; i += kSub) {
-      const int64_t at = part(i);
-      const float2 ml = __ldcg(ws.ml + at);
-      const float f = ex2(ml.x - m);
-      l = fmaf(ml.y, f, l);
+    for (int v = 0; v < G / 2; ++v) x[v] = __ldcg((const float2*)(ws.o + at * D + lane * G) + v);
+    const float mn = fmaxf(m, ml.x), f0 = ex2(m - mn), f1 = ex2(ml.x - mn);
+    m = mn;
+    l = l * f0 + ml.y * f1;
 #pragma unroll
-      for (int v = 0; v < G; v += 2) {
-        const float2 x = __ldcg((const float2*)(ws.o + at * D + lane * G + v));
-        acc[v] = fmaf(x.x, f, acc[v]);
-        acc[v + 1] = fmaf(x.y, f, acc[v + 1]);
-      }
+    for (int v = 0; v < G / 2; ++v) {
+      acc[2 * v] = acc[2 * v] * f0 + x[v].x * f1;
+      acc[2 * v + 1] = acc[2 * v + 1] * f0 + x[v].y * f1;
     }
   }
 #pragma unroll
@@ -703,11 +705,11 @@ __global__ void __launch_bounds__(1024) kv_stream_join_kernel(const __grid_const
   __syncthreads();
   if (sub == 0 && live) {
     float mt = kNone, lt = 0.f, x[G];
-    for (int k = 0; k < kSub; ++k) mt = fmaxf(mt, ml_s[col][k].x);
+    for (int k = 0; k < kSub<D>; ++k) mt = fmaxf(mt, ml_s[col][k].x);
 #pragma unroll
     for (int v = 0; v < G; ++v) x[v] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kSub; ++k) {
+    for (int k = 0; k < kSub<D>; ++k) {
       const float f = ex2(ml_s[col][k].x - mt);
       lt = fmaf(ml_s[col][k].y, f, lt);
 #pragma unroll
@@ -746,7 +748,7 @@ int launch_stream(AttnParams p, int ctas, cudaStream_t s) {
       cudaSuccess)
     return DQ_ERR_CUDA;
   if (alone) return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
-  if (launch_pdl(kv_stream_join_kernel<D>, dim3(ctas), dim3(1024), 0, s, 0, p) != cudaSuccess)
+  if (launch_pdl(kv_stream_join_kernel<D>, dim3(ctas), dim3(256 * kSub<D>), 0, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }

@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 // take the rows of the item that starts in CTA c's share and goes on behind it, four
 // values of a row per thread.  Bound by latency (partials are in L2), so all of it runs at
 // once: kJoinRows rows a thread whose loads overlap, and few registers.  (7 prompts, 12
-// heads of 64: 12.5 us with a warp to a row and 87 registers, 6.6 us so.)
+// heads of 64: 12.5 us with a warp to a row and 87 registers, @J2@ us so.)
 constexpr int kJoinRows = 2;
 template <int D>
 constexpr int kJoinPass = 256 / (D / 4);   // rows a CTA takes at once
