@@ -54,13 +54,18 @@ constexpr int kItemCost = 1;              // tiles' worth of starting and ending
 constexpr int kMaxCtas = 160;
 // Where the row tiles fit the GPU a CTA each, they may be left whole: no walk to find the shares and no
 // second launch, which take 4 to 5 us, but a warp has more tiles, at 1.2 us each (heads of 64), 1.3 (128) or
-// 1.8 (256).  Whole if it has at most this many more than equal shares would give it.  (Heads of 128, 8
-// row tiles: 977 tokens 9.2 us whole, 11.0 shared; 1500 tokens 11.0, 10.8; 4000 tokens 19.9, 11.9.  128 row tiles:
-// 977 tokens 9.6, 13.3; 2500 tokens 14.8, 16.6; 4000 tokens 20.1, 20.0.  Heads of 256, 64 row tiles: a window of 256
-// tokens 9.2, 12.0; of 1024 14.6, 13.9.)
+// 1.8 (256).  Where that would be more than 3 tiles, a row tile takes a cluster of 2 or 4 CTAs, whose
+// first one joins what the others leave (2 to 3 us, its launch included).  Whole if a warp has at most
+// kAloneTiles (half as many in a cluster) more than equal shares would give it.  Whole and in shares, us:
+//   heads of 128, 8 row tiles: 977 tokens 9.2, 11.0; 4000 tokens in fours 12.0, 12.0; 16000 tokens 23.0, 14.5
+//   64 row tiles: 1900 tokens in twos 11.8, 13.3; 4000 tokens 15.3, 15.4; 8000 tokens 22.3, 19.2
+//   128 row tiles: 977 tokens 9.6, 13.3; 2500 tokens 14.8, 16.6; 4000 tokens 20.1, 20.0
+//   heads of 256, 64 row tiles: a window of 256 tokens 9.4, 12.1; of 1024, in twos 13.2, 14.2
+//   heads of 64, 8 row tiles: 4000 tokens in twos 9.9, 11.1; 12000 tokens in fours 14.1, 12.7
 template <int D>
 constexpr int kAloneTiles = D == 256 ? 2 : 4;
 constexpr int kAloneMost = 10;             // and this many in all
+constexpr int kClusterCtas = 128;          // (not every SM is in reach of a whole cluster)
 
 // what a warp did not finish
 struct Left {
@@ -180,10 +185,11 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   int w0 = blockIdx.x * C::NW, N;          // the CTA's first share of N
   Place x;
   if (p.alone) {
-    if (!Wk::nth(p, blockIdx.x, p.alone, x.it)) return;
+    const int cl = (int)cluster_nctarank();             // CTAs of the row tile
+    if (!Wk::nth(p, blockIdx.x / cl, p.alone, x.it)) return;
     U = Wk::cost(p, x.it);
-    N = (int)min((int64_t)C::NW, U);
-    w0 = 0;
+    N = (int)min((int64_t)cl * C::NW, U);
+    w0 = (int)cluster_ctarank() * C::NW;
   } else {
     Wk::template sum_units<C::NTH>(p, pre, known);
     U = pre[C::NTH];
@@ -591,7 +597,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   const uint32_t head = __ballot_sync(0xffffffffu, fl & 1), open_head = __ballot_sync(0xffffffffu, (fl & 3) == 3),
                  tail = __ballot_sync(0xffffffffu, fl & 4);
   const uint32_t on = open_head & (head >> 1);
-  int job = 0;
+  int job = 0, begun = -1;                 // the warp whose second partial goes on behind this CTA
   for (uint32_t todo = (head & 1) | tail << 1; todo; todo &= todo - 1) {
     const int w = __ffs(todo) - 2;         // -1: the first warp's first partial, else warp w's second
     const Left& x = w < 0 ? left[0] : left[w * 2 + 1];
@@ -603,11 +609,12 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     const int n = run + (w < 0 ? 0 : 1);   // partials of the item in this CTA
     const bool open = more_here ? open_head >> (s0 + run - 1) & 1 : true;
     const bool whole = w >= 0 && !open;
+    if (w >= 0 && open) begun = w;
     auto part = [&](int i) -> const float* {
       return (const float*)(i == 0 && w >= 0 ? smem + C::OFF_RING + w * C::STAGES * C::STG
                                              : smem + C::OFF_HEAD + (w0 + i) * C::PART);
     };
-    if (open && w >= 0 && threadIdx.x == 0)
+    if (open && w >= 0 && !p.alone && threadIdx.x == 0)
       ws.desc[blockIdx.x] = make_int4(x.r, x.h, x.row0, share_of(x.last, N, U) / C::NW - (int)blockIdx.x);
     for (int col = 0; col < x.rows; ++col, ++job) {
       if (job % C::NW != warp) continue;
@@ -646,6 +653,37 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       }
     }
   }
+  // ---- a row tile's cluster: the first CTA joins what the others left, in their order
+  const int cl = p.alone ? (int)cluster_nctarank() : 1;
+  if (cl == 1) return;
+  if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, head & 1);
+  __syncwarp();
+  cluster_sync_all();
+  if (cluster_ctarank() != 0 || begun < 0) return;
+  const Left& x1 = left[begun * 2 + 1];
+  if (warp >= x1.rows) return;
+  const uint32_t have = __ballot_sync(0xffffffffu, lane > 0 && lane < cl && __ldcg(ws.desc + blockIdx.x + lane).w);
+  float m = kNone, sum = 0.f, acc[G];
+#pragma unroll
+  for (int v = 0; v < G; ++v) acc[v] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < cl; ++i) {
+    if (i > 0 && !(have >> i & 1)) continue;
+    const int64_t at = ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * C::ROWS + warp;
+    const float2 ml = __ldcg(ws.ml + at);
+    float2 y[G / 2];
+#pragma unroll
+    for (int v = 0; v < G / 2; ++v) y[v] = __ldcg((const float2*)(ws.o + at * D + lane * G) + v);
+    const float mn = fmaxf(m, ml.x), f0 = ex2(m - mn), f1 = ex2(ml.x - mn);
+    m = mn;
+    sum = sum * f0 + ml.y * f1;
+#pragma unroll
+    for (int v = 0; v < G / 2; ++v) {
+      acc[2 * v] = acc[2 * v] * f0 + y[v].x * f1;
+      acc[2 * v + 1] = acc[2 * v + 1] * f0 + y[v].y * f1;
+    }
+  }
+  store_row<D>(p, x1.r, x1.h, x1.row0 + warp, lane, acc, m, sum);
 }
 
 // Joins the partials of the items that go over several CTAs' shares.  CTA c
@@ -741,11 +779,14 @@ int launch_stream(AttnParams p, int ctas, cudaStream_t s) {
   const int64_t per = (std::min<int64_t>((int64_t)p.max_q_len * p.group, p.rows_upto) + C::ROWS - 1) / C::ROWS;
   const int64_t items = per * p.B * p.g.heads;
   const int64_t tiles = tokens / kTile + 2;
-  const bool alone = items <= ctas && tiles * (ctas - items) <= (int64_t)kAloneTiles<D> * C::NW * ctas &&
-                     tiles <= kAloneMost * C::NW;
+  int cl = 1;
+  while (cl < 4 && items * cl * 2 <= kClusterCtas && tiles > 3 * cl * C::NW) cl *= 2;
+  const int more = cl > 1 ? kAloneTiles<D> / 2 : kAloneTiles<D>;
+  const bool alone = items <= ctas && tiles * (ctas - items * cl) <= (int64_t)more * C::NW * cl * ctas &&
+                     tiles <= kAloneMost * C::NW * cl;
   p.alone = alone ? (int)per : 0;
-  if (launch_pdl(kv_stream_kernel<D>, dim3(alone ? (int)items : ctas), dim3(C::NTH), C::SMEM, s, 0, p) !=
-      cudaSuccess)
+  if (launch_pdl(kv_stream_kernel<D>, dim3(alone ? (int)items * cl : ctas), dim3(C::NTH), C::SMEM, s,
+                 alone && cl > 1 ? cl : 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   if (alone) return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
   if (launch_pdl(kv_stream_join_kernel<D>, dim3(ctas), dim3(256 * kSub<D>), 0, s, 0, p) != cudaSuccess)

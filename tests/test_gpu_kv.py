@@ -342,6 +342,28 @@ def test_attention_one_item_over_many_shares(dq, new, kv, H, n_kv, D):
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("longest", [20, 200, 900, 1500, 2500, 4500])
+@pytest.mark.parametrize("B,H,n_kv,D,rows,window", [
+    (1, 8, 2, 64, 1, 0), (3, 8, 8, 64, 1, 0), (1, 8, 2, 128, 1, 0), (5, 16, 4, 128, 2, 0), (7, 8, 8, 128, 1, 700),
+    (2, 9, 3, 256, 3, 0), (6, 4, 4, 256, 1, 300),
+])
+def test_attention_few_row_tiles(dq, B, H, n_kv, D, rows, window, longest):
+    # fewer row tiles than SMs: as the table's width and the window have it, each has a CTA, a cluster or shares;
+    # requests shorter than the table, of no tokens and of no rows among them
+    rng = np.random.default_rng(B * 1000 + longest)
+    new = [int(n) for n in rng.integers(0, rows + 1, B)]
+    kv = [int(n) for n in np.exp(rng.uniform(0, np.log(longest), B))]
+    new[0], kv[0] = rows, longest
+    if B > 2:
+        kv[1], new[1] = 0, 1
+        kv[2] = new[2] = rows
+    c = Case(dq, 23, new, kv, H, n_kv, D, 32, "fp16")
+    out, lse = c.run(max_q_len=rows, window=window)
+    c.check(out, lse, window=window)
+    again, _ = c.run(max_q_len=rows, window=window)
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("B,rows,most", [(1000, 1, 40), (600, 2, 300), (3000, 1, 20), (8192, 1, 3), (700, 70, 75)])
 def test_attention_many_requests(dq, B, rows, most):
     # many short requests, more of them than a CTA has threads: shares hold many items, warps none or several
