@@ -137,7 +137,7 @@ constexpr int kRowsUnroll = 2;   // chunks per thread, their loads all in flight
 // units, so that each stores one word too.
 //
 // Bound by latency for a step (64 tokens, 8 heads of 128: 2.7 us) and by issue for a
-// prompt (8191 tokens, bf16: 13 us, 43 MB at 3.3 TB/s; issue slots 61 % busy, ALU most).  1, 2
+// prompt (8191 tokens, bf16: 13 us, 43 MB at 3.3 TB/s; the ALU pipe 69 % busy).  1, 2
 // and 4 chunks a thread take 25.4, 23.1 and 22.5 us with the reading back, and four leave a
 // step on too few CTAs.  K and V are different CTAs: with both in one thread it was 31 us.
 template <int D, int DT, bool V>
