@@ -279,6 +279,7 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+constexpr float kLeastScale = 1.17549435e-38f;   // of a row's scores: times 0, a masked score would be NaN
 constexpr float kNone = -1e30f;           // the running maximum of a row that has seen nothing
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 

@@ -90,7 +90,7 @@ struct WarpState {
 template <int D>
 struct StreamCfg {
   // O (D / 4 registers), Q, its sums and the scores: 16 warps of 128 registers, 12 of 168 or 8 of 255.
-  // (64 requests, 576 MB, heads of 128: 12 warps with three tiles each 111.9 us, 16 with two 113.5.)
+  // (64 requests, 576 MB, heads of 128: 12 warps with three tiles each 107.3 us, 16 with two 112.3.)
   static constexpr int NW = D <= 64 ? 16 : D <= 128 ? 12 : 8;
   static constexpr int ROWS = 8;
   static constexpr int STG = kBlks * KvBlk<D>::BYTES;
@@ -312,8 +312,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
     const int e = mx > 0.f ? min(14 - ex, 100) : 0;
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-    const float c = p.scale * kLog2e * 16777216.f *
-                    __uint_as_float((uint32_t)(127 - e) << 23);
+    const float c = fmaxf(p.scale * kLog2e * 16777216.f * __uint_as_float((uint32_t)(127 - e) << 23),
+                          kLeastScale);
     float sum[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
             sts_u128(qrow + ch / 8 * 16384 + sw128_offset(tr, ch & 7), make_uint4(r4[0], r4[1], r4[2], r4[3]));
           }
         }
-        cf = p.scale * kLog2e / row_up(own);
+        cf = fmaxf(p.scale * kLog2e / row_up(own), kLeastScale);
         fence_proxy_async_smem();
         mbar_arrive(&q_full[tile]);
       }

@@ -405,6 +405,16 @@ def test_attention_lse_of_few_tokens(dq):
         assert (off <= 2.0 ** -18 * (1 + np.abs(rl))).all(), off.max()
 
 
+@pytest.mark.parametrize("new,kv", [([1] * 3, [900, 300, 5]), ([140, 1], [400, 300])])
+def test_attention_scores_that_vanish(dq, new, kv):
+    # a tiny scale on tiny rows: every visible token weighs the same, a masked one nothing
+    c = Case(dq, 24, new, kv, 4, 2, 128, 16, "bf16")
+    c.q = c.q * 2.0 ** -100
+    c.q64 = c.q64 * 2.0 ** -100
+    out, lse = c.run(max_q_len=max(new), scale=1e-25)
+    c.check(out, lse, scale=1e-25)
+
+
 def test_attention_rows_outside_are_not_written(dq):
     c = Case(dq, 11, [2, 3], [50, 70], 8, 2, 128, 16, "fp16")
     q = torch.cat([c.q, torch.full((4, 8, 128), float("nan"), dtype=c.q.dtype, device="cuda")])
