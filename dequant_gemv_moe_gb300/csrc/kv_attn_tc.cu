@@ -221,7 +221,7 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
 // a row sees few of them its lse and weights carry it (rel. 4e-5 in the lse of a 17-token prompt).  There K is
 // taken as two exact fp16 products, with the scale's top 8 bits and with the rest, and Q K^T as two sums; the
 // second one takes the K half of a second decoded buffer.
-// (7 prompts up to 3001 tokens, 12 heads of 64: 160 us with it, 143 us without, the kernel of that time.)
+// (7 prompts up to 3001 tokens, 12 heads of 64: 144 us with it, 133 us without.)
 constexpr int kFineTokens = 1024;
 __device__ __forceinline__ bool is_fine(const AttnParams& p, const Item& it) {
   return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;
