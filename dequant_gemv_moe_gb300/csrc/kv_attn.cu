@@ -73,7 +73,7 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
   p.q_dtype = a->q_dtype;
   p.n_q_heads = a->n_q_heads;
   p.group = a->n_q_heads / cache->n_kv_heads;
-  p.group_inv = p.group == 1 ? 0xFFFFFFFFu : (uint32_t)((1ULL << 32) / (uint32_t)p.group);
+  p.group_inv = group_inverse(p.group);
   p.T = a->T;
   p.B = a->B;
   p.q_start = a->q_start;

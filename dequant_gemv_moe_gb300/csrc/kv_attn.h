@@ -1,5 +1,7 @@
 // kv_attn.h — what the attention kernels over the 4-bit cache share: the call's
-// parameters and the workspace plan.
+// parameters, the workspace plan, and the arithmetic that cuts a call's work into
+// shares.  That arithmetic is host code too: tests/csrc/kv_walk.cu walks every
+// share of a call on the CPU.
 #pragma once
 
 #include "kv.cuh"
@@ -34,22 +36,36 @@ int launch_kv_stream(const AttnParams& p, int head_dim, cudaStream_t s);
 size_t kv_tc_workspace();
 int launch_kv_tc(const AttnParams& p, int head_dim, cudaStream_t s);
 
+#define DQ_HD __host__ __device__ __forceinline__
+
+DQ_HD int load_length(const int32_t* p) {
+#ifdef __CUDA_ARCH__
+  return __ldg(p);
+#else
+  return *p;
+#endif
+}
+
+inline uint32_t group_inverse(int group) {
+  return group == 1 ? 0xFFFFFFFFu : (uint32_t)((1ULL << 32) / (uint32_t)group);
+}
+
 // The token of row (token * group + head).  floor(row * floor(2^32 / g) / 2^32) is row / g or one less.
-__device__ __forceinline__ int row_token(const AttnParams& p, int row) {
-  const int t = (int)__umulhi((uint32_t)row, p.group_inv);
+DQ_HD int row_token(const AttnParams& p, int row) {
+  const int t = (int)((uint64_t)(uint32_t)row * p.group_inv >> 32);
   return row - t * p.group >= p.group ? t + 1 : t;
 }
 
 // the length of request r as the kernels read it
-__device__ __forceinline__ int kv_length(const AttnParams& p, int r) {
+DQ_HD int kv_length(const AttnParams& p, int r) {
   const int64_t cap = (int64_t)p.max_pages << p.g.page_shift;
-  return (int)min((int64_t)max(__ldg(p.kv_len + r), 0), cap);
+  return (int)min((int64_t)max(load_length(p.kv_len + r), 0), cap);
 }
-__device__ __forceinline__ int q_rows(const AttnParams& p, int r, int* first) {
-  const int a = __ldg(p.q_start + r);
+DQ_HD int q_rows(const AttnParams& p, int r, int* first) {
+  const int a = load_length(p.q_start + r);
   *first = a;
   // memory-safe whatever q_start holds
-  return a < 0 ? 0 : max(0, min(min(__ldg(p.q_start + r + 1), p.T) - a, p.max_q_len));
+  return a < 0 ? 0 : max(0, min(min(load_length(p.q_start + r + 1), p.T) - a, p.max_q_len));
 }
 
 
@@ -66,14 +82,14 @@ struct Item {
 // OV units before its tiles: what starting and ending one costs.  A tile takes one
 // unit, or WEIGHT::of(item).
 struct UnitWeight {
-  __device__ __forceinline__ static int of(const AttnParams&, const Item&) { return 1; }
+  DQ_HD static int of(const AttnParams&, const Item&) { return 1; }
 };
 template <int ROWS, int TILE, int OV, typename WEIGHT = UnitWeight>
 struct Walk {
-  __device__ __forceinline__ static int cost(const AttnParams& p, const Item& it) {
+  DQ_HD static int cost(const AttnParams& p, const Item& it) {
     return it.tiles * WEIGHT::of(p, it) + OV;
   }
-  __device__ __forceinline__ static void range(const AttnParams& p, Item& it) {
+  DQ_HD static void range(const AttnParams& p, Item& it) {
     const int shift = it.len - it.qlen;
     it.rows = min(ROWS, it.qlen * p.group - it.row0);
     const int lo = shift + row_token(p, it.row0), hi = shift + row_token(p, it.row0 + it.rows - 1);
@@ -83,14 +99,13 @@ struct Walk {
     it.tiles = it.end > it.begin ? (it.end + TILE - 1) / TILE - it.t0 : 1;
   }
   // the request's rows of q if this kernel looks after it, else 0
-  __device__ __forceinline__ static int tokens(const AttnParams& p, int r, int* first) {
+  DQ_HD static int tokens(const AttnParams& p, int r, int* first) {
     const int n = q_rows(p, r, first);
     const int64_t rows = (int64_t)n * p.group;
     return rows > p.rows_above && rows <= p.rows_upto ? n : 0;
   }
   // Request r.  `known`: rows, length and first row of q of every request, in shared memory, or null.
-  __device__ __forceinline__ static void request(const AttnParams& p, int r, Item& it,
-                                                 const int* known = nullptr) {
+  DQ_HD static void request(const AttnParams& p, int r, Item& it, const int* known = nullptr) {
     it.r = r;
     if (known) {
       it.qlen = known[3 * r];
@@ -102,7 +117,7 @@ struct Walk {
     }
   }
   // Units of the row tiles k, k + step, .. of the request in `it` (one head's).
-  __device__ __forceinline__ static int64_t row_tile_units(const AttnParams& p, Item& it, int k, int step) {
+  DQ_HD static int64_t row_tile_units(const AttnParams& p, Item& it, int k, int step) {
     int64_t u = 0;
     for (it.row0 = k * ROWS; it.row0 < it.qlen * p.group; it.row0 += step * ROWS) {
       range(p, it);
@@ -110,7 +125,7 @@ struct Walk {
     }
     return u;
   }
-  __device__ __forceinline__ static void next(const AttnParams& p, Item& it) {
+  DQ_HD static void next(const AttnParams& p, Item& it) {
     if (++it.h < p.g.heads) return;
     it.h = 0;
     it.row0 += ROWS;
@@ -125,7 +140,7 @@ struct Walk {
     range(p, it);
   }
   // Row tile i of all (request, row tile, K/V head) where every request takes the place of `per` row tiles.
-  __device__ __forceinline__ static bool nth(const AttnParams& p, int i, int per, Item& it) {
+  DQ_HD static bool nth(const AttnParams& p, int i, int per, Item& it) {
     const int k = i / p.g.heads;
     it.h = i - k * p.g.heads;
     const int r = k / per;
@@ -229,8 +244,8 @@ struct Walk {
   }
   // The tiles [a, b) of the item at unit iu that lie in the share [u0, u1); none: on to the next
   // item that has some.  False: the share holds no more.
-  __device__ __forceinline__ static bool here(const AttnParams& p, Item& it, int64_t& iu, int64_t u0,
-                                              int64_t u1, int& a, int& b) {
+  DQ_HD static bool here(const AttnParams& p, Item& it, int64_t& iu, int64_t u0, int64_t u1, int& a,
+                         int& b) {
     for (;;) {
       // tile t lies in the share that its first unit lies in
       const int w = WEIGHT::of(p, it);
@@ -247,30 +262,74 @@ struct Walk {
       next(p, it);
     }
   }
-  __device__ __forceinline__ static bool after(const AttnParams& p, Item& it, int64_t& iu, int64_t u0,
-                                               int64_t u1, int& a, int& b) {
+  DQ_HD static bool after(const AttnParams& p, Item& it, int64_t& iu, int64_t u0, int64_t u1, int& a,
+                          int& b) {
     iu += cost(p, it);
     if (iu >= u1) return false;
     next(p, it);
     return here(p, it, iu, u0, u1, a, b);
   }
   // the first unit of the item's last tile
-  __device__ __forceinline__ static int64_t last_unit(const AttnParams& p, const Item& it, int64_t iu) {
+  DQ_HD static int64_t last_unit(const AttnParams& p, const Item& it, int64_t iu) {
     return iu + OV + (int64_t)(it.tiles - 1) * WEIGHT::of(p, it);
   }
 };
 
 // The line of U units is cut into N <= U equal shares: share w is [floor(U w / N), floor(U (w + 1) / N)),
 // and unit u lies in share ceil((u + 1) N / U) - 1.
-__device__ __forceinline__ int64_t share_start(int64_t U, int N, int w) {
+DQ_HD int64_t share_start(int64_t U, int N, int w) {
   if (U < (1LL << 31)) {                   // 32-bit divisions: U w / N = (U / N) w + (U mod N) w / N
     const uint32_t q = (uint32_t)U / (uint32_t)N, r = (uint32_t)U - q * (uint32_t)N;
     return (int64_t)q * w + r * (uint32_t)w / (uint32_t)N;
   }
   return U * w / N;
 }
-__device__ __forceinline__ int share_of(int64_t u, int N, int64_t U) {
+DQ_HD int share_of(int64_t u, int N, int64_t U) {
   return (int)(((u + 1) * N + U - 1) / U - 1);
+}
+
+// Few rows: 8 rows and tiles of 32 tokens, a tile's worth for starting and ending an item.
+using StreamWalk = Walk<8, 32, 1>;
+
+// Rounding K to fp16 moves a score by about 2^-12 of itself.  Over many tokens that averages out, but where
+// a row sees few of them its lse and weights carry it (rel. 4e-5 in the lse of a 17-token prompt).  There K is
+// taken as two exact fp16 products, with the scale's top 8 bits and with the rest, and Q K^T as two sums; the
+// second one takes the K half of a second decoded buffer.
+// (7 prompts up to 3001 tokens, 12 heads of 64: 144 us with it, 133 us without.)
+constexpr int kFineTokens = 1024;
+DQ_HD bool is_fine(const AttnParams& p, const Item& it) {
+  return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;
+}
+
+// Two sums for a score, and half the decoded buffers: such a tile takes about twice as long.
+struct TcWeight {
+  DQ_HD static int of(const AttnParams& p, const Item& it) { return is_fine(p, it) ? 2 : 1; }
+};
+
+// Many rows: row tiles of 128 rows, two a CTA (one for head_dim 256), and tiles of 64 tokens; starting and
+// ending an item takes as long as four of them.
+constexpr int kTcTile = 64;
+template <int D>
+constexpr int kTcRowTiles = D == 256 ? 1 : 2;
+template <int D>
+using TcWalk = Walk<128 * kTcRowTiles<D>, kTcTile, 4, TcWeight>;
+// a line of U units is cut into this many shares, of two units at least: none inside an item is without a tile
+DQ_HD int tc_shares(int ctas, int64_t U) { return (int)min((int64_t)ctas, U / 2); }
+
+// The tiles [a, b) of the item's [ta, tb) that row tile i sees anything of: a causal item's first row
+// tile is done before its last one, a windowed item's last one starts behind its first one (with one head
+// to a K/V head two tiles behind, which may be behind tb), and rows behind the item's end see nothing.
+// ta <= a <= b <= tb, so that the tiles before, in and behind are the tb - ta that the share decodes.
+DQ_HD void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, int tb, int& a, int& b) {
+  a = b = ta;
+  const int last = min(it.rows, 128 * i + 128) - 1;
+  if (last < 128 * i) return;
+  const int shift = it.len - it.qlen;
+  const int end = p.causal ? min(it.len, shift + row_token(p, it.row0 + last) + 1) : it.len;
+  const int begin = p.window > 0 ? max(0, shift + row_token(p, it.row0 + 128 * i) - p.window + 1) : 0;
+  if (end <= begin) return;
+  a = min(tb, max(ta, begin / kTcTile - it.t0));
+  b = max(a, min(tb, (end + kTcTile - 1) / kTcTile - it.t0));
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -50,7 +50,6 @@ namespace {
 
 constexpr int kTile = 32;                 // tokens per unit
 constexpr int kBlks = kTile / kKvBlk;
-constexpr int kItemCost = 1;              // tiles' worth of starting and ending an item
 constexpr int kMaxCtas = 160;
 // Where the row tiles fit the GPU a CTA each, they may be left whole: no walk to find the shares and no
 // second launch, which take 4 to 5 us, but a warp has more tiles, at 1.2 us each (heads of 64), 1.3 (128) or
@@ -178,7 +177,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   pdl_wait();
   pdl_trigger();
 
-  using Wk = Walk<C::ROWS, kTile, kItemCost>;
+  using Wk = StreamWalk;
+  static_assert(C::ROWS == 8 && kTile == 32, "as StreamWalk has them");
   int* known = (int*)(smem + C::OFF_KNOWN);
   const StreamWs ws = stream_ws(p.ws);
   int64_t U;

@@ -46,12 +46,11 @@ namespace {
 
 constexpr int kMaxCtas = 160;
 constexpr int kPiece = 32;                 // tokens per copy stage
-constexpr int kItemCost = 4;               // tiles' worth of starting and ending an item
 
 template <int D>
 struct TcCfg {
-  static constexpr int NQ = D == 256 ? 1 : 2;        // 128-row tiles
-  static constexpr int TT = 64;                      // tokens per tile
+  static constexpr int NQ = kTcRowTiles<D>;          // 128-row tiles
+  static constexpr int TT = kTcTile;                 // tokens per tile
   static constexpr int KVS = D == 256 ? 2 : 4;   // decoded tiles
   static constexpr int ROWS = 128 * NQ;
   static constexpr int Q_TILE = 128 * D * 2;
@@ -217,37 +216,6 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
   }
 }
 
-// Rounding K to fp16 moves a score by about 2^-12 of itself.  Over many tokens that averages out, but where
-// a row sees few of them its lse and weights carry it (rel. 4e-5 in the lse of a 17-token prompt).  There K is
-// taken as two exact fp16 products, with the scale's top 8 bits and with the rest, and Q K^T as two sums; the
-// second one takes the K half of a second decoded buffer.
-// (7 prompts up to 3001 tokens, 12 heads of 64: 144 us with it, 133 us without.)
-constexpr int kFineTokens = 1024;
-__device__ __forceinline__ bool is_fine(const AttnParams& p, const Item& it) {
-  return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;
-}
-
-// Two sums for a score, and half the decoded buffers: such a tile takes about twice as long.
-struct TcWeight {
-  __device__ __forceinline__ static int of(const AttnParams& p, const Item& it) { return is_fine(p, it) ? 2 : 1; }
-};
-
-// The tiles [a, b) of the item's [ta, tb) that row tile i sees anything of: a causal item's first row
-// tile is done before its last one, and rows behind the item's end see nothing.
-template <int TT>
-__device__ __forceinline__ void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, int tb,
-                                               int& a, int& b) {
-  a = b = ta;
-  const int last = min(it.rows, 128 * i + 128) - 1;
-  if (last < 128 * i) return;
-  const int shift = it.len - it.qlen;
-  const int end = p.causal ? min(it.len, shift + row_token(p, it.row0 + last) + 1) : it.len;
-  const int begin = p.window > 0 ? max(0, shift + row_token(p, it.row0 + 128 * i) - p.window + 1) : 0;
-  if (end <= begin) return;
-  a = max(ta, begin / TT - it.t0);
-  b = max(a, min(tb, (end + TT - 1) / TT - it.t0));
-}
-
 // The power of two that brings a row's largest magnitude into [2^14, 2^15) (1 for a row of zeros).
 __device__ __forceinline__ float row_up(float mx) {
   const int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
@@ -258,7 +226,7 @@ template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
   using B = KvBlk<D>;
-  using Wk = Walk<C::ROWS, C::TT, kItemCost, TcWeight>;
+  using Wk = TcWalk<D>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
   constexpr int LPR = D / 8, RPI = 32 / LPR, QB = D == 64 ? 8 : 4;   // rows to and from the warps
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -282,8 +250,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   static_assert(C::NTH * 12 <= NQ * C::Q_TILE, "shared memory");
   Wk::template sum_units<C::NTH>(p, pre, known);
   const int64_t U = pre[C::NTH];
-  // shares of two units at least: none inside an item is without a tile
-  const int N = (int)min((int64_t)gridDim.x, U / 2);
+  const int N = tc_shares(gridDim.x, U);
   const TcWs ws = tc_ws(p.ws);
   if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x >= N) return;
@@ -337,7 +304,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
          more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
       const bool from_start = ta == 0, to_end = tb == it.tiles;
       int ra, rb;
-      row_tile_range<TT>(p, it, tile, ta, tb, ra, rb);
+      row_tile_range(p, it, tile, ta, tb, ra, rb);
       const int nt = rb - ra;              // tiles of this row tile
       // the row
       const int row = it.row0 + tile * 128 + trow;
@@ -815,7 +782,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
            more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
         int ra, rb;
-        row_tile_range<TT>(p, it, i, ta, tb, ra, rb);
+        row_tile_range(p, it, i, ta, tb, ra, rb);
         auto item = [&](auto fine_c) {
           constexpr int STEP = decltype(fine_c)::value ? 2 : 1;     // decoded buffers a tile takes
           // scores run two tiles ahead of the weights, or one where two tiles' buffers are not there

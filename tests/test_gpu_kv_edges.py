@@ -1,0 +1,50 @@
+"""dq_kv_attention where its work sharing is at its edges (-m gpu): windowed prompts.
+
+The bars are test_gpu_kv's.  Where no K is rounded (few rows, or rows that see at
+most 1024 tokens) the lse is held to what fp32 sums give: 2^-18 (1 + |lse|)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_ref
+from test_gpu_kv import Case, dq  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def definition(c, scale=None, causal=True, window=0):
+    return kv_ref.attention(c.host, c.ps, c.D, c.q64, c.start, c.kv, c.table, c.D ** -0.5 if scale is None else scale,
+                            causal, window, c.n_kv)
+
+
+def lse_is_exact(c, lse, **kw):
+    ref = definition(c, **kw)[1]
+    none = np.isneginf(ref)
+    got = lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(got), none)
+    ref, got = np.where(none, 0, ref), np.where(none, 0, got)
+    off = np.abs(got - ref)
+    assert (off <= 2.0 ** -18 * (1 + np.abs(ref))).all(), off.max()
+
+
+@pytest.mark.parametrize("new,kv,H,n_kv,D,window", [
+    ([300], [900], 8, 8, 128, 130),                # one head to a K/V head: an item's second row tile starts two tiles
+    ([2048], [2048], 8, 8, 128, 512),              # behind its first one
+    ([700, 129, 300], [700, 900, 310], 8, 8, 64, 42),
+    ([1000], [1500], 6, 6, 64, 1024),              # the widest window of exact scores
+    ([1300, 40], [2600, 2000], 5, 5, 64, 1100),    # and one beyond
+    ([900], [2500], 3, 3, 128, 2000),
+    ([513, 0, 257, 90], [513, 10, 2000, 60], 4, 4, 128, 1),
+    ([400, 333], [400, 800], 12, 6, 64, 77),
+    ([260, 300], [500, 300], 3, 3, 256, 65),
+])
+def test_windowed_prompts(dq, new, kv, H, n_kv, D, window):  # noqa: F811
+    c = Case(dq, 30, new, kv, H, n_kv, D, 16, "fp16")
+    out, lse = c.run(max_q_len=max(new), window=window)
+    torch.cuda.synchronize()
+    assert dq.device_status() == 0
+    c.check(out, lse, window=window)
+    if window <= 1024:
+        lse_is_exact(c, lse, window=window)
+    again, lse2 = c.run(max_q_len=max(new), window=window)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
