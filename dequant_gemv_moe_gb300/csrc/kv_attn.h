@@ -56,6 +56,12 @@ DQ_HD int row_token(const AttnParams& p, int row) {
   return row - t * p.group >= p.group ? t + 1 : t;
 }
 
+// The first position that a row at `pos` (below 0 where the cache starts behind it) sees.  The window may be
+// any positive int: pos - window is formed only where it is not negative.
+DQ_HD int first_seen(const AttnParams& p, int pos) {
+  return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
 // the length of request r as the kernels read it
 DQ_HD int kv_length(const AttnParams& p, int r) {
   const int64_t cap = (int64_t)p.max_pages << p.g.page_shift;
@@ -94,7 +100,7 @@ struct Walk {
     it.rows = min(ROWS, it.qlen * p.group - it.row0);
     const int lo = shift + row_token(p, it.row0), hi = shift + row_token(p, it.row0 + it.rows - 1);
     it.end = p.causal ? min(it.len, hi + 1) : it.len;
-    it.begin = p.window > 0 ? max(0, lo - p.window + 1) : 0;
+    it.begin = first_seen(p, lo);
     it.t0 = it.begin / TILE;
     it.tiles = it.end > it.begin ? (it.end + TILE - 1) / TILE - it.t0 : 1;
   }
@@ -326,7 +332,7 @@ DQ_HD void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, in
   if (last < 128 * i) return;
   const int shift = it.len - it.qlen;
   const int end = p.causal ? min(it.len, shift + row_token(p, it.row0 + last) + 1) : it.len;
-  const int begin = p.window > 0 ? max(0, shift + row_token(p, it.row0 + 128 * i) - p.window + 1) : 0;
+  const int begin = first_seen(p, shift + row_token(p, it.row0 + 128 * i));
   if (end <= begin) return;
   a = min(tb, max(ta, begin / kTcTile - it.t0));
   b = max(a, min(tb, (end + kTcTile - 1) / kTcTile - it.t0));

@@ -348,11 +348,11 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       const int lo_pos = it.len - it.qlen + row_token(p, it.row0);
       const int hi_pos = it.len - it.qlen + row_token(p, it.row0 + it.rows - 1);
       hi_all = p.causal ? min(it.len, lo_pos + 1) : it.len;
-      lo_all = p.window > 0 ? max(0, hi_pos - p.window + 1) : 0;
+      lo_all = first_seen(p, hi_pos);
       if (lane < C::ROWS) {
         const int pos = it.len - it.qlen + row_token(p, it.row0 + lane);
         S.hi[lane] = p.causal ? min(it.len, pos + 1) : it.len;
-        S.lo[lane] = p.window > 0 ? pos - p.window + 1 : 0;
+        S.lo[lane] = first_seen(p, pos);
       }
       __syncwarp();
     }

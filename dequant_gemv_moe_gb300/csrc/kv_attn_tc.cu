@@ -358,13 +358,13 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       }
       const int pos = it.len - it.qlen + tokq;
       const int hi = p.causal ? min(it.len, pos + 1) : it.len;
-      const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+      const int lo = first_seen(p, pos);
       int lo_all, hi_all;
       {
         const int pa = it.len - it.qlen + row_token(p, it.row0 + tile * 128);
         const int pb = it.len - it.qlen + row_token(p, it.row0 + min(it.rows, tile * 128 + 128) - 1);
         hi_all = p.causal ? min(it.len, pa + 1) : it.len;
-        lo_all = p.window > 0 ? max(0, pb - p.window + 1) : 0;
+        lo_all = first_seen(p, pb);
       }
       float M = kNone, l = 0.f;
       int tok0 = (it.t0 + ra) * TT;

@@ -214,6 +214,14 @@ Call prompts(Rng& g) {
   return c;
 }
 
+// windows up to the largest int ("no limit" to a caller), caches that start behind the requests' first rows
+Call wide_windows(Rng& g) {
+  Call c = prompts(g);
+  c.window = g() % 2 ? 2147483647 - upto(g, 0, 3000) : 2147483647;
+  for (int& n : c.kv) n = g() % 2 ? upto(g, 0, 40) : n;
+  return c;
+}
+
 void run(const char* mode, Rng& g) {
   if (!strcmp(mode, "prompts")) {
     const Call c = prompts(g);
@@ -221,6 +229,12 @@ void run(const char* mode, Rng& g) {
     many_rows<256>(c);
   } else if (!strcmp(mode, "few")) {
     Call c = prompts(g);
+    for (int& n : c.rows) n = n ? 1 + n % std::max(1, 64 / c.group) : 0;
+    few_rows(c);
+  } else if (!strcmp(mode, "wide_windows")) {
+    Call c = wide_windows(g);
+    many_rows<128>(c);
+    many_rows<256>(c);
     for (int& n : c.rows) n = n ? 1 + n % std::max(1, 64 / c.group) : 0;
     few_rows(c);
   } else {

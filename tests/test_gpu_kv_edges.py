@@ -1,4 +1,5 @@
-"""dq_kv_attention where its work sharing is at its edges (-m gpu): windowed prompts.
+"""dq_kv_attention where its work sharing is at its edges (-m gpu): windowed prompts,
+windows as large as an int.
 
 The bars are test_gpu_kv's.  Where no K is rounded (few rows, or rows that see at
 most 1024 tokens) the lse is held to what fp32 sums give: 2^-18 (1 + |lse|)."""
@@ -48,3 +49,21 @@ def test_windowed_prompts(dq, new, kv, H, n_kv, D, window):  # noqa: F811
         lse_is_exact(c, lse, window=window)
     again, lse2 = c.run(max_q_len=max(new), window=window)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("new,kv,H,n_kv,D", [
+    ([5, 8, 1], [2, 300, 77], 8, 8, 128),          # rows before the cache's first token
+    ([6, 6], [0, 3], 8, 2, 256),
+    ([300, 200], [90, 700], 4, 4, 64),
+    ([150], [20], 8, 2, 128),
+])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200])
+def test_window_of_any_int(dq, new, kv, H, n_kv, D, window):  # noqa: F811
+    c = Case(dq, 31, new, kv, H, n_kv, D, 16, "bf16")
+    out, lse = c.run(max_q_len=max(new), window=window)
+    torch.cuda.synchronize()
+    assert dq.device_status() == 0
+    c.check(out, lse)
+    lse_is_exact(c, lse)
+    plain, lse2 = c.run(max_q_len=max(new))
+    assert torch.allclose(out.float(), plain.float(), atol=2e-2) and torch.allclose(lse, lse2, atol=1e-4)
