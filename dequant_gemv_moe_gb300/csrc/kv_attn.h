@@ -62,6 +62,13 @@ DQ_HD int first_seen(const AttnParams& p, int pos) {
   return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
+// The entry of a request's row of the block table that lists the token `ahead` tokens behind the start of a
+// tile (ahead below 1024), or -1.  A token behind the last that a table can list may pass the largest int.
+DQ_HD int listed_page(const AttnParams& p, int tile, int tile_tokens, int ahead) {
+  const uint32_t page = ((uint32_t)tile * tile_tokens + ahead) >> p.g.page_shift;
+  return page < (uint32_t)p.max_pages ? (int)page : -1;
+}
+
 // the length of request r as the kernels read it
 DQ_HD int kv_length(const AttnParams& p, int r) {
   const int64_t cap = (int64_t)p.max_pages << p.g.page_shift;
@@ -102,7 +109,7 @@ struct Walk {
     it.end = p.causal ? min(it.len, hi + 1) : it.len;
     it.begin = first_seen(p, lo);
     it.t0 = it.begin / TILE;
-    it.tiles = it.end > it.begin ? (it.end + TILE - 1) / TILE - it.t0 : 1;
+    it.tiles = it.end > it.begin ? (it.end - 1) / TILE + 1 - it.t0 : 1;
   }
   // the request's rows of q if this kernel looks after it, else 0
   DQ_HD static int tokens(const AttnParams& p, int r, int* first) {
@@ -241,7 +248,10 @@ struct Walk {
           it.row0 = row0 + l * ROWS;
           range(p, it);
           const int each = cost(p, it);
-          it.h = (int)((uint32_t)(u - iu) / (uint32_t)each);
+          // the heads in front of u (of 1024 at most, whose units may pass 32 bits), 32 at a time
+          int h = 31 - __clz(__ballot_sync(0xffffffffu, (int64_t)(32 * lane) * each <= u - iu));
+          h = 32 * h + 31 - __clz(__ballot_sync(0xffffffffu, (int64_t)(32 * h + lane) * each <= u - iu));
+          it.h = h;
           return iu + (int64_t)it.h * each;
         }
         iu += __shfl_sync(0xffffffffu, inc, 31);
@@ -335,7 +345,7 @@ DQ_HD void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, in
   const int begin = first_seen(p, shift + row_token(p, it.row0 + 128 * i));
   if (end <= begin) return;
   a = min(tb, max(ta, begin / kTcTile - it.t0));
-  b = max(a, min(tb, (end + kTcTile - 1) / kTcTile - it.t0));
+  b = max(a, min(tb, (end - 1) / kTcTile + 1 - it.t0));
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -240,12 +240,12 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     if (used == 32) {
       used = 0;
       const Item& x = S.at[1].it;
-      const int tok = (x.t0 + pt) * kTile + lane * (kTile / runs);
-      const int pg = tok >> p.g.page_shift;
-      int page = pg < p.max_pages ? __ldg(p.table + (int64_t)x.r * p.max_pages + pg) : 0;
+      const int ahead = lane * (kTile / runs);
+      const int pg = listed_page(p, x.t0 + pt, kTile, ahead);
+      int page = pg >= 0 ? __ldg(p.table + (int64_t)x.r * p.max_pages + pg) : 0;
       if (page < 0 || page >= p.g.n_pages) page = 0;
-      src = p.g.pages + (int64_t)page * p.g.page_bytes + x.h * p.g.head_bytes +
-            (tok & (p.g.page_size - 1)) / kKvBlk * B::BYTES;
+      const uint32_t in_page = ((uint32_t)(x.t0 + pt) * kTile + ahead) & (p.g.page_size - 1);
+      src = p.g.pages + (int64_t)page * p.g.page_bytes + x.h * p.g.head_bytes + in_page / kKvBlk * B::BYTES;
     }
     if (lane == 0) mbar_arrive_expect_tx(&bars[stage], C::STG);
     __syncwarp();
@@ -358,13 +358,13 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     }
 
     const int tb = S.at[0].b;
-    int tok0 = (it.t0 + S.at[0].a) * kTile;
-    for (int tl = S.at[0].a; tl < tb; ++tl, tok0 += kTile) {
+    for (int tl = S.at[0].a; tl < tb; ++tl) {
+      const int tok0 = (it.t0 + tl) * kTile;
       ok = ok && mbar_wait(&bars[stage], phase);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t base = smem_u32(ring + stage * C::STG);
-      const bool inner = tok0 >= lo_all && tok0 + kTile <= hi_all;
+      const bool inner = tok0 >= lo_all && tok0 <= hi_all - kTile;
 
       // ---- scores
       float s[kBlks][4];

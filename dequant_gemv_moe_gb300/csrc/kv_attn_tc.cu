@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       row_tile_range(p, it, tile, ta, tb, ra, rb);
       const int nt = rb - ra;              // tiles of this row tile
       // the row
-      const int row = it.row0 + tile * 128 + trow;
       const bool live = tile * 128 + trow < it.rows;
+      const int row = it.row0 + min(tile * 128 + trow, it.rows - 1);   // (the last row again behind it)
       const int tokq = row_token(p, row), uq = row - tokq * p.group;
       const int64_t q_at = it.first + tokq;
       const int head = it.h * p.group + uq;
@@ -361,21 +361,21 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const int lo = first_seen(p, pos);
       int lo_all, hi_all;
       {
-        const int pa = it.len - it.qlen + row_token(p, it.row0 + tile * 128);
+        const int pa = it.len - it.qlen + row_token(p, it.row0 + min(it.rows - 1, tile * 128));
         const int pb = it.len - it.qlen + row_token(p, it.row0 + min(it.rows, tile * 128 + 128) - 1);
         hi_all = p.causal ? min(it.len, pa + 1) : it.len;
         lo_all = first_seen(p, pb);
       }
       float M = kNone, l = 0.f;
-      int tok0 = (it.t0 + ra) * TT;
-      for (int j = 0; j < nt; ++j, ++gt, tok0 += TT) {
+      for (int j = 0; j < nt; ++j, ++gt) {
+        const int tok0 = (it.t0 + ra + j) * TT;
         const int sl = tile * 2 + (gt & 1);
         ok = ok && mbar_wait(&s_full[sl], (gt >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
-        const bool inner = tok0 >= lo_all && tok0 + TT <= hi_all;
+        const bool inner = tok0 >= lo_all && tok0 <= hi_all - TT;
         // 32 scores of this thread's row, those that it does not see as -inf
         auto load = [&](int c, uint32_t (&r)[32]) {
           tmem_ld32(s_addr + c, r);
@@ -574,10 +574,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     int gt = 0, st = pc, st_phase = 0;     // every other stage is this warp's
     for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
          more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
-      int tok0 = (it.t0 + ta) * TT;
       const bool fine = is_fine(p, it);
-      for (int j = ta; j < tb && ok; ++j, tok0 += TT) {
-        const bool inner = tok0 >= it.begin && tok0 + TT <= it.end;
+      for (int j = ta; j < tb && ok; ++j) {
+        const int tok0 = (it.t0 + j) * TT;
+        const bool inner = tok0 >= it.begin && tok0 <= it.end - TT;
         const int buf = gt % C::KVS, buf2 = (gt + 1) % C::KVS;
         if (gt >= C::KVS) ok = mbar_wait(&kv_empty[buf], (gt / C::KVS - 1) & 1);
         if (fine && ok && gt + 1 >= C::KVS) ok = mbar_wait(&kv_empty[buf2], ((gt + 1) / C::KVS - 1) & 1);

@@ -185,7 +185,14 @@ void few_rows(const Call& c) {
   if (U == 0) return;
   for (const Placed& x : items) check_item(c, x.it, 32);
   const int N = (int)std::min<int64_t>((int64_t)c.ctas * 12, U);
-  walk<Wk>(c, q.p, U, N, items, [](const Item&, int, int, int) {});
+  walk<Wk>(c, q.p, U, N, items, [&](const Item& it, int, int tb, int) {
+    // the page of every run that is looked up ahead of a share's last tile
+    for (int ahead = 0; ahead < 1024; ahead += 16) {
+      const int64_t page = ((int64_t)(it.t0 + tb - 1) * 32 + ahead) / c.page_size;
+      const int got = listed_page(q.p, it.t0 + tb - 1, 32, ahead);
+      CHECK(got == (page < c.max_pages ? page : -1), "page %d for %lld of %d", got, (long long)page, c.max_pages);
+    }
+  });
 }
 
 using Rng = std::mt19937_64;
@@ -222,6 +229,20 @@ Call wide_windows(Rng& g) {
   return c;
 }
 
+// lengths up to the last that a block table can list, and so many heads that an item's units pass 32 bits
+Call long_caches(Rng& g) {
+  Call c = prompts(g);
+  c.max_pages = 2147483647 / c.page_size;
+  const int most = c.max_pages * c.page_size;
+  for (int& n : c.kv) n = g() % 4 == 0 ? upto(g, 0, 3000) : 2147483647 - upto(g, 0, 2000);
+  c.window = g() % 3 == 0 ? 0 : g() % 3 == 0 ? upto(g, 1, 2147483647) : upto(g, 1, 100000);
+  if (g() % 2) c.heads = upto(g, 900, 1024);
+  for (int& n : c.kv) n = std::min(n, most);
+  for (int& n : c.rows) n = std::min(n, c.heads > 8 ? 40 : 600);
+  c.rows[0] = std::max(c.rows[0], 16);
+  return c;
+}
+
 void run(const char* mode, Rng& g) {
   if (!strcmp(mode, "prompts")) {
     const Call c = prompts(g);
@@ -235,6 +256,11 @@ void run(const char* mode, Rng& g) {
     Call c = wide_windows(g);
     many_rows<128>(c);
     many_rows<256>(c);
+    for (int& n : c.rows) n = n ? 1 + n % std::max(1, 64 / c.group) : 0;
+    few_rows(c);
+  } else if (!strcmp(mode, "long_caches")) {
+    Call c = long_caches(g);
+    many_rows<128>(c);
     for (int& n : c.rows) n = n ? 1 + n % std::max(1, 64 / c.group) : 0;
     few_rows(c);
   } else {

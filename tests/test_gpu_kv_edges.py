@@ -1,5 +1,5 @@
 """dq_kv_attention where its work sharing is at its edges (-m gpu): windowed prompts,
-windows as large as an int.
+windows as large as an int, lengths as large as a table can list.
 
 The bars are test_gpu_kv's.  Where no K is rounded (few rows, or rows that see at
 most 1024 tokens) the lse is held to what fp32 sums give: 2^-18 (1 + |lse|)."""
@@ -67,3 +67,26 @@ def test_window_of_any_int(dq, new, kv, H, n_kv, D, window):  # noqa: F811
     lse_is_exact(c, lse)
     plain, lse2 = c.run(max_q_len=max(new))
     assert torch.allclose(out.float(), plain.float(), atol=2e-2) and torch.allclose(lse, lse2, atol=1e-4)
+
+
+@pytest.mark.parametrize("new,kv,H,n_kv,D,ps", [
+    ([1], [688], 8, 1, 64, 16),                    # the table's last token
+    ([7], [681], 4, 2, 128, 16),
+    ([1, 3], [768, 700], 2, 1, 256, 256),
+    ([150], [688], 2, 1, 64, 16),
+    ([130, 200], [768, 755], 1, 1, 128, 256),
+])
+def test_the_last_tokens_that_a_table_can_list(dq, new, kv, H, n_kv, D, ps):  # noqa: F811
+    # the requests' pages stand at the end of rows that list 2^31 - page_size tokens; the window keeps to them
+    c = Case(dq, 32, new, kv, H, n_kv, D, ps, "fp16")
+    width = (2 ** 31 - 1) // ps
+    pages = -(-max(kv) // ps)
+    table = torch.full((len(new), width), -1, dtype=torch.int32, device="cuda")
+    table[:, width - pages:] = torch.tensor(c.table[:, :pages], dtype=torch.int32, device="cuda")
+    kv_len = torch.tensor([(width - pages) * ps + n for n in kv], dtype=torch.int32, device="cuda")
+    start = torch.tensor(c.start, dtype=torch.int32, device="cuda")
+    out, lse = dq.kv_attention(c.cache, c.q, start, kv_len, table, window=90, max_q_len=max(new))
+    torch.cuda.synchronize()
+    assert dq.device_status() == 0
+    c.check(out, lse, window=90)
+    lse_is_exact(c, lse, window=90)
