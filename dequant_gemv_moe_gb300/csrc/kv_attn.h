@@ -74,18 +74,24 @@ DQ_HD int kv_length(const AttnParams& p, int r) {
   const int64_t cap = (int64_t)p.max_pages << p.g.page_shift;
   return (int)min((int64_t)max(load_length(p.kv_len + r), 0), cap);
 }
-DQ_HD int q_rows(const AttnParams& p, int r, int* first) {
-  const int a = load_length(p.q_start + r);
+// The rows of request r that are looked after, and how many it has in all (at least as many: rows past
+// max_q_len and past T are left out, the others stand where they stand).
+DQ_HD int q_rows(const AttnParams& p, int r, int* first, int* all) {
+  const int a = load_length(p.q_start + r), b = load_length(p.q_start + r + 1);
   *first = a;
+  *all = a >= 0 && b > a ? b - a : 0;
   // memory-safe whatever q_start holds
-  return a < 0 ? 0 : max(0, min(min(load_length(p.q_start + r + 1), p.T) - a, p.max_q_len));
+  return a < 0 ? 0 : max(0, min(min(b, p.T) - a, p.max_q_len));
 }
+// A row at `pos` sees the positions below this one.
+DQ_HD int seen_end(const AttnParams& p, int len, int pos) { return p.causal ? max(0, min(len, pos + 1)) : len; }
 
 
 // One row tile of a request and the tokens that its rows may see.
 struct Item {
   int r, h, row0, rows;        // request, K/V head, first row (token * group + head), rows
   int len, qlen, first;        // kv length, tokens of the request, its first row of q
+  int shift;                   // position of its first token
   int begin, end;              // tokens that some row sees
   int t0, tiles;               // first tile, tiles (at least one)
 };
@@ -103,30 +109,33 @@ struct Walk {
     return it.tiles * WEIGHT::of(p, it) + OV;
   }
   DQ_HD static void range(const AttnParams& p, Item& it) {
-    const int shift = it.len - it.qlen;
     it.rows = min(ROWS, it.qlen * p.group - it.row0);
-    const int lo = shift + row_token(p, it.row0), hi = shift + row_token(p, it.row0 + it.rows - 1);
-    it.end = p.causal ? min(it.len, hi + 1) : it.len;
+    const int lo = it.shift + row_token(p, it.row0), hi = it.shift + row_token(p, it.row0 + it.rows - 1);
+    it.end = seen_end(p, it.len, hi);
     it.begin = first_seen(p, lo);
     it.t0 = it.begin / TILE;
     it.tiles = it.end > it.begin ? (it.end - 1) / TILE + 1 - it.t0 : 1;
   }
   // the request's rows of q if this kernel looks after it, else 0
-  DQ_HD static int tokens(const AttnParams& p, int r, int* first) {
-    const int n = q_rows(p, r, first);
+  DQ_HD static int tokens(const AttnParams& p, int r, int* first, int* all) {
+    const int n = q_rows(p, r, first, all);
     const int64_t rows = (int64_t)n * p.group;
     return rows > p.rows_above && rows <= p.rows_upto ? n : 0;
   }
-  // Request r.  `known`: rows, length and first row of q of every request, in shared memory, or null.
+  // Request r.  `known`: rows, length, first row of q and first position of every request, in shared
+  // memory, or null.
   DQ_HD static void request(const AttnParams& p, int r, Item& it, const int* known = nullptr) {
     it.r = r;
     if (known) {
-      it.qlen = known[3 * r];
-      it.len = known[3 * r + 1];
-      it.first = known[3 * r + 2];
+      it.qlen = known[4 * r];
+      it.len = known[4 * r + 1];
+      it.first = known[4 * r + 2];
+      it.shift = known[4 * r + 3];
     } else {
-      it.qlen = tokens(p, r, &it.first);
+      int all;
+      it.qlen = tokens(p, r, &it.first, &all);
       it.len = kv_length(p, r);
+      it.shift = it.len - all;
     }
   }
   // Units of the row tiles k, k + step, .. of the request in `it` (one head's).
@@ -144,11 +153,13 @@ struct Walk {
     it.row0 += ROWS;
     if (it.row0 >= it.qlen * p.group) {
       it.row0 = 0;
+      int all;
       do {
         if (++it.r >= p.B) return;       // past the last unit: never read
-        it.qlen = tokens(p, it.r, &it.first);
+        it.qlen = tokens(p, it.r, &it.first, &all);
       } while (it.qlen == 0);
       it.len = kv_length(p, it.r);
+      it.shift = it.len - all;
     }
     range(p, it);
   }
@@ -167,7 +178,7 @@ struct Walk {
   // (every thread of the block calls it).  The warps' sums lie behind them: NTH + 1 + NTH / 32
   // entries, in the caller's dynamic shared memory (static shared memory in front of it would
   // shift it off the alignment that swizzled operands need).
-  // `known` (3 NTH ints, may be null) is filled where every thread has one request at most.
+  // `known` (4 NTH ints, may be null) is filled where every thread has one request at most.
   template <int NTH>
   __device__ __forceinline__ static void sum_units(const AttnParams& p, int64_t* pre, int* known = nullptr) {
     int64_t* wsum = pre + NTH + 1;
@@ -178,7 +189,7 @@ struct Walk {
     for (int i = 0; i < chunk; ++i) {
       const int r = threadIdx.x * chunk + i;
       if (r < p.B) request(p, r, it);
-      else it.qlen = it.len = it.first = 0;
+      else it.qlen = it.len = it.first = it.shift = 0;
       // a request of few row tiles by its thread, one of many by the warp
       const bool few = (int64_t)it.qlen * p.group <= 8 * ROWS;
       if (few) u += row_tile_units(p, it, 0, 1) * p.g.heads;
@@ -187,6 +198,7 @@ struct Walk {
         Item x;
         x.qlen = __shfl_sync(0xffffffffu, it.qlen, src);
         x.len = __shfl_sync(0xffffffffu, it.len, src);
+        x.shift = __shfl_sync(0xffffffffu, it.shift, src);
         int64_t n = row_tile_units(p, x, lane, 32);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -194,9 +206,10 @@ struct Walk {
       }
     }
     if (known && chunk == 1 && (int)threadIdx.x < p.B) {
-      known[3 * threadIdx.x] = it.qlen;
-      known[3 * threadIdx.x + 1] = it.len;
-      known[3 * threadIdx.x + 2] = it.first;
+      known[4 * threadIdx.x] = it.qlen;
+      known[4 * threadIdx.x + 1] = it.len;
+      known[4 * threadIdx.x + 2] = it.first;
+      known[4 * threadIdx.x + 3] = it.shift;
     }
     int64_t inc = u;
 #pragma unroll
@@ -340,9 +353,8 @@ DQ_HD void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, in
   a = b = ta;
   const int last = min(it.rows, 128 * i + 128) - 1;
   if (last < 128 * i) return;
-  const int shift = it.len - it.qlen;
-  const int end = p.causal ? min(it.len, shift + row_token(p, it.row0 + last) + 1) : it.len;
-  const int begin = first_seen(p, shift + row_token(p, it.row0 + 128 * i));
+  const int end = seen_end(p, it.len, it.shift + row_token(p, it.row0 + last));
+  const int begin = first_seen(p, it.shift + row_token(p, it.row0 + 128 * i));
   if (end <= begin) return;
   a = min(tb, max(ta, begin / kTcTile - it.t0));
   b = max(a, min(tb, (end - 1) / kTcTile + 1 - it.t0));

@@ -98,8 +98,8 @@ struct StreamCfg {
   static constexpr int PART = ROWS * D * 4 + ROWS * 8;              // rows of O, then (M, l)
   static constexpr int OFF_LEFT = 512;                              // Left [NW][2]
   static constexpr int OFF_PRE = 1792;                              // int64 [NTH + 1 + NW]
-  static constexpr int OFF_KNOWN = OFF_PRE + (NTH + 1 + NW) * 8;   // int [3 NTH]
-  static constexpr int OFF_STATE = (OFF_KNOWN + NTH * 12 + 15) / 16 * 16;
+  static constexpr int OFF_KNOWN = OFF_PRE + (NTH + 1 + NW) * 8;   // int [4 NTH]
+  static constexpr int OFF_STATE = (OFF_KNOWN + NTH * 16 + 15) / 16 * 16;
   static constexpr int OFF_RING = (OFF_STATE + NW * (int)sizeof(WarpState) + 127) / 128 * 128;
   static constexpr int OFF_HEAD = OFF_RING + NW * STAGES * STG;     // the warps' first partials
   static constexpr int SMEM = OFF_HEAD + NW * PART;                 // (the second ones lie in the rings)
@@ -345,13 +345,13 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     // the positions that every row of the item sees, and each row's own limits
     int lo_all, hi_all;
     {
-      const int lo_pos = it.len - it.qlen + row_token(p, it.row0);
-      const int hi_pos = it.len - it.qlen + row_token(p, it.row0 + it.rows - 1);
-      hi_all = p.causal ? min(it.len, lo_pos + 1) : it.len;
+      const int lo_pos = it.shift + row_token(p, it.row0);
+      const int hi_pos = it.shift + row_token(p, it.row0 + it.rows - 1);
+      hi_all = seen_end(p, it.len, lo_pos);
       lo_all = first_seen(p, hi_pos);
       if (lane < C::ROWS) {
-        const int pos = it.len - it.qlen + row_token(p, it.row0 + lane);
-        S.hi[lane] = p.causal ? min(it.len, pos + 1) : it.len;
+        const int pos = it.shift + row_token(p, it.row0 + lane);
+        S.hi[lane] = seen_end(p, it.len, pos);
         S.lo[lane] = first_seen(p, pos);
       }
       __syncwarp();
@@ -709,8 +709,8 @@ __global__ void __launch_bounds__(256 * kSub<D>) kv_stream_join_kernel(const __g
   if (follow == 0) return;                 // uniform for the CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp >> 3, col = warp & 7;
-  int first;
-  const int rows = min(C::ROWS, q_rows(p, d.x, &first) * p.group - d.z);
+  int first, all;
+  const int rows = min(C::ROWS, q_rows(p, d.x, &first, &all) * p.group - d.z);
   const bool live = col < rows;
   // partial 0 is this CTA's second one, the others the first ones of the CTAs after it
   auto part = [&](int i) -> int64_t {

@@ -57,6 +57,7 @@ struct TcCfg {
   static constexpr int KV_BUF = TT * D * 2;
   static constexpr int PIECE_B = kPiece / kKvBlk * KvBlk<D>::BYTES;
   static constexpr int RS = D == 64 ? 8 : D == 128 ? 6 : 3;
+  static constexpr int OFF_SHARE = 496;              // int64 [2], behind the barriers
   static constexpr int OFF_PRE = 512;
   static constexpr int OFF_Q = 6144;
   static constexpr int OFF_K = OFF_Q + NQ * Q_TILE;
@@ -70,7 +71,8 @@ struct TcCfg {
   static constexpr int COL_S = NQ * D;
   static_assert(COL_S + NQ * 2 * TT <= 512, "tensor memory");
   static_assert(TT == 2 * kPiece && RS >= 3, "a tile is two pieces");
-  static_assert((NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE && SMEM <= 232448, "shared memory");
+  static_assert((2 * RS + 2 * KVS + 14) * 8 + 4 <= OFF_SHARE && (NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE &&
+                    SMEM <= 232448, "shared memory");
 };
 
 constexpr size_t kTcO = (size_t)kMaxCtas * 2 * 256 * 128 * 4;   // ROWS * D is at most 256 * 128
@@ -247,16 +249,19 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   int* known = (int*)(smem + C::OFF_Q);    // (Q comes after the walk's start)
-  static_assert(C::NTH * 12 <= NQ * C::Q_TILE, "shared memory");
+  static_assert(C::NTH * 16 <= NQ * C::Q_TILE, "shared memory");
   Wk::template sum_units<C::NTH>(p, pre, known);
   const int64_t U = pre[C::NTH];
   const int N = tc_shares(gridDim.x, U);
   const TcWs ws = tc_ws(p.ws);
   if (threadIdx.x == 0) ws.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x >= N) return;
-  const int64_t u0 = share_start(U, N, blockIdx.x), u1 = share_start(U, N, blockIdx.x + 1);
-
+  // the share, in shared memory: the roles' loops need their registers (prompts with heads of 64 147 -> 141
+  // us, the long chunk 947 -> 930)
+  int64_t* share = (int64_t*)(smem + C::OFF_SHARE);
   if (threadIdx.x == 0) {
+    share[0] = share_start(U, N, blockIdx.x);
+    share[1] = share_start(U, N, blockIdx.x + 1);
     for (int i = 0; i < C::RS; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
                  vs = smem_u32(smem + C::OFF_V);
 
   Item it;
-  int64_t iu = Wk::template seek<C::NTH>(p, pre, u0, it, known);
+  int64_t iu = Wk::template seek<C::NTH>(p, pre, share[0], it, known);
   int ta, tb;                              // the tiles of the item that this share holds
   bool ok = true;
   __syncthreads();
@@ -300,8 +305,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint32_t qrow = qs + tile * C::Q_TILE;
     int slot = 0;                          // of this CTA's partials
     int gt = 0;                            // tiles so far
-    for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more;
-         more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+    for (bool more = Wk::here(p, it, iu, share[0], share[1], ta, tb); more;
+         more = Wk::after(p, it, iu, share[0], share[1], ta, tb)) {
       const bool from_start = ta == 0, to_end = tb == it.tiles;
       int ra, rb;
       row_tile_range(p, it, tile, ta, tb, ra, rb);
@@ -356,14 +361,14 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         fence_proxy_async_smem();
         mbar_arrive(&q_full[tile]);
       }
-      const int pos = it.len - it.qlen + tokq;
-      const int hi = p.causal ? min(it.len, pos + 1) : it.len;
+      const int pos = it.shift + tokq;
+      const int hi = seen_end(p, it.len, pos);
       const int lo = first_seen(p, pos);
       int lo_all, hi_all;
       {
-        const int pa = it.len - it.qlen + row_token(p, it.row0 + min(it.rows - 1, tile * 128));
-        const int pb = it.len - it.qlen + row_token(p, it.row0 + min(it.rows, tile * 128 + 128) - 1);
-        hi_all = p.causal ? min(it.len, pa + 1) : it.len;
+        const int pa = it.shift + row_token(p, it.row0 + min(it.rows - 1, tile * 128));
+        const int pb = it.shift + row_token(p, it.row0 + min(it.rows, tile * 128 + 128) - 1);
+        hi_all = seen_end(p, it.len, pa);
         lo_all = first_seen(p, pb);
       }
       float M = kNone, l = 0.f;
@@ -572,8 +577,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint32_t v_at[2] = {sw128_offset(vrow, r4), sw128_offset(vrow + 1, r4)};
     const uint32_t raw0 = smem_u32(smem + C::OFF_RAW) + blk * B::BYTES;
     int gt = 0, st = pc, st_phase = 0;     // every other stage is this warp's
-    for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
-         more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+    for (bool more = Wk::here(p, it, iu, share[0], share[1], ta, tb); more && ok;
+         more = Wk::after(p, it, iu, share[0], share[1], ta, tb)) {
       const bool fine = is_fine(p, it);
       for (int j = ta; j < tb && ok; ++j) {
         const int tok0 = (it.t0 + j) * TT;
@@ -669,8 +674,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint64_t pol = l2_evict_first_policy();
     const int shift = p.g.page_shift;
     int piece = 0, st = 0, st_phase = 0;
-    for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
-         more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+    for (bool more = Wk::here(p, it, iu, share[0], share[1], ta, tb); more && ok;
+         more = Wk::after(p, it, iu, share[0], share[1], ta, tb)) {
       int tbase = -1, tent = 0;
       for (int j = ta; j < tb && ok; ++j) {
         const int tok0 = (it.t0 + j) * TT;
@@ -779,8 +784,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         if (lane == 0) mbar_arrive(&kv_empty[buf]);
         return true;
       };
-      for (bool more = Wk::here(p, it, iu, u0, u1, ta, tb); more && ok;
-           more = Wk::after(p, it, iu, u0, u1, ta, tb)) {
+      for (bool more = Wk::here(p, it, iu, share[0], share[1], ta, tb); more && ok;
+           more = Wk::after(p, it, iu, share[0], share[1], ta, tb)) {
         int ra, rb;
         row_tile_range(p, it, i, ta, tb, ra, rb);
         auto item = [&](auto fine_c) {
@@ -834,8 +839,8 @@ __global__ void __launch_bounds__(256, 6) kv_tc_join_kernel(const __grid_constan
   const int4 d = __ldcg(ws.desc + blockIdx.x);
   const int follow = d.w >> 1;
   if (follow == 0) return;
-  int first;
-  const int rows = min(C::ROWS, q_rows(p, d.x, &first) * p.group - d.z);
+  int first, all;
+  const int rows = min(C::ROWS, q_rows(p, d.x, &first, &all) * p.group - d.z);
   const int c = threadIdx.x % (D / 4), row0 = blockIdx.y * (kJoinPass<D> * kJoinRows) + threadIdx.x / (D / 4);
   float m[kJoinRows], l[kJoinRows];
   float4 acc[kJoinRows];

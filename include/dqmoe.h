@@ -549,14 +549,14 @@ typedef struct {
   int32_t n_q_heads;          /* a multiple of n_kv_heads, <= 4096 */
   int32_t T;                  /* rows of q, out and lse; >= 1 */
   int32_t B;                  /* requests, 1..DQ_KV_MAX_REQUESTS */
-  const int32_t* q_start;     /* device [B+1], ascending from 0, q_start[B] <= T; rows from
-                                 q_start[B] on are not written */
+  const int32_t* q_start;     /* device [B+1], ascending from 0; rows of q from q_start[B] on are not
+                                 written, and rows behind T (which dq_kv_plan leaves out) are no rows */
   const int32_t* kv_len;      /* device [B] */
   const int32_t* block_table; /* device [B][max_pages]; entries of the pages below kv_len are read,
                                  one outside the cache reads as page 0 */
   int32_t max_pages;          /* a kv_len above max_pages * page_size reads as that many */
-  int32_t max_q_len;          /* no request has more rows, <= T; it chooses the kernels and
-                                 rows above it are not written */
+  int32_t max_q_len;          /* the most rows a request has, <= T; it chooses the kernels.  A request's
+                                 rows above it are not written, its others are as they would be */
   float scale;                /* finite, > 0 */
   int32_t causal;             /* 0 or 1 */
   int32_t window;             /* 0: none */

@@ -24,6 +24,7 @@ namespace {
 struct Call {
   int heads, group, page_size, max_pages, causal, window, ctas;
   std::vector<int> rows, kv;               // of each request
+  int most = 0, behind = 0;                // max_q_len if not the largest of rows; rows of q that are missing at its end
 };
 
 #define CHECK(cond, ...)                                                              \
@@ -54,12 +55,12 @@ struct Params {
     p.group = c.group;
     p.group_inv = group_inverse(c.group);
     p.n_q_heads = c.heads * c.group;
-    p.T = start.back();
+    p.T = start.back() - c.behind;
     p.B = (int)c.rows.size();
     p.q_start = start.data();
     p.kv_len = kv.data();
     p.max_pages = c.max_pages;
-    p.max_q_len = *std::max_element(c.rows.begin(), c.rows.end());
+    p.max_q_len = c.most ? c.most : *std::max_element(c.rows.begin(), c.rows.end());
     p.causal = c.causal;
     p.window = c.window;
   }
@@ -243,6 +244,14 @@ Call long_caches(Rng& g) {
   return c;
 }
 
+// requests with more rows than the call looks after: the others stand where they stood
+Call more_rows(Rng& g) {
+  Call c = prompts(g);
+  c.most = upto(g, 1, c.rows[0]);
+  if (g() % 2) c.behind = upto(g, 0, c.rows.back());
+  return c;
+}
+
 void run(const char* mode, Rng& g) {
   if (!strcmp(mode, "prompts")) {
     const Call c = prompts(g);
@@ -258,6 +267,14 @@ void run(const char* mode, Rng& g) {
     many_rows<256>(c);
     for (int& n : c.rows) n = n ? 1 + n % std::max(1, 64 / c.group) : 0;
     few_rows(c);
+  } else if (!strcmp(mode, "more_rows")) {
+    Call c = more_rows(g);
+    many_rows<64>(c);
+    many_rows<256>(c);
+    if (c.group <= 8) {
+      c.most = upto(g, 1, 8);
+      few_rows(c);
+    }
   } else if (!strcmp(mode, "long_caches")) {
     Call c = long_caches(g);
     many_rows<128>(c);

@@ -1,5 +1,6 @@
 """dq_kv_attention where its work sharing is at its edges (-m gpu): windowed prompts,
-windows as large as an int, lengths as large as a table can list.
+windows as large as an int, lengths as large as a table can list,
+rows that a call leaves out.
 
 The bars are test_gpu_kv's.  Where no K is rounded (few rows, or rows that see at
 most 1024 tokens) the lse is held to what fp32 sums give: 2^-18 (1 + |lse|)."""
@@ -90,3 +91,31 @@ def test_the_last_tokens_that_a_table_can_list(dq, new, kv, H, n_kv, D, ps):  # 
     assert dq.device_status() == 0
     c.check(out, lse, window=90)
     lse_is_exact(c, lse, window=90)
+
+
+@pytest.mark.parametrize("most,new,kv,H,n_kv,D", [
+    (2, [3, 2, 7], [200, 300, 5], 2, 2, 64),
+    (1, [8, 1], [1000, 90], 8, 2, 128),
+    (70, [90, 65, 71], [200, 300, 60], 2, 2, 64),
+    (130, [400, 130], [500, 130], 4, 1, 128),
+    (20, [300, 20], [300, 700], 2, 2, 256),
+])
+@pytest.mark.parametrize("window", [0, 40])
+def test_rows_above_max_q_len_leave_the_others_where_they_stand(dq, most, new, kv, H, n_kv, D, window):  # noqa: F811
+    c = Case(dq, 33, new, kv, H, n_kv, D, 16, "fp16")
+    T = sum(new)
+    behind = 1                                     # and the last row of the last request lies behind T
+    q = c.q[:T - behind]
+    out, lse = torch.full_like(q, 7.0), torch.full((T - behind, H), 7.0, device="cuda")
+    dev = [torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda") for x in (c.start, c.kv, c.table)]
+    dq.kv_attention(c.cache, q, *dev, max_q_len=most, window=window, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert dq.device_status() == 0
+    row = np.concatenate([np.arange(n) for n in new])[:T - behind]
+    done = torch.tensor(row < most, device="cuda")
+    assert (out[~done] == 7).all() and (lse[~done] == 7).all()
+    # the whole result with those rows put in, held to the definition
+    full, fl = c.run(max_q_len=max(new), window=window)
+    full[:T - behind][done], fl[:T - behind][done] = out[done], lse[done]
+    c.check(full, fl, window=window)
+    lse_is_exact(c, fl, window=window)

@@ -27,7 +27,7 @@ def _run(walk, mode, seed, calls):
     assert r.returncode == 0, (r.returncode, r.stderr)
 
 
-@pytest.mark.parametrize("mode", ["prompts", "few", "wide_windows", "long_caches"])
+@pytest.mark.parametrize("mode", ["prompts", "few", "wide_windows", "long_caches", "more_rows"])
 @pytest.mark.parametrize("seed", [1, 2])
 def test_shares_of_random_calls(walk, mode, seed):
     _run(walk, mode, seed, 400)
