@@ -17,11 +17,12 @@
 //   P' = fp16(p) * d (one HMUL2 for two tokens).  The codes lose their offset before the product (one
 //   more addition per register: taking 8 sum(p') off the sums instead left 1e-7 of the largest scale in
 //   values whose own scales are small).  O's even and odd values carry 2^-24 and 2^-20 to the end.
-// * fp16 weights: p = 2^(s - M) with M = max - b, renewed only when a score passes
-//   M + b + 4, so p <= 2^(b + 4).  b = 10 while every V scale is below 2 (p' < 2^15), and
-//   -2 for good once one is not (p' <= 2^2 * 8188): no overflow, and weights down to
-//   2^-24 of the largest keep at least one bit.  Rounding p and p' to fp16 (2^-11 each)
-//   is the price of 16-bit operands; s, M, the sum of p and O stay fp32.
+// * fp16 weights: p = 2^(s - M) with M = max - 10, renewed only when a score passes
+//   M + 14, so p <= 2^14 and weights down to 2^-34 of the largest keep at least one bit.
+//   A group whose V scales reach 2 is taken in units of a power of two that brings them below
+//   it (p' < 2^15: no overflow), each group in its own, so that a group of small scales loses
+//   nothing beside a large one.  Rounding p and p' to fp16 (2^-11 each) is the price of
+//   16-bit operands; s, M, the sum of p and O stay fp32.
 //
 // Work.  All (request, K/V head, row tile, 32-token tile) units of the call in
 // one line, cut into equal contiguous shares, one per warp: any mix of lengths
@@ -41,6 +42,7 @@
 // Each warp has a ring of tiles filled by its own bulk copies (a tile of a page
 // is one contiguous run), all but one in flight while one is computed.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_attn.h"
 
@@ -283,7 +285,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
   float o[G][2][4];
   float M[2], lim[2];
   float2 l;
-  float b = 10.f;
+  uint32_t unit = 0;                       // four bits a group: V is taken in units of 2^unit
   bool ok = true;
 
   int stage = 0, phase = 0;
@@ -341,7 +343,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[g][0][k] = o[g][1][k] = 0.f;
-    b = 10.f;
+    unit = 0;
     // the positions that every row of the item sees, and each row's own limits
     int lo_all, hi_all;
     {
@@ -357,184 +359,238 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       __syncwarp();
     }
 
+    // The item's tiles.  UNITS false: every group's unit is 1, and true comes back at the first tile that needs
+    // another one (its copy is still there).  An instance of its own, so that caches without such scales
+    // do not pay: one loop for both took 111.4 us for 64 requests, this 106.8 (where every tile has such
+    // scales, 122).
     const int tb = S.at[0].b;
-    for (int tl = S.at[0].a; tl < tb; ++tl) {
-      const int tok0 = (it.t0 + tl) * kTile;
-      ok = ok && mbar_wait(&bars[stage], phase);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t base = smem_u32(ring + stage * C::STG);
-      const bool inner = tok0 >= lo_all && tok0 <= hi_all - kTile;
+    int tl = S.at[0].a;
+    auto tiles = [&](auto units_c) -> bool {
+      constexpr bool UNITS = decltype(units_c)::value;
+      for (; tl < tb; ++tl) {
+        const int tok0 = (it.t0 + tl) * kTile;
+        ok = ok && mbar_wait(&bars[stage], phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        const uint32_t base = smem_u32(ring + stage * C::STG);
+        const bool inner = tok0 >= lo_all && tok0 <= hi_all - kTile;
 
-      // ---- scores
-      float s[kBlks][4];
-#pragma unroll
-      for (int k = 0; k < kBlks; ++k) {
-        const uint32_t kb = base + k * B::BYTES;
-#pragma unroll
-        for (int gh = 0; gh < GH; ++gh) {
-          uint32_t wa[W], wb[W];
-          lds_words<W>(kb + (((gh * 16 + lr) * 4 + lt) * W) * 4, wa);
-          lds_words<W>(kb + (((gh * 16 + lr + 8) * 4 + lt) * W) * 4, wb);
-          uint32_t da[W / 2], db[W / 2];
-          if (W == 4) {
-            const uint2 x = lds_u64(kb + B::OFF_KD + 2 * (lr * G + gh * W));
-            const uint2 y = lds_u64(kb + B::OFF_KD + 2 * ((lr + 8) * G + gh * W));
-            da[0] = x.x; da[W / 2 - 1] = x.y;
-            db[0] = y.x; db[W / 2 - 1] = y.y;
-          } else {
-            da[0] = lds_u32(kb + B::OFF_KD + 2 * (lr * G));
-            db[0] = lds_u32(kb + B::OFF_KD + 2 * ((lr + 8) * G));
-          }
-#pragma unroll
-          for (int gw2 = 0; gw2 < W; ++gw2) {
-            const int g = gh * W + gw2;
-            const uint32_t x = wa[gw2], y = wb[gw2], x8 = x >> 8, y8 = y >> 8;
-            const float2 fa = __half22float2(u32_as_h2(da[gw2 / 2])),
-                         fb = __half22float2(u32_as_h2(db[gw2 / 2]));
-            const float sa = (gw2 & 1) ? fa.y : fa.x, sb = (gw2 & 1) ? fb.y : fb.x;
-            float acc[4];
-            mma_16816_c(acc, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
-                        qf[g][0], qf[g][1], qi[g][0], qi[g][1]);
-            mma_16816_nv(acc, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u,
-                         y8 & 0x00F000F0u, qf[g][2], qf[g][3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              s[k][i] = g == 0 ? (i < 2 ? sa : sb) * acc[i] : fmaf(i < 2 ? sa : sb, acc[i], s[k][i]);
-          }
-        }
-      }
-      // the V scales of block k for this lane's tokens, pairs (2t, 2t + 1) and (2t + 8, 2t + 9)
-      auto v_scales = [&](int k, uint32_t (&dv)[G][2]) {
-        const uint32_t va = base + k * B::BYTES + B::OFF_VD + 8 * lt * G;
-#pragma unroll
-        for (int g = 0; g < G; g += 2) {
-          const uint4 x = lds_u128(va + 8 * g);
-          dv[g][0] = x.x; dv[g][1] = x.y;
-          dv[g + 1][0] = x.z; dv[g + 1][1] = x.w;
-        }
-        if (!inner) {
-          // tokens that no row sees may hold anything: their scales become 0
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int a = tok0 + k * 16 + 8 * j + 2 * lt;
-            const int from = S.at[0].it.begin, to = S.at[0].it.end;
-            const uint32_t keep = ((a >= from && a < to) ? 0x0000FFFFu : 0u) |
-                                  ((a + 1 >= from && a + 1 < to) ? 0xFFFF0000u : 0u);
-#pragma unroll
-            for (int g = 0; g < G; ++g) dv[g][j] &= keep;
-          }
-        }
-      };
-      uint32_t big = 0;                    // has bit 14 of either half set: some V scale is 2 or more
-      if (inner) {
-        // the tile's scales once over the lanes
-        const uint32_t va = base + (lane >> 4) * B::BYTES + B::OFF_VD + (lane & 15) * (D / 16);
-        if (D == 64) {
-          big = lds_u32(va);
-        } else if (D == 128) {
-          const uint2 x = lds_u64(va);
-          big = x.x | x.y;
-        } else {
-          const uint4 x = lds_u128(va);
-          big = x.x | x.y | x.z | x.w;
-        }
-      } else {
+        // ---- scores
+        float s[kBlks][4];
 #pragma unroll
         for (int k = 0; k < kBlks; ++k) {
-          uint32_t dv[G][2];
-          v_scales(k, dv);
+          const uint32_t kb = base + k * B::BYTES;
 #pragma unroll
-          for (int g = 0; g < G; ++g) big |= dv[g][0] | dv[g][1];
+          for (int gh = 0; gh < GH; ++gh) {
+            uint32_t wa[W], wb[W];
+            lds_words<W>(kb + (((gh * 16 + lr) * 4 + lt) * W) * 4, wa);
+            lds_words<W>(kb + (((gh * 16 + lr + 8) * 4 + lt) * W) * 4, wb);
+            uint32_t da[W / 2], db[W / 2];
+            if (W == 4) {
+              const uint2 x = lds_u64(kb + B::OFF_KD + 2 * (lr * G + gh * W));
+              const uint2 y = lds_u64(kb + B::OFF_KD + 2 * ((lr + 8) * G + gh * W));
+              da[0] = x.x; da[W / 2 - 1] = x.y;
+              db[0] = y.x; db[W / 2 - 1] = y.y;
+            } else {
+              da[0] = lds_u32(kb + B::OFF_KD + 2 * (lr * G));
+              db[0] = lds_u32(kb + B::OFF_KD + 2 * ((lr + 8) * G));
+            }
+#pragma unroll
+            for (int gw2 = 0; gw2 < W; ++gw2) {
+              const int g = gh * W + gw2;
+              const uint32_t x = wa[gw2], y = wb[gw2], x8 = x >> 8, y8 = y >> 8;
+              const float2 fa = __half22float2(u32_as_h2(da[gw2 / 2])),
+                           fb = __half22float2(u32_as_h2(db[gw2 / 2]));
+              const float sa = (gw2 & 1) ? fa.y : fa.x, sb = (gw2 & 1) ? fb.y : fb.x;
+              float acc[4];
+              mma_16816_c(acc, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
+                          qf[g][0], qf[g][1], qi[g][0], qi[g][1]);
+              mma_16816_nv(acc, x8 & 0x000F000Fu, y8 & 0x000F000Fu, x8 & 0x00F000F0u,
+                           y8 & 0x00F000F0u, qf[g][2], qf[g][3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                s[k][i] = g == 0 ? (i < 2 ? sa : sb) * acc[i] : fmaf(i < 2 ? sa : sb, acc[i], s[k][i]);
+            }
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int lo = S.lo[2 * lt + i], hi = S.hi[2 * lt + i];
+        // tokens 2t + 8j of block k, and the one behind: those that no row sees may hold anything, their V scales
+        // become 0
+        auto kept = [&](int k, int j) -> uint32_t {
+          const int a = tok0 + k * 16 + 8 * j + 2 * lt;
+          const int from = S.at[0].it.begin, to = S.at[0].it.end;
+          return ((a >= from && a < to) ? 0x0000FFFFu : 0u) | ((a + 1 >= from && a + 1 < to) ? 0xFFFF0000u : 0u);
+        };
+        // the V scales of block k and group g for this lane's tokens, pairs (2t, 2t + 1) and (2t + 8, 2t + 9)
+        auto v_scales = [&](int k, int g) -> uint2 {
+          uint2 x = lds_u64(base + k * B::BYTES + B::OFF_VD + 8 * (lt * G + g));
+          if (!inner) {
+            x.x &= kept(k, 0);
+            x.y &= kept(k, 1);
+          }
+          return x;
+        };
+        // Some bit of `kBig` is set in `big` if some V scale is 2 units of its group or more: bit 14 where every
+        // unit is 1, else the carry into bit 15 of the magnitude and 2^15 less that limit.
+        constexpr uint32_t kBig = UNITS ? 0x80008000u : 0x40004000u;
+        auto carry = [&](uint32_t x, int g) -> uint32_t {
+          return UNITS ? (x & 0x7FFF7FFFu) + (0x8000u - ((16 + (unit >> 4 * g & 15)) << 10)) * 0x10001u : x;
+        };
+        uint32_t big = 0;
+        if (inner) {
+          // the tile's scales once over the lanes
+          const uint32_t va = base + (lane >> 4) * B::BYTES + B::OFF_VD + (lane & 15) * (D / 16);
+          if (D == 64) {
+            big = carry(lds_u32(va), lane >> 1 & 1);
+          } else if (D == 128) {
+            const uint2 x = lds_u64(va);
+            big = carry(x.x, lane & 3) | carry(x.y, lane & 3);
+          } else {
+            const uint4 x = lds_u128(va);
+            big = carry(x.x, 2 * (lane & 3)) | carry(x.y, 2 * (lane & 3)) | carry(x.z, 2 * (lane & 3) + 1) |
+                  carry(x.w, 2 * (lane & 3) + 1);
+          }
+        } else {
 #pragma unroll
           for (int k = 0; k < kBlks; ++k)
 #pragma unroll
-            for (int hrow = 0; hrow < 2; ++hrow) {
-              const int a = tok0 + k * 16 + 8 * hrow + lr;
-              if (a < lo || a >= hi) s[k][2 * hrow + i] = -INFINITY;
+            for (int g = 0; g < G; ++g) {
+              const uint2 x = v_scales(k, g);
+              big |= carry(x.x, g) | carry(x.y, g);
             }
-        }
-      }
-      // ---- weights
-      float top[2];
-      bool over = b > 0.f && (big & 0x40004000u) != 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i])) * cf[i];
-        over = over || top[i] > lim[i];
-      }
-      if (__any_sync(0xffffffffu, over)) {
-        const float bn = __any_sync(0xffffffffu, (big & 0x40004000u) != 0) ? -2.f : b;
+          for (int i = 0; i < 2; ++i) {
+            const int lo = S.lo[2 * lt + i], hi = S.hi[2 * lt + i];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float m = top[i];
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          const float mo = M[i], mn = fmaxf(mo + (b - bn), m - bn), corr = ex2(mo - mn);
-          M[i] = mn;
-          lim[i] = mn + bn + 4.f;
-          (i == 0 ? l.x : l.y) *= corr;
+            for (int k = 0; k < kBlks; ++k)
 #pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int k = i; k < 4; k += 2) {
-              o[g][0][k] *= corr;
-              o[g][1][k] *= corr;
-            }
-        }
-        b = bn;
-      }
-      // ---- p and P V
-#pragma unroll
-      for (int k = 0; k < kBlks; ++k) {
-        uint32_t pt[2];
-#pragma unroll
-        for (int hrow = 0; hrow < 2; ++hrow) {
-          const float2 w = make_float2(ex2(fmaf(s[k][2 * hrow], cf[0], -M[0])),
-                                       ex2(fmaf(s[k][2 * hrow + 1], cf[1], -M[1])));
-          l = fadd2(l, w);
-          pt[hrow] = transpose8x8(h2_as_u32(__floats2half2_rn(w.x, w.y)));
-        }
-        uint32_t dv[G][2];
-        v_scales(k, dv);
-        const uint32_t vb = base + k * B::BYTES + B::OFF_V;
-#pragma unroll
-        for (int gh = 0; gh < GH; ++gh) {
-          uint32_t v0[W], v1[W];            // tokens 2t, 2t+1 and 2t+8, 2t+9: W / 2 words each
-          lds_words<W>(vb + ((0 * GH + gh) * 32 + lane) * 4 * W, v0);
-          lds_words<W>(vb + ((1 * GH + gh) * 32 + lane) * 4 * W, v1);
-#pragma unroll
-          for (int gw2 = 0; gw2 < W; ++gw2) {
-            const int g = gh * W + gw2;
-            const uint32_t sel = (gw2 & 1) ? 0x7632u : 0x5410u;
-            const uint32_t z0 = __byte_perm(v0[gw2 / 2], v0[W / 2 + gw2 / 2], sel);
-            const uint32_t z1 = __byte_perm(v1[gw2 / 2], v1[W / 2 + gw2 / 2], sel);
-            const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
-            const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(pt[0]), u32_as_h2(dv[g][0])));
-            const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(pt[1]), u32_as_h2(dv[g][1])));
-            mma_16816_nv(o[g][0], less8(z0, 0), less8(z0, 1), less8(z1, 0), less8(z1, 1), b0, b1);
-            mma_16816_nv(o[g][1], less8(y0, 0), less8(y0, 1), less8(y1, 0), less8(y1, 1), b0, b1);
+              for (int hrow = 0; hrow < 2; ++hrow) {
+                const int a = tok0 + k * 16 + 8 * hrow + lr;
+                if (a < lo || a >= hi) s[k][2 * hrow + i] = -INFINITY;
+              }
           }
         }
-      }
-      // every load of the stage has fed an instruction before its next copy is issued
+        // ---- weights
+        float top[2];
+        bool over = (big & kBig) != 0;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        keep_before_release<4>(o[g][0]);
-        keep_before_release<4>(o[g][1]);
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i])) * cf[i];
+          over = over || top[i] > lim[i];
+        }
+        if (__any_sync(0xffffffffu, over)) {
+          if (__any_sync(0xffffffffu, (big & kBig) != 0)) {
+            if (!UNITS) return true;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              uint32_t m = 0;
+#pragma unroll
+              for (int k = 0; k < kBlks; ++k) {
+                const uint2 x = v_scales(k, g);
+                m = max(max(m, max(x.x & 0x7FFFu, x.x >> 16 & 0x7FFFu)), max(x.y & 0x7FFFu, x.y >> 16 & 0x7FFFu));
+              }
+              // the exponent of the group's largest scale above that of 1 (12 at most: 8188)
+              const int had = unit >> 4 * g & 15;
+              const int add = min((int)(__reduce_max_sync(0xffffffffu, m) >> 10) - 15, 14) - had;
+              if (add > 0) {
+                unit += (uint32_t)add << 4 * g;
+                const float f = __uint_as_float((uint32_t)(127 - add) << 23);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  o[g][0][k] *= f;
+                  o[g][1][k] *= f;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float m = top[i];
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float mo = M[i], mn = fmaxf(mo, m - 10.f), corr = ex2(mo - mn);
+            M[i] = mn;
+            lim[i] = mn + 14.f;
+            (i == 0 ? l.x : l.y) *= corr;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int k = i; k < 4; k += 2) {
+                o[g][0][k] *= corr;
+                o[g][1][k] *= corr;
+              }
+          }
+        }
+        // ---- p and P V
+#pragma unroll
+        for (int k = 0; k < kBlks; ++k) {
+          uint32_t pt[2];
+#pragma unroll
+          for (int hrow = 0; hrow < 2; ++hrow) {
+            const float2 w = make_float2(ex2(fmaf(s[k][2 * hrow], cf[0], -M[0])),
+                                         ex2(fmaf(s[k][2 * hrow + 1], cf[1], -M[1])));
+            l = fadd2(l, w);
+            pt[hrow] = transpose8x8(h2_as_u32(__floats2half2_rn(w.x, w.y)));
+          }
+          uint32_t dv[G][2];
+#pragma unroll
+          for (int g = 0; g < G; g += 2) {
+            const uint4 x = lds_u128(base + k * B::BYTES + B::OFF_VD + 8 * (lt * G + g));
+            dv[g][0] = x.x; dv[g][1] = x.y;
+            dv[g + 1][0] = x.z; dv[g + 1][1] = x.w;
+          }
+          if (!inner) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t keep = kept(k, j);
+#pragma unroll
+              for (int g = 0; g < G; ++g) dv[g][j] &= keep;
+            }
+          }
+          if (UNITS) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const uint32_t f = (15 - (unit >> 4 * g & 15)) * 0x04000400u;    // 2^-unit, twice
+#pragma unroll
+              for (int j = 0; j < 2; ++j) dv[g][j] = h2_as_u32(__hmul2(u32_as_h2(dv[g][j]), u32_as_h2(f)));
+            }
+          }
+          const uint32_t vb = base + k * B::BYTES + B::OFF_V;
+#pragma unroll
+          for (int gh = 0; gh < GH; ++gh) {
+            uint32_t v0[W], v1[W];            // tokens 2t, 2t+1 and 2t+8, 2t+9: W / 2 words each
+            lds_words<W>(vb + ((0 * GH + gh) * 32 + lane) * 4 * W, v0);
+            lds_words<W>(vb + ((1 * GH + gh) * 32 + lane) * 4 * W, v1);
+#pragma unroll
+            for (int gw2 = 0; gw2 < W; ++gw2) {
+              const int g = gh * W + gw2;
+              const uint32_t sel = (gw2 & 1) ? 0x7632u : 0x5410u;
+              const uint32_t z0 = __byte_perm(v0[gw2 / 2], v0[W / 2 + gw2 / 2], sel);
+              const uint32_t z1 = __byte_perm(v1[gw2 / 2], v1[W / 2 + gw2 / 2], sel);
+              const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
+              const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(pt[0]), u32_as_h2(dv[g][0])));
+              const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(pt[1]), u32_as_h2(dv[g][1])));
+              mma_16816_nv(o[g][0], less8(z0, 0), less8(z0, 1), less8(z1, 0), less8(z1, 1), b0, b1);
+              mma_16816_nv(o[g][1], less8(y0, 0), less8(y0, 1), less8(y1, 0), less8(y1, 1), b0, b1);
+            }
+          }
+        }
+        // every load of the stage has fed an instruction before its next copy is issued
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          keep_before_release<4>(o[g][0]);
+          keep_before_release<4>(o[g][1]);
+        }
+        __syncwarp();
+        produce(stage);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      __syncwarp();
-      produce(stage);
-      if (++stage == C::STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
+      return false;
+    };
+    if (tiles(std::false_type())) tiles(std::true_type());
     if (!ok) break;
 
     // ---- the item's rows: whole, or a partial (the second one over the ring, whose copies have all
@@ -561,10 +617,9 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       const int head = done.h * p.group + uq;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float x[4] = {(o[g][0][i]) * (k24 * inv),
-                            (o[g][0][2 + i]) * (k20 * inv),
-                            (o[g][1][i]) * (k24 * inv),
-                            (o[g][1][2 + i]) * (k20 * inv)};
+        const float f = inv * __uint_as_float((127 + (unit >> 4 * g & 15)) << 23);
+        const float x[4] = {o[g][0][i] * (k24 * f), o[g][0][2 + i] * (k20 * f), o[g][1][i] * (k24 * f),
+                            o[g][1][2 + i] * (k20 * f)};
         if (whole)
           store_out4(p, qrow * p.out_stride + (int64_t)head * D + 32 * g + 4 * lr, x);
         else

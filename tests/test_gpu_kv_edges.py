@@ -1,6 +1,6 @@
 """dq_kv_attention where its work sharing is at its edges (-m gpu): windowed prompts,
 windows as large as an int, lengths as large as a table can list,
-rows that a call leaves out.
+rows that a call leaves out, groups of V of very different sizes.
 
 The bars are test_gpu_kv's.  Where no K is rounded (few rows, or rows that see at
 most 1024 tokens) the lse is held to what fp32 sums give: 2^-18 (1 + |lse|)."""
@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import kv_ref
-from test_gpu_kv import Case, dq  # noqa: F401  (the fixture)
+from test_gpu_kv import Case, bar_of, dq  # noqa: F401  (dq is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,37 @@ def test_rows_above_max_q_len_leave_the_others_where_they_stand(dq, most, new, k
     full[:T - behind][done], fl[:T - behind][done] = out[done], lse[done]
     c.check(full, fl, window=window)
     lse_is_exact(c, fl, window=window)
+
+
+@pytest.mark.parametrize("new,kv,H,n_kv", [
+    ([1] * 5, [1, 5, 17, 40, 300], 8, 2),
+    ([3, 8], [4, 500], 8, 8),
+    ([1], [3000], 4, 1),
+    ([1], [20000], 8, 1),                          # over many shares, joined
+    ([140, 70], [140, 900], 4, 2),
+])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("large", [2.5, 700.0, 8188.0])
+def test_v_groups_of_very_different_scales(dq, new, kv, H, n_kv, D, large):  # noqa: F811
+    # Values of one group of 32 beside groups whose scales are up to 2^33 as large.  Each group is held to its own
+    # size: test_gpu_kv's bar with vmax of the group, and 2^-32 max(1, scale) a token for a product of a weight and
+    # a scale that is rounded below fp16's normal range (2^-25 times 8, the row's largest weight being 2^10).
+    c = Case(dq, 34, new, kv, H, n_kv, D, 16, "fp16")
+    vs = c.host[..., 17 * D:].view(np.float16)
+    size = np.array([large, 2.0 ** -17, 2.0 ** -4, 2.0 ** -20, 1.0, 2.0 ** -14, 2.0 ** -9, 2.0 ** -17])
+    top = {}
+    for g in range(D // 32):
+        at = [(kv_ref.v_scale(D, i, g) - 17 * D) // 2 for i in range(16)]
+        x = np.clip(vs[..., at].astype(np.float64), -0.6, 0.6) / 0.6 * size[g]
+        vs[..., at] = x.astype(np.float16)
+        top[g] = np.nanmax(np.abs(vs[..., at].astype(np.float64)))
+    c.cache.pages.copy_(torch.from_numpy(c.host))
+    out, lse = c.run(max_q_len=max(new), out_dtype=torch.float32)
+    ref, rl, mag, big = definition(c)
+    lse_is_exact(c, lse)
+    scale = np.array([top[x // 32] for x in range(D)])
+    n = max(kv)
+    bar = bar_of(torch.float32, ref, mag, big, n, 8 * scale) + n * 2.0 ** -32 * np.maximum(1.0, scale)
+    off = np.abs(out.double().cpu().numpy() - ref)
+    worst = (off / np.maximum(bar, 1e-300)).max((0, 1)).reshape(-1, 32).max(1)
+    assert (worst <= 1).all(), worst
