@@ -26,9 +26,16 @@ def _raise(name, rc):
     raise DqError(name, rc)
 
 
-def _check(t, name, dtype, shape=None):
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous CUDA tensor of %s" % (name, dtype))
+def _device(t, name):
+    """The index of t's CUDA device, on which all of a call's tensors have to lie."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _check(t, name, dtype, dev, shape=None):
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor of %s on device %d" % (name, dtype, dev))
     if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
 
@@ -37,7 +44,7 @@ class KvPlan:
     """A step's outputs of kv_plan: kv_len, q_start, positions, free_count, unserved (int32) and
     slots (int64), for B requests and n_tokens rows; a step may write to an earlier one's."""
 
-    __slots__ = ("kv_len", "q_start", "slots", "positions", "free_count", "unserved", "size", "_ptrs")
+    __slots__ = ("kv_len", "q_start", "slots", "positions", "free_count", "unserved", "size", "dev", "_ptrs")
 
     def __init__(self, B, n_tokens, device="cuda"):
         i32 = torch.empty(2 * B + 3 + n_tokens, dtype=torch.int32, device=device)
@@ -46,6 +53,7 @@ class KvPlan:
         self.positions = i32[2 * B + 3:]
         self.slots = torch.empty(n_tokens, dtype=torch.int64, device=device)
         self.size = (B, n_tokens)
+        self.dev = _device(i32, "a plan")
         self._ptrs = tuple(t.data_ptr() for t in (self.kv_len, self.q_start, self.slots, self.positions,
                                                   self.free_count, self.unserved))
 
@@ -60,7 +68,8 @@ class KvCache:
     def __init__(self, pages, page_size, n_kv_heads, head_dim, fmt=Q4_0):
         d = KvCacheDesc(fmt, n_kv_heads, head_dim, page_size, 1, None)
         per_page = _size(d)
-        _check(pages, "pages", torch.uint8)
+        self.dev = _device(pages, "pages")
+        _check(pages, "pages", torch.uint8, self.dev)
         if pages.numel() < per_page or pages.numel() % per_page:
             raise ValueError("pages must hold a whole number of pages of %d bytes" % per_page)
         d.n_pages = pages.numel() // per_page
@@ -97,18 +106,20 @@ def kv_plan(ctx_len, new_len, block_table, free_pages, free_count, page_size, n_
     out: a KvPlan of an earlier step to write to (its free_count and kv_len may
     not be this call's inputs).
     """
-    B = ctx_len.numel()
-    _check(ctx_len, "ctx_len", torch.int32)
-    _check(new_len, "new_len", torch.int32, (B,))
-    _check(block_table, "block_table", torch.int32)
+    B, dev = ctx_len.numel(), _device(ctx_len, "ctx_len")
+    _check(ctx_len, "ctx_len", torch.int32, dev)
+    _check(new_len, "new_len", torch.int32, dev, (B,))
+    _check(block_table, "block_table", torch.int32, dev)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B][max_pages]")
-    _check(free_pages, "free_pages", torch.int32)
-    _check(free_count, "free_count", torch.int32, (1,))
+    _check(free_pages, "free_pages", torch.int32, dev)
+    _check(free_count, "free_count", torch.int32, dev, (1,))
     if out is None:
         out = KvPlan(B, n_tokens, ctx_len.device)
     elif out.size != (B, n_tokens):
         raise ValueError("out holds %d requests and %d rows, not %d and %d" % (*out.size, B, n_tokens))
+    elif out.dev != dev:
+        raise ValueError("out must lie on device %d" % dev)
     rc = _plan(ctx_len.data_ptr(), new_len.data_ptr(), B, page_size, block_table.data_ptr(),
                block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
                n_tokens, *out._ptrs, _stream(ctx_len))
@@ -119,9 +130,10 @@ def _rows(cache, t, name):
     """The token stride of rows [T][n_kv_heads][head_dim] (only the first may be strided)."""
     T, H, D = t.shape
     a, b, c = t.stride()
-    if H != cache.n_kv_heads or D != cache.head_dim or not t.is_cuda or c != 1 or (b != D and H > 1):
-        raise ValueError("%s must be a CUDA tensor [T][%d][%d] with consecutive heads" %
-                         (name, cache.n_kv_heads, cache.head_dim))
+    if (H != cache.n_kv_heads or D != cache.head_dim or t.get_device() != cache.dev or c != 1 or
+            (b != D and H > 1)):
+        raise ValueError("%s must be a CUDA tensor [T][%d][%d] on device %d with consecutive heads" %
+                         (name, cache.n_kv_heads, cache.head_dim, cache.dev))
     return a if T > 1 else H * D
 
 
@@ -132,7 +144,7 @@ def kv_append(cache, k, v, slots):
     if k.dtype != v.dtype or k.dtype not in _DT or v.shape[0] != T:
         raise ValueError("k and v must be rows of one dtype: float32, float16 or bfloat16")
     ks, vs = _rows(cache, k, "k"), _rows(cache, v, "v")
-    _check(slots, "slots", torch.int64, (T,))
+    _check(slots, "slots", torch.int64, cache.dev, (T,))
     if T:
         rc = _append(cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, _DT[k.dtype], slots.data_ptr(), T,
                      _stream(k))
@@ -143,7 +155,7 @@ def kv_append(cache, k, v, slots):
 def kv_read(cache, slots, dtype=torch.float32, out=None):
     """The values that slots stand for: (k, v), each [T][n_kv_heads][head_dim]."""
     T = slots.numel()
-    _check(slots, "slots", torch.int64)
+    _check(slots, "slots", torch.int64, cache.dev)
     shape = (T, cache.n_kv_heads, cache.head_dim)
     if out is None:
         out = (torch.empty(shape, dtype=dtype, device=slots.device),
@@ -151,8 +163,8 @@ def kv_read(cache, slots, dtype=torch.float32, out=None):
     k, v = out
     if k.dtype not in _DT:
         raise ValueError("values are float32, float16 or bfloat16")
-    _check(k, "k", k.dtype, shape)
-    _check(v, "v", k.dtype, shape)
+    _check(k, "k", k.dtype, cache.dev, shape)
+    _check(v, "v", k.dtype, cache.dev, shape)
     if T:
         rc = _read(cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _DT[k.dtype], _stream(k))
         if rc != 0:
@@ -174,29 +186,32 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
 
     q_start int32 [B+1], kv_len int32 [B], block_table int32 [B][max_pages] as
     kv_plan leaves them; scale: head_dim ** -0.5 unless given; max_q_len: the
-    most rows a request has (T unless given).
+    most rows a request has (T unless given; a step that says 1 is one launch or two
+    instead of four).  ws: kv_attention_workspace_size bytes for these T and max_q_len, or more.
     """
     T, H, D = q.shape
     qs, qh, qd = q.stride()
-    B = kv_len.numel()
+    B, dev = kv_len.numel(), cache.dev
     if q.dtype not in _DT:
         raise TypeError("q must be float16 or bfloat16, got %s" % q.dtype)
-    if D != cache.head_dim or not q.is_cuda or qd != 1 or (qh != D and H > 1):
-        raise ValueError("q must be a CUDA tensor [T][n_q_heads][%d] with consecutive heads" % cache.head_dim)
-    _check(q_start, "q_start", torch.int32, (B + 1,))
-    _check(kv_len, "kv_len", torch.int32)
-    _check(block_table, "block_table", torch.int32)
+    if D != cache.head_dim or q.get_device() != dev or qd != 1 or (qh != D and H > 1):
+        raise ValueError("q must be a CUDA tensor [T][n_q_heads][%d] on device %d with consecutive heads" %
+                         (cache.head_dim, dev))
+    _check(q_start, "q_start", torch.int32, dev, (B + 1,))
+    _check(kv_len, "kv_len", torch.int32, dev)
+    _check(block_table, "block_table", torch.int32, dev)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B][max_pages]")
     if out is None:
         out = torch.empty((T, H, D), dtype=out_dtype or q.dtype, device=q.device)
     os, oh, od = out.stride()
-    if out.dtype not in _DT or out.shape != (T, H, D) or not out.is_cuda or od != 1 or (oh != D and H > 1):
-        raise ValueError("out must be a CUDA tensor [T][n_q_heads][head_dim] with consecutive heads")
+    if (out.dtype not in _DT or out.shape != (T, H, D) or out.get_device() != dev or od != 1 or
+            (oh != D and H > 1)):
+        raise ValueError("out must be a CUDA tensor [T][n_q_heads][head_dim] on device %d with consecutive heads" % dev)
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     else:
-        _check(lse, "lse", torch.float32, (T, H))
+        _check(lse, "lse", torch.float32, dev, (T, H))
     if T == 0:
         return out, lse
     if max_q_len is None:
@@ -204,9 +219,11 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
     if ws is None:
         ws = torch.empty(kv_attention_workspace_size(cache, H, B, T, max_q_len), dtype=torch.uint8,
                          device=q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor on device %d" % dev)
     a = KvAttn(q.data_ptr(), qs if T > 1 else H * D, _DT[q.dtype], H, T, B, q_start.data_ptr(),
                kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1], max_q_len,
                D ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
                os if T > 1 else H * D, _DT[out.dtype], lse.data_ptr())
-    rc = _attention(cache._ref, ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream(q))
+    rc = _attention(cache._ref, ctypes.byref(a), ws.data_ptr(), ws.nbytes, _stream(q))
     return (out, lse) if rc == 0 else _raise("dq_kv_attention", rc)

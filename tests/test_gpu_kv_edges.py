@@ -1,6 +1,7 @@
 """dq_kv_attention where its work sharing is at its edges (-m gpu): windowed prompts,
 windows as large as an int, lengths as large as a table can list,
-rows that a call leaves out, groups of V of very different sizes.
+rows that a call leaves out, groups of V of very different sizes;
+and the binding's refusals.
 
 The bars are test_gpu_kv's.  Where no K is rounded (few rows, or rows that see at
 most 1024 tokens) the lse is held to what fp32 sums give: 2^-18 (1 + |lse|)."""
@@ -153,3 +154,36 @@ def test_v_groups_of_very_different_scales(dq, new, kv, H, n_kv, D, large):  # n
     off = np.abs(out.double().cpu().numpy() - ref)
     worst = (off / np.maximum(bar, 1e-300)).max((0, 1)).reshape(-1, 32).max(1)
     assert (worst <= 1).all(), worst
+
+
+def test_binding_refuses_tensors_off_the_device(dq):  # noqa: F811
+    # none of these calls launches anything
+    c = Case(dq, 35, [1, 2], [20, 40], 4, 2, 64, 16, "fp16")
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+    size = dq.kv_attention_workspace_size(c.cache, 4, 2, 3)
+    good = dict(q=c.q, q_start=i32(c.start), kv_len=i32(c.kv), block_table=i32(c.table),
+                ws=torch.empty(size, dtype=torch.uint8, device="cuda"), out=torch.empty_like(c.q),
+                lse=torch.empty(3, 4, device="cuda"))
+    for name in good:
+        with pytest.raises(ValueError):
+            dq.kv_attention(c.cache, **{**good, name: good[name].cpu()})
+    with pytest.raises(ValueError):
+        dq.kv_attention(c.cache, **{**good, "ws": torch.empty(2 * size, dtype=torch.uint8, device="cuda")[::2]})
+    with pytest.raises(dq.DqError):
+        dq.kv_attention(c.cache, **{**good, "ws": good["ws"][:size - 1]})
+    c.check(*dq.kv_attention(c.cache, **good))
+    c.check(*dq.kv_attention(c.cache, **{**good, "ws": torch.empty(-(-size // 4), device="cuda")}))    # bytes count
+    k, slots = torch.zeros(3, 2, 64, device="cuda"), torch.full((3,), -1, dtype=torch.int64, device="cuda")
+    for a in ((k.cpu(), k, slots), (k, k.cpu(), slots), (k, k, slots.cpu())):
+        with pytest.raises(ValueError):
+            dq.kv_append(c.cache, *a)
+    with pytest.raises(ValueError):
+        dq.kv_read(c.cache, slots.cpu())
+    with pytest.raises(ValueError):
+        dq.kv_read(c.cache, slots, out=(k, k.cpu()))
+    with pytest.raises(ValueError):
+        dq.KvCache(c.cache.pages.cpu(), 16, 2, 64)
+    plan = [i32([3, 4]), i32([1, 1]), i32([[0, 1], [2, 3]]), i32([4, 5]), i32([2])]
+    for i in range(5):
+        with pytest.raises(ValueError):
+            dq.kv_plan(*[t.cpu() if j == i else t for j, t in enumerate(plan)], page_size=16, n_tokens=2)
