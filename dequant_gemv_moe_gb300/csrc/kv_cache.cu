@@ -486,7 +486,8 @@ int dq_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int B, int page_s
   if (B <= 0 || T < 0 || max_pages <= 0 || n_pages <= 0 || !kv_page_size_ok(page_size))
     return DQ_ERR_ARG;
   if ((int64_t)max_pages * page_size > 2147483647LL) return DQ_ERR_ARG;
-  if (free_count_out == free_count || kv_len == ctx_len) return DQ_ERR_ARG;
+  // (every CTA reads the lengths and the count, whenever it runs)
+  if (free_count_out == free_count || kv_len == ctx_len || kv_len == new_len) return DQ_ERR_ARG;
   if (B > DQ_KV_MAX_REQUESTS) return DQ_ERR_UNSUPPORTED;
   const void* p4[] = {ctx_len, new_len, block_table, free_pages, free_count,
                       kv_len, q_start, positions, free_count_out, unserved};

@@ -498,8 +498,9 @@ int dq_kv_cache_size(const dq_kv_cache* cache, size_t* bytes);
  *                      new tokens behind row T are left out.
  *   kv_len [B], q_start [B+1], slots int64 [T], positions int32 [T],
  *   free_count_out [1], unserved [1] (how many requests were not served):
- *                      device outputs; free_count_out may not be free_count and
- *                      kv_len may not be ctx_len (a step swaps them).
+ *                      device outputs, apart from the inputs and from one another:
+ *                      free_count_out may not be free_count (a step swaps them),
+ *                      kv_len neither ctx_len nor new_len.
  * Errors: DQ_ERR_ARG (null, sizes, page_size, aliased outputs, max_pages *
  *         page_size above 2^31 - 1), DQ_ERR_ALIGN (a pointer not aligned to its
  *         element), DQ_ERR_UNSUPPORTED (B above the limit), DQ_ERR_CUDA. */
