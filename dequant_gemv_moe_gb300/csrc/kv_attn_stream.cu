@@ -643,6 +643,14 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       x.last = done_last;
     }
   }
+  if (!ok) {
+    // the copies of this tile and of those behind it may be under way (a stage that none was issued for costs
+    // the whole time)
+    for (int s = 0; s < C::STAGES; ++s) {
+      const int at = stage + s < C::STAGES ? stage + s : stage + s - C::STAGES;
+      mbar_drain(&bars[at], stage + s < C::STAGES ? phase : phase ^ 1);
+    }
+  }
   __syncthreads();
 
   // ---- the CTA's partials.  An item starts with a warp's second partial (or with the first warp's

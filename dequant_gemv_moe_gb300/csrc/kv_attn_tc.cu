@@ -71,7 +71,7 @@ struct TcCfg {
   static constexpr int COL_S = NQ * D;
   static_assert(COL_S + NQ * 2 * TT <= 512, "tensor memory");
   static_assert(TT == 2 * kPiece && RS >= 3, "a tile is two pieces");
-  static_assert((2 * RS + 2 * KVS + 14) * 8 + 4 <= OFF_SHARE && (NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE &&
+  static_assert((2 * RS + 2 * KVS + 16) * 8 + 4 <= OFF_SHARE && (NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE &&
                     SMEM <= 232448, "shared memory");
 };
 
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   uint64_t* p_full = s_full + 4;
   uint64_t* pv_done = p_full + 4;
   uint64_t* q_full = pv_done + 4;
-  uint32_t* tmem_slot = (uint32_t*)(q_full + 2);
+  uint64_t* drained = q_full + 2;
+  uint32_t* tmem_slot = (uint32_t*)(drained + 2);
   int64_t* pre = (int64_t*)(smem + C::OFF_PRE);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -277,6 +278,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     }
     mbar_init(&q_full[0], 128);
     mbar_init(&q_full[1], 128);
+    mbar_init(&drained[0], 1);
+    mbar_init(&drained[1], 1);
     fence_barrier_init();
   }
   if (warp == C::MMA) {
@@ -713,6 +716,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         }
       }
     }
+    // every copy has landed when the CTA ends, whichever wait ran out
+    for (int s = 0; s < piece; ++s) mbar_drain(&raw_full[s], s < st ? st_phase : st_phase ^ 1);
     } else {
       // ------------------------------ products ------------------------------
       // A warp per row tile, so that neither waits for the other's softmax.  The whole warp walks the loop,
@@ -809,8 +814,11 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         if (is_fine(p, it)) item(std::true_type());
         else item(std::false_type());
       }
-      // no arrival is under way when the CTA ends
+      // no arrival and no product is under way when the CTA ends, whichever wait ran out
       if (ok && ring > 0) mbar_wait(&kv_empty[(ring - 1) % C::KVS], ((ring - 1) / C::KVS) & 1);
+      if (elect_one()) tc_commit(&drained[i]);
+      __syncwarp();
+      mbar_drain(&drained[i], 0);
     }
   }
   tc_fence_before();
