@@ -187,3 +187,16 @@ def test_binding_refuses_tensors_off_the_device(dq):  # noqa: F811
     for i in range(5):
         with pytest.raises(ValueError):
             dq.kv_plan(*[t.cpu() if j == i else t for j, t in enumerate(plan)], page_size=16, n_tokens=2)
+
+
+def test_plan_that_runs_out_counts_no_page_of_the_unserved(dq):  # noqa: F811
+    # request 0 needs two pages of the one there is; request 1, behind it, needs none, request 2 one: it is not served
+    # either (the needs up to it do not fit), and the page stays on the stack
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = [[3, -1, -1], [5, -1, -1], [6, -1, -1]]
+    args = ([16, 4, 16], [32, 2, 1], table, [9, -1, -1, -1], 1)
+    ref = kv_ref.plan(*[np.array(a) for a in args[:3]], args[3], 1, 16, 35)
+    p = dq.kv_plan(i32(args[0]), i32(args[1]), i32(table), i32(args[3]), i32([1]), page_size=16, n_tokens=35)
+    assert p.free_count.item() == ref["free_count"] == 1 and p.unserved.item() == ref["unserved"] == 2
+    assert p.kv_len.tolist() == ref["kv_len"] == [16, 6, 16]
+    assert p.slots.tolist() == ref["slots"] and p.slots.tolist()[32:34] == [5 * 16 + 4, 5 * 16 + 5]
