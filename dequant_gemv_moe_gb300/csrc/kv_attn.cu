@@ -88,7 +88,6 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
   p.out_dtype = a->out_dtype;
   p.out_stride = a->out_stride;
   p.lse = a->lse;
-  p.ws = (uint8_t*)ws;
   // Requests with at most kStreamRows rows per K/V head stream.  If one may have more, so that the
   // tensor-core kernel is launched anyway, those with more than half as many go there: what streams is
   // then a launch of its own beside it (one request of 45 rows among prompts: 11 us more as a stream).

@@ -360,6 +360,18 @@ DQ_HD void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, in
   b = max(a, min(tb, (end - 1) / kTcTile + 1 - it.t0));
 }
 
+// W consecutive words (2 or 4) from shared memory
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
+  if (W == 4) {
+    const uint4 x = lds_u128(addr);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else {
+    const uint2 x = lds_u64(addr);
+    v[0] = x.x; v[1] = x.y;
+  }
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

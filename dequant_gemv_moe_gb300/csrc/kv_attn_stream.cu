@@ -148,18 +148,6 @@ __device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
-// W consecutive words (2 or 4) from shared memory
-template <int W>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
-  if (W == 4) {
-    const uint4 x = lds_u128(addr);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  } else {
-    const uint2 x = lds_u64(addr);
-    v[0] = x.x; v[1] = x.y;
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(StreamCfg<D>::NTH, 1)
 kv_stream_kernel(const __grid_constant__ AttnParams p) {

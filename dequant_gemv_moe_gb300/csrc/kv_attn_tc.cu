@@ -183,7 +183,9 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t p
 }
 constexpr uint32_t kBRowsAlongN = 1u << 16;
 
-// the 8 codes of a word as c - 8: four pairs, in the order of the nibble pairs
+// The 8 codes of a word as c - 8: four pairs, in the order of the nibble pairs.  By the well-known exponent
+// trick: a nibble or-ed into the mantissa of 1024 is 1024 + c, or 1024 + 16 c one nibble up; one addition, or one
+// FMA with 1/16, takes off what is too much.
 __device__ __forceinline__ void decode8(uint32_t w, __half2 (&c)[4]) {
   const __half2 bias = u32_as_h2(0x64086408u);        // 1032
   const __half2 sixteenth = u32_as_h2(0x2C002C00u), m72 = u32_as_h2(0xD480D480u);
@@ -205,17 +207,6 @@ __device__ __forceinline__ void sts_u128(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
                : "memory");
-}
-
-template <int W>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* v) {
-  if (W == 4) {
-    const uint4 x = lds_u128(addr);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  } else {
-    const uint2 x = lds_u64(addr);
-    v[0] = x.x; v[1] = x.y;
-  }
 }
 
 // The power of two that brings a row's largest magnitude into [2^14, 2^15) (1 for a row of zeros).

@@ -5,7 +5,7 @@ prompts of their own lengths and then decode token by token.
 Per step, all on the GPU and with no length read by the host:
   kv_plan       the step's pages, slots and query rows from the requests' lengths
   qgemv         x -> q | k | v (Q4_K weights)
-  kv_append     k, v rows (fp32, slices of that product) into the cache as Q4_0 blocks
+  kv_append     k, v rows (fp32; v as the slice of that product) into the cache as Q4_0 blocks
   kv_attention  the query rows over the cache
   qgemv         attention output -> hidden
   moe_forward   the layer's experts
@@ -62,7 +62,7 @@ class Layer:
         qkv = self.linear(self.w_qkv, self.n_qkv, self.hidden, self.norm(x))
         q, k, v = (t.view(T, -1, D) for t in qkv.split([H * D, self.kv_heads * D, self.kv_heads * D], 1))
         q, k = self.norm(q), self.norm(k).float() * 2.0     # per head, as recent models do
-        dq.kv_append(cache, k, v.contiguous(), plan.slots)
+        dq.kv_append(cache, k, v, plan.slots)               # v: the slice of the product as it is
         att, lse = dq.kv_attention(cache, q, plan.q_start, plan.kv_len, table, max_q_len=max_q_len, ws=ws)
         x = x + 1e-2 * self.linear(self.w_out, self.hidden, H * D, att.view(T, H * D))
         return x + 1e-3 * dq.moe_forward(self.desc, self.norm(x)), q, att, lse
