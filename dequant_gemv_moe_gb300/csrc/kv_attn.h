@@ -324,7 +324,8 @@ using StreamWalk = Walk<8, 32, 1>;
 // a row sees few of them its lse and weights carry it (rel. 4e-5 in the lse of a 17-token prompt).  There K is
 // taken as two exact fp16 products, with the scale's top 8 bits and with the rest, and Q K^T as two sums; the
 // second one takes the K half of a second decoded buffer.
-// (7 prompts up to 3001 tokens, 12 heads of 64: 144 us with it, 133 us without.)
+// (7 prompts up to 3001 tokens, 12 heads of 64: 142 us so, 136 with one product everywhere, 180 with two.
+// The long chunk, none of whose rows sees that few: 935 us so, 1856 with two products.)
 constexpr int kFineTokens = 1024;
 DQ_HD bool is_fine(const AttnParams& p, const Item& it) {
   return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;

@@ -33,11 +33,13 @@
 // in another CTA (again at most two partials) is left to kv_stream_join_kernel.  The
 // order of every sum is fixed, so results do not depend on timing.
 //
-// What bounds it: HBM, and next to it the issue of the decoding (a warp's tile of 32 tokens and
-// 8 rows takes 1.3 us with heads of 128 when 12 warps share an SM, which is 6.4 TB/s).  64
-// requests of up to 16384 tokens, 8 K/V heads of 128, 576 MB: 108 us, 5.3 TB/s, 79 % of what a copy
-// reaches; 3 requests of up to 131072 tokens the same share.  Rows above 8 decode the
-// page again: 20 requests of up to 42 rows 39 us for 36 MB.
+// What bounds it: next to HBM the decoding of a tile, a chain of loads, products and exponentials that three
+// warps a scheduler do not hide (issue in 57 % of the cycles, ALU pipe 51 %): a warp's tile of 32 tokens
+// and 8 rows takes 1.3 us with heads of 128 when 12 warps share an SM, which is 6.4 TB/s at most.  64
+// requests of up to 16384 tokens, 8 K/V heads of 128, 576 MB: 106 us, 5.4 TB/s, 80 % of what a copy
+// reaches; 3 requests of up to 131072 tokens 81 %; the 64 requests with heads of 256 200 us, 84 %, with heads
+// of 64, whose tile has half the bytes for the same fixed work, 79 us, 53 %.  Rows above 8 decode the
+// page again: 20 requests of up to 42 rows 38 us for 36 MB.
 //
 // Each warp has a ring of tiles filled by its own bulk copies (a tile of a page
 // is one contiguous run), all but one in flight while one is computed.

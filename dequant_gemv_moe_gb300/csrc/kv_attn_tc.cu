@@ -15,7 +15,10 @@
 //   a tile's weights passes 2^15: fp16 weights stay between 2^8 and 2^15 at the top, no
 //   maximum is taken of most tiles, and O, which lives in tensor memory, is rescaled a
 //   few times per row at most.  Rounding K, V and p to fp16 (2^-11 each) is the price of
-//   16-bit operands; S, M, the sum of p and O are fp32.
+//   16-bit operands; S, M, the sum of p and O are fp32.  (Against 64 bits, norm over norm: fp32 outputs
+//   2.8e-4 for 7 prompts of heads of 64, 4.0e-4 for the long chunk below, of which fp16 and bf16 outputs
+//   round off 2.1e-4 and 1.7e-3; lse 6.0e-6 and 2.6e-6.  The streaming kernel, which takes K exactly:
+//   1.6e-4 to 2.1e-4, lse 1.2e-7.)
 //
 // Roles.  Warp groups of the row tiles do the softmax (a thread per row); eight
 // warps decode; one warp copies the pages' blocks (bulk copies, 32 tokens at a
@@ -27,13 +30,13 @@
 // head, token tile) units in equal shares, one per CTA, the partials of items
 // that cross shares joined in order by a second kernel.
 //
-// What bounds it: the instructions of the softmax (160 for 64 scores) and of the
-// decoding (13 for 8 values) beside each other on four schedulers that issue in 0.61 of
-// all cycles; the tensor pipe is busy in half of them.  2 requests' chunks of 2048 tokens
-// over up to 16384, 32 query heads on 8 of 128: 943 us, 1.24 PFLOP/s.  Left out for a
-// measurement, the decoding's arithmetic takes 15 % of the time, the exponentials none,
-// three quarters of the products 6 %.  Four warps decoding and 64 scores a thread at a time
-// take 966 us, two warps to a row 1088 (registers).
+// What bounds it: the turns that softmax, decoding and products take.  The softmax (160
+// instructions for 64 scores) and the decoding (13 for 8 values) share four schedulers that
+// issue in 0.59 of the cycles, the tensor pipe is busy in half of them, and neither is full.  2
+// requests' chunks of 2048 tokens over up to 16384, 32 query heads on 8 of 128: 935 to 945 us, 1.24
+// PFLOP/s.  Left out for a measurement (of 955 us then), the decoding's arithmetic took 15 % of
+// the time, the exponentials none, three quarters of the products 6 %.  Four warps decoding and 64
+// scores a thread at a time took 966 us, two warps to a row 1088 (registers).
 #include <algorithm>
 #include <type_traits>
 
@@ -824,7 +827,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 // take the rows of the item that starts in CTA c's share and goes on behind it, four
 // values of a row per thread.  Bound by latency (partials are in L2), so all of it runs at
 // once: kJoinRows rows a thread whose loads overlap, and few registers.  (7 prompts, 12
-// heads of 64: 12.5 us with a warp to a row and 87 registers, @J2@ us so.)
+// heads of 64: 12.5 us with a warp to a row and 87 registers, 6.6 us so.)
 constexpr int kJoinRows = 2;
 template <int D>
 constexpr int kJoinPass = 256 / (D / 4);   // rows a CTA takes at once

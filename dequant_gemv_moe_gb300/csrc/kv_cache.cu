@@ -136,8 +136,10 @@ constexpr int kRowsUnroll = 2;   // chunks per thread, their loads all in flight
 // layout; for V two lanes whose groups are neighbours exchange halves of their
 // units, so that each stores one word too.
 //
-// Bound by latency for a step (64 tokens, 8 heads of 128: 2.7 us) and by issue for a
-// prompt (8191 tokens, bf16: 13 us, 43 MB at 3.3 TB/s; the ALU pipe 69 % busy).  1, 2
+// Bound by latency for a step (64 tokens, 8 heads of 128: 2.7 us).  A prompt (8191
+// tokens, bf16: 13 us, 43 MB at 3.3 TB/s) is near no single limit: range, quotient, clamp and packing of
+// each value keep issue and the ALU pipe busy in 69 % of the cycles, beside HBM at half.  fp32 rows
+// with one true division each, appended and read back: 38 us for 8191 tokens, 4.1 TB/s.  1, 2
 // and 4 chunks a thread take 25.4, 23.1 and 22.5 us with the reading back, and four leave a
 // step on too few CTAs.  K and V are different CTAs: with both in one thread it was 31 us.
 template <int D, int DT, bool V>
@@ -188,7 +190,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv_append_kernel(const __grid_co
 }
 
 // The way back, by the same chunks: the codes' words are gathered, whole rows are written.
-// (8191 tokens, 8 heads of 128, bf16: 10.5 us, 43 MB at 4.1 TB/s.)
+// (8191 tokens, 8 heads of 128, bf16: 10.5 us, 43 MB at 4.1 TB/s: below HBM's rate because V's units, two tokens
+// side by side, are gathered by 2-byte loads, two a lane.)
 template <int D, int DT, bool V>
 __device__ __forceinline__ void read_rows(const KvRows& p) {
   using B = KvBlk<D>;

@@ -188,6 +188,11 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
     kv_plan leaves them; scale: head_dim ** -0.5 unless given; max_q_len: the
     most rows a request has (T unless given; a step that says 1 is one launch or two
     instead of four).  ws: kv_attention_workspace_size bytes for these T and max_q_len, or more.
+
+    Sums are fp32, operands fp16: weights are rounded to it, and where a request has
+    many rows V and K as decoded too.  Whatever out_dtype is, out carries 1.5e-4 to
+    4e-4 of its size from that; lse 1e-7, or up to 6e-6 for many rows that see more
+    than 1024 tokens.
     """
     T, H, D = q.shape
     qs, qh, qd = q.stride()

@@ -541,8 +541,12 @@ int dq_kv_read(const dq_kv_cache* cache, const int64_t* slots, int T, void* k, v
  *   lse = log sum_j e^{s_j}.
  * A row that sees nothing (kv_len 0, a position below 0) gets out = 0 and
  * lse = -inf.  The new tokens' own K/V are in the cache already (dq_kv_append).
- * The pages are read once for up to 8 rows per K/V head; 16-bit operands with
- * fp32 sums, so fp32 queries are refused (as dq_moe_forward). */
+ * The pages are read once for up to 8 rows per K/V head.  Sums are fp32, operands fp16, so fp32
+ * queries are refused (as dq_moe_forward) and fp32 outputs hold no more than those give:
+ * weights are rounded to fp16, and times V's scale once more; where a request has more than
+ * 64 rows per K/V head (32 if max_q_len allows more than 64), V as decoded is rounded, and so is K for
+ * rows that see more than 1024 tokens.  That leaves out off by 1.5e-4 to 4e-4 of its size, and
+ * lse by 1e-7, or up to 6e-6 where K is rounded. */
 typedef struct {
   const void* q;              /* device [T][n_q_heads][head_dim], 16-byte aligned */
   int64_t q_stride;           /* elements between two rows' first heads, a multiple of 8 */
