@@ -34,6 +34,12 @@ class MoeDesc(ctypes.Structure):
                 ("sh_gate", _P), ("sh_up", _P), ("sh_down", _P)]
 
 
+class MoeRoutingDesc(ctypes.Structure):
+    _fields_ = [("scores", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias", _P)]
+
+
 class KvCacheDesc(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
@@ -68,6 +74,11 @@ _SIGS = {
 _OPTIONAL_SIGS = {
     "dq_moe_workspace_size": [ctypes.POINTER(MoeDesc), _I, _P],
     "dq_moe_router": [_P, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P],
+    "dq_moe_route": [_P, _I, _I64, _I, _I, _I, _P, _P, _P, _P],
+    "dq_moe_router_ex": [_P, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P],
+    "dq_moe_forward_ex": [ctypes.POINTER(MoeDesc), _P, _P, _I, _I, _P, _P, _SZ, _P, _P, _P, _P],
+    "dq_moe_forward_noalloc_ex": [ctypes.POINTER(MoeDesc), _P, _P, _I, _I, _P, _P, _P, _P, _P],
+    "dq_expert_cache_set_routing": [_P, _P],
     "dq_moe_permute": [_P, _I, _I, _I, _P, _P, _P],
     "dq_moe_forward": [ctypes.POINTER(MoeDesc), _P, _I, _I, _P, _P, _SZ, _P, _P, _P, _P],
     "dq_moe_forward_noalloc": [ctypes.POINTER(MoeDesc), _P, _I, _I, _P, _P, _P, _P, _P],

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "moe_plan.h"
+#include "moe_route.h"
 #include "stream_cache.h"
 
 namespace dqmoe {
@@ -94,8 +95,10 @@ int check_desc(const dq_moe_desc* d, int T) {
 
 int dqmoe::moe_forward_checked(const dq_moe_desc* desc, const void* x, int x_dtype, int T,
                                float* y, void* ws, size_t ws_bytes, int32_t* topk_idx,
-                               float* topk_gate, float* logits, void* stream, bool side) {
+                               float* topk_gate, float* logits, void* stream, bool side,
+                               const dq_moe_routing* routing) {
   int rc = check_desc(desc, T);
+  if (rc == DQ_OK && routing) rc = check_routing(routing, desc->E, desc->top_k);
   if (rc != DQ_OK) return rc;
   if (!x || !y || !dtype_ok(x_dtype)) return DQ_ERR_ARG;
   // the experts run on 16-bit tensor-core operands: fp32 activations would
@@ -109,7 +112,7 @@ int dqmoe::moe_forward_checked(const dq_moe_desc* desc, const void* x, int x_dty
   if (!aligned(ws, 256)) return DQ_ERR_ALIGN;
   if (ws_bytes < moe_plan(*desc, T).total) return DQ_ERR_WORKSPACE;
   return launch_moe_forward(*desc, x, x_dtype, T, y, ws, topk_idx, topk_gate, logits,
-                            (cudaStream_t)stream, nullptr, 3, side);
+                            (cudaStream_t)stream, nullptr, 3, side, routing);
 }
 
 extern "C" {
@@ -161,15 +164,26 @@ int dq_moe_workspace_size(const dq_moe_desc* desc, int T, size_t* bytes) {
 
 int dq_moe_router(const float* router_W, int E, int H, const void* x, int x_dtype, int T,
                   int top_k, float* logits, int32_t* topk_idx, float* topk_gate, void* stream) {
+  return dq_moe_router_ex(router_W, E, H, x, x_dtype, T, top_k, nullptr, logits, topk_idx, topk_gate, stream);
+}
+
+int dq_moe_router_ex(const float* router_W, int E, int H, const void* x, int x_dtype, int T,
+                     int top_k, const dq_moe_routing* routing, float* logits, int32_t* topk_idx,
+                     float* topk_gate, void* stream) {
   if (!router_W || !x || !logits || !topk_idx || !topk_gate || !dtype_ok(x_dtype)) return DQ_ERR_ARG;
   if (E <= 0 || H <= 0 || T <= 0 || top_k <= 0 || top_k > E || H % 32) return DQ_ERR_ARG;
   if (E > 256 || top_k > 8 || T > 65536) return DQ_ERR_UNSUPPORTED;
+  int rc = routing ? check_routing(routing, E, top_k) : DQ_OK;
+  if (rc != DQ_OK) return rc;
   if (!aligned(router_W, 4) || !aligned(x, 4) || !aligned(logits, 4) || !aligned(topk_idx, 4) ||
       !aligned(topk_gate, 4))
     return DQ_ERR_ALIGN;
   // one hidden-dimension slice: the logits buffer holds the single partial sum
-  return launch_router(router_W, E, H, x, x_dtype, T, top_k, 1, logits, logits, topk_idx,
-                       topk_gate, (cudaStream_t)stream);
+  rc = launch_router(router_W, E, H, x, x_dtype, T, top_k, 1, logits, logits, topk_idx,
+                     topk_gate, (cudaStream_t)stream, !routing);
+  if (rc != DQ_OK || !routing) return rc;
+  return launch_route(logits, DQ_F32, E, 1, T, E, top_k, *routing, nullptr, topk_idx, topk_gate,
+                      (cudaStream_t)stream);
 }
 
 int dq_moe_permute(const int32_t* topk_idx, int T, int top_k, int E, int32_t* offsets,
@@ -182,10 +196,16 @@ int dq_moe_permute(const int32_t* topk_idx, int T, int top_k, int E, int32_t* of
 int dq_moe_forward(const dq_moe_desc* desc, const void* x, int x_dtype, int T, float* y, void* ws,
                    size_t ws_bytes, int32_t* topk_idx, float* topk_gate, float* logits,
                    void* stream) {
-  return dqmoe::moe_forward_checked(desc, x, x_dtype, T, y, ws, ws_bytes, topk_idx, topk_gate,
-                                    logits, stream, true);
+  return dq_moe_forward_ex(desc, nullptr, x, x_dtype, T, y, ws, ws_bytes, topk_idx, topk_gate, logits,
+                           stream);
 }
 
+int dq_moe_forward_ex(const dq_moe_desc* desc, const dq_moe_routing* routing, const void* x,
+                      int x_dtype, int T, float* y, void* ws, size_t ws_bytes, int32_t* topk_idx,
+                      float* topk_gate, float* logits, void* stream) {
+  return dqmoe::moe_forward_checked(desc, x, x_dtype, T, y, ws, ws_bytes, topk_idx, topk_gate,
+                                    logits, stream, true, routing);
+}
 
 int dq_expert_cache_create(const dq_moe_desc* d, int slots, void* slot_gate, void* slot_up,
                            void* slot_down, int max_tokens, int phases, dq_expert_cache** cache) {
@@ -246,6 +266,17 @@ int dq_moe_forward_streamed(dq_expert_cache* cache, const void* x, int x_dtype, 
   if (ws_bytes < dqmoe::stream_workspace(*cache, T, &a, &b)) return DQ_ERR_WORKSPACE;
   return dqmoe::stream_forward(cache, x, x_dtype, T, y, ws, (cudaStream_t)stream,
                                (cudaStream_t)copy_stream);
+}
+
+int dq_expert_cache_set_routing(dq_expert_cache* cache, const dq_moe_routing* routing) {
+  if (!cache) return DQ_ERR_ARG;
+  if (routing) {
+    const int rc = check_routing(routing, cache->d.E, cache->d.top_k);
+    if (rc != DQ_OK) return rc;
+    cache->routing = *routing;
+  }
+  cache->routed = routing != nullptr;
+  return DQ_OK;
 }
 
 int dq_expert_cache_stats(const dq_expert_cache* cache, long long* hits, long long* misses,

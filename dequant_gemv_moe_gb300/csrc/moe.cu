@@ -23,6 +23,7 @@
 #include <utility>
 
 #include "moe_plan.h"
+#include "moe_route.h"
 #include "qgemv_mma.cuh"
 #include "tmap.h"
 
@@ -1361,7 +1362,7 @@ struct ForkJoin {
 // ms (nullable): the streamed layer's slot cache and copy/compute phases.
 int launch_moe_forward(const dq_moe_desc& d, const void* x, int xdt, int T, float* y, void* ws,
                        int32_t* topk_idx, float* topk_gate, float* logits, cudaStream_t s,
-                       const MoeStream* ms, int stages, bool side) {
+                       const MoeStream* ms, int stages, bool side, const dq_moe_routing* routing) {
   const MoePlan pl = moe_plan(d, T, ms == nullptr);
   uint8_t* w = (uint8_t*)ws;
   float* part = (float*)(w + pl.off_part);
@@ -1380,10 +1381,12 @@ int launch_moe_forward(const dq_moe_desc& d, const void* x, int xdt, int T, floa
   int rc = DQ_OK;
   // up to 32 tokens in one call: the permute CTA takes the top-k too (one
   // warp per token), one launch less on the decode path
-  const bool fuse_topk = (stages & 3) == 3 && T <= 32;
+  const bool fuse_topk = (stages & 3) == 3 && T <= 32 && !routing;
   if (stages & 1) {
     rc = launch_router(d.router_W, d.E, d.hidden, x, xdt, T, d.top_k, pl.KS, part, lg, idx, gate,
-                       s, !fuse_topk);
+                       s, !fuse_topk && !routing);
+    if (rc == DQ_OK && routing)
+      rc = launch_route(part, DQ_F32, d.E, pl.KS, T, d.E, d.top_k, *routing, lg, idx, gate, s);
     if (rc != DQ_OK) return rc;
   }
   if (!(stages & 2)) return DQ_OK;

@@ -56,6 +56,13 @@ int scratch_on_current_device(cudaStream_t stream, void** out) {
 extern "C" int dq_moe_forward_noalloc(const dq_moe_desc* desc, const void* x, int x_dtype, int T,
                                       float* y, int32_t* topk_idx, float* topk_gate,
                                       float* logits, void* stream) {
+  return dq_moe_forward_noalloc_ex(desc, nullptr, x, x_dtype, T, y, topk_idx, topk_gate, logits, stream);
+}
+
+extern "C" int dq_moe_forward_noalloc_ex(const dq_moe_desc* desc, const dq_moe_routing* routing,
+                                         const void* x, int x_dtype, int T, float* y,
+                                         int32_t* topk_idx, float* topk_gate, float* logits,
+                                         void* stream) {
   using namespace dqmoe;
   size_t need = 0;
   const int rc = dq_moe_workspace_size(desc, T, &need);
@@ -66,5 +73,5 @@ extern "C" int dq_moe_forward_noalloc(const dq_moe_desc* desc, const void* x, in
   if (src != DQ_OK) return src;
   // one stream only: the layer's second stream would be created on first use
   return moe_forward_checked(desc, x, x_dtype, T, y, ws, (size_t)DQ_NOALLOC_SCRATCH_BYTES,
-                             topk_idx, topk_gate, logits, stream, false);
+                             topk_idx, topk_gate, logits, stream, false, routing);
 }

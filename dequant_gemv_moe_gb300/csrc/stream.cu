@@ -91,7 +91,8 @@ int stream_forward(dq_expert_cache* c, const void* x, int xdt, int T, float* y, 
   ms.slots = c->slots;
 
   // 1. routing on the device, read back
-  int rc = launch_moe_forward(d, x, xdt, T, y, ws, nullptr, nullptr, nullptr, s, &ms, 1);
+  int rc = launch_moe_forward(d, x, xdt, T, y, ws, nullptr, nullptr, nullptr, s, &ms, 1, true,
+                              c->routed ? &c->routing : nullptr);
   if (rc != DQ_OK) return rc;
   const int P = T * d.top_k;
   if (cudaMemcpyAsync(c->h_idx, w + pl.off_idx, (size_t)P * 4, cudaMemcpyDeviceToHost, s) !=

@@ -28,4 +28,6 @@ struct dq_expert_cache {
   cudaEvent_t gu_ready[dqmoe::kMaxStreamPhases];
   cudaEvent_t dn_ready[dqmoe::kMaxStreamPhases];
   long long hits, misses, bytes_copied;
+  bool routed = false;    // `routing` is used instead of the layer's own
+  dq_moe_routing routing;
 };

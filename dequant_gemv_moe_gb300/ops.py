@@ -3,13 +3,24 @@ import ctypes
 
 import torch
 
-from ._lib import F16, F32, BF16, DqError, MoeDesc, lib
+from ._lib import F16, F32, BF16, DqError, MoeDesc, MoeRoutingDesc, lib
 
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t):
+    """The handle of the current stream; t has to lie on the current device, where kernels are launched."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors lie on device %d, the current device is %d" % (dev, torch.cuda.current_device()))
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _ptr(t):
@@ -102,14 +113,70 @@ def moe_workspace_size(desc, T):
     return n.value
 
 
-def moe_router(router_W, E, H, x, top_k, logits=None):
+class MoeRouting:
+    """How a layer's tokens choose their experts (dq_moe_routing of include/dqmoe.h).
+
+    scores: "softmax" or "sigmoid"; bias: fp32 CUDA tensor [E] added to the scores for the choice alone, or
+    None; n_groups groups of experts, of which a token keeps the top_groups best by group_score, "max" or "top2"
+    (the sum of the two largest); renormalize: gates are shares of the chosen scores' sum; scale: of the gates.
+    """
+
+    def __init__(self, scores="softmax", bias=None, n_groups=1, top_groups=1, group_score="max", renormalize=True,
+                 scale=1.0):
+        if scores not in ("softmax", "sigmoid") or group_score not in ("max", "top2"):
+            raise ValueError('scores are "softmax" or "sigmoid", group_score is "max" or "top2"')
+        if bias is not None and (bias.dtype is not torch.float32 or not bias.is_cuda or not bias.is_contiguous() or
+                                 bias.dim() != 1):
+            raise ValueError("bias must be a contiguous CUDA tensor [E] of float32")
+        self.bias = bias
+        self.desc = MoeRoutingDesc(int(scores == "sigmoid"), n_groups, top_groups, int(group_score == "top2"),
+                                   int(bool(renormalize)), scale, bias.data_ptr() if bias is not None else None)
+        self._ref = ctypes.byref(self.desc)
+
+    def check(self, E, dev):
+        if self.bias is not None and (self.bias.numel() != E or self.bias.get_device() != dev):
+            raise ValueError("the routing's bias must hold %d experts' on device %d" % (E, dev))
+        return self._ref
+
+
+_DEFAULT_ROUTING = MoeRouting()
+_route = lib.dq_moe_route
+
+
+def moe_route(logits, top_k, routing=None, out=None):
+    """The experts and gates of logits [T][E] (fp32/fp16/bf16; the row stride is free): (int32 [T][top_k],
+    fp32 [T][top_k]).  routing: a MoeRouting (softmax over all experts, renormalised, unless given)."""
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor [T][E] with consecutive experts")
+    T, E = logits.shape
+    dev = logits.get_device()
+    ref = (routing or _DEFAULT_ROUTING).check(E, dev)
+    if out is None:
+        out = (torch.empty(T, top_k, dtype=torch.int32, device=logits.device),
+               torch.empty(T, top_k, dtype=torch.float32, device=logits.device))
+    idx, gate = out
+    if (idx.dtype is not torch.int32 or gate.dtype is not torch.float32 or idx.shape != (T, top_k) or
+            gate.shape != (T, top_k) or idx.get_device() != dev or gate.get_device() != dev or
+            not idx.is_contiguous() or not gate.is_contiguous()):
+        raise ValueError("out must be contiguous CUDA tensors [%d][%d] of int32 and float32 on device %d" %
+                         (T, top_k, dev))
+    if T:
+        rc = _route(logits.data_ptr(), _dtype_code(logits), logits.stride(0) if T > 1 else E, T, E, top_k, ref,
+                    idx.data_ptr(), gate.data_ptr(), _stream_of(logits))
+        if rc != 0:
+            raise DqError("dq_moe_route", rc)
+    return out
+
+
+def moe_router(router_W, E, H, x, top_k, logits=None, routing=None):
     T = x.shape[0]
     dev = x.device
     if logits is None:
         logits = torch.empty(T, E, dtype=torch.float32, device=dev)
     idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
     gate = torch.empty(T, top_k, dtype=torch.float32, device=dev)
-    _call("dq_moe_router", _ptr(router_W), E, H, _ptr(x), _dtype_code(x), T, top_k, _ptr(logits),
+    ref = routing.check(E, x.get_device()) if routing is not None else None
+    _call("dq_moe_router_ex", _ptr(router_W), E, H, _ptr(x), _dtype_code(x), T, top_k, ref, _ptr(logits),
           _ptr(idx), _ptr(gate), _stream())
     return logits, idx, gate
 
@@ -123,8 +190,9 @@ def moe_permute(topk_idx, E):
     return offsets, sorted_
 
 
-def moe_forward(desc, x, y=None, ws=None, want_routing=False):
-    """The whole MoE layer.  Returns y (and idx, gate, logits if want_routing)."""
+def moe_forward(desc, x, y=None, ws=None, want_routing=False, routing=None):
+    """The whole MoE layer.  Returns y (and idx, gate, logits if want_routing).
+    routing: a MoeRouting in place of the layer's softmax top-k."""
     T = x.shape[0]
     dev = x.device
     if y is None:
@@ -137,7 +205,8 @@ def moe_forward(desc, x, y=None, ws=None, want_routing=False):
         idx = torch.empty(T, desc.top_k, dtype=torch.int32, device=dev)
         gate = torch.empty(T, desc.top_k, dtype=torch.float32, device=dev)
         logits = torch.empty(T, desc.E, dtype=torch.float32, device=dev)
-    _call("dq_moe_forward", ctypes.byref(desc), _ptr(x), _dtype_code(x), T, _ptr(y), _ptr(ws),
+    ref = routing.check(desc.E, x.get_device()) if routing is not None else None
+    _call("dq_moe_forward_ex", ctypes.byref(desc), ref, _ptr(x), _dtype_code(x), T, _ptr(y), _ptr(ws),
           ws.numel(), _ptr(idx), _ptr(gate), _ptr(logits), _stream())
     if want_routing:
         return y, idx, gate, logits
@@ -156,7 +225,7 @@ class ExpertCache:
 
     def __init__(self, E, top_k, hidden, ffn, n_shared, fmt, router_W, host_w_gate, host_w_up,
                  host_w_down, sh_gate=None, sh_up=None, sh_down=None, slots=None,
-                 max_tokens=1, phases=2):
+                 max_tokens=1, phases=2, routing=None):
         self.desc = make_desc(E, top_k, hidden, ffn, n_shared, fmt, router_W, host_w_gate,
                               host_w_up, host_w_down, sh_gate, sh_up, sh_down)
         self._keep = (router_W, host_w_gate, host_w_up, host_w_down, sh_gate, sh_up, sh_down)
@@ -173,7 +242,14 @@ class ExpertCache:
         _call("dq_expert_cache_create", ctypes.byref(self.desc), slots, _ptr(self.slot_gate),
               _ptr(self.slot_up), _ptr(self.slot_down), max_tokens, phases, ctypes.byref(h))
         self.handle = h
+        self.set_routing(routing)
         self.copy_stream = torch.cuda.Stream(device=dev)
+
+    def set_routing(self, routing):
+        """The routing of the calls that follow: a MoeRouting, or None for the layer's softmax top-k."""
+        ref = routing.check(self.desc.E, self.slot_gate.get_device()) if routing is not None else None
+        _call("dq_expert_cache_set_routing", self.handle, ref)
+        self.routing = routing
 
     def workspace_size(self, T):
         n = ctypes.c_size_t()

@@ -346,6 +346,65 @@ int dq_moe_forward_noalloc(const dq_moe_desc* desc, const void* x, int x_dtype, 
                            void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Routing other than the layer's own: models balance their experts by a bias */
+/* on the scores, score them by a sigmoid, and send a token to few groups of  */
+/* experts only.                                                             */
+/*   s_e   = sigmoid(l_e), or softmax(l)_e over all E                        */
+/*   v_e   = s_e + bias_e                                                    */
+/*   The E experts are n_groups groups of E / n_groups consecutive ones.  A   */
+/*   group's score is the largest v in it, or the sum of its two largest     */
+/*   (of its only one); the top_groups best groups are kept, the lowest first */
+/*   among equal ones.                                                       */
+/*   sel   = the top_k largest v of the kept groups, in descending order, the */
+/*           lowest index first among equal ones                             */
+/*   gate  = scale * s_e / (sum over sel of s + 1e-20), or scale * s_e        */
+/* The selection is that of exact arithmetic on the given logits (values that */
+/* fp32 cannot tell apart are compared in 64 bits); gates are fp32.  A logit  */
+/* that is -inf or NaN takes its expert out: it is chosen only where nothing  */
+/* else is left (the lowest index first), with gate 0; +inf counts as the     */
+/* largest float.  A bias is finite.                                         */
+/* ------------------------------------------------------------------------ */
+#define DQ_ROUTE_SOFTMAX 0
+#define DQ_ROUTE_SIGMOID 1
+#define DQ_ROUTE_GROUP_MAX 0
+#define DQ_ROUTE_GROUP_TOP2 1
+typedef struct {
+  int32_t scores;       /* DQ_ROUTE_SOFTMAX or DQ_ROUTE_SIGMOID */
+  int32_t n_groups;     /* divides E; 1: no groups.  1, 2, 4, 8, 16 or 32 */
+  int32_t top_groups;   /* 1..n_groups, with at least top_k experts */
+  int32_t group_score;  /* DQ_ROUTE_GROUP_MAX or DQ_ROUTE_GROUP_TOP2 */
+  int32_t renormalize;  /* 0 or 1 */
+  float scale;          /* > 0 */
+  const float* bias;    /* device fp32 [E], 4-byte aligned, or NULL */
+} dq_moe_routing;
+
+/* dq_moe_route — the selection and the gates of T tokens from their logits.
+ *   logits   : device, rows of E values of `dtype` (F32, F16, BF16), `stride`
+ *              elements apart (>= E), aligned to their element.
+ *   topk_idx : device int32 [T][top_k]; topk_gate: device fp32 [T][top_k].
+ * Errors: DQ_ERR_ARG (null, sizes, a malformed routing), DQ_ERR_ALIGN,
+ *         DQ_ERR_UNSUPPORTED (E > 256, top_k > 8, other n_groups), DQ_ERR_CUDA. */
+int dq_moe_route(const void* logits, int dtype, int64_t stride, int T, int E, int top_k,
+                 const dq_moe_routing* routing, int32_t* topk_idx, float* topk_gate, void* stream);
+
+/* dq_moe_router_ex — dq_moe_router with a routing (NULL: dq_moe_router).
+ * Errors: as dq_moe_router and, for the routing, dq_moe_route. */
+int dq_moe_router_ex(const float* router_W, int E, int H, const void* x, int x_dtype, int T,
+                     int top_k, const dq_moe_routing* routing, float* logits, int32_t* topk_idx,
+                     float* topk_gate, void* stream);
+
+/* dq_moe_forward_ex, dq_moe_forward_noalloc_ex — the layer with a routing (NULL: as without _ex): the
+ * selection and the gates are those that dq_moe_route gives for the layer's logits, all else is as it is
+ * there, the shared experts' weight of 1 and the workspace's size too.
+ * Errors: as dq_moe_forward, dq_moe_forward_noalloc and, for the routing, dq_moe_route. */
+int dq_moe_forward_ex(const dq_moe_desc* desc, const dq_moe_routing* routing, const void* x,
+                      int x_dtype, int T, float* y, void* ws, size_t ws_bytes, int32_t* topk_idx,
+                      float* topk_gate, float* logits, void* stream);
+int dq_moe_forward_noalloc_ex(const dq_moe_desc* desc, const dq_moe_routing* routing, const void* x,
+                              int x_dtype, int T, float* y, int32_t* topk_idx, float* topk_gate,
+                              float* logits, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Expert streaming: the routed experts in page-locked host memory, a device */
 /* cache of expert slots ([Titan Engine, §MoE 专家流式加载]: experts loaded   */
 /* on demand, an LRU cache of hot experts, asynchronous loads hiding the     */
@@ -400,6 +459,10 @@ int dq_expert_cache_workspace_size(const dq_expert_cache* cache, int T, size_t* 
  *         dq_moe_forward), DQ_ERR_WORKSPACE, DQ_ERR_CUDA. */
 int dq_moe_forward_streamed(dq_expert_cache* cache, const void* x, int x_dtype, int T, float* y,
                             void* ws, size_t ws_bytes, void* stream, void* copy_stream);
+
+/* The routing of the calls that follow (NULL: the layer's own).  It is copied; its bias has to stay where it is
+ * until the cache is destroyed or has another routing.  Errors: as dq_moe_route's routing. */
+int dq_expert_cache_set_routing(dq_expert_cache* cache, const dq_moe_routing* routing);
 
 /* Cumulative counts: experts found in the cache, experts copied, bytes copied. */
 int dq_expert_cache_stats(const dq_expert_cache* cache, long long* hits, long long* misses,
