@@ -46,6 +46,14 @@ class KvCacheDesc(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("pages", _P)]
 
 
+class KvRope(ctypes.Structure):
+    _fields_ = [("q", _P), ("q_stride", ctypes.c_int64), ("k", _P), ("k_stride", ctypes.c_int64), ("v", _P),
+                ("v_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("slots", _P), ("positions", _P), ("inv_freq", _P),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float),
+                ("q_out", _P), ("out_stride", ctypes.c_int64), ("out_dtype", ctypes.c_int32)]
+
+
 class KvAttn(ctypes.Structure):
     _fields_ = [("q", _P), ("q_stride", ctypes.c_int64), ("q_dtype", ctypes.c_int32),
                 ("n_q_heads", ctypes.c_int32), ("T", ctypes.c_int32), ("B", ctypes.c_int32),
@@ -67,6 +75,7 @@ _SIGS = {
     "dq_kv_cache_size": [_P, _P],
     "dq_kv_plan": [_P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P],
     "dq_kv_append": [_P, _P, _I64, _P, _I64, _I, _P, _I, _P],
+    "dq_kv_append_rope": [_P, _P, _P],
     "dq_kv_read": [_P, _P, _I, _P, _P, _I, _P],
     "dq_kv_attention_workspace_size": [_P, _I, _I, _I, _I, _P],
     "dq_kv_attention": [_P, _P, _P, _SZ, _P],

@@ -4,11 +4,11 @@ import ctypes
 
 import torch
 
-from ._lib import F16, F32, BF16, Q4_0, DqError, KvAttn, KvCacheDesc, lib
+from ._lib import F16, F32, BF16, Q4_0, DqError, KvAttn, KvCacheDesc, KvRope, lib
 
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-_plan, _append, _read, _attention = (lib.dq_kv_plan, lib.dq_kv_append, lib.dq_kv_read,
-                                     lib.dq_kv_attention)
+_plan, _append, _read, _attention, _rope = (lib.dq_kv_plan, lib.dq_kv_append, lib.dq_kv_read,
+                                            lib.dq_kv_attention, lib.dq_kv_append_rope)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 # A decode step's calls take a few microseconds on the GPU, so the wrappers keep to few Python
@@ -16,9 +16,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(t):
-    """The handle of the current stream of t's device."""
+    """The handle of the current stream; t has to lie on the current device, where kernels are launched."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors lie on device %d, the current device is %d" % (dev, torch.cuda.current_device()))
     if _raw_stream is not None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(dev)
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -150,6 +153,57 @@ def kv_append(cache, k, v, slots):
                      _stream(k))
         if rc != 0:
             _raise("dq_kv_append", rc)
+
+
+def _heads(t, D, dev, name):
+    """The row stride of t [T][heads][D], whose heads are consecutive."""
+    if t.dim() != 3:
+        raise ValueError("%s must be [T][heads][%d]" % (name, D))
+    T, H, d = t.shape
+    a, b, c = t.stride()
+    if d != D or t.get_device() != dev or c != 1 or (b != D and H > 1) or t.dtype not in _DT:
+        raise ValueError("%s must be a CUDA tensor [T][heads][%d] of float32, float16 or bfloat16 on device %d "
+                         "with consecutive heads" % (name, D, dev))
+    return a if T > 1 else H * D
+
+
+def kv_append_rope(cache, q, k, v, slots, positions, inv_freq, interleaved=False, factor=1.0, out=None,
+                   out_dtype=None):
+    """kv_append of k rotated by its positions, and q rotated: the rows [T][n_q_heads][head_dim] of out.
+
+    q, k, v: rows of one type (fp32/fp16/bf16; the token strides are free); q may be None.  positions int32 [T]:
+    rows below 0 are left out; slots int64 [T] as kv_append's.  inv_freq fp32 [rotary_dim / 2]: the first
+    rotary_dim values of a head turn, in pairs half of them apart or, interleaved, next to one another;
+    factor: of cos and sin.  out: fp32/fp16/bf16 rows (out_dtype, q's unless given); q itself may be given.
+    K's codes are those of the rotated values before any rounding.
+    """
+    T, D, dev = k.shape[0], cache.head_dim, cache.dev
+    if k.dtype != v.dtype or k.dtype not in _DT or v.shape[0] != T:
+        raise ValueError("k and v must be rows of one dtype: float32, float16 or bfloat16")
+    ks, vs = _rows(cache, k, "k"), _rows(cache, v, "v")
+    _check(slots, "slots", torch.int64, dev, (T,))
+    _check(positions, "positions", torch.int32, dev, (T,))
+    _check(inv_freq, "inv_freq", torch.float32, dev)
+    a = KvRope(None, 0, k.data_ptr(), ks, v.data_ptr(), vs, _DT[k.dtype], 0, T, slots.data_ptr(),
+               positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), interleaved, factor, None, 0, 0)
+    if q is not None:
+        qs = _heads(q, D, dev, "q")
+        if q.dtype != k.dtype or q.shape[0] != T:
+            raise ValueError("q must be rows of k's dtype")
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        a.q, a.q_stride, a.n_q_heads = q.data_ptr(), qs, q.shape[1]
+        a.q_out, a.out_stride = out.data_ptr(), _heads(out, D, dev, "out")
+        a.out_dtype = _DT[out.dtype]
+    elif out is not None:
+        raise ValueError("out is for q's rows")
+    if T:
+        rc = _rope(cache._ref, ctypes.byref(a), _stream(k))
+        if rc != 0:
+            _raise("dq_kv_append_rope", rc)
+    return out
 
 
 def kv_read(cache, slots, dtype=torch.float32, out=None):

@@ -588,6 +588,41 @@ int dq_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int B, int page_s
 int dq_kv_append(const dq_kv_cache* cache, const void* k, int64_t k_stride, const void* v,
                  int64_t v_stride, int dtype, const int64_t* slots, int T, void* stream);
 
+/* dq_kv_append_rope — dq_kv_append with the rotation by position on the way, of k and of the step's q rows.
+ * Of the first rotary_dim values of a head, the pairs (a, b) = (x[i], x[i + rotary_dim / 2]), or
+ * (x[2i], x[2i + 1]) if interleaved, become
+ *   a' = factor * (a cos - b sin),  b' = factor * (b cos + a sin),  angle = position * inv_freq[i];
+ * the others stay.  q' is rounded once to out_dtype (rotations are fp32: off by 5e-7 of |a| + |b|; angles are
+ * exact to 2e-7 at positions below 2^24, to 1e-6 above).  k' is not rounded before it becomes blocks: codes and
+ * scales are those of k' in 64 bits, with dq_kv_append's formula in exact arithmetic.  v is written as dq_kv_append
+ * writes it.  Infinite and NaN values are out of contract.
+ * A row with a position below 0 (dq_kv_plan's rows behind the last token) is left out: neither its q row nor
+ * the cache is written.  A row whose slot lies outside the cache has its q row alone. */
+typedef struct {
+  const void* q;            /* device [T][n_q_heads][head_dim] of dtype, 16-byte aligned; NULL: no q */
+  int64_t q_stride;         /* elements between two rows, as k_stride and v_stride a multiple of 16 bytes */
+  const void* k;            /* device [T][n_kv_heads][head_dim] of dtype, 16-byte aligned */
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  int32_t dtype;            /* DQ_F32, DQ_F16 or DQ_BF16 */
+  int32_t n_q_heads;        /* 1..4096 */
+  int32_t T;                /* rows, >= 1 */
+  const int64_t* slots;     /* device [T], as dq_kv_append's */
+  const int32_t* positions; /* device [T] */
+  const float* inv_freq;    /* device fp32 [rotary_dim / 2], radians per position */
+  int32_t rotary_dim;       /* a multiple of 16 (others: DQ_ERR_UNSUPPORTED), <= head_dim */
+  int32_t interleaved;      /* 0 or 1 */
+  float factor;             /* of cos and sin: 1, or a long-context scheme's; in (0, 1e4] */
+  void* q_out;              /* device [T][n_q_heads][head_dim] of out_dtype, 16-byte aligned: apart from q, or q
+                               itself with its stride and type */
+  int64_t out_stride;       /* a multiple of 16 bytes */
+  int32_t out_dtype;
+} dq_kv_rope;
+
+/* Errors: DQ_ERR_ARG, DQ_ERR_ALIGN, DQ_ERR_UNSUPPORTED, DQ_ERR_CUDA. */
+int dq_kv_append_rope(const dq_kv_cache* cache, const dq_kv_rope* args, void* stream);
+
 /* dq_kv_read — the values that T slots stand for, d * (code - 8) rounded once
  * to `dtype`; zeros for a slot outside the cache.
  *   k, v : device [T][n_kv_heads][head_dim] of `dtype`, 16-byte aligned.
