@@ -64,6 +64,10 @@ class KvAttn(ctypes.Structure):
                 ("lse", _P)]
 
 
+class KvScores(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", _P), ("prefix_len", _P), ("first_pos", _P)]
+
+
 _SIGS = {
     "dq_block_geometry": [_I, _P, _P],
     "dq_dequant": [_I, _P, _I64, _P, _P],
@@ -79,6 +83,7 @@ _SIGS = {
     "dq_kv_read": [_P, _P, _I, _P, _P, _I, _P],
     "dq_kv_attention_workspace_size": [_P, _I, _I, _I, _I, _P],
     "dq_kv_attention": [_P, _P, _P, _SZ, _P],
+    "dq_kv_attention_ex": [_P, _P, _P, _P, _SZ, _P],
 }
 _OPTIONAL_SIGS = {
     "dq_moe_workspace_size": [ctypes.POINTER(MoeDesc), _I, _P],

@@ -10,6 +10,10 @@ namespace {
 // 16000 tokens): 134 us streaming, 257 us on the tensor core; they meet at about 64 rows.
 constexpr int kStreamRows = 64;
 
+// tanh(u) / u in powers of u^2: interpolated at the Chebyshev points of [0, 1]
+constexpr double kTanh[7] = {0.9999999486455697,  -0.333328279786008,    0.13325076146118553, -0.053451646370382085,
+                             0.02027970828675751, -0.006194324834556632, 0.0010380250969887872};
+
 int attn_sizes_ok(const dq_kv_cache* cache, int n_q_heads, int T, int B, int max_q_len) {
   if (n_q_heads <= 0 || T <= 0 || B <= 0 || max_q_len <= 0 || max_q_len > T) return DQ_ERR_ARG;
   if (n_q_heads % cache->n_kv_heads) return DQ_ERR_ARG;
@@ -41,6 +45,11 @@ int dq_kv_attention_workspace_size(const dq_kv_cache* cache, int n_q_heads, int 
 
 int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, size_t ws_bytes,
                     void* stream) {
+  return dq_kv_attention_ex(cache, a, nullptr, ws, ws_bytes, stream);
+}
+
+int dq_kv_attention_ex(const dq_kv_cache* cache, const dq_kv_attn* a, const dq_kv_scores* x, void* ws,
+                       size_t ws_bytes, void* stream) {
   AttnParams p;
   int rc = kv_check(cache, &p.g, true);
   if (rc != DQ_OK) return rc;
@@ -56,11 +65,14 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
       a->out_stride > (1LL << 31) || !(a->scale > 0.f) || !(a->scale <= 3.4e38f) ||
       (a->causal != 0 && a->causal != 1) || a->window < 0)
     return DQ_ERR_ARG;
+  if (x && x->softcap != 0.f && !(x->softcap >= 0.01f && x->softcap <= 1e6f)) return DQ_ERR_ARG;
   // fp32 queries would be held to a bar that 16-bit operands cannot meet
   if (a->q_dtype == DQ_F32) return DQ_ERR_UNSUPPORTED;
   if (!kv_aligned(a->q, 16) || !kv_aligned(a->out, 16) || a->q_stride % 8 || a->out_stride % 8 ||
       !kv_aligned(a->q_start, 4) || !kv_aligned(a->kv_len, 4) || !kv_aligned(a->block_table, 4) ||
       !kv_aligned(a->lse, 4))
+    return DQ_ERR_ALIGN;
+  if (x && (!kv_aligned(x->slopes, 4) || !kv_aligned(x->prefix_len, 4) || !kv_aligned(x->first_pos, 4)))
     return DQ_ERR_ALIGN;
   size_t need = 0;
   rc = dq_kv_attention_workspace_size(cache, a->n_q_heads, a->T, a->B, a->max_q_len, &need);
@@ -88,6 +100,13 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
   p.out_dtype = a->out_dtype;
   p.out_stride = a->out_stride;
   p.lse = a->lse;
+  const bool ext = x && (x->softcap != 0.f || x->slopes || x->prefix_len || x->first_pos);
+  p.cap = ext ? (float)(x->softcap * 1.4426950408889634) : 0.f;
+  p.cap_inv = p.cap > 0.f ? 1.f / p.cap : 1.f;
+  for (int k = 0; k < 7; ++k) p.cap_c[k] = (float)(kTanh[k] * p.cap);
+  p.slopes = ext ? x->slopes : nullptr;
+  p.prefix = ext && a->causal ? x->prefix_len : nullptr;
+  p.first_pos = ext ? x->first_pos : nullptr;
   // Requests with at most kStreamRows rows per K/V head stream.  If one may have more, so that the
   // tensor-core kernel is launched anyway, those with more than half as many go there: what streams is
   // then a launch of its own beside it (one request of 45 rows among prompts: 11 us more as a stream).
@@ -96,12 +115,12 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* a, void* ws, siz
   p.alone = 0;
   p.rows_upto = many ? kStreamRows / 2 : kStreamRows;
   p.ws = (uint8_t*)ws;
-  rc = launch_kv_stream(p, cache->head_dim, (cudaStream_t)stream);
+  rc = launch_kv_stream(p, cache->head_dim, ext, (cudaStream_t)stream);
   if (rc != DQ_OK || !many) return rc;
   p.rows_above = p.rows_upto;
   p.rows_upto = 1 << 30;
   p.ws = (uint8_t*)ws + kv_stream_workspace();
-  return launch_kv_tc(p, cache->head_dim, (cudaStream_t)stream);
+  return launch_kv_tc(p, cache->head_dim, ext, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -27,14 +27,21 @@ struct AttnParams {
   uint8_t* ws;
   int rows_above, rows_upto;   // the kernel looks after requests with rows_above < rows <= rows_upto
   int alone;                   // streaming: 0, or every row tile has a CTA of its own, and a request this many
+  // what the kernels with EXT read besides (dq_kv_scores)
+  float cap;                   // of a score in units of log 2, 0: none
+  float cap_inv;               // its inverse
+  float cap_c[7];              // times tanh's polynomial (soft_cap)
+  const float* slopes;         // per query head, or null
+  const int32_t* prefix;       // per request, or null
+  const int32_t* first_pos;    // per row of q, or null
 };
 
-// few rows per K/V head (kv_attn_stream.cu)
+// few rows per K/V head (kv_attn_stream.cuh); ext: scores and masks other than the plain ones
 size_t kv_stream_workspace();
-int launch_kv_stream(const AttnParams& p, int head_dim, cudaStream_t s);
-// many rows (kv_attn_tc.cu)
+int launch_kv_stream(const AttnParams& p, int head_dim, bool ext, cudaStream_t s);
+// many rows (kv_attn_tc.cuh)
 size_t kv_tc_workspace();
-int launch_kv_tc(const AttnParams& p, int head_dim, cudaStream_t s);
+int launch_kv_tc(const AttnParams& p, int head_dim, bool ext, cudaStream_t s);
 
 #define DQ_HD __host__ __device__ __forceinline__
 
@@ -83,8 +90,13 @@ DQ_HD int q_rows(const AttnParams& p, int r, int* first, int* all) {
   // memory-safe whatever q_start holds
   return a < 0 ? 0 : max(0, min(min(b, p.T) - a, p.max_q_len));
 }
-// A row at `pos` sees the positions below this one.
-DQ_HD int seen_end(const AttnParams& p, int len, int pos) { return p.causal ? max(0, min(len, pos + 1)) : len; }
+// A row at `pos` sees the positions below this one; of a request with a prefix, those in it too.
+DQ_HD int seen_end(const AttnParams& p, int len, int pos, int prefix = 0) {
+  return p.causal ? max(0, min(len, max(pos + 1, prefix))) : len;
+}
+// The prefix of request r, and the first position that row `row` of q may see.
+DQ_HD int prefix_of(const AttnParams& p, int r) { return p.prefix ? max(load_length(p.prefix + r), 0) : 0; }
+DQ_HD int row_first(const AttnParams& p, int row) { return p.first_pos ? max(load_length(p.first_pos + row), 0) : 0; }
 
 
 // One row tile of a request and the tokens that its rows may see.
@@ -94,16 +106,19 @@ struct Item {
   int shift;                   // position of its first token
   int begin, end;              // tokens that some row sees
   int t0, tiles;               // first tile, tiles (at least one)
+  int prefix, fine;            // EXT: the request's prefix; whether its last row sees few tokens (is_fine)
 };
+
+constexpr int kFineTokens = 1024;          // (see is_fine)
 
 // A call's work as one line of units: (request, row tile, K/V head, tile of
 // TILE tokens), the tokens fastest.  An item (all of them but the tokens) takes
 // OV units before its tiles: what starting and ending one costs.  A tile takes one
-// unit, or WEIGHT::of(item).
+// unit, or WEIGHT::of(item).  EXT: rows may have a prefix and a first position.
 struct UnitWeight {
   DQ_HD static int of(const AttnParams&, const Item&) { return 1; }
 };
-template <int ROWS, int TILE, int OV, typename WEIGHT = UnitWeight>
+template <int ROWS, int TILE, int OV, typename WEIGHT = UnitWeight, bool EXT = false>
 struct Walk {
   DQ_HD static int cost(const AttnParams& p, const Item& it) {
     return it.tiles * WEIGHT::of(p, it) + OV;
@@ -111,8 +126,15 @@ struct Walk {
   DQ_HD static void range(const AttnParams& p, Item& it) {
     it.rows = min(ROWS, it.qlen * p.group - it.row0);
     const int lo = it.shift + row_token(p, it.row0), hi = it.shift + row_token(p, it.row0 + it.rows - 1);
-    it.end = seen_end(p, it.len, hi);
+    it.end = seen_end(p, it.len, hi, EXT ? it.prefix : 0);
     it.begin = first_seen(p, lo);
+    if (EXT) {
+      // first positions ascend within a request: the first row's is the least, the last row's the largest
+      const int last = row_first(p, it.first + hi - it.shift);
+      it.begin = min(max(it.begin, row_first(p, it.first + lo - it.shift)), it.end);
+      const int span = it.end - last;
+      it.fine = (p.window > 0 ? min(p.window, span) : span) <= kFineTokens;
+    }
     it.t0 = it.begin / TILE;
     it.tiles = it.end > it.begin ? (it.end - 1) / TILE + 1 - it.t0 : 1;
   }
@@ -137,6 +159,7 @@ struct Walk {
       it.len = kv_length(p, r);
       it.shift = it.len - all;
     }
+    if (EXT) it.prefix = prefix_of(p, r);
   }
   // Units of the row tiles k, k + step, .. of the request in `it` (one head's).
   DQ_HD static int64_t row_tile_units(const AttnParams& p, Item& it, int k, int step) {
@@ -160,6 +183,7 @@ struct Walk {
       } while (it.qlen == 0);
       it.len = kv_length(p, it.r);
       it.shift = it.len - all;
+      if (EXT) it.prefix = prefix_of(p, it.r);
     }
     range(p, it);
   }
@@ -189,7 +213,7 @@ struct Walk {
     for (int i = 0; i < chunk; ++i) {
       const int r = threadIdx.x * chunk + i;
       if (r < p.B) request(p, r, it);
-      else it.qlen = it.len = it.first = it.shift = 0;
+      else it.qlen = it.len = it.first = it.shift = it.prefix = 0;
       // a request of few row tiles by its thread, one of many by the warp
       const bool few = (int64_t)it.qlen * p.group <= 8 * ROWS;
       if (few) u += row_tile_units(p, it, 0, 1) * p.g.heads;
@@ -199,6 +223,10 @@ struct Walk {
         x.qlen = __shfl_sync(0xffffffffu, it.qlen, src);
         x.len = __shfl_sync(0xffffffffu, it.len, src);
         x.shift = __shfl_sync(0xffffffffu, it.shift, src);
+        if (EXT) {
+          x.first = __shfl_sync(0xffffffffu, it.first, src);
+          x.prefix = __shfl_sync(0xffffffffu, it.prefix, src);
+        }
         int64_t n = row_tile_units(p, x, lane, 32);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -318,7 +346,9 @@ DQ_HD int share_of(int64_t u, int N, int64_t U) {
 }
 
 // Few rows: 8 rows and tiles of 32 tokens, a tile's worth for starting and ending an item.
-using StreamWalk = Walk<8, 32, 1>;
+template <bool EXT>
+using StreamWalkOf = Walk<8, 32, 1, UnitWeight, EXT>;
+using StreamWalk = StreamWalkOf<false>;
 
 // Rounding K to fp16 moves a score by about 2^-12 of itself.  Over many tokens that averages out, but where
 // a row sees few of them its lse and weights carry it (rel. 4e-5 in the lse of a 17-token prompt).  There K is
@@ -326,14 +356,21 @@ using StreamWalk = Walk<8, 32, 1>;
 // second one takes the K half of a second decoded buffer.
 // (7 prompts up to 3001 tokens, 12 heads of 64: 142 us so, 136 with one product everywhere, 180 with two.
 // The long chunk, none of whose rows sees that few: 935 us so, 1856 with two products.)
-constexpr int kFineTokens = 1024;
 DQ_HD bool is_fine(const AttnParams& p, const Item& it) {
   return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;
 }
 
+// With first positions it is the last row's tokens that count (a document that begins among the rows has
+// rows that see few).
+template <bool EXT>
+DQ_HD bool is_fine_of(const AttnParams& p, const Item& it) {
+  return EXT ? it.fine != 0 : is_fine(p, it);
+}
+
 // Two sums for a score, and half the decoded buffers: such a tile takes about twice as long.
-struct TcWeight {
-  DQ_HD static int of(const AttnParams& p, const Item& it) { return is_fine(p, it) ? 2 : 1; }
+template <bool EXT>
+struct TcWeightOf {
+  DQ_HD static int of(const AttnParams& p, const Item& it) { return is_fine_of<EXT>(p, it) ? 2 : 1; }
 };
 
 // Many rows: row tiles of 128 rows, two a CTA (one for head_dim 256), and tiles of 64 tokens; starting and
@@ -341,8 +378,8 @@ struct TcWeight {
 constexpr int kTcTile = 64;
 template <int D>
 constexpr int kTcRowTiles = D == 256 ? 1 : 2;
-template <int D>
-using TcWalk = Walk<128 * kTcRowTiles<D>, kTcTile, 4, TcWeight>;
+template <int D, bool EXT = false>
+using TcWalk = Walk<128 * kTcRowTiles<D>, kTcTile, 4, TcWeightOf<EXT>, EXT>;
 // a line of U units is cut into this many shares, of two units at least: none inside an item is without a tile
 DQ_HD int tc_shares(int ctas, int64_t U) { return (int)min((int64_t)ctas, U / 2); }
 
@@ -350,12 +387,15 @@ DQ_HD int tc_shares(int ctas, int64_t U) { return (int)min((int64_t)ctas, U / 2)
 // tile is done before its last one, a windowed item's last one starts behind its first one (with one head
 // to a K/V head two tiles behind, which may be behind tb), and rows behind the item's end see nothing.
 // ta <= a <= b <= tb, so that the tiles before, in and behind are the tb - ta that the share decodes.
+template <bool EXT = false>
 DQ_HD void row_tile_range(const AttnParams& p, const Item& it, int i, int ta, int tb, int& a, int& b) {
   a = b = ta;
   const int last = min(it.rows, 128 * i + 128) - 1;
   if (last < 128 * i) return;
-  const int end = seen_end(p, it.len, it.shift + row_token(p, it.row0 + last));
-  const int begin = first_seen(p, it.shift + row_token(p, it.row0 + 128 * i));
+  const int end = seen_end(p, it.len, it.shift + row_token(p, it.row0 + last), EXT ? it.prefix : 0);
+  const int tok = row_token(p, it.row0 + 128 * i);
+  int begin = first_seen(p, it.shift + tok);
+  if (EXT) begin = max(begin, row_first(p, it.first + tok));
   if (end <= begin) return;
   a = min(tb, max(ta, begin / kTcTile - it.t0));
   b = max(a, min(tb, (end - 1) / kTcTile + 1 - it.t0));
@@ -382,6 +422,27 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr float kLeastScale = 1.17549435e-38f;   // of a row's scores: times 0, a masked score would be NaN
 constexpr float kNone = -1e30f;           // the running maximum of a row that has seen nothing
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Capped scores in units of log 2 from u = score / cap.  tanh(u) / u is a polynomial in u^2 of degree 6 where
+// |u| <= 1 (its Chebyshev interpolation: 2.5e-7 of itself, fp32's roundings included); beyond, tanh(|u|) = 1 - 2 / (1 + e^2|u|), whose
+// terms do not cancel there.
+__device__ __forceinline__ float2 soft_cap(const AttnParams& p, float2 u) {
+  const float2 y = fmul2(u, u);
+  float2 r = make_float2(p.cap_c[6], p.cap_c[6]);
+#pragma unroll
+  for (int k = 5; k >= 0; --k) r = ffma2(r, y, make_float2(p.cap_c[k], p.cap_c[k]));
+  return fmul2(r, u);
+}
+__device__ __forceinline__ float soft_cap_far(const AttnParams& p, float u) {
+  return copysignf(p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fabsf(u) * (2.f * kLog2e))), u);
+}
+
 
 template <int DT>
 __device__ __forceinline__ void store_dims4(void* out, int64_t at, const float (&x)[4]) {

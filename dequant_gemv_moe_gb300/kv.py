@@ -4,11 +4,11 @@ import ctypes
 
 import torch
 
-from ._lib import F16, F32, BF16, Q4_0, DqError, KvAttn, KvCacheDesc, KvRope, lib
+from ._lib import F16, F32, BF16, Q4_0, DqError, KvAttn, KvCacheDesc, KvRope, KvScores, lib
 
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _plan, _append, _read, _attention, _rope = (lib.dq_kv_plan, lib.dq_kv_append, lib.dq_kv_read,
-                                            lib.dq_kv_attention, lib.dq_kv_append_rope)
+                                            lib.dq_kv_attention_ex, lib.dq_kv_append_rope)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 # A decode step's calls take a few microseconds on the GPU, so the wrappers keep to few Python
@@ -234,7 +234,8 @@ def kv_attention_workspace_size(cache, n_q_heads, B, T, max_q_len=None):
 
 
 def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True, window=0,
-                 max_q_len=None, out=None, out_dtype=None, lse=None, ws=None):
+                 max_q_len=None, out=None, out_dtype=None, lse=None, ws=None, softcap=0.0, slopes=None,
+                 prefix_len=None, first_pos=None):
     """Attention of q [T][n_q_heads][head_dim] (fp16/bf16; the row stride is
     free) over the cache: (out, lse), lse fp32 [T][n_q_heads].
 
@@ -242,6 +243,10 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
     kv_plan leaves them; scale: head_dim ** -0.5 unless given; max_q_len: the
     most rows a request has (T unless given; a step that says 1 is one launch or two
     instead of four).  ws: kv_attention_workspace_size bytes for these T and max_q_len, or more.
+
+    softcap: scores become softcap * tanh(scores / softcap); slopes fp32 [n_q_heads]: a head's scores lose its
+    slope times the distance; prefix_len int32 [B]: the rows of a request see the positions below it whatever
+    their own; first_pos int32 [T], not descending within a request: a row sees no position below it.
 
     Sums are fp32, operands fp16: weights are rounded to it, and where a request has
     many rows V and K as decoded too.  Whatever out_dtype is, out carries 1.5e-4 to
@@ -284,5 +289,18 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
                kv_len.data_ptr(), block_table.data_ptr(), block_table.shape[1], max_q_len,
                D ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
                os if T > 1 else H * D, _DT[out.dtype], lse.data_ptr())
-    rc = _attention(cache._ref, ctypes.byref(a), ws.data_ptr(), ws.nbytes, _stream(q))
+    x = None
+    if softcap or slopes is not None or prefix_len is not None or first_pos is not None:
+        x = KvScores(softcap)
+        if slopes is not None:
+            _check(slopes, "slopes", torch.float32, dev, (H,))
+            x.slopes = slopes.data_ptr()
+        if prefix_len is not None:
+            _check(prefix_len, "prefix_len", torch.int32, dev, (B,))
+            x.prefix_len = prefix_len.data_ptr()
+        if first_pos is not None:
+            _check(first_pos, "first_pos", torch.int32, dev, (T,))
+            x.first_pos = first_pos.data_ptr()
+        x = ctypes.byref(x)
+    rc = _attention(cache._ref, ctypes.byref(a), x, ws.data_ptr(), ws.nbytes, _stream(q))
     return (out, lse) if rc == 0 else _raise("dq_kv_attention", rc)

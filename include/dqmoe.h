@@ -681,6 +681,28 @@ int dq_kv_attention_workspace_size(const dq_kv_cache* cache, int n_q_heads, int 
 int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* args, void* ws, size_t ws_bytes,
                     void* stream);
 
+/* dq_kv_attention_ex — dq_kv_attention with other scores and masks (NULL, or all of its fields 0: dq_kv_attention):
+ *   s_j = scale * (q . k_j);  softcap > 0: s_j = softcap * tanh(s_j / softcap);
+ *   slopes: s_j -= slopes[h] * |p - j|;
+ * and a row at position p sees what is left of
+ *   j <= p, or j < prefix_len[r]  (causal; not causal: every j);
+ *   j > p - window  (window > 0; of a prefix too);
+ *   j >= first_pos[row].
+ * So a prefix is read both ways (its rows see all of it), and rows of a request that holds several documents
+ * see their own one.  Rows that see nothing, garbage in unseen places, types, limits, the workspace: as
+ * dq_kv_attention.  Caps are held to 2.5e-7 of a score; a bias is fp32 of fp32 slopes. */
+typedef struct {
+  float softcap;              /* 0: none; else 0.01 to 1e6 */
+  const float* slopes;        /* device fp32 [n_q_heads], finite, or NULL */
+  const int32_t* prefix_len;  /* device [B], or NULL; above kv_len it reads as that, below 0 as 0 */
+  const int32_t* first_pos;   /* device [T], not descending within a request (else rows may miss positions that
+                                 they should see), or NULL; below 0 reads as 0 */
+} dq_kv_scores;
+
+/* Errors: as dq_kv_attention; DQ_ERR_ARG for another softcap. */
+int dq_kv_attention_ex(const dq_kv_cache* cache, const dq_kv_attn* args, const dq_kv_scores* scores,
+                       void* ws, size_t ws_bytes, void* stream);
+
 /* Human-readable name of a dq_status value (static string, never NULL). */
 const char* dq_status_string(int status);
 
