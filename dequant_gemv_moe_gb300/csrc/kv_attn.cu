@@ -103,7 +103,7 @@ int dq_kv_attention_ex(const dq_kv_cache* cache, const dq_kv_attn* a, const dq_k
   const bool ext = x && (x->softcap != 0.f || x->slopes || x->prefix_len || x->first_pos);
   p.cap = ext ? (float)(x->softcap * 1.4426950408889634) : 0.f;
   p.cap_inv = p.cap > 0.f ? 1.f / p.cap : 1.f;
-  for (int k = 0; k < 7; ++k) p.cap_c[k] = (float)(kTanh[k] * p.cap);
+  for (int k = 0; k < 7; ++k) p.cap_c[k].x = p.cap_c[k].y = (float)(kTanh[k] * p.cap);
   p.slopes = ext ? x->slopes : nullptr;
   p.prefix = ext && a->causal ? x->prefix_len : nullptr;
   p.first_pos = ext ? x->first_pos : nullptr;

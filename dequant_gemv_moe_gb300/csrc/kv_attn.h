@@ -30,7 +30,7 @@ struct AttnParams {
   // what the kernels with EXT read besides (dq_kv_scores)
   float cap;                   // of a score in units of log 2, 0: none
   float cap_inv;               // its inverse
-  float cap_c[7];              // times tanh's polynomial (soft_cap)
+  float2 cap_c[7];             // times tanh's polynomial, every coefficient twice (soft_cap4)
   const float* slopes;         // per query head, or null
   const int32_t* prefix;       // per request, or null
   const int32_t* first_pos;    // per row of q, or null
@@ -432,15 +432,33 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 // Capped scores in units of log 2 from u = score / cap.  tanh(u) / u is a polynomial in u^2 of degree 6 where
 // |u| <= 1 (its Chebyshev interpolation: 2.5e-7 of itself, fp32's roundings included); beyond, tanh(|u|) = 1 - 2 / (1 + e^2|u|), whose
 // terms do not cancel there.
-__device__ __forceinline__ float2 soft_cap(const AttnParams& p, float2 u) {
-  const float2 y = fmul2(u, u);
-  float2 r = make_float2(p.cap_c[6], p.cap_c[6]);
+//
+// Eight scores at a time: four chains of packed steps keep the pipe busy, and a coefficient is fetched once.
+__device__ __forceinline__ void soft_cap4(const AttnParams& p, float2 (&u)[4], bool beyond) {
+  float2 y[4], r[4];
 #pragma unroll
-  for (int k = 5; k >= 0; --k) r = ffma2(r, y, make_float2(p.cap_c[k], p.cap_c[k]));
-  return fmul2(r, u);
-}
-__device__ __forceinline__ float soft_cap_far(const AttnParams& p, float u) {
-  return copysignf(p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fabsf(u) * (2.f * kLog2e))), u);
+  for (int i = 0; i < 4; ++i) {
+    y[i] = fmul2(u[i], u[i]);
+    r[i] = p.cap_c[6];
+  }
+#pragma unroll
+  for (int k = 5; k >= 0; --k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = ffma2(r[i], y[i], p.cap_c[k]);
+  if (beyond) {
+    auto far = [&](float x) {
+      return copysignf(p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fabsf(x) * (2.f * kLog2e))), x);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = fmul2(r[i], u[i]);
+      u[i].x = fabsf(u[i].x) > 1.f ? far(u[i].x) : t.x;
+      u[i].y = fabsf(u[i].y) > 1.f ? far(u[i].y) : t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = fmul2(r[i], u[i]);
+  }
 }
 
 

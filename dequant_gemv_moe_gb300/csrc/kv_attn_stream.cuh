@@ -427,15 +427,15 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
               far = fmaxf(far, fabsf(s[k][i]));
             }
           if (p.cap > 0.f) {
-            const bool beyond = __any_sync(0xffffffffu, far > 1.f);
+            float2 u[4];
 #pragma unroll
-            for (int k = 0; k < kBlks; ++k)
+            for (int i = 0; i < 4; ++i) u[i] = make_float2(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
+            soft_cap4(p, u, __any_sync(0xffffffffu, far > 1.f));
 #pragma unroll
-              for (int i = 0; i < 4; i += 2) {
-                const float2 t = make_float2(s[k][i], s[k][i + 1]), c = soft_cap(p, t);
-                s[k][i] = beyond && fabsf(t.x) > 1.f ? soft_cap_far(p, t.x) : c.x;
-                s[k][i + 1] = beyond && fabsf(t.y) > 1.f ? soft_cap_far(p, t.y) : c.y;
-              }
+            for (int i = 0; i < 4; ++i) {
+              s[i >> 1][2 * (i & 1)] = u[i].x;
+              s[i >> 1][2 * (i & 1) + 1] = u[i].y;
+            }
           }
           if (p.slopes) {
 #pragma unroll

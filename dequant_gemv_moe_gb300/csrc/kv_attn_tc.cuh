@@ -112,6 +112,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -122,6 +138,10 @@ __device__ __forceinline__ void tmem_use(uint32_t* r) {
     asm volatile(""
                  : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
                    "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_use8(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -375,6 +395,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         lo_all = first_seen(p, pb);
         if (EXT) lo_all = max(lo_all, row_first(p, it.first + pb - it.shift));
       }
+      const float cfs = EXT && (p.cap > 0.f || p.slopes) ? 1.f : cf;      // of the scores that the softmax reads
       const float slope = EXT && p.slopes ? __ldg(p.slopes + head) * -kLog2e : 0.f;
       float M = kNone, l = 0.f;
       for (int j = 0; j < nt; ++j, ++gt) {
@@ -386,43 +407,62 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
         const bool inner = tok0 >= lo_all && tok0 <= hi_all - TT;
+        // EXT: the scores, in units of log 2, capped and biased, take their own place.  A pass of its own
+        // beside the softmax's keeps the code short (in the softmax's passes, over 16 scores at a time, it
+        // missed the instruction cache: 7188 us for cap_chunk below), and what is done again with a new M is
+        // not capped again.
+        if (EXT && (p.cap > 0.f || p.slopes)) {
+          // a bias is linear in the position on either side of the row's own
+          const bool one_side = (p.causal && !p.prefix) || __all_sync(0xffffffffu, pos >= tok0 + TT);
+#pragma unroll 1
+          for (int c = 0; c < TT; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(s_addr + c, r);
+            const float d = (float)(pos - tok0 - c);
+            tmem_wait_ld();
+            tmem_use8(r);
+            tmem_use8(r + 8);
+#pragma unroll
+            for (int h = 0; h < 16; h += 8) {
+              float2 t[4];
+              float far = 0.f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                t[i] = fmul2(make_float2(__uint_as_float(r[h + 2 * i]), __uint_as_float(r[h + 2 * i + 1])),
+                             make_float2(cf, cf));
+                far = max3(far, fabsf(t[i].x), fabsf(t[i].y));
+              }
+              if (p.cap > 0.f) soft_cap4(p, t, __any_sync(0xffffffffu, far > 1.f));
+              if (p.slopes) {
+                if (one_side) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float at = d - (float)(h + 2 * i);
+                    t[i] = ffma2(make_float2(at, at - 1.f), make_float2(slope, slope), t[i]);
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    t[i].x = fmaf(fabsf(d - (float)(h + 2 * i)), slope, t[i].x);
+                    t[i].y = fmaf(fabsf(d - (float)(h + 2 * i + 1)), slope, t[i].y);
+                  }
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                r[h + 2 * i] = __float_as_uint(t[i].x);
+                r[h + 2 * i + 1] = __float_as_uint(t[i].y);
+              }
+            }
+            tmem_st16(s_addr + c, r);
+          }
+          tmem_wait_st();
+        }
         // 32 scores of this thread's row, those that it does not see as -inf
         auto load = [&](int c, uint32_t (&r)[32]) {
           tmem_ld32(s_addr + c, r);
           tmem_wait_ld();
           tmem_use(r);
-          if (EXT) {
-            // in units of log 2 (or of the cap), capped and biased
-            const float2 cf2 = make_float2(cf, cf);
-            float far = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 t = fmul2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), cf2);
-              far = max3(far, fabsf(t.x), fabsf(t.y));
-              r[i] = __float_as_uint(t.x);
-              r[i + 1] = __float_as_uint(t.y);
-            }
-            if (p.cap > 0.f) {
-              const bool beyond = __any_sync(0xffffffffu, far > 1.f);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 t = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-                float2 y = soft_cap(p, t);
-                if (beyond) {
-                  if (fabsf(t.x) > 1.f) y.x = soft_cap_far(p, t.x);
-                  if (fabsf(t.y) > 1.f) y.y = soft_cap_far(p, t.y);
-                }
-                r[i] = __float_as_uint(y.x);
-                r[i + 1] = __float_as_uint(y.y);
-              }
-            }
-            if (p.slopes) {
-              const float d = (float)(pos - tok0 - c);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                r[i] = __float_as_uint(fmaf(fabsf(d - (float)i), slope, __uint_as_float(r[i])));
-            }
-          }
           if (!inner) {
             const int n = hi - tok0 - c;
 #pragma unroll
@@ -453,7 +493,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
                   mx4[k] = max3(mx4[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
               mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             }
-            if (!EXT) mx *= cf;
+            mx *= cfs;
             const float mn = mx > M + 9.f ? mx - 8.f : M;     // (at most M + 9: a sum of 64 2^9 at most)
             const float corr = ex2(M - mn);
             M = mn;
@@ -476,7 +516,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
               }
             }
           }
-          const float2 cf2 = make_float2(cf, cf), m2 = make_float2(-M, -M);
+          const float2 cf2 = make_float2(cfs, cfs), m2 = make_float2(-M, -M);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < TT; h += 32) {
@@ -485,8 +525,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
             // in three passes over the registers: the exponentials' latencies overlap
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              const float2 x = make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-              const float2 t = EXT ? fadd2(x, m2) : ffma2(x, cf2, m2);
+              const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), cf2, m2);
               r[k] = __float_as_uint(t.x);
               r[k + 1] = __float_as_uint(t.y);
             }
