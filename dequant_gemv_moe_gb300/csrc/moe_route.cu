@@ -8,8 +8,11 @@
 // equal ones.  The order is that of exact arithmetic:
 //  * Without a bias the scores rise with the logits, so logits are compared.
 //  * Else v is computed in fp32 (ex2 and rcp approximations) with a known bound on its error, and
-//    wherever two values that the selection has to tell apart are closer than the bound allows, the token's
-//    warp does it again in 64 bits.  (256 experts with normal logits: one token in a few hundred.)
+//    wherever two values that the selection has to tell apart are closer than the bound allows, they are formed
+//    again to 64 bits, and compared so.  (256 experts with normal logits: one token in a few hundred.  A warp's
+//    instruction in 64 bits takes some 60 cycles here, and code that runs once is fetched from far: scores
+//    come from pairs of fp32, and only those of the experts in doubt.  All 256 in 64 bits took 25 us,
+//    longer than all other tokens together.)
 //
 // A warp takes a token, eight experts a lane.  A group is 32 / n_groups neighbouring
 // lanes, so that its score is a few shuffles; lanes hold ascending experts, so
@@ -17,8 +20,12 @@
 // index.  A lane sorts its values as integer keys whose lowest three bits are the
 // place in the lane, then k + 1 rounds take the best head (one warp reduction
 // and a vote) and advance that lane's list.
-#include <algorithm>
-
+//
+// What bounds it: instructions, 760 a token (the rounds 170, keys and sort 100, scores and groups 180), with issue in
+// 0.6 of the cycles; a warp of its own for every token, so that the GPU evens out what the doubts cost.
+// 16384 tokens of 256 experts, 8 of 4 in 8 groups: 17.9 us (bytes alone: 2.7); 8 tokens 3.1 us, a
+// launch and one token's chain.  Eight tokens to a warp, four lanes each, took 560 instructions a token but 21 us:
+// too few warps to hide their chains.
 #include "common.cuh"
 #include "moe_route.h"
 
@@ -87,66 +94,131 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int64_t at) {
 // A logit as it is used: NaN and -inf take an expert out (as -inf), +inf counts as the largest float.
 __device__ __forceinline__ float usable(float x) { return x >= -kMostLogit ? fminf(x, kMostLogit) : -INFINITY; }
 
-__device__ __forceinline__ double shfl_xor_d(double x, int o) {
-  return __longlong_as_double(__shfl_xor_sync(0xffffffffu, __double_as_longlong(x), o));
+// ---------------------------------------------------------------- pairs of floats
+// A number as the sum h + l, |l| at most half a unit in the last place of h (Dekker's and Knuth's exact sums and
+// products, with FMA).
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair quick_sum(float a, float b) {          // |a| >= |b|, or a = 0
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
 }
+__device__ __forceinline__ Pair sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = sum(a.h, b.h), t = sum(a.l, b.l);
+  const Pair u = quick_sum(s.h, __fadd_rn(s.l, t.h));
+  return quick_sum(u.h, __fadd_rn(u.l, t.l));
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);
+  const float e = __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p)));
+  return quick_sum(p, e);
+}
+__device__ __forceinline__ Pair divide(Pair a, Pair b) {
+  const float q = __fdiv_rn(a.h, b.h);
+  // the rest of a - q b, over b
+  const float p = __fmul_rn(q, b.h), e = __fmaf_rn(q, b.h, -p);
+  const float r = __fadd_rn(__fsub_rn(__fsub_rn(a.h, p), e), __fmaf_rn(-q, b.l, a.l));
+  return quick_sum(q, __fdiv_rn(r, b.h));
+}
+// e^x for x <= 0: x = k ln 2 + r, the power series of e^r from its 12th term, in pairs from the 7th on.
+__device__ Pair exp_pair(Pair x) {
+  if (!(x.h > -87.f)) return {0.f, 0.f};
+  const float k = rintf(x.h * 1.44269504f);
+  // ln 2 in 16 bits, whose products with k are exact, and the rest as a pair
+  Pair r = add({x.h, x.l}, {__fmul_rn(-k, 0x1.62e4p-1f), 0.f});
+  r = add(r, mul({-k, 0.f}, {0x1.7f7d1cp-20f, 0x1.ef357ap-45f}));
+  const float f = r.h;
+  float t = 1.f / 479001600.f;             // 1 / 12!
+  t = fmaf(t, f, 1.f / 39916800.f);
+  t = fmaf(t, f, 1.f / 3628800.f);
+  t = fmaf(t, f, 1.f / 362880.f);
+  t = fmaf(t, f, 1.f / 40320.f);
+  // 1 / n! as pairs, n = 7 .. 1
+  const float ch[7] = {0x1.a01a02p-13f, 0x1.6c16c2p-10f, 0x1.111112p-7f, 0x1.555556p-5f, 0x1.555556p-3f, 0.5f, 1.f};
+  const float cl[7] = {-0x1.7f97fap-39f, -0x1.27d27ep-35f, -0x1.dddddep-32f, -0x1.555556p-30f, -0x1.555556p-28f, 0.f, 0.f};
+  Pair y = {t, 0.f};
+#pragma unroll
+  for (int i = 0; i < 7; ++i) y = add(mul(y, r), {ch[i], cl[i]});
+  y = add(mul(y, r), {1.f, 0.f});
+  const float s = exp2f(k);
+  return {y.h * s, y.l * s};
+}
+// The score of a logit: a sigmoid, or e^(x - top).
+__device__ __noinline__ Pair score_pair(int sigmoid, float x, float top) {
+  if (!sigmoid) return exp_pair(sum(x, -top));
+  // e = e^-|x| is the small one of both terms: e / (1 + e), or 1 less that
+  const Pair e = exp_pair({-fabsf(x), 0.f});
+  const Pair q = divide(e, add({1.f, 0.f}, e));
+  return x >= 0.f ? add({1.f, 0.f}, {-q.h, -q.l}) : q;
+}
+__device__ __forceinline__ Pair shfl_xor_pair(Pair a, int o) {
+  return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
+}
+// 64-bit values as whole numbers of the same order (compared four times as fast), and back.
+typedef long long Key64;
+constexpr Key64 kNoKey = -0x7ff0000000000000LL;       // below every finite value's
+__device__ __forceinline__ Key64 key64(double x) {
+  const Key64 b = __double_as_longlong(x);
+  return b ^ ((b >> 63) & 0x7fffffffffffffffLL);
+}
+__device__ __forceinline__ double value64(Key64 k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL)); }
+__device__ __forceinline__ Key64 key64(Pair a, float bias) { return key64((double)a.h + (double)a.l + (double)bias); }
 
 // The token's selection in 64 bits: lane i < k gets pick i and its score.
-// `row`: the token's logits, `fp32` if they are.
+// `row`: the token's logits, or `summed`.
 template <int DT>
 __device__ __noinline__ void route_exact(const RouteParams& p, const float* summed, int64_t row, int lane, int& pick,
-                                         double& score) {
-  const int n = lane_experts(p, lane);
-  float l[8];
-  double s[8], v[8];
-  double top = -INFINITY;
+                                         float& score) {
+  const int n = lane_experts(p, lane), e0 = expert_of(p, lane, 0);
+  float l[8], top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int e = expert_of(p, lane, j);
-    l[j] = -INFINITY;
-    if (j < n) l[j] = usable(summed ? summed[e] : logit_at<DT>(p, row + e));
-    s[j] = l[j];
-    top = fmax(top, s[j]);
+    l[j] = j < n ? usable(summed ? summed[e0 + j] : logit_at<DT>(p, row + e0 + j)) : -INFINITY;
+    top = fmaxf(top, l[j]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  Pair e[8], z = {0.f, 0.f};
+  Key64 v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    e[j] = {0.f, 0.f};
+    if (l[j] > -INFINITY) e[j] = score_pair(p.sigmoid, l[j], top);
+    z = add(z, e[j]);
   }
   if (!p.sigmoid) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmax(top, shfl_xor_d(top, o));
+    for (int o = 16; o > 0; o >>= 1) z = add(z, shfl_xor_pair(z, o));
   }
-  double z = 0.;
+  Key64 g1 = kNoKey, g2 = kNoKey;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const bool on = l[j] > -INFINITY;
-    s[j] = !on ? 0. : p.sigmoid ? 1. / (1. + exp(-s[j])) : exp(s[j] - top);
-    z += s[j];
-  }
-  if (!p.sigmoid) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += shfl_xor_d(z, o);
-  }
-  double g1 = -INFINITY, g2 = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (!p.sigmoid) s[j] = z > 0. ? s[j] / z : 0.;
+    if (!p.sigmoid && z.h > 0.f) e[j] = divide(e[j], z);
     // (without a bias logits are compared, which differ where scores of 1 or 0 do not; only sums take scores)
-    v[j] = !(l[j] > -INFINITY) ? -INFINITY
-           : p.bias            ? s[j] + (double)__ldg(p.bias + expert_of(p, lane, j))
-           : p.top2            ? s[j]
-                               : (double)l[j];
-    if (!(v[j] > -INFINITY)) v[j] = -INFINITY;
-    g2 = fmax(g2, fmin(g1, v[j]));
-    g1 = fmax(g1, v[j]);
+    if (!(l[j] > -INFINITY)) v[j] = kNoKey;
+    else if (p.bias) v[j] = key64(e[j], __ldg(p.bias + e0 + j));
+    else v[j] = p.top2 ? key64(e[j], 0.f) : key64((double)l[j]);
+    g2 = max(g2, min(g1, v[j]));
+    g1 = max(g1, v[j]);
   }
   if (p.top_groups < p.groups) {
+#pragma unroll 1
     for (int o = 1; o < 1 << p.lane_shift; o <<= 1) {
-      const double a1 = shfl_xor_d(g1, o), a2 = shfl_xor_d(g2, o);
-      g2 = fmax(fmin(g1, a1), fmax(g2, a2));
-      g1 = fmax(g1, a1);
+      const Key64 a1 = __shfl_xor_sync(0xffffffffu, g1, o), a2 = __shfl_xor_sync(0xffffffffu, g2, o);
+      g2 = max(min(g1, a1), max(g2, a2));
+      g1 = max(g1, a1);
     }
-    const double sc = p.top2 && g2 > -INFINITY ? g1 + g2 : g1;
+    const Key64 sc = p.top2 && g2 > kNoKey ? key64(value64(g1) + value64(g2)) : g1;
     const int g = lane >> p.lane_shift;
     int better = 0;
+#pragma unroll 1
     for (int x = 0; x < p.groups; ++x) {
-      const double y = __longlong_as_double(__shfl_sync(0xffffffffu, __double_as_longlong(sc), x << p.lane_shift));
+      const Key64 y = __shfl_sync(0xffffffffu, sc, x << p.lane_shift);
       better += y > sc || (y == sc && x < g) ? 1 : 0;
     }
     if (better >= p.top_groups) {
@@ -156,27 +228,29 @@ __device__ __noinline__ void route_exact(const RouteParams& p, const float* summ
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (!p.bias || !(l[j] > -INFINITY)) v[j] = l[j];
+    if (!p.bias) v[j] = key64((double)l[j]);
+    if (!(l[j] > -INFINITY)) v[j] = kNoKey;
   }
   uint32_t left = (1u << n) - 1;           // places that are not taken yet
   pick = 0;
-  score = 0.;
+  score = 0.f;
+#pragma unroll 1
   for (int r = 0; r < p.k; ++r) {
-    double best = -INFINITY, bs = 0.;
+    Key64 best = kNoKey;
+    float bs = 0.f;
     int at = 0x7fffffff;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (!(left >> j & 1)) continue;
-      const int e = expert_of(p, lane, j);
-      if (v[j] > best || at == 0x7fffffff) {
+      if ((left >> j & 1) && (at == 0x7fffffff || v[j] > best)) {
         best = v[j];
-        bs = v[j] > -INFINITY ? s[j] : 0.;
-        at = e;
+        bs = v[j] > kNoKey ? e[j].h : 0.f;
+        at = e0 + j;
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const double b = shfl_xor_d(best, o), c = shfl_xor_d(bs, o);
+      const Key64 b = __shfl_xor_sync(0xffffffffu, best, o);
+      const float c = __shfl_xor_sync(0xffffffffu, bs, o);
       const int a = __shfl_xor_sync(0xffffffffu, at, o);
       if (a != 0x7fffffff && (at == 0x7fffffff || b > best || (b == best && a < at))) {
         best = b;
@@ -188,9 +262,7 @@ __device__ __noinline__ void route_exact(const RouteParams& p, const float* summ
       pick = at;
       score = bs;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (expert_of(p, lane, j) == at && (left >> j & 1)) left &= ~(1u << j);
+    if (at >= e0 && at < e0 + n) left &= ~(1u << (at - e0));
   }
 }
 
@@ -200,28 +272,102 @@ __device__ __forceinline__ void cas_keys(uint32_t& a, uint32_t& b) {
   b = lo;
 }
 
-// Routes token t by one warp.
-template <int DT>
-__device__ __forceinline__ void route_token(const RouteParams& p, int t, int lane) {
-  const int n = lane_experts(p, lane), e0 = expert_of(p, lane, 0);
+// Batcher's odd-even merge sort of 8, descending
+__device__ __forceinline__ void sort8(uint32_t (&key)[8]) {
+#define DQ_CAS(a, b) cas_keys(key[a], key[b])
+  DQ_CAS(0, 1); DQ_CAS(2, 3); DQ_CAS(4, 5); DQ_CAS(6, 7);
+  DQ_CAS(0, 2); DQ_CAS(1, 3); DQ_CAS(4, 6); DQ_CAS(5, 7);
+  DQ_CAS(1, 2); DQ_CAS(5, 6);
+  DQ_CAS(0, 4); DQ_CAS(1, 5); DQ_CAS(2, 6); DQ_CAS(3, 7);
+  DQ_CAS(2, 4); DQ_CAS(3, 5);
+  DQ_CAS(1, 2); DQ_CAS(3, 4); DQ_CAS(5, 6);
+#undef DQ_CAS
+}
+
+// The lane's eight logits; FULL: every lane has eight, on a 16-byte boundary.
+template <int DT, bool FULL>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t at, int n, float (&l)[8]) {
+  if (FULL && DT == DQ_F32) {
+    const float4* q = (const float4*)((const float*)p.logits + at);
+    const float4 a = q[0], b = q[1];
+    l[0] = a.x; l[1] = a.y; l[2] = a.z; l[3] = a.w;
+    l[4] = b.x; l[5] = b.y; l[6] = b.z; l[7] = b.w;
+  } else if (FULL) {
+    const uint4 v = *(const uint4*)((const unsigned short*)p.logits + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = DT == DQ_F16 ? __half22float2(u32_as_h2(w[j]))
+                                    : make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+      l[2 * j] = f.x;
+      l[2 * j + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) l[j] = j < n ? logit_at<DT>(p, at + j) : -kMostLogit;
+  }
+}
+
+// How many places the lanes in front have marked in `may`, and all of them.
+__device__ __forceinline__ int count_before(uint32_t may, int lane, int& all) {
+  int upto = __popc(may);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  all = __shfl_sync(0xffffffffu, upto, 31);
+  return upto - __popc(may);
+}
+// The marked experts (32 at most) into the warp's list.
+__device__ __forceinline__ void list_experts(int* list, int at, int e0, uint32_t may) {
+  for (; may; may &= may - 1) list[at++] = e0 + __ffs(may) - 1;
+  __syncwarp();
+}
+
+// The selection from the lane's logits.  ODD: some of them are infinite or NaN.
+template <int DT, bool FULL, bool ODD>
+__device__ __forceinline__ void route_logits(const RouteParams& p, int t, int lane, float (&l)[8], const float* summed,
+                                             int64_t row, int* list);
+
+// Routes token t by one warp; `list`: the warp's 32 ints of shared memory.
+template <int DT, bool FULL>
+__device__ __forceinline__ void route_token(const RouteParams& p, int t, int lane, int* list) {
+  const int n = FULL ? 8 : lane_experts(p, lane), e0 = expert_of(p, lane, 0);
   const int64_t row = (int64_t)t * p.stride;
   float* summed = p.sum_out ? p.sum_out + (int64_t)t * p.E : nullptr;
   float l[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) l[j] = j < n ? logit_at<DT>(p, row + e0 + j) : -INFINITY;
+  load_logits<DT, FULL>(p, row + e0, n, l);
   if (summed) {
     // the partial sums in order
-    for (int q = 1; q < p.KS; ++q)
+    for (int q = 1; q < p.KS; ++q) {
+      float a[8];
+      load_logits<DT, FULL>(p, q * p.part_stride + row + e0, n, a);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n) l[j] += logit_at<DT>(p, q * p.part_stride + row + e0 + j);
+        if (FULL || j < n) l[j] += a[j];
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) summed[e0 + j] = l[j];
+      if (FULL || j < n) summed[e0 + j] = l[j];
     __syncwarp();
   }
+  // infinite logits and NaN, which few rows have
+  uint32_t most = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) l[j] = usable(l[j]);
+  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(l[j]) & 0x7FFFFFFFu);
+  if (__any_sync(0xffffffffu, most >= 0x7F800000u)) route_logits<DT, FULL, true>(p, t, lane, l, summed, row, list);
+  else route_logits<DT, FULL, false>(p, t, lane, l, summed, row, list);
+}
+
+template <int DT, bool FULL, bool ODD>
+__device__ __forceinline__ void route_logits(const RouteParams& p, int t, int lane, float (&l)[8], const float* summed,
+                                             int64_t row, int* list) {
+  const int n = FULL ? 8 : lane_experts(p, lane), e0 = expert_of(p, lane, 0);
+  if (ODD) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) l[j] = usable(l[j]);
+  }
 
   // ---- scores, where they are needed to compare
   const bool by_logit = p.bias == nullptr;
@@ -229,12 +375,13 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
   float v[8], top = 0.f, z = 1.f;
   if (!p.sigmoid) {
     top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = route_value(__reduce_max_sync(0xffffffffu, route_key(top)));
     z = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = l[j] > -INFINITY ? ex2_approx((l[j] - top) * kLog2eR) : 0.f;
+      v[j] = ex2_approx((l[j] - top) * kLog2eR);
+      if (ODD) v[j] = l[j] > -INFINITY ? v[j] : 0.f;
+      if (!FULL && j >= n) v[j] = 0.f;
       z += v[j];
     }
 #pragma unroll
@@ -247,13 +394,23 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
     for (int j = 0; j < 8; ++j) v[j] = rcp_approx(1.f + ex2_approx(l[j] * -kLog2eR));
   }
   if (!by_logit) {
+    if (FULL) {
+      const float4 a = __ldg((const float4*)(p.bias + e0)), b = __ldg((const float4*)(p.bias + e0) + 1);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] + __ldg(p.bias + e0 + j) : 0.f;
+      for (int j = 0; j < 8; ++j)
+        if (j < n) v[j] += __ldg(p.bias + e0 + j);
+    }
+  } else if (!group_sums) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = l[j];
   }
+  if (ODD || !FULL) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (by_logit && !group_sums) v[j] = l[j];
-    if (!(l[j] > -INFINITY) || !(v[j] > -INFINITY)) v[j] = -INFINITY;
+    for (int j = 0; j < 8; ++j)
+      if (j >= n || !(l[j] > -INFINITY) || !(v[j] > -INFINITY)) v[j] = -INFINITY;
   }
 
   // ---- groups.  A sigmoid is known to 3e-7 (ex2's and the product's error enter times s (1 - s) |l|, at most
@@ -261,31 +418,70 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
   // bias' sum.
   bool doubtful = false, in = true;
   if (p.top_groups < p.groups) {
-    float g1 = -INFINITY, g2 = -INFINITY;
+    float g1 = v[0], g2 = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 1; j < 8; ++j) {
       g2 = fmaxf(g2, fminf(g1, v[j]));
       g1 = fmaxf(g1, v[j]);
     }
-    for (int o = 1; o < 1 << p.lane_shift; o <<= 1) {
+    const int lanes = 1 << p.lane_shift;
+    for (int o = 1; o < lanes; o <<= 1) {
       const float a1 = __shfl_xor_sync(0xffffffffu, g1, o), a2 = __shfl_xor_sync(0xffffffffu, g2, o);
       g2 = fmaxf(fminf(g1, a1), fmaxf(g2, a2));
       g1 = fmaxf(g1, a1);
     }
     const float sc = p.top2 && g2 > -INFINITY ? g1 + g2 : g1;
+    // the groups that beat this lane's: its lanes take one other group each
     const int g = lane >> p.lane_shift;
     int better = 0;
-    for (int x = 0; x < p.groups; ++x) {
+    for (int x0 = 0; x0 < p.groups; x0 += lanes) {
+      const int x = x0 + (lane & (lanes - 1));
       const float y = __shfl_sync(0xffffffffu, sc, x << p.lane_shift);
-      better += y > sc || (y == sc && x < g) ? 1 : 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, x < p.groups && (y > sc || (y == sc && x < g)));
+      better += __popc(m >> (g << p.lane_shift) & (uint32_t)((1ULL << lanes) - 1));
     }
     in = better < p.top_groups;
     if (!by_logit || group_sums) {
       const uint32_t key = route_key(sc);
       const float worst_in = route_value(__reduce_min_sync(0xffffffffu, in ? key : 0xffffffffu));
       const float best_out = route_value(__reduce_max_sync(0xffffffffu, in ? 0u : key));
-      doubtful = worst_in > -INFINITY && best_out > -INFINITY &&
-                 worst_in - best_out <= (p.sigmoid ? 1.6e-6f : 5e-6f) + 6e-7f * (fabsf(worst_in) + fabsf(best_out));
+      const float tol = (p.sigmoid ? 1.6e-6f : 5e-6f) + 6e-7f * (fabsf(worst_in) + fabsf(best_out));
+      if (worst_in > -INFINITY && best_out > -INFINITY && worst_in - best_out <= tol) {
+        // The two largest values of the groups at the border, and what may be one of them, a lane each: the
+        // groups are ranked by their sums.
+        const bool near = sc >= best_out - tol && sc <= worst_in + tol;
+        const float least = (p.top2 && g2 > -INFINITY ? g2 : g1) - (0.5f * tol + 1e-6f * fabsf(g2 > -INFINITY ? g2 : g1));
+        uint32_t may = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) may |= j < n && near && v[j] >= least ? 1u << j : 0u;
+        int all = 0;
+        const int at = count_before(may, lane, all);
+        if (all <= 32 && p.sigmoid) {
+          list_experts(list, at, e0, may);
+          const int e = list[min(lane, all - 1)];
+          const float x = usable(summed ? summed[e] : logit_at<DT>(p, row + e));
+          const Key64 y = key64(score_pair(1, x, 0.f), p.bias ? __ldg(p.bias + e) : 0.f);
+          Key64 k1 = kNoKey, k2 = kNoKey;
+#pragma unroll 1
+          for (int i = 0; i < all; ++i) {
+            const Key64 o = __shfl_sync(0xffffffffu, y, i);
+            if (list[i] / p.per != g) continue;
+            k2 = max(k2, min(k1, o));
+            k1 = max(k1, o);
+          }
+          const Key64 sum = !near ? key64((double)sc) : p.top2 && k2 > kNoKey ? key64(value64(k1) + value64(k2)) : k1;
+          better = 0;
+#pragma unroll 1
+          for (int x = 0; x < p.groups; ++x) {
+            const Key64 o = __shfl_sync(0xffffffffu, sum, x << p.lane_shift);
+            better += o > sum || (o == sum && x < g) ? 1 : 0;
+          }
+          in = better < p.top_groups;
+          __syncwarp();
+        } else {
+          doubtful = true;
+        }
+      }
     }
   }
 
@@ -295,17 +491,11 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float x = by_logit ? l[j] : v[j];
-    key[j] = j >= n ? 0u : (!in || !(x > -INFINITY) ? 8u : route_key(x) & ~7u) | (7u - j);
+    key[j] = (in ? route_key(x) & ~7u : 8u) | (7u - j);
+    if (ODD) key[j] = x > -INFINITY ? key[j] : 8u | (7u - j);
+    if (!FULL && j >= n) key[j] = 0;
   }
-  // Batcher's odd-even merge sort of 8
-#define DQ_CAS(a, b) cas_keys(key[a], key[b])
-  DQ_CAS(0, 1); DQ_CAS(2, 3); DQ_CAS(4, 5); DQ_CAS(6, 7);
-  DQ_CAS(0, 2); DQ_CAS(1, 3); DQ_CAS(4, 6); DQ_CAS(5, 7);
-  DQ_CAS(1, 2); DQ_CAS(5, 6);
-  DQ_CAS(0, 4); DQ_CAS(1, 5); DQ_CAS(2, 6); DQ_CAS(3, 7);
-  DQ_CAS(2, 4); DQ_CAS(3, 5);
-  DQ_CAS(1, 2); DQ_CAS(3, 4); DQ_CAS(5, 6);
-#undef DQ_CAS
+  sort8(key);
   uint32_t mine = 0;
   int from = 0;
 #pragma unroll
@@ -318,34 +508,65 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
       mine = head;
       from = w;
     }
-    if (lane == w) {
+    if (lane == w) {                       // (what the rounds that are left can reach)
 #pragma unroll
-      for (int j = 0; j < 7; ++j) key[j] = key[j + 1];
-      key[7] = 0;
+      for (int j = 0; j < 8 - r; ++j) key[j] = j < 7 ? key[j + 1] : 0;
     }
   }
   // ---- two picks in a row, or the last one and the best that is left, too close to tell
+  // (fp32 logits lose three bits to the place; a value has its own error too)
+  auto tolerance = [&](float a) {
+    return by_logit ? (DT == DQ_F32 ? 2e-6f * fabsf(a) + 1e-37f : -1.f)
+                    : (p.sigmoid ? 8e-7f : 2.5e-6f) + 2.5e-6f * fabsf(a);
+  };
+  const float mine_v = route_value(mine & ~7u);
+  bool close = false;
   {
     const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
-    const float a = route_value(mine & ~7u), b = route_value(next & ~7u);
-    // fp32 logits lose three bits to the place; a value has its own error too
-    const float tol = by_logit ? (DT == DQ_F32 ? 2e-6f * fabsf(a) + 1e-37f : -1.f)
-                               : (p.sigmoid ? 8e-7f : 2.5e-6f) + 2.5e-6f * fabsf(a);
-    if (lane < p.k && next >= 16u && a - b <= tol) doubtful = true;
+    close = lane < p.k && next >= 16u && mine_v - route_value(next & ~7u) <= tolerance(mine_v);
   }
   int pick = expert_of(p, from, 7 - (int)(mine & 7u));
-  float s;
-  if (__any_sync(0xffffffffu, doubtful)) {
-    int pick64;
-    double s64;
-    route_exact<DT>(p, summed, row, lane, pick64, s64);
-    pick = pick64;
-    s = (float)s64;
-  } else {
-    s = 0.f;
-    if (lane < p.k && mine >= 16u) {
-      const float x = usable(summed ? summed[pick] : logit_at<DT>(p, row + pick));
-      s = p.sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) / z;
+  float s = 0.f;
+  if (lane < p.k && mine >= 16u) {
+    const float x = usable(summed ? summed[pick] : logit_at<DT>(p, row + pick));
+    s = p.sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) / z;
+  }
+  if (__any_sync(0xffffffffu, doubtful || close)) {
+    // The experts that may be among the picks, a lane each, where they are so few that they find room and a value
+    // can be had of a logit alone: they are ranked.
+    const float last = __shfl_sync(0xffffffffu, mine_v, p.k - 1);
+    const float least = last - fmaxf(tolerance(last), 0.f);
+    uint32_t may = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) may |= j < n && in && (by_logit ? l[j] : v[j]) >= least ? 1u << j : 0u;
+    int all = 0;
+    const int at = count_before(may, lane, all);
+    const bool few = !__any_sync(0xffffffffu, doubtful) && all <= 32 && all >= p.k && (by_logit || p.sigmoid) &&
+                     __shfl_sync(0xffffffffu, mine, p.k - 1) >= 16u;
+    if (few) {
+      list_experts(list, at, e0, may);
+      const int e = list[min(lane, all - 1)];
+      const float x = usable(summed ? summed[e] : logit_at<DT>(p, row + e));
+      const Key64 y = by_logit ? key64((double)x) : key64(score_pair(1, x, 0.f), __ldg(p.bias + e));
+      int rank = 0;
+#pragma unroll 1
+      for (int i = 0; i < all; ++i) {
+        const Key64 o = __shfl_sync(0xffffffffu, y, i);
+        rank += o > y || (o == y && i < lane) ? 1 : 0;        // (the list is in the order of experts)
+      }
+      __syncwarp();
+      if (lane < all && rank < p.k) list[rank] = e;
+      __syncwarp();
+      if (lane < p.k) {
+        pick = list[lane];
+        const float x = usable(summed ? summed[pick] : logit_at<DT>(p, row + pick));
+        s = p.sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) / z;
+      }
+      __syncwarp();
+    } else {
+      int exact_pick;
+      route_exact<DT>(p, summed, row, lane, exact_pick, s);
+      pick = exact_pick;
     }
   }
   float sum = lane < p.k ? s : 0.f;
@@ -359,13 +580,14 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
 
 constexpr int kRouteWarps = 4;
 
-template <int DT>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
+template <int DT, bool FULL>
+__global__ void __launch_bounds__(kRouteWarps * 32, 8) route_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ int list[kRouteWarps][32];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < p.T; t += (int64_t)gridDim.x * kRouteWarps)
-    route_token<DT>(p, (int)t, lane);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+  if (t < p.T) route_token<DT, FULL>(p, (int)t, lane, list[warp]);
 }
 
 }  // namespace
@@ -407,11 +629,21 @@ int launch_route(const void* logits, int dtype, int64_t stride, int KS, int T, i
   p.sum_out = sum_out;
   p.idx = idx;
   p.gate = gate;
-  const int ctas = std::min((T + kRouteWarps - 1) / kRouteWarps, 152 * 12);
-  cudaError_t e;
-  if (dtype == DQ_F32) e = launch_pdl(route_kernel<DQ_F32>, dim3(ctas), dim3(kRouteWarps * 32), 0, s, 0, p);
-  else if (dtype == DQ_F16) e = launch_pdl(route_kernel<DQ_F16>, dim3(ctas), dim3(kRouteWarps * 32), 0, s, 0, p);
-  else e = launch_pdl(route_kernel<DQ_BF16>, dim3(ctas), dim3(kRouteWarps * 32), 0, s, 0, p);
+  const int ctas = (int)(((int64_t)T + kRouteWarps - 1) / kRouteWarps);
+  // rows and bias that the lanes take in 16-byte words
+  const int el = dtype == DQ_F32 ? 4 : 2;
+  const bool full = E == 256 && (uintptr_t)logits % 16 == 0 && stride * el % 16 == 0 && (uintptr_t)r.bias % 16 == 0;
+  cudaError_t e = cudaSuccess;
+#define DQ_ROUTE(DT, FULL)        \
+  if (dtype == DT && full == FULL) \
+    e = launch_pdl(route_kernel<DT, FULL>, dim3(ctas), dim3(kRouteWarps * 32), 0, s, 0, p);
+  DQ_ROUTE(DQ_F32, true)
+  DQ_ROUTE(DQ_F16, true)
+  DQ_ROUTE(DQ_BF16, true)
+  DQ_ROUTE(DQ_F32, false)
+  DQ_ROUTE(DQ_F16, false)
+  DQ_ROUTE(DQ_BF16, false)
+#undef DQ_ROUTE
   if (e != cudaSuccess) return DQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }

@@ -358,8 +358,8 @@ int dq_moe_forward_noalloc(const dq_moe_desc* desc, const void* x, int x_dtype, 
 /*   sel   = the top_k largest v of the kept groups, in descending order, the */
 /*           lowest index first among equal ones                             */
 /*   gate  = scale * s_e / (sum over sel of s + 1e-20), or scale * s_e        */
-/* The selection is that of exact arithmetic on the given logits (values that */
-/* fp32 cannot tell apart are compared in 64 bits); gates are fp32.  A logit  */
+/* The selection is that of 64-bit arithmetic on the given logits (without a  */
+/* bias experts are compared by their logits); gates are fp32.  A logit       */
 /* that is -inf or NaN takes its expert out: it is chosen only where nothing  */
 /* else is left (the lowest index first), with gate 0; +inf counts as the     */
 /* largest float.  A bias is finite.                                         */

@@ -126,6 +126,36 @@ def test_many_tokens_and_guard_rows(dq):
     assert (idx[[0, -1]] == -7).all() and (gate[[0, -1]] == -7).all()
 
 
+@pytest.mark.parametrize("E,groups,top,k", [(256, 8, 4, 8), (256, 1, 1, 8), (160, 8, 3, 6), (60, 1, 1, 4), (16, 4, 2, 7),
+                                            (4, 1, 1, 4), (36, 1, 1, 8), (256, 8, 4, 1)])
+@pytest.mark.parametrize("scores,group_score,bias,renorm", [("sigmoid", "top2", True, True), ("sigmoid", "max", True, False),
+                                                            ("sigmoid", "top2", False, True), ("softmax", "max", False, False),
+                                                            ("sigmoid", "max", False, True), ("softmax", "top2", True, True)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_prompts(dq, E, groups, top, k, scores, group_score, bias, renorm, dtype):
+    T = 2051
+    b = np.linspace(-0.2, 0.2, E)[np.random.default_rng(E).permutation(E)] if bias else None
+    l = normal(T, E, dtype, seed=E + k)
+    if dtype == "fp32":                          # rows that a warp takes by itself: beyond the fixed point, out, tied
+        l[3] *= 20.0
+        l[100, ::2] = float("-inf")
+        l[101, 1] = float("nan")
+        l[500] = 0.25
+        l[777, : E // 2] = l[777, 0]
+        l[2050] = float("-inf")
+    check(dq, l, k, scores=scores, bias=b, n_groups=groups, top_groups=top, group_score=group_score, renormalize=renorm)
+
+
+def test_prompts_biased_beyond_the_fixed_point(dq):
+    l = normal(2048, 64, seed=1)
+    for b in (np.linspace(-5, 5, 64), np.full(64, 1.99), np.linspace(100, 101, 64)):
+        check(dq, l, 8, scores="sigmoid", bias=b, n_groups=4, top_groups=2, group_score="top2")
+    # a row stride and a base that are no multiples of four logits
+    wide = normal(2048, 70, seed=3)
+    check(dq, wide[:, 1:65], 8, scores="sigmoid", bias=np.zeros(64))
+    check(dq, wide[:, 2:66].bfloat16(), 8)
+
+
 def test_capture_and_streams(dq):
     l = normal(50, 256, seed=4)
     r = dq.MoeRouting("sigmoid", torch.zeros(256, device="cuda"), 8, 4, "top2", scale=2.5)
