@@ -4,18 +4,22 @@
 // Mathematics.  The pair (a, b) of frequency i turns by angle = position * inv_freq[i]:
 //   a' = f (a cos - b sin),  b' = f (b cos + a sin).
 // * Angles.  A position times a frequency reaches 10^6 and more, where fp32 holds no fraction of a turn.
-//   With inv_freq / 2 pi as two floats (from one product in 64 bits) the turns are a product and its
-//   exact error (FMA) and the low part's; the whole turns are taken off exactly, and what the last
-//   addition rounds off comes back as a first-order term: cos and sin within 2e-7, for positions below
-//   2^24.  Beyond, the turns are formed in 64 bits.
+//   With inv_freq / 2 pi as two floats the turns are a product and its exact error (FMA) and the low part's;
+//   the whole turns are taken off exactly, and what the last addition rounds off comes back as a first-order
+//   term: cos and sin within 2.3e-7, for positions below 2^24.  Beyond, the turns are formed in 64 bits.
 // * K's codes are those of the rotated row in 64 bits, not of its rounding: a code or a scale next to a
 //   border would otherwise depend on how the rotation was rounded, and an equal pair of largest magnitudes
 //   decides the sign of a scale.  The fp32 rotation knows its error (kErr of |a| + |b|), and where a group has
-//   a value that close to a border, that value is formed in 64 bits.  (bf16 rows, heads of 128: a
+//   a value that close to a border, that value is formed again, to 2^-44 (pair.cuh).  (bf16 rows, heads of 128: a
 //   warp's 256 values in about 250.)
-#include <algorithm>
-
+//
+// What bounds it.  A prompt of 8191 tokens (32 query heads, 8 K/V heads of 128, bf16: 177 MB) takes 44.7 us, 4.0
+// TB/s: K and V by themselves 23.4 us, which are instructions (a K value's range, bounds, quotient, clamp and
+// packing; issue in 0.58 of the cycles), q the rest, which waits for its loads (two heads' worth a lane in flight).
+// With an angle per head and thread from shared memory, and K's doubts in 64 bits, it was 96 us.  64 tokens
+// 4.7 us, of which K's doubts, one warp's or two's, are 1.6.
 #include "kv_rows.cuh"
+#include "pair.cuh"
 
 namespace dqmoe {
 
@@ -35,6 +39,8 @@ struct RopeParams {
   int interleaved;
   float factor;
   int T, q_heads;
+  int q_each, q_splits;        // heads of a warp, warps of a token
+  uint32_t k_inv;              // of the K/V heads, for row_of
   void* out;
   int64_t out_stride;
   int out_dtype;
@@ -42,57 +48,77 @@ struct RopeParams {
 };
 
 constexpr int kRopeThreads = 256;
-constexpr int kMostTile = 4;
-// of |a| + |b|: cos and sin 2e-7, their product with the factor, the product and the sum 2^-24 each
+constexpr int kMostTile = 8;             // tokens of a CTA in a long call
+constexpr int kLongCall = 1024;
+// of |a| + |b|: cos and sin 2.3e-7 with the factor's product, a product and a sum of 2^-24 each
 constexpr float kErr = 4.5e-7f;
 constexpr int kFarPosition = 1 << 24;
 constexpr float kErrFar = 2e-6f;           // (positions above it, whose turns are known to 2^-52 of themselves)
 
+// (of its own, so that nothing of it is worked out for nearer positions)
+__device__ __noinline__ float far_turns(int pos, float freq) {
+  const double t = (double)pos * ((double)freq * 0.15915494309189533577);      // 1 / 2 pi
+  return (float)(t - rint(t));
+}
+
 // cos and sin of pos * freq, times the factor
 __device__ __forceinline__ float2 turn(int pos, float freq, float factor) {
-  const double g = (double)freq * 0.15915494309189533577;        // 1 / 2 pi
-  float r, rest;
-  if (pos < kFarPosition) {
-    const float gh = (float)g, gl = (float)(g - (double)gh), p = (float)pos;
-    const float hi = p * gh, lo = fmaf(p, gl, fmaf(p, gh, -hi));
-    const float part = hi - rintf(hi);
-    r = part + lo;
-    rest = lo - (r - part);
-  } else {
-    const double t = (double)pos * g;
-    r = (float)(t - rint(t));
+  // freq / 2 pi
+  const float ch = 0x1.45f306p-3f, cl = 0x1.b9391p-28f;
+  const float gh = __fmul_rn(freq, ch), gl = fmaf(freq, cl, __fmaf_rn(freq, ch, -gh)), p = (float)pos;
+  const float hi = __fmul_rn(p, gh), lo = fmaf(p, gl, __fmaf_rn(p, gh, -hi));
+  const float part = hi - rintf(hi);
+  float r = __fadd_rn(part, lo), rest = (lo - (r - part)) * 6.2831853f;
+  if (pos >= kFarPosition) {
+    r = far_turns(pos, freq);
     rest = 0.f;
   }
   float s, c;
   sincospif(2.f * r, &s, &c);
-  rest *= 6.2831853f;
   return make_float2(fmaf(-rest, s, c) * factor, fmaf(rest, c, s) * factor);
 }
 
-// eight values that this thread may overwrite later
+// a row of `tile` tokens' heads as (token, head): floor(r / heads) by its inverse, floor(2^32 / heads) + 1
+__device__ __forceinline__ int row_of(int r, int heads, uint32_t inv, int& head) {
+  const int t = heads == 1 ? r : (int)__umulhi((uint32_t)r, inv);
+  head = r - t * heads;
+  return t;
+}
+
+// eight values as they stand, which this thread may overwrite later
 template <int DT>
-__device__ __forceinline__ void load8_rw(const void* p, int64_t i, float (&x)[8]) {
-  if (DT == DQ_F32) {
-    const float4* s = (const float4*)((const float*)p + i);
-    const float4 a = s[0], b = s[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const uint4 v = *(const uint4*)((const unsigned short*)p + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Raw8 {
+  uint4 v[DT == DQ_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if (DT == DQ_F32) {
+      v[0] = ((const uint4*)((const float*)p + i))[0];
+      v[DT == DQ_F32] = ((const uint4*)((const float*)p + i))[1];
+    } else {
+      v[0] = *(const uint4*)((const unsigned short*)p + i);
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    if (DT == DQ_F32) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (DT == DQ_BF16) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(u32_as_h2(w[k]));
+      for (int k = 0; k < 2; ++k) {
+        const uint4 w = v[DT == DQ_F32 ? k : 0];
+        x[4 * k] = __uint_as_float(w.x);
+        x[4 * k + 1] = __uint_as_float(w.y);
+        x[4 * k + 2] = __uint_as_float(w.z);
+        x[4 * k + 3] = __uint_as_float(w.w);
+      }
+    } else {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = DT == DQ_F16 ? __half22float2(u32_as_h2(w[k]))
+                                      : make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
         x[2 * k] = f.x;
         x[2 * k + 1] = f.y;
       }
     }
   }
-}
+};
 
 __device__ __forceinline__ void store8_any(int dtype, void* p, int64_t i, const float (&x)[8]) {
   if (dtype == DQ_BF16) store8<DQ_BF16>(p, i, x);
@@ -100,54 +126,145 @@ __device__ __forceinline__ void store8_any(int dtype, void* p, int64_t i, const 
   else store8<DQ_F32>(p, i, x);
 }
 
+// What a CTA keeps of its tokens: cosines and sines apart, so that neighbouring pairs' are packed operands.
+template <int D>
+struct Angles {
+  float c[kMostTile * D / 2], s[kMostTile * D / 2];
+  int pos[kMostTile];
+  int64_t slot[kMostTile];
+};
+
 // ---------------------------------------------------------------- q
-// A thread takes the sixteen values of eight pairs: two chunks of eight that stand `half` apart, or
-// next to one another; the values that do not turn go through in sixteens.
+// A warp takes a token and up to `q_each` of its heads, by itself: 32 / U heads at a time, of which a lane
+// takes sixteen values, eight pairs: two chunks of eight that stand `half` apart, or next to one another (the
+// values that do not turn go through in sixteens).  A lane's eight angles are those of all its heads; the lanes of
+// one unit work out a share of them each.  The first heads' loads are under way meanwhile.
 template <int D, int DT>
-__device__ __forceinline__ void rope_q(const RopeParams& p, const float2* cs, int t0, int n) {
-  constexpr int U = D / 16, ROWS = kRopeThreads / U;
-  const int u = threadIdx.x % U;
-  const bool turns = 8 * u < p.half;
-  const int c0 = p.interleaved || !turns ? 2 * u : u, c1 = p.interleaved || !turns ? 2 * u + 1 : u + p.half / 8;
-  for (int r = threadIdx.x / U; r < n * p.q_heads; r += ROWS) {
-    const int tt = r / p.q_heads, h = r - tt * p.q_heads, t = t0 + tt;
-    if (__ldg(p.pos + t) < 0) continue;
-    const int64_t at = (int64_t)t * p.q_stride + (int64_t)h * D, to = (int64_t)t * p.out_stride + (int64_t)h * D;
-    float x[8], y[8];
-    load8_rw<DT>(p.q, at + 8 * c0, x);
-    load8_rw<DT>(p.q, at + 8 * c1, y);
-    if (turns) {
-      const float2* w = cs + tt * p.half + 8 * u;
+__device__ __forceinline__ void rope_q(const RopeParams& p, int item) {
+  constexpr int U = D / 16, HL = 32 / U, PER = 8 / HL;       // units, heads at a time, angles a lane works out
+  constexpr int N = DT == DQ_F32 ? 1 : 2;                    // such steps whose loads are in flight together
+  const int lane = threadIdx.x & 31, u = lane % U, hl = lane / U;
+  const int t = item / p.q_splits, h0 = (item - t * p.q_splits) * p.q_each, h1 = min(h0 + p.q_each, p.q_heads);
+  if (t >= p.T) return;
+  const int pos = __ldg(p.pos + t);
+  if (pos < 0) return;
+  const bool turns = 8 * u < p.half, near = p.interleaved || !turns;
+  const int c0 = near ? 2 * u : u, c1 = near ? 2 * u + 1 : u + p.half / 8;
+  const int64_t at = (int64_t)t * p.q_stride, to = (int64_t)t * p.out_stride;
+  Raw8<DT> a[N], b[N];
+  auto load = [&](int h) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float& a = p.interleaved ? (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]) : x[i];
-        float& b = p.interleaved ? (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]) : y[i];
-        const float2 z = w[i];
-        const float na = fmaf(a, z.x, -(b * z.y)), nb = fmaf(b, z.x, a * z.y);
-        a = na;
-        b = nb;
+    for (int j = 0; j < N; ++j) {
+      if (h + j * HL >= h1) continue;
+      a[j].load(p.q, at + (int64_t)(h + j * HL) * D + 8 * c0);
+      b[j].load(p.q, at + (int64_t)(h + j * HL) * D + 8 * c1);
+    }
+  };
+  int h = h0 + hl;
+  load(h);
+  float2 c[4], z[4];                                         // cosines and sines, two pairs' together
+  {
+    float2 mine[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      mine[k] = turns ? turn(pos, __ldg(p.freq + 8 * u + hl * PER + k), p.factor) : make_float2(1.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = __shfl_sync(0xffffffffu, mine[i % PER].x, u + U * (i / PER));
+      const float y = __shfl_sync(0xffffffffu, mine[i % PER].y, u + U * (i / PER));
+      if (i & 1) {
+        c[i / 2].y = x;
+        z[i / 2].y = y;
+      } else {
+        c[i / 2].x = x;
+        z[i / 2].x = y;
       }
     }
-    store8_any(p.out_dtype, p.out, to + 8 * c0, x);
-    store8_any(p.out_dtype, p.out, to + 8 * c1, y);
+  }
+  while (true) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (h + j * HL >= h1) continue;
+      float x[8], y[8];
+      a[j].values(x);
+      b[j].values(y);
+      if (turns) {
+        auto pair = [&](int i, float& v0, float& v1) {
+          const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, zi = i & 1 ? z[i / 2].y : z[i / 2].x;
+          const float w = fmaf(v0, ci, -(v1 * zi));
+          v1 = fmaf(v1, ci, v0 * zi);
+          v0 = w;
+        };
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            pair(i, x[2 * i], x[2 * i + 1]);
+            pair(i + 4, y[2 * i], y[2 * i + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pair(i, x[i], y[i]);
+        }
+      }
+      store8_any(p.out_dtype, p.out, to + (int64_t)(h + j * HL) * D + 8 * c0, x);
+      store8_any(p.out_dtype, p.out, to + (int64_t)(h + j * HL) * D + 8 * c1, y);
+    }
+    h += N * HL;
+    if (h >= h1) break;                                      // (lanes of the last heads alone may go on)
+    load(h);
   }
 }
 
 // ---------------------------------------------------------------- k
-// A value in 64 bits: own cos + sign other sin.
-__device__ __noinline__ double turned64(float own, float other, float sign, int pos, float freq, float factor) {
-  double s, c;
-  sincos((double)pos * (double)freq, &s, &c);
-  const double x = ((double)own * c + (double)sign * (double)other * s) * (double)factor;
-  return fmin(fmax(x, -65504.), 65504.);
+// A value to 2^-44 of |own| + |other|: (own cos + sign other sin) factor, the angle as 64 bits round it.
+__device__ __noinline__ Pair turned_pair(float own, float other, float sign, int pos, float freq, float factor) {
+  const double a = (double)pos * (double)freq;
+  const double k = rint(a * 0.63661977236758134308);   // 2 / pi
+  const double r = fma(-k, 0x1.1a62633145c07p-54, fma(-k, 0x1.921fb54442d18p+0, a));
+  const Pair x = {(float)r, (float)(r - (double)(float)r)};
+  const int quarter = (int)((long long)k & 3);
+  // the power series of both, in pairs up to x^9 and x^10
+  const Pair y = mul(x, x);
+  Pair s = {fmaf(fmaf(-1.f / 1307674368000.f, y.h, 1.f / 6227020800.f), y.h, -1.f / 39916800.f), 0.f};
+  Pair c = {fmaf(fmaf(1.f / 20922789888000.f, y.h, -1.f / 87178291200.f), y.h, 1.f / 479001600.f), 0.f};
+  const float sh[5] = {0x1.71de3ap-19f, -0x1.a01a02p-13f, 0x1.111112p-7f, -0x1.555556p-3f, 1.f};
+  const float sl[5] = {0x1.55b1ccp-45f, 0x1.7f97fap-39f, -0x1.dddddep-32f, 0x1.555556p-28f, 0.f};
+  const float ch[6] = {-0x1.27e4fcp-22f, 0x1.a01a02p-16f, -0x1.6c16c2p-10f, 0x1.555556p-5f, -0.5f, 1.f};
+  const float cl[6] = {0x1.10ec14p-47f, -0x1.7f97fap-42f, 0x1.27d27ep-35f, -0x1.555556p-30f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 5; ++i) s = add(mul(s, y), {sh[i], sl[i]});
+#pragma unroll
+  for (int i = 0; i < 6; ++i) c = add(mul(c, y), {ch[i], cl[i]});
+  s = mul(s, x);
+  // the quarter turns
+  Pair cs = quarter & 1 ? s : c, sn = quarter & 1 ? c : s;
+  if (quarter == 1 || quarter == 2) cs = {-cs.h, -cs.l};
+  if (quarter >= 2) sn = {-sn.h, -sn.l};
+  const Pair v = add(mul({own, 0.f}, cs), mul({sign * other, 0.f}, sn));
+  return factor == 1.f ? v : mul(v, {factor, 0.f});
 }
 
-// The four lanes of a group hold eight values x each, known to `err`; `exact(e)` gives value e in 64 bits.  Returns
+// |a| against |b|
+__device__ __forceinline__ bool larger(Pair a, Pair b) {
+  const float la = a.h < 0.f ? -a.l : a.l, lb = b.h < 0.f ? -b.l : b.l;
+  return fabsf(a.h) > fabsf(b.h) || (fabsf(a.h) == fabsf(b.h) && la > lb);
+}
+// The fp16 nearest to -x / 8: the last bit of x.h stands for what lies behind it (rounded to odd), so that one rounding
+// is all there is.
+__device__ __forceinline__ __half scale_of(Pair x) {
+  uint32_t b = __float_as_uint(x.h);
+  if (x.l != 0.f) b = (b - ((x.l < 0.f) != (x.h < 0.f) ? 1u : 0u)) | 1u;
+  return __float2half_rn(__uint_as_float(b) * -0.125f);
+}
+__device__ __forceinline__ Pair within_fp16(Pair x) {
+  return fabsf(x.h) > 65504.f || (fabsf(x.h) == 65504.f && (x.l < 0.f) == (x.h < 0.f)) ? Pair{copysignf(65504.f, x.h), 0.f} : x;
+}
+
+// The four lanes of a group hold eight values x each, known to `err`; `exact(e)` forms value e again.  Returns
 // the word of codes and the scale.  Every lane of the warp calls it.
 template <typename F>
 __device__ __forceinline__ uint32_t k_word_known(const float (&x)[8], float err, int lane, __half& d, F exact) {
-  float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-  float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+  float hi = max_of8(x), lo = min_of8(x);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
@@ -155,58 +272,65 @@ __device__ __forceinline__ uint32_t k_word_known(const float (&x)[8], float err,
     err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, o));
   }
   const float top = fmaxf(hi, -lo);
-  float m = hi > -lo ? hi : lo;
-  d = __float2half_rn(m * -0.125f);
+  d = __float2half_rn((hi > -lo ? hi : lo) * -0.125f);
   // which sign the largest has, and which scale its eighth rounds to
+  const __half2 around = __floats2half2_rn((top - err) * 0.125f, (top + err) * 0.125f);
   const bool unsure = fabsf(hi + lo) <= 2.f * err || top + err >= 65504.f ||
-                      __half_as_ushort(__float2half_rn((top - err) * 0.125f)) !=
-                          __half_as_ushort(__float2half_rn((top + err) * 0.125f));
+                      __half_as_ushort(__low2half(around)) != __half_as_ushort(__high2half(around));
   if (__any_sync(0xffffffffu, unsure)) {
-    double best = -1., val = 0.;
+    Pair best = {0.f, 0.f};
     if (unsure) {
 #pragma unroll 1
       for (int e = 0; e < 8; ++e) {
         float xe = x[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) xe = e == i ? x[i] : xe;
-        if (fabsf(xe) >= top - 2.f * err) {
-          const double y = exact(e);
-          if (fabs(y) > best) {
-            best = fabs(y);
-            val = y;
-          }
+        if (fabsf(xe) >= fminf(top, 65504.f) - 2.f * err) {       // (beyond fp16 all are equal)
+          const Pair y = within_fp16(exact(e));
+          if (larger(y, best)) best = y;
         }
       }
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-      const double ob = __longlong_as_double(__shfl_xor_sync(0xffffffffu, __double_as_longlong(best), o));
-      const double ov = __longlong_as_double(__shfl_xor_sync(0xffffffffu, __double_as_longlong(val), o));
-      if (ob > best || (ob == best && (lane & o) != 0)) {
-        best = ob;
-        val = ov;
-      }
+      const Pair y = {__shfl_xor_sync(0xffffffffu, best.h, o), __shfl_xor_sync(0xffffffffu, best.l, o)};
+      if (larger(y, best) || ((lane & o) != 0 && !larger(best, y))) best = y;
     }
-    if (unsure) d = __double2half(val * -0.125);
+    if (unsure) d = scale_of(best);
   }
   const float df = __half2float(d), inv = df == 0.f ? 0.f : __frcp_rn(df);
   // the quotient's own error: the reciprocal, the product and the sum
-  const float room = err * fabsf(inv) + 1.5e-6f;
-  uint32_t word = 0, near = 0;
+  // (taken in units of 15.5, where the saturating FMA clamps it; no value is below the largest's code 0)
+  const float room = 0.5f - (err * fabsf(inv) + 3e-6f), scaled = inv * (1.f / 15.5f);
+  uint32_t word = 0;
+  float most = 0.f;                        // the distance from the middle of the code
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float y = fmaf(x[e], inv, 8.5f);
-    const float c = fminf(fmaxf(floorf(y), 0.f), 15.f);
-    const float k = rintf(y);
-    near |= fabsf(y - k) <= room && k >= 1.f && k <= 15.f && df != 0.f ? 1u << e : 0u;
-    word |= (uint32_t)c << (4 * (e >> 1) + 16 * (e & 1));
+    const uint32_t unit = 1u << (4 * (e >> 1) + 16 * (e & 1));
+    const float y = __saturatef(fmaf(x[e], scaled, 8.5f / 15.5f));
+    const float t = __fmaf_rz(y, 15.5f, 8388608.f);
+    most = fmaxf(most, fabsf(fmaf(y, 15.5f, 8388607.5f - t)));
+    word += __float_as_uint(t) * unit;
   }
-  if (__any_sync(0xffffffffu, near != 0)) {
+  word -= 0x4B000000u * 0x11111111u;
+  if (__any_sync(0xffffffffu, most > room && df != 0.f)) {
 #pragma unroll 1
-    for (; near; near &= near - 1) {
-      const int e = __ffs(near) - 1, at = 4 * (e >> 1) + 16 * (e & 1);
-      const double c = fmin(fmax(floor(exact(e) / (double)df + 8.5), 0.), 15.);
-      word = (word & ~(15u << at)) | (uint32_t)c << at;
+    for (int e = 0; e < 8; ++e) {
+      float xe = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) xe = e == i ? x[i] : xe;
+      const float near = 0.5f - room, y = fmaf(xe, inv, 8.5f), k = rintf(y);
+      if (df == 0.f || (near < 0.4f && (fabsf(y - k) >= near || k < 1.f || k > 15.f))) continue;
+      const Pair v = exact(e);
+      const float z = fmaf(v.h, inv, 8.5f), b = rintf(z);
+      uint32_t code = (uint32_t)fminf(fmaxf(floorf(z), 0.f), 15.f);
+      if (fabsf(z - b) < 2e-6f && b >= 1.f && b <= 15.f) {
+        // against the border (b - 8.5) d, which is exact
+        const float past = (v.h - (b - 8.5f) * df) + v.l;
+        code = (uint32_t)b - ((df > 0.f ? past >= 0.f : past <= 0.f) ? 0u : 1u);
+      }
+      const int at = 4 * (e >> 1) + 16 * (e & 1);
+      word = (word & ~(15u << at)) | code << at;
     }
   }
   return word;
@@ -215,22 +339,22 @@ __device__ __forceinline__ uint32_t k_word_known(const float (&x)[8], float err,
 // Eight values per thread, a group of 32 four lanes, as in dq_kv_append; the other halves of the pairs are
 // loaded too (from L1: their own threads load them).
 template <int D, int DT>
-__device__ __forceinline__ void rope_k(const RopeParams& p, const float2* cs, int t0, int n) {
+__device__ __forceinline__ void rope_k(const RopeParams& p, const Angles<D>& A, int t0, int n) {
   using B = KvBlk<D>;
   constexpr int C = D / 8, ROWS = kRopeThreads / C;
   const int lane = threadIdx.x & 31, c = threadIdx.x % C, g = c / 4, t4 = c & 3;
   const int rows = n * p.g.heads;
-  const bool turns = 4 * c < p.half;
+  const bool turns = 8 * c < 2 * p.half;
   const bool second = !p.interleaved && 8 * c >= p.half;      // of its pairs (half apart)
   const int i0 = p.interleaved ? 4 * c : second ? 8 * c - p.half : 8 * c;
   const int other = p.interleaved || !turns ? c : second ? c - p.half / 8 : c + p.half / 8;
   for (int r0 = 0; r0 < rows; r0 += ROWS) {
     const int r = r0 + (int)threadIdx.x / C;
     const bool in = r < rows;                                  // (the shuffles below take whole warps)
-    const int tt = in ? r / p.g.heads : 0, h = in ? r - tt * p.g.heads : 0, t = t0 + tt;
-    const int pos = __ldg(p.pos + t);
-    int64_t slot = in && pos >= 0 ? __ldg(p.slots + t) : -1;
-    if (slot >= p.n_slots) slot = -1;
+    int h;
+    const int tt = row_of(in ? r : 0, p.g.heads, p.k_inv, h), t = t0 + tt;
+    const int pos = A.pos[tt];
+    const int64_t slot = in ? A.slot[tt] : -1;
     const int64_t at = (int64_t)t * p.k_stride + (int64_t)h * D;
     float raw[8], oth[8], x[8], err = 0.f;
     load8<DT>(p.k, at + 8 * c, raw);
@@ -238,14 +362,24 @@ __device__ __forceinline__ void rope_k(const RopeParams& p, const float2* cs, in
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = raw[e];
     if (turns && pos >= 0) {
-      const float2* w = cs + tt * p.half + i0;
+      const float* cc = A.c + tt * p.half + i0;
+      const float* ss = A.s + tt * p.half + i0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 z = p.interleaved ? w[e >> 1] : w[e];
-        const float b = p.interleaved ? raw[e ^ 1] : oth[e];
-        const float s = p.interleaved ? ((e & 1) ? z.y : -z.y) : second ? z.y : -z.y;
-        x[e] = fmaf(raw[e], z.x, b * s);
-        err = fmaxf(err, fabsf(raw[e]) + fabsf(b));
+      for (int e = 0; e < 8; e += 2) {
+        float2 z, s;
+        if (p.interleaved) {
+          z = make_float2(cc[e >> 1], cc[e >> 1]);
+          s = make_float2(-ss[e >> 1], ss[e >> 1]);
+        } else {
+          z = *(const float2*)(cc + e);
+          s = *(const float2*)(ss + e);
+          if (!second) s = make_float2(-s.x, -s.y);
+        }
+        const float2 b = p.interleaved ? make_float2(raw[e + 1], raw[e]) : make_float2(oth[e], oth[e + 1]);
+        const float2 v = ffma2(make_float2(raw[e], raw[e + 1]), z, fmul2(b, s));
+        x[e] = v.x;
+        x[e + 1] = v.y;
+        err = max_of3(err, fabsf(raw[e]) + fabsf(b.x), fabsf(raw[e + 1]) + fabsf(b.y));
       }
       err *= p.factor * (pos < kFarPosition ? kErr : kErrFar);
     }
@@ -256,18 +390,16 @@ __device__ __forceinline__ void rope_k(const RopeParams& p, const float2* cs, in
       d = __float2half_rn(first_largest(x, lane) * -0.125f);
       word = q4_word<DT, false>(x, d);
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -65504.f), 65504.f);
-      word = k_word_known(x, err, lane, d, [&](int e) -> double {
+      word = k_word_known(x, err, lane, d, [&](int e) -> Pair {
         float own = raw[0], b = p.interleaved ? raw[1] : oth[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) {
           own = e == i ? raw[i] : own;
           b = e == i ? (p.interleaved ? raw[i ^ 1] : oth[i]) : b;
         }
-        if (!turns) return fmin(fmax((double)own, -65504.), 65504.);
+        if (!turns) return {own, 0.f};
         const bool minus = p.interleaved ? (e & 1) == 0 : !second;
-        return turned64(own, b, minus ? -1.f : 1.f, pos, __ldg(p.freq + i0 + (p.interleaved ? e >> 1 : e)), p.factor);
+        return turned_pair(own, b, minus ? -1.f : 1.f, pos, __ldg(p.freq + i0 + (p.interleaved ? e >> 1 : e)), p.factor);
       });
     }
     if (slot < 0) continue;
@@ -280,7 +412,7 @@ __device__ __forceinline__ void rope_k(const RopeParams& p, const float2* cs, in
 
 // ---------------------------------------------------------------- v, as dq_kv_append writes it
 template <int D, int DT>
-__device__ __forceinline__ void rope_v(const RopeParams& p, int t0, int n) {
+__device__ __forceinline__ void rope_v(const RopeParams& p, const Angles<D>& A, int t0, int n) {
   using B = KvBlk<D>;
   constexpr int C = D / 8, ROWS = kRopeThreads / C;
   const int lane = threadIdx.x & 31, c = threadIdx.x % C, g = c / 4, t4 = c & 3;
@@ -288,9 +420,9 @@ __device__ __forceinline__ void rope_v(const RopeParams& p, int t0, int n) {
   for (int r0 = 0; r0 < rows; r0 += ROWS) {
     const int r = r0 + (int)threadIdx.x / C;
     const bool in = r < rows;
-    const int tt = in ? r / p.g.heads : 0, h = in ? r - tt * p.g.heads : 0, t = t0 + tt;
-    int64_t slot = in && __ldg(p.pos + t) >= 0 ? __ldg(p.slots + t) : -1;
-    if (slot >= p.n_slots) slot = -1;
+    int h;
+    const int tt = row_of(in ? r : 0, p.g.heads, p.k_inv, h), t = t0 + tt;
+    const int64_t slot = in ? A.slot[tt] : -1;
     float x[8];
     load8<DT>(p.v, (int64_t)t * p.v_stride + (int64_t)h * D + 8 * c, x);
     const __half d = __float2half_rn(first_largest(x, lane) * -0.125f);
@@ -305,29 +437,55 @@ __device__ __forceinline__ void rope_v(const RopeParams& p, int t0, int n) {
   }
 }
 
-// blockIdx.y: 0 K, 1 V, 2 q (what takes longest to start first); blockIdx.x: `tile` tokens.
-template <int D, int DT>
-__global__ void __launch_bounds__(kRopeThreads) kv_rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 cs[kMostTile * D / 2];
-  pdl_wait();
-  pdl_trigger();
-  const int t0 = blockIdx.x * p.tile, n = min(p.tile, p.T - t0);
-  if (blockIdx.y == 1) {
-    rope_v<D, DT>(p, t0, n);
-    return;
+// The angles of the CTA's tokens, their positions and slots.
+template <int D>
+__device__ __forceinline__ void find_angles(const RopeParams& p, Angles<D>& A, int t0, int n, bool turns) {
+  if ((int)threadIdx.x < n) {
+    const int pos = __ldg(p.pos + t0 + threadIdx.x);
+    int64_t slot = pos >= 0 ? __ldg(p.slots + t0 + threadIdx.x) : -1;
+    A.pos[threadIdx.x] = pos;
+    A.slot[threadIdx.x] = slot < p.n_slots ? slot : -1;
   }
-  for (int i = threadIdx.x; i < n * p.half; i += kRopeThreads) {
-    const int tt = i / p.half;
-    cs[i] = turn(max(0, __ldg(p.pos + t0 + tt)), __ldg(p.freq + i - tt * p.half), p.factor);
+  if (turns) {
+    // a thread keeps to one frequency
+    const int at_once = kRopeThreads / p.half, t = (int)threadIdx.x / p.half, i = (int)threadIdx.x - t * p.half;
+    const float freq = __ldg(p.freq + i);
+    for (int tt = t; t < at_once && tt < n; tt += at_once) {
+      const float2 z = turn(max(0, __ldg(p.pos + t0 + tt)), freq, p.factor);
+      A.c[tt * p.half + i] = z.x;
+      A.s[tt * p.half + i] = z.y;
+    }
   }
   __syncthreads();
-  if (blockIdx.y == 0) rope_k<D, DT>(p, cs, t0, n);
-  else rope_q<D, DT>(p, cs, t0, n);
+}
+
+// blockIdx.x: K's CTAs of `tile` tokens, as many for V, and q's.
+template <int D, int DT>
+__global__ void __launch_bounds__(kRopeThreads, 4) kv_rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ __align__(16) Angles<D> A;
+  pdl_wait();
+  pdl_trigger();
+  const int kv_ctas = (p.T + p.tile - 1) / p.tile, cta = (int)blockIdx.x;
+  if (cta >= 2 * kv_ctas) {
+    rope_q<D, DT>(p, (cta - 2 * kv_ctas) * (kRopeThreads / 32) + (int)threadIdx.x / 32);
+    return;
+  }
+  const bool k = cta < kv_ctas;
+  const int t0 = (k ? cta : cta - kv_ctas) * p.tile, n = min(p.tile, p.T - t0);
+  find_angles<D>(p, A, t0, n, k);
+  if (k) rope_k<D, DT>(p, A, t0, n);
+  else rope_v<D, DT>(p, A, t0, n);
 }
 
 template <int D>
-int launch_rope(const RopeParams& p, int dtype, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.T + p.tile - 1) / p.tile), p.q ? 3 : 2), block(kRopeThreads);
+int launch_rope(RopeParams p, int dtype, cudaStream_t s) {
+  constexpr int HL = 32 / (D / 16);
+  // long calls spread an angle's price over more heads, short ones the work over more warps
+  p.q_each = HL * (p.T >= kLongCall ? 8 : 2);
+  p.q_splits = (p.q_heads + p.q_each - 1) / p.q_each;
+  const int64_t ctas = 2 * (((int64_t)p.T + p.tile - 1) / p.tile) + ((int64_t)p.T * p.q_splits + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  if (ctas > 2147483647 || (int64_t)p.T * p.q_splits > 2147483647) return DQ_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)ctas), block(kRopeThreads);
 #define DQ_KV_ROPE(DT) \
   if (dtype == DT) return launched(launch_pdl(kv_rope_kernel<D, DT>, grid, block, 0, s, 0, p));
   DQ_KV_ROPE(DQ_F32)
@@ -384,10 +542,11 @@ extern "C" int dq_kv_append_rope(const dq_kv_cache* cache, const dq_kv_rope* a, 
   p.factor = a->factor;
   p.T = a->T;
   p.q_heads = a->q ? a->n_q_heads : 0;
+  p.k_inv = (uint32_t)((1ULL << 32) / (uint32_t)p.g.heads) + 1;
   p.out = a->q_out;
   p.out_stride = a->out_stride;
   p.out_dtype = a->out_dtype;
-  p.tile = a->T >= 1024 ? kMostTile : 1;
+  p.tile = a->T >= kLongCall ? kMostTile : 1;
   return by_dim(cache->head_dim,
                 [&](auto d) { return launch_rope<decltype(d)::value>(p, a->dtype, (cudaStream_t)stream); });
 }

@@ -51,12 +51,28 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8]) 
   }
 }
 
+__device__ __forceinline__ float max_of3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min_of3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max_of8(const float (&x)[8]) {
+  return max_of3(max_of3(x[0], x[1], x[2]), max_of3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+}
+__device__ __forceinline__ float min_of8(const float (&x)[8]) {
+  return min_of3(min_of3(x[0], x[1], x[2]), min_of3(x[3], x[4], x[5]), fminf(x[6], x[7]));
+}
+
 // The value of the largest magnitude of the 32 that 4 consecutive lanes hold eight of each, the first of
 // equal ones; values beyond +-65504 count as that.  The largest and the smallest value tell it, unless they
 // are equal in magnitude (or beyond): then, for the whole warp, the values are gone through in order.
 __device__ __forceinline__ float first_largest(const float (&x)[8], int lane) {
-  float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-  float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+  float hi = max_of8(x), lo = min_of8(x);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));

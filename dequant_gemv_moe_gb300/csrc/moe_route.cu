@@ -28,6 +28,7 @@
 // too few warps to hide their chains.
 #include "common.cuh"
 #include "moe_route.h"
+#include "pair.cuh"
 
 namespace dqmoe {
 
@@ -94,37 +95,6 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int64_t at) {
 // A logit as it is used: NaN and -inf take an expert out (as -inf), +inf counts as the largest float.
 __device__ __forceinline__ float usable(float x) { return x >= -kMostLogit ? fminf(x, kMostLogit) : -INFINITY; }
 
-// ---------------------------------------------------------------- pairs of floats
-// A number as the sum h + l, |l| at most half a unit in the last place of h (Dekker's and Knuth's exact sums and
-// products, with FMA).
-struct Pair {
-  float h, l;
-};
-__device__ __forceinline__ Pair quick_sum(float a, float b) {          // |a| >= |b|, or a = 0
-  const float s = __fadd_rn(a, b);
-  return {s, __fsub_rn(b, __fsub_rn(s, a))};
-}
-__device__ __forceinline__ Pair sum(float a, float b) {
-  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
-}
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
-  const Pair s = sum(a.h, b.h), t = sum(a.l, b.l);
-  const Pair u = quick_sum(s.h, __fadd_rn(s.l, t.h));
-  return quick_sum(u.h, __fadd_rn(u.l, t.l));
-}
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-  const float p = __fmul_rn(a.h, b.h);
-  const float e = __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p)));
-  return quick_sum(p, e);
-}
-__device__ __forceinline__ Pair divide(Pair a, Pair b) {
-  const float q = __fdiv_rn(a.h, b.h);
-  // the rest of a - q b, over b
-  const float p = __fmul_rn(q, b.h), e = __fmaf_rn(q, b.h, -p);
-  const float r = __fadd_rn(__fsub_rn(__fsub_rn(a.h, p), e), __fmaf_rn(-q, b.l, a.l));
-  return quick_sum(q, __fdiv_rn(r, b.h));
-}
 // e^x for x <= 0: x = k ln 2 + r, the power series of e^r from its 12th term, in pairs from the 7th on.
 __device__ Pair exp_pair(Pair x) {
   if (!(x.h > -87.f)) return {0.f, 0.f};
