@@ -10,6 +10,10 @@ namespace {
 // 16000 tokens): 134 us streaming, 257 us on the tensor core; they meet at about 64 rows.
 constexpr int kStreamRows = 64;
 
+// Many rows: tanh from the exponential's unit is off by 4e-7 whatever the score, where the polynomial is off by
+// 2.5e-7 of itself: 4e-5 in a score for this cap, which is less than what rounded keys leave (2^-12 of a score).
+constexpr float kSmallCap = 100.f;
+
 // tanh(u) / u in powers of u^2: interpolated at the Chebyshev points of [0, 1]
 constexpr double kTanh[7] = {0.9999999486455697,  -0.333328279786008,    0.13325076146118553, -0.053451646370382085,
                              0.02027970828675751, -0.006194324834556632, 0.0010380250969887872};
@@ -103,6 +107,7 @@ int dq_kv_attention_ex(const dq_kv_cache* cache, const dq_kv_attn* a, const dq_k
   const bool ext = x && (x->softcap != 0.f || x->slopes || x->prefix_len || x->first_pos);
   p.cap = ext ? (float)(x->softcap * 1.4426950408889634) : 0.f;
   p.cap_inv = p.cap > 0.f ? 1.f / p.cap : 1.f;
+  p.cap_small = p.cap > 0.f && x->softcap <= kSmallCap;
   for (int k = 0; k < 7; ++k) p.cap_c[k].x = p.cap_c[k].y = (float)(kTanh[k] * p.cap);
   p.slopes = ext ? x->slopes : nullptr;
   p.prefix = ext && a->causal ? x->prefix_len : nullptr;

@@ -30,7 +30,8 @@ struct AttnParams {
   // what the kernels with EXT read besides (dq_kv_scores)
   float cap;                   // of a score in units of log 2, 0: none
   float cap_inv;               // its inverse
-  float2 cap_c[7];             // times tanh's polynomial, every coefficient twice (soft_cap4)
+  int cap_small;               // so small that tanh's absolute error may be taken times it (kv_attn.cu)
+  float2 cap_c[7];             // times tanh's polynomial, every coefficient twice (soft_cap)
   const float* slopes;         // per query head, or null
   const int32_t* prefix;       // per request, or null
   const int32_t* first_pos;    // per row of q, or null
@@ -433,31 +434,36 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 // |u| <= 1 (its Chebyshev interpolation: 2.5e-7 of itself, fp32's roundings included); beyond, tanh(|u|) = 1 - 2 / (1 + e^2|u|), whose
 // terms do not cancel there.
 //
-// Eight scores at a time: four chains of packed steps keep the pipe busy, and a coefficient is fetched once.
-__device__ __forceinline__ void soft_cap4(const AttnParams& p, float2 (&u)[4], bool beyond) {
-  float2 y[4], r[4];
+// Eight scores at a time: chains of packed steps keep the pipe busy, and a coefficient is fetched once.
+template <int N>
+__device__ __forceinline__ void soft_cap(const AttnParams& p, float2 (&u)[N]) {
+  float2 y[N], r[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N; ++i) {
     y[i] = fmul2(u[i], u[i]);
     r[i] = p.cap_c[6];
   }
 #pragma unroll
   for (int k = 5; k >= 0; --k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = ffma2(r[i], y[i], p.cap_c[k]);
-  if (beyond) {
-    auto far = [&](float x) {
-      return copysignf(p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fabsf(x) * (2.f * kLog2e))), x);
-    };
+    for (int i = 0; i < N; ++i) r[i] = ffma2(r[i], y[i], p.cap_c[k]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = fmul2(r[i], u[i]);
-      u[i].x = fabsf(u[i].x) > 1.f ? far(u[i].x) : t.x;
-      u[i].y = fabsf(u[i].y) > 1.f ? far(u[i].y) : t.y;
-    }
-  } else {
+  for (int i = 0; i < N; ++i) u[i] = fmul2(r[i], u[i]);
+}
+// The same for any u.
+template <int N>
+__device__ __forceinline__ void soft_cap_far(const AttnParams& p, float2 (&u)[N]) {
+  float2 near[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = fmul2(r[i], u[i]);
+  for (int i = 0; i < N; ++i) near[i] = u[i];
+  soft_cap(p, near);
+  auto far = [&](float x) {
+    return copysignf(p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fabsf(x) * (2.f * kLog2e))), x);
+  };
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    u[i].x = fabsf(u[i].x) > 1.f ? far(u[i].x) : near[i].x;
+    u[i].y = fabsf(u[i].y) > 1.f ? far(u[i].y) : near[i].y;
   }
 }
 

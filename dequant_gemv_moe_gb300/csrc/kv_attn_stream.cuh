@@ -430,7 +430,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             float2 u[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) u[i] = make_float2(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
-            soft_cap4(p, u, __any_sync(0xffffffffu, far > 1.f));
+            if (__any_sync(0xffffffffu, far > 1.f)) soft_cap_far(p, u);
+            else soft_cap(p, u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               s[i >> 1][2 * (i & 1)] = u[i].x;

@@ -37,8 +37,9 @@
 // PFLOP/s.  Left out for a measurement (of 955 us then), the decoding's arithmetic took 15 % of
 // the time, the exponentials none, three quarters of the products 6 %.  Four warps decoding and 64
 // scores a thread at a time took 966 us, two warps to a row 1088 (registers).
-// EXT: capped scores, a distance bias, prefixes and first positions (dq_kv_scores), taken as the scores are
-// read.
+// Modes other than kPlain: prefixes and first positions, capped scores, a distance bias (dq_kv_scores), an instance each:
+// the softmax's loop misses the instruction cache where it holds more than it needs (7 prompts with masks alone: 137
+// us, 159 in an instance that can cap as well).
 #pragma once
 
 #include <algorithm>
@@ -53,6 +54,8 @@ namespace {
 
 constexpr int kMaxCtas = 160;
 constexpr int kPiece = 32;                 // tokens per copy stage
+
+enum TcMode { kPlain, kMasks, kSmallCaps, kBias, kAnyScores };
 
 template <int D>
 struct TcCfg {
@@ -242,10 +245,12 @@ __device__ __forceinline__ float row_up(float mx) {
   return mx > 0.f ? __uint_as_float((uint32_t)(127 + min(14 - ex, 100)) << 23) : 1.f;
 }
 
-template <int D, bool EXT>
+template <int D, int MODE>
 __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
   using C = TcCfg<D>;
   using B = KvBlk<D>;
+  constexpr bool EXT = MODE != kPlain, ANY = MODE == kAnyScores, BIAS = MODE == kBias || ANY;
+  constexpr bool VALUES = MODE == kSmallCaps || MODE == kBias;     // scores are changed as they are read
   using Wk = TcWalk<D, EXT>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
   constexpr int LPR = D / 8, RPI = 32 / LPR, QB = D == 64 ? 8 : 4;   // rows to and from the warps
@@ -378,7 +383,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
             sts_u128(qrow + ch / 8 * 16384 + sw128_offset(tr, ch & 7), make_uint4(r4[0], r4[1], r4[2], r4[3]));
           }
         }
-        cf = fmaxf(p.scale * kLog2e / row_up(own), kLeastScale) * (EXT ? p.cap_inv : 1.f);
+        cf = fmaxf(p.scale * kLog2e / row_up(own), kLeastScale);
+        if (MODE == kSmallCaps) cf *= p.cap_inv * (2.f * kLog2e);
+        if (ANY) cf *= p.cap_inv;
         fence_proxy_async_smem();
         mbar_arrive(&q_full[tile]);
       }
@@ -395,8 +402,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         lo_all = first_seen(p, pb);
         if (EXT) lo_all = max(lo_all, row_first(p, it.first + pb - it.shift));
       }
-      const float cfs = EXT && (p.cap > 0.f || p.slopes) ? 1.f : cf;      // of the scores that the softmax reads
-      const float slope = EXT && p.slopes ? __ldg(p.slopes + head) * -kLog2e : 0.f;
+      const float cfs = ANY ? 1.f : cf;    // of the scores that the softmax reads
+      const float slope = BIAS && p.slopes ? __ldg(p.slopes + head) * -kLog2e : 0.f;
       float M = kNone, l = 0.f;
       for (int j = 0; j < nt; ++j, ++gt) {
         const int tok0 = (it.t0 + ra + j) * TT;
@@ -407,11 +414,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
         const bool inner = tok0 >= lo_all && tok0 <= hi_all - TT;
-        // EXT: the scores, in units of log 2, capped and biased, take their own place.  A pass of its own
-        // beside the softmax's keeps the code short (in the softmax's passes, over 16 scores at a time, it
-        // missed the instruction cache: 7188 us for cap_chunk below), and what is done again with a new M is
-        // not capped again.
-        if (EXT && (p.cap > 0.f || p.slopes)) {
+        // Any cap, any bias: the scores, in units of log 2, capped and biased, take their own place in a pass in front of
+        // the softmax's.  (1050 -> 1870 us for cap_chunk below, in its warps or in others: tensor memory's
+        // bandwidth.  The polynomial in the softmax's passes misses the instruction cache: 3970.)
+        if (ANY) {
           // a bias is linear in the position on either side of the row's own
           const bool one_side = (p.causal && !p.prefix) || __all_sync(0xffffffffu, pos >= tok0 + TT);
 #pragma unroll 1
@@ -432,7 +438,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
                              make_float2(cf, cf));
                 far = max3(far, fabsf(t[i].x), fabsf(t[i].y));
               }
-              if (p.cap > 0.f) soft_cap4(p, t, __any_sync(0xffffffffu, far > 1.f));
+              if (p.cap > 0.f) {
+                if (__any_sync(0xffffffffu, far > 1.f)) soft_cap_far(p, t);
+                else soft_cap(p, t);
+              }
               if (p.slopes) {
                 if (one_side) {
 #pragma unroll
@@ -458,6 +467,60 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           }
           tmem_wait_st();
         }
+        // 32 values of this thread's row in units of log 2, capped or biased, less `less`; -inf where it does not see
+        auto values = [&](int c, float less, uint32_t (&r)[32]) {
+          tmem_ld32(s_addr + c, r);
+          tmem_wait_ld();
+          tmem_use(r);
+          if (MODE == kSmallCaps) {
+            // cap tanh(u) = cap - 2 cap / (1 + e^2u), cf from the score to 2 u log2 e
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 t = fmul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(cf, cf));
+              r[k] = __float_as_uint(t.x);
+              r[k + 1] = __float_as_uint(t.y);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+r"(r[k]));
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 t = fadd2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(1.f, 1.f));
+              r[k] = __float_as_uint(t.x);
+              r[k + 1] = __float_as_uint(t.y);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+r"(r[k]));
+            const float2 f2 = make_float2(-2.f * p.cap, -2.f * p.cap), m2 = make_float2(p.cap - less, p.cap - less);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2, m2);
+              r[k] = __float_as_uint(t.x);
+              r[k + 1] = __float_as_uint(t.y);
+            }
+          } else {
+            // a bias is linear in the position on either side of the row's own
+            const float d = (float)(pos - tok0 - c);
+            if ((p.causal && !p.prefix) || __all_sync(0xffffffffu, pos >= tok0 + TT)) {
+              float2 z = make_float2(fmaf(d, slope, -less), fmaf(d - 1.f, slope, -less));
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(cf, cf), z);
+                z = fadd2(z, make_float2(-2.f * slope, -2.f * slope));
+                r[k] = __float_as_uint(t.x);
+                r[k + 1] = __float_as_uint(t.y);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                r[k] = __float_as_uint(fmaf(__uint_as_float(r[k]), cf, fmaf(fabsf(d - (float)k), slope, -less)));
+            }
+          }
+          if (!inner) {
+            const int n = hi - tok0 - c, f = lo - tok0 - c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = i < n && i >= f ? r[i] : 0xFF800000u;
+          }
+        };
         // 32 scores of this thread's row, those that it does not see as -inf
         auto load = [&](int c, uint32_t (&r)[32]) {
           tmem_ld32(s_addr + c, r);
@@ -484,7 +547,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 #pragma unroll 1
             for (int c = 0; c < TT; c += 32) {
               uint32_t r[32];
-              load(c, r);
+              if (VALUES) values(c, 0.f, r);
+              else load(c, r);
               float mx4[4] = {mx, mx, mx, mx};
 #pragma unroll
               for (int i = 0; i < 32; i += 8)
@@ -493,8 +557,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
                   mx4[k] = max3(mx4[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
               mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             }
-            mx *= cfs;
-            const float mn = mx > M + 9.f ? mx - 8.f : M;     // (at most M + 9: a sum of 64 2^9 at most)
+            if (!VALUES) mx *= cfs;
+            // (at most M + 9: a sum of 64 2^9 at most.  A cap lets few scores pass and a bias all rise: more
+            // room above, for less below.)
+            const float mn = mx > M + 9.f ? mx - (VALUES || ANY ? 4.f : 8.f) : M;
             const float corr = ex2(M - mn);
             M = mn;
             l *= corr;
@@ -521,6 +587,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 #pragma unroll
           for (int h = 0; h < TT; h += 32) {
             uint32_t r[32];
+            if (VALUES) {
+              values(h, M, r);
+            } else {
             load(h, r);
             // in three passes over the registers: the exponentials' latencies overlap
 #pragma unroll
@@ -528,6 +597,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
               const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), cf2, m2);
               r[k] = __float_as_uint(t.x);
               r[k + 1] = __float_as_uint(t.y);
+            }
             }
 #pragma unroll
             for (int k = 0; k < 32; ++k) asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+r"(r[k]));
@@ -963,35 +1033,35 @@ __global__ void __launch_bounds__(256, 6) kv_tc_join_kernel(const __grid_constan
   }
 }
 
-template <int D, bool EXT>
+template <int D, int MODE>
 int launch_tc(const AttnParams& p, int ctas, cudaStream_t s) {
   using C = TcCfg<D>;
   static bool attr[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cudaFuncSetAttribute(kv_tc_kernel<D, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+    if (cudaFuncSetAttribute(kv_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
       return DQ_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
   }
-  if (launch_pdl(kv_tc_kernel<D, EXT>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) != cudaSuccess)
+  if (launch_pdl(kv_tc_kernel<D, MODE>, dim3(ctas), dim3(C::NTH), C::SMEM, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   if (launch_pdl(kv_tc_join_kernel<D>, dim3(ctas, C::ROWS / (kJoinPass<D> * kJoinRows)), dim3(256), 0, s, 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }
 
-template <bool EXT>
+template <int MODE>
 int launch_tc_any(const AttnParams& p, int head_dim, cudaStream_t s) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DQ_ERR_CUDA;
   const int ctas = std::min(sms, kMaxCtas);
-  if (head_dim == 64) return launch_tc<64, EXT>(p, ctas, s);
-  if (head_dim == 128) return launch_tc<128, EXT>(p, ctas, s);
-  return launch_tc<256, EXT>(p, ctas, s);
+  if (head_dim == 64) return launch_tc<64, MODE>(p, ctas, s);
+  if (head_dim == 128) return launch_tc<128, MODE>(p, ctas, s);
+  return launch_tc<256, MODE>(p, ctas, s);
 }
 
 }  // namespace

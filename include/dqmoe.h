@@ -690,7 +690,8 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* args, void* ws, 
  *   j >= first_pos[row].
  * So a prefix is read both ways (its rows see all of it), and rows of a request that holds several documents
  * see their own one.  Rows that see nothing, garbage in unseen places, types, limits, the workspace: as
- * dq_kv_attention.  Caps are held to 2.5e-7 of a score; a bias is fp32 of fp32 slopes. */
+ * dq_kv_attention.  Capped scores are off by 2.5e-7 of themselves, or, up to
+ * 100 and where a request has more rows per K/V head than stream, by 4e-7 of the cap; a bias is fp32 of fp32 slopes. */
 typedef struct {
   float softcap;              /* 0: none; else 0.01 to 1e6 */
   const float* slopes;        /* device fp32 [n_q_heads], finite, or NULL */
