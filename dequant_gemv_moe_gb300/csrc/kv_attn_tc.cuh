@@ -57,7 +57,7 @@ constexpr int kPiece = 32;                 // tokens per copy stage
 
 enum TcMode { kPlain, kMasks, kSmallCaps, kBias, kAnyScores };
 
-template <int D>
+template <int D, int MODE = kPlain>
 struct TcCfg {
   static constexpr int NQ = kTcRowTiles<D>;          // 128-row tiles
   static constexpr int TT = kTcTile;                 // tokens per tile
@@ -75,7 +75,10 @@ struct TcCfg {
   static constexpr int OFF_RAW = OFF_V + KVS * KV_BUF;
   static constexpr int SMEM = OFF_RAW + RS * PIECE_B;
   static constexpr int DEC0 = 4 * NQ;                // first decoding warp
-  static constexpr int PROD = DEC0 + 8, MMA = DEC0 + 9;   // one warp of products per row tile
+  // decoding warps: capped scores keep the softmax so long that four are enough, and the registers of the others
+  // let its threads hold 64 scores (cap_chunk below 1625 -> 1571 us; a bias 1046 -> 1090)
+  static constexpr int DW = MODE == kSmallCaps ? 4 : 8;
+  static constexpr int PROD = DEC0 + DW, MMA = PROD + 1;  // one warp of products per row tile
   static constexpr int NTH = 32 * (MMA + NQ);
   // tensor memory columns: O of every row tile, then two score buffers of each
   static constexpr int COL_S = NQ * D;
@@ -246,10 +249,12 @@ __device__ __forceinline__ float row_up(float mx) {
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
-  using C = TcCfg<D>;
+__global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __grid_constant__ AttnParams p) {
+  using C = TcCfg<D, MODE>;
   using B = KvBlk<D>;
   constexpr bool EXT = MODE != kPlain, ANY = MODE == kAnyScores, BIAS = MODE == kBias || ANY;
+  // A bias falls with the distance: from the last tile to the first one, M hardly has to follow.
+  constexpr bool BACK = BIAS;
   constexpr bool VALUES = MODE == kSmallCaps || MODE == kBias;     // scores are changed as they are read
   using Wk = TcWalk<D, EXT>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < C::KVS; ++i) {
-      mbar_init(&kv_full[i], 256);
+      mbar_init(&kv_full[i], 32 * C::DW);
       mbar_init(&kv_empty[i], NQ);
     }
     for (int i = 0; i < 4; ++i) {
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
       const float slope = BIAS && p.slopes ? __ldg(p.slopes + head) * -kLog2e : 0.f;
       float M = kNone, l = 0.f;
       for (int j = 0; j < nt; ++j, ++gt) {
-        const int tok0 = (it.t0 + ra + j) * TT;
+        const int tok0 = (it.t0 + (BACK ? rb - 1 - j : ra + j)) * TT;
         const int sl = tile * 2 + (gt & 1);
         ok = ok && mbar_wait(&s_full[sl], (gt >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -469,31 +474,33 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         }
         // 32 values of this thread's row in units of log 2, capped or biased, less `less`; -inf where it does not see
         auto values = [&](int c, float less, uint32_t (&r)[32]) {
-          tmem_ld32(s_addr + c, r);
-          tmem_wait_ld();
-          tmem_use(r);
           if (MODE == kSmallCaps) {
-            // cap tanh(u) = cap - 2 cap / (1 + e^2u), cf from the score to 2 u log2 e
+            // cap tanh(u) = cap - 2 cap / (1 + e^2u), cf from the score to 2 u log2 e; two inverses from that of the
+            // product, which 2^60 keeps finite (tanh is 1 there)
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               const float2 t = fmul2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(cf, cf));
-              r[k] = __float_as_uint(t.x);
-              r[k + 1] = __float_as_uint(t.y);
+              r[k] = __float_as_uint(fminf(t.x, 60.f));
+              r[k + 1] = __float_as_uint(fminf(t.y, 60.f));
             }
 #pragma unroll
             for (int k = 0; k < 32; ++k) asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+r"(r[k]));
+            uint32_t m[16];
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               const float2 t = fadd2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(1.f, 1.f));
               r[k] = __float_as_uint(t.x);
               r[k + 1] = __float_as_uint(t.y);
+              m[k / 2] = __float_as_uint(t.x * t.y);
             }
 #pragma unroll
-            for (int k = 0; k < 32; ++k) asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+r"(r[k]));
+            for (int k = 0; k < 16; ++k) asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+r"(m[k]));
             const float2 f2 = make_float2(-2.f * p.cap, -2.f * p.cap), m2 = make_float2(p.cap - less, p.cap - less);
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2, m2);
+              const float i = __uint_as_float(m[k / 2]);
+              const float2 v = fmul2(make_float2(__uint_as_float(r[k + 1]), __uint_as_float(r[k])), make_float2(i, i));
+              const float2 t = ffma2(v, f2, m2);
               r[k] = __float_as_uint(t.x);
               r[k + 1] = __float_as_uint(t.y);
             }
@@ -547,8 +554,14 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
 #pragma unroll 1
             for (int c = 0; c < TT; c += 32) {
               uint32_t r[32];
-              if (VALUES) values(c, 0.f, r);
-              else load(c, r);
+              if (MODE == kBias) {
+                tmem_ld32(s_addr + c, r);
+                tmem_wait_ld();
+                tmem_use(r);
+                values(c, 0.f, r);
+              } else {
+                load(c, r);
+              }
               float mx4[4] = {mx, mx, mx, mx};
 #pragma unroll
               for (int i = 0; i < 32; i += 8)
@@ -557,10 +570,12 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
                   mx4[k] = max3(mx4[k], __uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1]));
               mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             }
-            if (!VALUES) mx *= cfs;
-            // (at most M + 9: a sum of 64 2^9 at most.  A cap lets few scores pass and a bias all rise: more
-            // room above, for less below.)
-            const float mn = mx > M + 9.f ? mx - (VALUES || ANY ? 4.f : 8.f) : M;
+            if (MODE != kBias) mx *= cfs;
+            // (a cap rises with its score)
+            if (MODE == kSmallCaps && mx > -INFINITY) mx = p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fminf(mx, 60.f)));
+            // (At most M + 9: a sum of 64 2^9 at most.  Scores that a cap is for lie further apart: more room
+            // above, for less below; cap_chunk's rows follow 20 % less often.)
+            const float mn = mx > M + 9.f ? mx - (MODE == kSmallCaps || ANY ? 4.f : 8.f) : M;
             const float corr = ex2(M - mn);
             M = mn;
             l *= corr;
@@ -584,10 +599,28 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           }
           const float2 cf2 = make_float2(cfs, cfs), m2 = make_float2(-M, -M);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t both[MODE == kSmallCaps ? TT : 1];
+          if (MODE == kSmallCaps) {
+            tmem_ld32(s_addr, both);
+            tmem_wait_ld();
+            tmem_use(both);
+            tmem_ld32(s_addr + 32, both + (MODE == kSmallCaps ? 32 : 0));
+          }
 #pragma unroll
           for (int h = 0; h < TT; h += 32) {
             uint32_t r[32];
-            if (VALUES) {
+            if (MODE == kSmallCaps) {
+              if (h > 0) {
+                tmem_wait_ld();
+                tmem_use(both + (MODE == kSmallCaps ? 32 : 0));
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) r[k] = both[MODE == kSmallCaps ? h + k : 0];
+              values(h, M, r);
+            } else if (MODE == kBias) {
+              tmem_ld32(s_addr + h, r);
+              tmem_wait_ld();
+              tmem_use(r);
               values(h, M, r);
             } else {
             load(h, r);
@@ -713,7 +746,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
   } else if (warp < C::PROD) {
     // ------------------------------ decoding ------------------------------
     const int dw = warp - C::DEC0;
-    const int pc = dw >> 2, blk = (dw >> 1) & 1, half = dw & 1;      // piece of the tile, block, its half
+    // piece of the tile (four warps: one after the other), block, its half
+    constexpr int PIECES = 8 / C::DW;
+    const int pc0 = C::DW == 8 ? dw >> 2 : 0, blk = (dw >> 1) & 1, half = dw & 1;
     // K: lane = (token, t); odd rows take their words in swapped order, so that 8 lanes' stores meet
     // 8 different chunks.  V: lane = (a, t): tokens 2t and 2t + 1 of the half block.
     const int r4 = lane >> 2, t = lane & 3;
@@ -723,12 +758,12 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
     const uint32_t k_sel[2] = {odd ? 0x3232u : 0x1010u, odd ? 0x1010u : 0x3232u};
     const uint32_t v_at[2] = {sw128_offset(vrow, r4), sw128_offset(vrow + 1, r4)};
     const uint32_t raw0 = smem_u32(smem + C::OFF_RAW) + blk * B::BYTES;
-    int gt = 0, st = pc, st_phase = 0;     // every other stage is this warp's
+    int gt = 0, st = pc0, st_phase = 0;    // every other stage is this warp's, or all are
     for (bool more = Wk::here(p, it, iu, share[0], share[1], ta, tb); more && ok;
          more = Wk::after(p, it, iu, share[0], share[1], ta, tb)) {
       const bool fine = is_fine_of<EXT>(p, it);
       for (int j = ta; j < tb && ok; ++j) {
-        const int tok0 = (it.t0 + j) * TT;
+        const int tok0 = (it.t0 + (BACK ? ta + tb - 1 - j : j)) * TT;
         const bool inner = tok0 >= it.begin && tok0 <= it.end - TT;
         const int buf = gt % C::KVS, buf2 = (gt + 1) % C::KVS;
         if (gt >= C::KVS) ok = mbar_wait(&kv_empty[buf], (gt / C::KVS - 1) & 1);
@@ -736,6 +771,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t kb = ks + buf * C::KV_BUF, kb2 = ks + buf2 * C::KV_BUF, vb = vs + buf * C::KV_BUF;
+#pragma unroll 1
+        for (int pc = pc0; pc < pc0 + PIECES; ++pc) {
         ok = mbar_wait(&raw_full[st], st_phase);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -804,11 +841,13 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
         else decode(std::false_type());
         __syncwarp();
         if (lane == 0) mbar_arrive(&raw_empty[st]);
-        st += 2;
+        st += 2 / PIECES;
         if (st >= C::RS) {
           st -= C::RS;
           st_phase ^= 1;
         }
+        }
+        if (!ok) break;
         fence_proxy_async_smem();
         mbar_arrive(&kv_full[buf]);
         if (fine) mbar_arrive(&kv_full[buf2]);
@@ -825,7 +864,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
          more = Wk::after(p, it, iu, share[0], share[1], ta, tb)) {
       int tbase = -1, tent = 0;
       for (int j = ta; j < tb && ok; ++j) {
-        const int tok0 = (it.t0 + j) * TT;
+        const int tok0 = (it.t0 + (BACK ? ta + tb - 1 - j : j)) * TT;
         for (int pc = 0; pc < TT / kPiece && ok; ++pc) {
           if (piece >= C::RS) ok = mbar_wait(&raw_empty[st], st_phase ^ 1);
           ok = __all_sync(0xffffffffu, ok);
@@ -837,8 +876,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           while (run < kPiece) {
             const int pg = (tok + run) >> shift;
             if (tbase < 0 || pg < tbase || pg >= tbase + 32) {
-              tbase = pg;
-              const int e = pg + lane;
+              tbase = BACK ? max(pg - 31, 0) : pg;
+              const int e = tbase + lane;
               tent = e < p.max_pages ? __ldg(p.table + (int64_t)it.r * p.max_pages + e) : 0;
               if (tent < 0 || tent >= p.g.n_pages) tent = 0;
             }
@@ -941,7 +980,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NTH, 1) kv_tc_kernel(const __grid_co
           constexpr int STEP = decltype(fine_c)::value ? 2 : 1;     // decoded buffers a tile takes
           // scores run two tiles ahead of the weights, or one where two tiles' buffers are not there
           constexpr int AHEAD = C::KVS >= 2 * STEP ? 2 : 1;
-          const int before = uniform(ra - ta) * STEP, nt = uniform(rb - ra), behind = uniform(tb - rb) * STEP;
+          const int before = uniform(BACK ? tb - rb : ra - ta) * STEP, nt = uniform(rb - ra),
+                    behind = uniform(BACK ? ra - ta : tb - rb) * STEP;
           for (int k = 0; k < before && ok; ++k) ok = pass(ring++);
           if (nt > 0 && ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
@@ -1035,7 +1075,7 @@ __global__ void __launch_bounds__(256, 6) kv_tc_join_kernel(const __grid_constan
 
 template <int D, int MODE>
 int launch_tc(const AttnParams& p, int ctas, cudaStream_t s) {
-  using C = TcCfg<D>;
+  using C = TcCfg<D, MODE>;
   static bool attr[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ERR_CUDA;
