@@ -37,6 +37,9 @@ struct AttnParams {
   const int32_t* first_pos;    // per row of q, or null
 };
 
+// The kernels' instances: plain, masks alone, capped scores (many rows: caps up to 100), biased ones, anything.
+enum ScoreMode { kPlain, kMasks, kCaps, kBias, kAnyScores };
+
 // few rows per K/V head (kv_attn_stream.cuh); ext: scores and masks other than the plain ones
 size_t kv_stream_workspace();
 int launch_kv_stream(const AttnParams& p, int head_dim, bool ext, cudaStream_t s);

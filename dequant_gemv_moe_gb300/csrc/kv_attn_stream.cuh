@@ -43,8 +43,8 @@
 //
 // Each warp has a ring of tiles filled by its own bulk copies (a tile of a page
 // is one contiguous run), all but one in flight while one is computed.
-// EXT: capped scores, a distance bias, prefixes and first positions (dq_kv_scores).  Scores are then taken
-// into units of log 2, capped and biased before the softmax; everything else is the same.
+// Modes other than kPlain: prefixes and first positions, capped scores, a distance bias (dq_kv_scores), an instance each.
+// Scores that are changed are taken into units of log 2 first; everything else is the same.
 #pragma once
 
 #include <algorithm>
@@ -156,9 +156,10 @@ __device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
-template <int D, bool EXT>
+template <int D, int MODE>
 __global__ void __launch_bounds__(StreamCfg<D>::NTH, 1)
 kv_stream_kernel(const __grid_constant__ AttnParams p) {
+  constexpr bool EXT = MODE != kPlain, CAPS = MODE == kCaps || MODE == kAnyScores, BIAS = MODE == kBias || MODE == kAnyScores;
   using B = KvBlk<D>;
   using C = StreamCfg<D>;
   constexpr int G = B::G, W = B::W, GH = G / W;
@@ -311,7 +312,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
     const int e = mx > 0.f ? min(14 - ex, 100) : 0;
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     const float c = fmaxf(p.scale * kLog2e * 16777216.f * __uint_as_float((uint32_t)(127 - e) << 23),
-                          kLeastScale) * (EXT ? p.cap_inv : 1.f);
+                          kLeastScale) * (CAPS ? p.cap_inv : 1.f);
     float sum[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -357,7 +358,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         if (EXT) {
           S.lo[lane] = max(S.lo[lane], row_first(p, it.first + tokq));
           S.pos[lane] = pos;
-          S.slope[lane] = p.slopes ? __ldg(p.slopes + it.h * p.group + row - tokq * p.group) * kLog2e : 0.f;
+          S.slope[lane] = BIAS && p.slopes ? __ldg(p.slopes + it.h * p.group + row - tokq * p.group) * kLog2e : 0.f;
         }
       }
       __syncwarp();
@@ -417,28 +418,24 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
             }
           }
         }
-        if (EXT) {
-          float far = 0.f;
+        if (CAPS || BIAS) {
+          float2 u[4];                                    // in units of log 2, or of the cap
 #pragma unroll
-          for (int k = 0; k < kBlks; ++k)
+          for (int i = 0; i < 4; ++i)
+            u[i] = fmul2(make_float2(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]), make_float2(cf[0], cf[1]));
+          if (CAPS && p.cap > 0.f) {
+            float far = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              s[k][i] *= cf[i & 1];                       // (score / cap where there is one)
-              far = fmaxf(far, fabsf(s[k][i]));
-            }
-          if (p.cap > 0.f) {
-            float2 u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = make_float2(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
+            for (int i = 0; i < 4; ++i) far = fmaxf(far, fmaxf(fabsf(u[i].x), fabsf(u[i].y)));
             if (__any_sync(0xffffffffu, far > 1.f)) soft_cap_far(p, u);
             else soft_cap(p, u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              s[i >> 1][2 * (i & 1)] = u[i].x;
-              s[i >> 1][2 * (i & 1) + 1] = u[i].y;
-            }
           }
-          if (p.slopes) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[i >> 1][2 * (i & 1)] = u[i].x;
+            s[i >> 1][2 * (i & 1) + 1] = u[i].y;
+          }
+          if (BIAS && p.slopes) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float d = (float)(S.pos[2 * lt + i] - tok0 - lr), slope = -S.slope[2 * lt + i];
@@ -511,7 +508,7 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         bool over = (big & kBig) != 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          top[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i])) * (EXT ? 1.f : cf[i]);
+          top[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i])) * (CAPS || BIAS ? 1.f : cf[i]);
           over = over || top[i] > lim[i];
         }
         if (__any_sync(0xffffffffu, over)) {
@@ -564,8 +561,8 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
           uint32_t pt[2];
 #pragma unroll
           for (int hrow = 0; hrow < 2; ++hrow) {
-            const float2 w = make_float2(ex2(EXT ? s[k][2 * hrow] - M[0] : fmaf(s[k][2 * hrow], cf[0], -M[0])),
-                                         ex2(EXT ? s[k][2 * hrow + 1] - M[1] : fmaf(s[k][2 * hrow + 1], cf[1], -M[1])));
+            const float2 w = make_float2(ex2(CAPS || BIAS ? s[k][2 * hrow] - M[0] : fmaf(s[k][2 * hrow], cf[0], -M[0])),
+                                         ex2(CAPS || BIAS ? s[k][2 * hrow + 1] - M[1] : fmaf(s[k][2 * hrow + 1], cf[1], -M[1])));
             l = fadd2(l, w);
             pt[hrow] = transpose8x8(h2_as_u32(__floats2half2_rn(w.x, w.y)));
           }
@@ -861,14 +858,14 @@ __global__ void __launch_bounds__(256 * kSub<D>) kv_stream_join_kernel(const __g
   }
 }
 
-template <int D, bool EXT>
+template <int D, int MODE>
 int launch_stream(AttnParams p, int ctas, cudaStream_t s) {
   using C = StreamCfg<D>;
   static bool attr[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cudaFuncSetAttribute(kv_stream_kernel<D, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(kv_stream_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM) != cudaSuccess)
       return DQ_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
@@ -885,7 +882,7 @@ int launch_stream(AttnParams p, int ctas, cudaStream_t s) {
   const bool alone = items <= ctas && tiles * (ctas - items * cl) <= (int64_t)more * C::NW * cl * ctas &&
                      tiles <= kAloneMost * C::NW * cl;
   p.alone = alone ? (int)per : 0;
-  if (launch_pdl(kv_stream_kernel<D, EXT>, dim3(alone ? (int)items * cl : ctas), dim3(C::NTH), C::SMEM, s,
+  if (launch_pdl(kv_stream_kernel<D, MODE>, dim3(alone ? (int)items * cl : ctas), dim3(C::NTH), C::SMEM, s,
                  alone && cl > 1 ? cl : 0, p) != cudaSuccess)
     return DQ_ERR_CUDA;
   if (alone) return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
@@ -894,16 +891,16 @@ int launch_stream(AttnParams p, int ctas, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }
 
-template <bool EXT>
+template <int MODE>
 int launch_stream_any(const AttnParams& p, int head_dim, cudaStream_t s) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DQ_ERR_CUDA;
   const int ctas = std::min(sms, kMaxCtas);
-  if (head_dim == 64) return launch_stream<64, EXT>(p, ctas, s);
-  if (head_dim == 128) return launch_stream<128, EXT>(p, ctas, s);
-  return launch_stream<256, EXT>(p, ctas, s);
+  if (head_dim == 64) return launch_stream<64, MODE>(p, ctas, s);
+  if (head_dim == 128) return launch_stream<128, MODE>(p, ctas, s);
+  return launch_stream<256, MODE>(p, ctas, s);
 }
 
 }  // namespace

@@ -55,8 +55,6 @@ namespace {
 constexpr int kMaxCtas = 160;
 constexpr int kPiece = 32;                 // tokens per copy stage
 
-enum TcMode { kPlain, kMasks, kSmallCaps, kBias, kAnyScores };
-
 template <int D, int MODE = kPlain>
 struct TcCfg {
   static constexpr int NQ = kTcRowTiles<D>;          // 128-row tiles
@@ -77,7 +75,7 @@ struct TcCfg {
   static constexpr int DEC0 = 4 * NQ;                // first decoding warp
   // decoding warps: capped scores keep the softmax so long that four are enough, and the registers of the others
   // let its threads hold 64 scores (cap_chunk below 1625 -> 1571 us; a bias 1046 -> 1090)
-  static constexpr int DW = MODE == kSmallCaps ? 4 : 8;
+  static constexpr int DW = MODE == kCaps ? 4 : 8;
   static constexpr int PROD = DEC0 + DW, MMA = PROD + 1;  // one warp of products per row tile
   static constexpr int NTH = 32 * (MMA + NQ);
   // tensor memory columns: O of every row tile, then two score buffers of each
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
   constexpr bool EXT = MODE != kPlain, ANY = MODE == kAnyScores, BIAS = MODE == kBias || ANY;
   // A bias falls with the distance: from the last tile to the first one, M hardly has to follow.
   constexpr bool BACK = BIAS;
-  constexpr bool VALUES = MODE == kSmallCaps || MODE == kBias;     // scores are changed as they are read
+  constexpr bool VALUES = MODE == kCaps || MODE == kBias;     // scores are changed as they are read
   using Wk = TcWalk<D, EXT>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
   constexpr int LPR = D / 8, RPI = 32 / LPR, QB = D == 64 ? 8 : 4;   // rows to and from the warps
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
           }
         }
         cf = fmaxf(p.scale * kLog2e / row_up(own), kLeastScale);
-        if (MODE == kSmallCaps) cf *= p.cap_inv * (2.f * kLog2e);
+        if (MODE == kCaps) cf *= p.cap_inv * (2.f * kLog2e);
         if (ANY) cf *= p.cap_inv;
         fence_proxy_async_smem();
         mbar_arrive(&q_full[tile]);
@@ -474,7 +472,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
         }
         // 32 values of this thread's row in units of log 2, capped or biased, less `less`; -inf where it does not see
         auto values = [&](int c, float less, uint32_t (&r)[32]) {
-          if (MODE == kSmallCaps) {
+          if (MODE == kCaps) {
             // cap tanh(u) = cap - 2 cap / (1 + e^2u), cf from the score to 2 u log2 e; two inverses from that of the
             // product, which 2^60 keeps finite (tanh is 1 there)
 #pragma unroll
@@ -572,10 +570,10 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
             }
             if (MODE != kBias) mx *= cfs;
             // (a cap rises with its score)
-            if (MODE == kSmallCaps && mx > -INFINITY) mx = p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fminf(mx, 60.f)));
+            if (MODE == kCaps && mx > -INFINITY) mx = p.cap - 2.f * p.cap * rcp_ftz(1.f + ex2(fminf(mx, 60.f)));
             // (At most M + 9: a sum of 64 2^9 at most.  Scores that a cap is for lie further apart: more room
             // above, for less below; cap_chunk's rows follow 20 % less often.)
-            const float mn = mx > M + 9.f ? mx - (MODE == kSmallCaps || ANY ? 4.f : 8.f) : M;
+            const float mn = mx > M + 9.f ? mx - (MODE == kCaps || ANY ? 4.f : 8.f) : M;
             const float corr = ex2(M - mn);
             M = mn;
             l *= corr;
@@ -599,23 +597,23 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
           }
           const float2 cf2 = make_float2(cfs, cfs), m2 = make_float2(-M, -M);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          uint32_t both[MODE == kSmallCaps ? TT : 1];
-          if (MODE == kSmallCaps) {
+          uint32_t both[MODE == kCaps ? TT : 1];
+          if (MODE == kCaps) {
             tmem_ld32(s_addr, both);
             tmem_wait_ld();
             tmem_use(both);
-            tmem_ld32(s_addr + 32, both + (MODE == kSmallCaps ? 32 : 0));
+            tmem_ld32(s_addr + 32, both + (MODE == kCaps ? 32 : 0));
           }
 #pragma unroll
           for (int h = 0; h < TT; h += 32) {
             uint32_t r[32];
-            if (MODE == kSmallCaps) {
+            if (MODE == kCaps) {
               if (h > 0) {
                 tmem_wait_ld();
-                tmem_use(both + (MODE == kSmallCaps ? 32 : 0));
+                tmem_use(both + (MODE == kCaps ? 32 : 0));
               }
 #pragma unroll
-              for (int k = 0; k < 32; ++k) r[k] = both[MODE == kSmallCaps ? h + k : 0];
+              for (int k = 0; k < 32; ++k) r[k] = both[MODE == kCaps ? h + k : 0];
               values(h, M, r);
             } else if (MODE == kBias) {
               tmem_ld32(s_addr + h, r);

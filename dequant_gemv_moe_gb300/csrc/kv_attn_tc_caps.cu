@@ -4,7 +4,7 @@
 namespace dqmoe {
 
 int launch_kv_tc_caps(const AttnParams& p, int head_dim, cudaStream_t s) {
-  return launch_tc_any<kSmallCaps>(p, head_dim, s);
+  return launch_tc_any<kCaps>(p, head_dim, s);
 }
 
 }  // namespace dqmoe
