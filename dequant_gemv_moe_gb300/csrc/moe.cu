@@ -23,7 +23,7 @@
 #include <utility>
 
 #include "moe_plan.h"
-#include "moe_route.h"
+#include "moe_route.cuh"
 #include "qgemv_mma.cuh"
 #include "tmap.h"
 
@@ -579,6 +579,8 @@ struct TopkIn {
   float* gate;
 };
 
+// ROUTED: that selection is rp's instead of the softmax top-k.
+template <bool ROUTED>
 __global__ void __launch_bounds__(1024) permute_kernel(int32_t* idx, int T,
                                                        int k, int E, int n_shared, int gw,
                                                        int32_t* __restrict__ offsets,
@@ -593,7 +595,8 @@ __global__ void __launch_bounds__(1024) permute_kernel(int32_t* idx, int T,
                                                        int cK, __half* __restrict__ cx16,
                                                        float* __restrict__ cxinv, TopkIn tk,
                                                        int4* __restrict__ groups1,
-                                                       int32_t* __restrict__ n_groups1) {
+                                                       int32_t* __restrict__ n_groups1,
+                                                       const __grid_constant__ RouteParams rp) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[32];
@@ -608,6 +611,7 @@ __global__ void __launch_bounds__(1024) permute_kernel(int32_t* idx, int T,
   __shared__ int osc[257];
   __shared__ int sidx[256];       // the top-k's indices (T * k <= 256)
   __shared__ int stok[256];       // the token of an expert's pair, for experts with one pair
+  __shared__ int list[ROUTED ? 32 : 1][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = T * k;
   const bool own = tk.part != nullptr;   // the indices are chosen here: read them from sidx
@@ -635,15 +639,20 @@ __global__ void __launch_bounds__(1024) permute_kernel(int32_t* idx, int T,
     }
     __syncthreads();
     if (warp != 0) return;
-    float v[8];
-    int id[8];
+    if (ROUTED) {
+      const int pick = route_one(rp, 0, lane, lg, list[0]);
+      if (lane < k) sidx[lane] = pick;
+    } else {
+      float v[8];
+      int id[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = lane + 32 * j;
-      v[j] = e < E ? lg[e] : -INFINITY;
-      id[j] = e < E ? e : 0x7fffffff;
+      for (int j = 0; j < 8; ++j) {
+        const int e = lane + 32 * j;
+        v[j] = e < E ? lg[e] : -INFINITY;
+        id[j] = e < E ? e : 0x7fffffff;
+      }
+      topk_select(v, id, k, 0, lane, idx, tk.gate, sidx);
     }
-    topk_select(v, id, k, 0, lane, idx, tk.gate, sidx);
     __syncwarp();
     int sel[8];
 #pragma unroll
@@ -700,7 +709,12 @@ __global__ void __launch_bounds__(1024) permute_kernel(int32_t* idx, int T,
       if (tk.logits) tk.logits[i] = v;
     }
     __syncthreads();
-    if (warp < T) {
+    if (ROUTED) {
+      if (warp < T) {
+        const int pick = route_one(rp, warp, lane, lg + warp * E, list[warp]);
+        if (lane < k) sidx[warp * k + lane] = pick;
+      }
+    } else if (warp < T) {
       float v[8];
       int id[8];
 #pragma unroll
@@ -1291,9 +1305,9 @@ int launch_router(const float* Wr, int E, int H, const void* x, int xdt, int T, 
 
 int launch_permute(const int32_t* idx, int T, int k, int E, int32_t* offsets, int32_t* sorted,
                    cudaStream_t s) {
-  launch_pdl(permute_kernel, dim3(1), dim3(1024), 0, s, 0, const_cast<int32_t*>(idx), T, k, E, 0,
+  launch_pdl(permute_kernel<false>, dim3(1), dim3(1024), 0, s, 0, const_cast<int32_t*>(idx), T, k, E, 0,
              8, offsets, sorted, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0,
-             0, nullptr, nullptr, TopkIn{nullptr, 0, nullptr, nullptr}, nullptr, nullptr);
+             0, nullptr, nullptr, TopkIn{nullptr, 0, nullptr, nullptr}, nullptr, nullptr, RouteParams{});
   return cudaGetLastError() == cudaSuccess ? DQ_OK : DQ_ERR_CUDA;
 }
 
@@ -1381,11 +1395,11 @@ int launch_moe_forward(const dq_moe_desc& d, const void* x, int xdt, int T, floa
   int rc = DQ_OK;
   // up to 32 tokens in one call: the permute CTA takes the top-k too (one
   // warp per token), one launch less on the decode path
-  const bool fuse_topk = (stages & 3) == 3 && T <= 32 && !routing;
+  const bool fuse_topk = (stages & 3) == 3 && T <= 32;
   if (stages & 1) {
     rc = launch_router(d.router_W, d.E, d.hidden, x, xdt, T, d.top_k, pl.KS, part, lg, idx, gate,
                        s, !fuse_topk && !routing);
-    if (rc == DQ_OK && routing)
+    if (rc == DQ_OK && routing && !fuse_topk)
       rc = launch_route(part, DQ_F32, d.E, pl.KS, T, d.E, d.top_k, *routing, lg, idx, gate, s);
     if (rc != DQ_OK) return rc;
   }
@@ -1403,12 +1417,19 @@ int launch_moe_forward(const dq_moe_desc& d, const void* x, int xdt, int T, floa
   // one or two tokens of bf16/fp32 x: the permute CTA also makes their fp16
   // copy (measured: one launch less at T=1; at T=8 eight CTAs are faster)
   const bool fuse_x16 = general && xdt != DQ_F16 && T <= 2 && d.hidden <= 8192;
-  launch_pdl(permute_kernel, dim3(1), dim3(1024), 0, s, 0, idx, T, d.top_k, d.E, d.n_shared,
+  RouteParams rp = {};
+  if (routing) {
+    rp = route_params(*routing, d.E, d.top_k);
+    rp.T = T;
+    rp.idx = idx;
+    rp.gate = gate;
+  }
+  launch_pdl(routing && fuse_topk ? permute_kernel<true> : permute_kernel<false>, dim3(1), dim3(1024), 0, s, 0, idx, T, d.top_k, d.E, d.n_shared,
              pl.GW, offsets, sorted, inv, tok, groups, ngroups, pl.wide ? units : nullptr, nunits,
              fuse_x16 ? x : nullptr, xdt, d.hidden, fuse_x16 ? x16t : nullptr,
              fuse_x16 ? xinvt : nullptr,
              fuse_topk ? TopkIn{part, pl.KS, lg, gate} : TopkIn{nullptr, 0, nullptr, nullptr},
-             pl.single ? groups1 : nullptr, pl.single ? ng1 : nullptr);
+             pl.single ? groups1 : nullptr, pl.single ? ng1 : nullptr, rp);
   if (cudaGetLastError() != cudaSuccess) return DQ_ERR_CUDA;
 
   const int q = qk(d.fmt), bb = blk_bytes(d.fmt);
