@@ -1,6 +1,7 @@
 """torch-facing wrappers of the 4-bit paged K/V cache (marshalling only; see
 the dq_kv_* section of include/dqmoe.h for what each call computes)."""
 import ctypes
+import struct
 
 import torch
 
@@ -10,6 +11,10 @@ _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _plan, _append, _read, _attention, _rope = (lib.dq_kv_plan, lib.dq_kv_append, lib.dq_kv_read,
                                             lib.dq_kv_attention_ex, lib.dq_kv_append_rope)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+# dq_kv_rope's fields as the compiler lays them out (a packed string is made in a third of a structure's time)
+_ROPE = struct.Struct("@QqQqQqiiiQQQiifQqi0q")
+assert _ROPE.size == ctypes.sizeof(KvRope)
 
 # A decode step's calls take a few microseconds on the GPU, so the wrappers keep to few Python
 # operations: bound functions, plain integers, the stream's handle without a Stream object.
@@ -18,8 +23,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream(t):
     """The handle of the current stream; t has to lie on the current device, where kernels are launched."""
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError("tensors lie on device %d, the current device is %d" % (dev, torch.cuda.current_device()))
+    if dev != _current_device():
+        raise ValueError("tensors lie on device %d, the current device is %d" % (dev, _current_device()))
     if _raw_stream is not None:
         return _raw_stream(dev)
     return torch.cuda.current_stream(t.device).cuda_stream
@@ -157,9 +162,10 @@ def kv_append(cache, k, v, slots):
 
 def _heads(t, D, dev, name):
     """The row stride of t [T][heads][D], whose heads are consecutive."""
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError("%s must be [T][heads][%d]" % (name, D))
-    T, H, d = t.shape
+    T, H, d = shape
     a, b, c = t.stride()
     if d != D or t.get_device() != dev or c != 1 or (b != D and H > 1) or t.dtype not in _DT:
         raise ValueError("%s must be a CUDA tensor [T][heads][%d] of float32, float16 or bfloat16 on device %d "
@@ -177,30 +183,44 @@ def kv_append_rope(cache, q, k, v, slots, positions, inv_freq, interleaved=False
     factor: of cos and sin.  out: fp32/fp16/bf16 rows (out_dtype, q's unless given); q itself may be given.
     K's codes are those of the rotated values before any rounding.
     """
-    T, D, dev = k.shape[0], cache.head_dim, cache.dev
-    if k.dtype != v.dtype or k.dtype not in _DT or v.shape[0] != T:
-        raise ValueError("k and v must be rows of one dtype: float32, float16 or bfloat16")
-    ks, vs = _rows(cache, k, "k"), _rows(cache, v, "v")
-    _check(slots, "slots", torch.int64, dev, (T,))
-    _check(positions, "positions", torch.int32, dev, (T,))
+    shape, D, dev = k.shape, cache.head_dim, cache.dev
+    T, dt = shape[0], k.dtype
+    (ks, kh, kd), (vs, vh, vd) = k.stride(), v.stride()
+    H = cache.n_kv_heads
+    # one test of all that has to hold; what is wrong is found out after it fails
+    if not (shape == (T, H, D) and v.shape == shape and v.dtype is dt and dt in _DT and kd == 1 and vd == 1 and
+            (H == 1 or (kh == D and vh == D)) and k.get_device() == dev and v.get_device() == dev and
+            slots.shape == (T,) and slots.dtype is torch.int64 and slots.get_device() == dev and
+            positions.shape == (T,) and positions.dtype is torch.int32 and positions.get_device() == dev and
+            (T < 2 or (slots.stride(0) == 1 and positions.stride(0) == 1))):
+        if k.dtype != v.dtype or k.dtype not in _DT or v.shape[0] != T:
+            raise ValueError("k and v must be rows of one dtype: float32, float16 or bfloat16")
+        _rows(cache, k, "k")
+        _rows(cache, v, "v")
+        _check(slots, "slots", torch.int64, dev, (T,))
+        _check(positions, "positions", torch.int32, dev, (T,))
+        raise ValueError("k, v, slots and positions do not fit together")
     _check(inv_freq, "inv_freq", torch.float32, dev)
-    a = KvRope(None, 0, k.data_ptr(), ks, v.data_ptr(), vs, _DT[k.dtype], 0, T, slots.data_ptr(),
-               positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), interleaved, factor, None, 0, 0)
+    row = H * D
+    n_q = qs = q_ptr = os = out_ptr = out_dt = 0
     if q is not None:
         qs = _heads(q, D, dev, "q")
-        if q.dtype != k.dtype or q.shape[0] != T:
+        qshape = q.shape
+        if q.dtype is not dt or qshape[0] != T:
             raise ValueError("q must be rows of k's dtype")
         if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-        elif out.shape != q.shape:
+            out = torch.empty(qshape, dtype=out_dtype or dt, device=q.device)
+        elif out.shape != qshape:
             raise ValueError("out must have q's shape")
-        a.q, a.q_stride, a.n_q_heads = q.data_ptr(), qs, q.shape[1]
-        a.q_out, a.out_stride = out.data_ptr(), _heads(out, D, dev, "out")
-        a.out_dtype = _DT[out.dtype]
+        n_q, q_ptr, out_ptr = qshape[1], q.data_ptr(), out.data_ptr()
+        os, out_dt = _heads(out, D, dev, "out"), _DT[out.dtype]
     elif out is not None:
         raise ValueError("out is for q's rows")
     if T:
-        rc = _rope(cache._ref, ctypes.byref(a), _stream(k))
+        a = _ROPE.pack(q_ptr, qs, k.data_ptr(), ks if T > 1 else row, v.data_ptr(), vs if T > 1 else row, _DT[dt], n_q, T,
+                       slots.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), interleaved,
+                       factor, out_ptr, os, out_dt)
+        rc = _rope(cache._ref, a, _stream(k))
         if rc != 0:
             _raise("dq_kv_append_rope", rc)
     return out
@@ -215,12 +235,13 @@ def kv_read(cache, slots, dtype=torch.float32, out=None):
         out = (torch.empty(shape, dtype=dtype, device=slots.device),
                torch.empty(shape, dtype=dtype, device=slots.device))
     k, v = out
-    if k.dtype not in _DT:
+    dt = k.dtype
+    if dt not in _DT:
         raise ValueError("values are float32, float16 or bfloat16")
-    _check(k, "k", k.dtype, cache.dev, shape)
-    _check(v, "v", k.dtype, cache.dev, shape)
+    _check(k, "k", dt, cache.dev, shape)
+    _check(v, "v", dt, cache.dev, shape)
     if T:
-        rc = _read(cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _DT[k.dtype], _stream(k))
+        rc = _read(cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _DT[dt], _stream(k))
         if rc != 0:
             _raise("dq_kv_read", rc)
     return k, v

@@ -13,13 +13,14 @@ def _stream():
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_of(t):
     """The handle of the current stream; t has to lie on the current device, where kernels are launched."""
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError("tensors lie on device %d, the current device is %d" % (dev, torch.cuda.current_device()))
+    if dev != _current_device():
+        raise ValueError("tensors lie on device %d, the current device is %d" % (dev, _current_device()))
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -132,9 +133,10 @@ class MoeRouting:
         self.desc = MoeRoutingDesc(int(scores == "sigmoid"), n_groups, top_groups, int(group_score == "top2"),
                                    int(bool(renormalize)), scale, bias.data_ptr() if bias is not None else None)
         self._ref = ctypes.byref(self.desc)
+        self._bias_of = None if bias is None else (bias.numel(), bias.get_device())
 
     def check(self, E, dev):
-        if self.bias is not None and (self.bias.numel() != E or self.bias.get_device() != dev):
+        if self._bias_of is not None and self._bias_of != (E, dev):
             raise ValueError("the routing's bias must hold %d experts' on device %d" % (E, dev))
         return self._ref
 
@@ -146,10 +148,13 @@ _route = lib.dq_moe_route
 def moe_route(logits, top_k, routing=None, out=None):
     """The experts and gates of logits [T][E] (fp32/fp16/bf16; the row stride is free): (int32 [T][top_k],
     fp32 [T][top_k]).  routing: a MoeRouting (softmax over all experts, renormalised, unless given)."""
-    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    shape, dev = logits.shape, logits.get_device()
+    if len(shape) != 2 or dev < 0:
         raise ValueError("logits must be a CUDA tensor [T][E] with consecutive experts")
-    T, E = logits.shape
-    dev = logits.get_device()
+    T, E = shape
+    stride, one = logits.stride()
+    if one != 1 and E > 1:
+        raise ValueError("logits must be a CUDA tensor [T][E] with consecutive experts")
     ref = (routing or _DEFAULT_ROUTING).check(E, dev)
     if out is None:
         out = (torch.empty(T, top_k, dtype=torch.int32, device=logits.device),
@@ -161,7 +166,7 @@ def moe_route(logits, top_k, routing=None, out=None):
         raise ValueError("out must be contiguous CUDA tensors [%d][%d] of int32 and float32 on device %d" %
                          (T, top_k, dev))
     if T:
-        rc = _route(logits.data_ptr(), _dtype_code(logits), logits.stride(0) if T > 1 else E, T, E, top_k, ref,
+        rc = _route(logits.data_ptr(), _dtype_code(logits), stride if T > 1 else E, T, E, top_k, ref,
                     idx.data_ptr(), gate.data_ptr(), _stream_of(logits))
         if rc != 0:
             raise DqError("dq_moe_route", rc)
