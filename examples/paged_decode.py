@@ -9,10 +9,13 @@ Per step, all on the GPU and with no length read by the host:
   kv_attention  the query rows over the cache
   qgemv         attention output -> hidden
   moe_forward   the layer's experts
+With --rope the heads turn by their positions as they are appended (kv_append_rope takes
+kv_append's place), with --softcap the scores are capped, with --alibi they fall with the
+distance, and with --groups the experts are chosen by groups from sigmoid scores and a bias.
 The prompts run first, through the same calls; the decode step is captured once in a
 CUDA graph and replayed while every request grows.
 
-  python examples/paged_decode.py [--steps 32] [--requests 8]
+  python examples/paged_decode.py [--steps 32] [--requests 8] [--rope] [--softcap 30] [--alibi] [--groups 4]
 """
 import argparse
 import os
@@ -30,9 +33,13 @@ import synth  # noqa: E402
 
 
 class Layer:
-    """Synthetic weights: q|k|v and output projections and a small MoE in Q4_K."""
+    """Synthetic weights: q|k|v and output projections and a small MoE in Q4_K.
 
-    def __init__(self, hidden=1024, heads=8, kv_heads=2, head_dim=128, experts=8, top_k=2, ffn=512, seed=1):
+    rope: pairs of a head's values turn with its position; softcap, alibi: of the attention's scores; groups:
+    of experts, half of which a token keeps (0: the experts of the largest logits)."""
+
+    def __init__(self, hidden=1024, heads=8, kv_heads=2, head_dim=128, experts=8, top_k=2, ffn=512, seed=1, rope=False,
+                 softcap=0.0, alibi=False, groups=0):
         self.hidden, self.heads, self.kv_heads, self.head_dim = hidden, heads, kv_heads, head_dim
         self.n_qkv = (heads + 2 * kv_heads) * head_dim
         g = synth.streams(synth.BASE_SEED + seed, 2)
@@ -43,6 +50,16 @@ class Layer:
         self.moe = {k: up(v) for k, v in w.items() if v is not None}
         self.desc = dq.ops.make_desc(experts, top_k, hidden, ffn, 0, dq.Q4_K, self.moe["router_W"],
                                      self.moe["w_gate"], self.moe["w_up"], self.moe["w_down"])
+        self.inv_freq = self.slopes = self.routing = None
+        if rope:
+            self.inv_freq = 1e4 ** (torch.arange(0, head_dim, 2, dtype=torch.float64) / -head_dim)
+            self.inv_freq = self.inv_freq.float().cuda()
+        self.softcap = softcap
+        if alibi:
+            self.slopes = torch.exp2(-8.0 * torch.arange(1, heads + 1, dtype=torch.float32) / heads).cuda()
+        if groups:
+            self.routing = dq.MoeRouting(scores="sigmoid", bias=torch.linspace(-0.1, 0.1, experts, device="cuda"),
+                                         n_groups=groups, top_groups=max(groups // 2, 1), group_score="top2", scale=2.5)
 
     @staticmethod
     def norm(x):
@@ -62,10 +79,15 @@ class Layer:
         qkv = self.linear(self.w_qkv, self.n_qkv, self.hidden, self.norm(x))
         q, k, v = (t.view(T, -1, D) for t in qkv.split([H * D, self.kv_heads * D, self.kv_heads * D], 1))
         q, k = self.norm(q), self.norm(k).float() * 2.0     # per head, as recent models do
-        dq.kv_append(cache, k, v, plan.slots)               # v: the slice of the product as it is
-        att, lse = dq.kv_attention(cache, q, plan.q_start, plan.kv_len, table, max_q_len=max_q_len, ws=ws)
+        if self.inv_freq is None:
+            dq.kv_append(cache, k, v, plan.slots)           # v: the slice of the product as it is
+        else:
+            q = dq.kv_append_rope(cache, q.float(), k, v, plan.slots, plan.positions, self.inv_freq,
+                                  out_dtype=torch.bfloat16)
+        att, lse = dq.kv_attention(cache, q, plan.q_start, plan.kv_len, table, max_q_len=max_q_len, ws=ws,
+                                   softcap=self.softcap, slopes=self.slopes)
         x = x + 1e-2 * self.linear(self.w_out, self.hidden, H * D, att.view(T, H * D))
-        return x + 1e-3 * dq.moe_forward(self.desc, self.norm(x)), q, att, lse
+        return x + 1e-3 * dq.moe_forward(self.desc, self.norm(x), routing=self.routing), q, att, lse
 
 
 class Server:
@@ -129,8 +151,13 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--requests", type=int, default=8)
+    ap.add_argument("--rope", action="store_true")
+    ap.add_argument("--softcap", type=float, default=0.0)
+    ap.add_argument("--alibi", action="store_true")
+    ap.add_argument("--groups", type=int, default=0)
     a = ap.parse_args()
-    server, last, ms = run(a.requests, a.steps)
+    layer = Layer(rope=a.rope, softcap=a.softcap, alibi=a.alibi, groups=a.groups)
+    server, last, ms = run(a.requests, a.steps, layer=layer)
     print("prompts %s\nlengths %s\n%.3f ms per decode step of %d requests" %
           (last["prompts"], server.length.tolist(), ms, a.requests))
 
