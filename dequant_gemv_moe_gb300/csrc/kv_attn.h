@@ -378,12 +378,14 @@ struct TcWeightOf {
 };
 
 // Many rows: row tiles of 128 rows, two a CTA (one for head_dim 256), and tiles of 64 tokens; starting and
-// ending an item takes as long as four of them.
+// ending an item takes as long as four of them, or ten where scores are masked, capped or biased (7 prompts of
+// documents up to 3001 tokens, 12 heads of 64: 115 us with four, 108 with ten; 32 heads of 128 on 8: 347 and 290, with
+// a bias and no masks 546 and 425; one of 9000 tokens 108 and 111).
 constexpr int kTcTile = 64;
 template <int D>
 constexpr int kTcRowTiles = D == 256 ? 1 : 2;
 template <int D, bool EXT = false>
-using TcWalk = Walk<128 * kTcRowTiles<D>, kTcTile, 4, TcWeightOf<EXT>, EXT>;
+using TcWalk = Walk<128 * kTcRowTiles<D>, kTcTile, EXT ? 10 : 4, TcWeightOf<EXT>, EXT>;
 // a line of U units is cut into this many shares, of two units at least: none inside an item is without a tile
 DQ_HD int tc_shares(int ctas, int64_t U) { return (int)min((int64_t)ctas, U / 2); }
 

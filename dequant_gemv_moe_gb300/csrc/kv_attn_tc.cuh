@@ -38,8 +38,12 @@
 // the time, the exponentials none, three quarters of the products 6 %.  Four warps decoding and 64
 // scores a thread at a time took 966 us, two warps to a row 1088 (registers).
 // Modes other than kPlain: prefixes and first positions, capped scores, a distance bias (dq_kv_scores), an instance each:
-// the softmax's loop misses the instruction cache where it holds more than it needs (7 prompts with masks alone: 137
-// us, 159 in an instance that can cap as well).
+// the softmax's loop misses the instruction cache where it holds more than it needs (7 prompts of documents with
+// prefixes up to 3001 tokens, 12 heads of 64, docs_prompts below: 137 us with masks alone, 159 in an instance that can
+// cap as well; 107 since masks are bits).  cap_chunk below: the chunks of above with scores capped at 30, 1372 us;
+// with a bias 1052.  A cap takes an ex2 and half an inverse a score beside the softmax's own ex2: its pipe is
+// busy in 0.35 of the cycles, issue in 0.46, the tensor pipe in 0.23, and two softmax warps to a scheduler do not hide the
+// chain from a score to its weight.
 #pragma once
 
 #include <algorithm>
@@ -54,6 +58,14 @@ namespace {
 
 constexpr int kMaxCtas = 160;
 constexpr int kPiece = 32;                 // tokens per copy stage
+
+// Bits f to n - 1 of 32: predicates come out of a register's bits by the seven, where a comparison makes one.
+__device__ __forceinline__ uint32_t seen_bits(int f, int n) {
+  uint32_t m;
+  f = max(f, 0);
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(m) : "r"(f), "r"(max(n - f, 0)));
+  return m;
+}
 
 template <int D, int MODE = kPlain>
 struct TcCfg {
@@ -251,6 +263,9 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
   using C = TcCfg<D, MODE>;
   using B = KvBlk<D>;
   constexpr bool EXT = MODE != kPlain, ANY = MODE == kAnyScores, BIAS = MODE == kBias || ANY;
+  // Masks as bits, and by the warp's rows (docs_prompts below 130 -> 115 us, cap_chunk 1400 -> 1378; without masks and
+  // with a bias comparisons by the row tile's take less: 880 and 1052 us for the chunk so, 908 and 1086 with bits)
+  constexpr bool BITS = MODE != kPlain && MODE != kBias;
   // A bias falls with the distance: from the last tile to the first one, M hardly has to follow.
   constexpr bool BACK = BIAS;
   constexpr bool VALUES = MODE == kCaps || MODE == kBias;     // scores are changed as they are read
@@ -399,8 +414,10 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
       if (EXT) lo = max(lo, row_first(p, (int)q_at));
       int lo_all, hi_all;
       {
-        const int pa = it.shift + row_token(p, it.row0 + min(it.rows - 1, tile * 128));
-        const int pb = it.shift + row_token(p, it.row0 + min(it.rows, tile * 128 + 128) - 1);
+        // (the warp's rows, or the row tile's)
+        const int wr = tile * 128 + (BITS ? 32 * (warp & 3) : 0);
+        const int pa = it.shift + row_token(p, it.row0 + min(it.rows - 1, wr));
+        const int pb = it.shift + row_token(p, it.row0 + min(it.rows - 1, wr + (BITS ? 31 : 127)));
         hi_all = seen_end(p, it.len, pa, prefix);
         lo_all = first_seen(p, pb);
         if (EXT) lo_all = max(lo_all, row_first(p, it.first + pb - it.shift));
@@ -522,8 +539,9 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
           }
           if (!inner) {
             const int n = hi - tok0 - c, f = lo - tok0 - c;
+            const uint32_t see = BITS ? seen_bits(f, n) : 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = i < n && i >= f ? r[i] : 0xFF800000u;
+            for (int i = 0; i < 32; ++i) r[i] = (BITS ? see >> i & 1 : i < n && i >= f) ? r[i] : 0xFF800000u;
           }
         };
         // 32 scores of this thread's row, those that it does not see as -inf
@@ -531,7 +549,11 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
           tmem_ld32(s_addr + c, r);
           tmem_wait_ld();
           tmem_use(r);
-          if (!inner) {
+          if (BITS && !inner) {
+            const uint32_t see = seen_bits(lo - tok0 - c, hi - tok0 - c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = see >> i & 1 ? r[i] : 0xFF800000u;
+          } else if (!inner) {
             const int n = hi - tok0 - c;
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = i < n ? r[i] : 0xFF800000u;
