@@ -111,7 +111,17 @@ struct Item {
   int begin, end;              // tokens that some row sees
   int t0, tiles;               // first tile, tiles (at least one)
   int prefix, fine;            // EXT: the request's prefix; whether its last row sees few tokens (is_fine)
+  int sure;                    // EXT: the tokens from begin up to here are seen by its first row
 };
+
+// Whether some row of the item sees token a.  Of a window or a prefix every token of [begin, end) is seen; rows with
+// first positions may see nothing, between two documents or at the end, and a token that its own row does not see
+// is seen by none: the rows in front of it do not reach it, those behind it start later.
+template <bool EXT>
+DQ_HD bool token_seen(const AttnParams& p, const Item& it, int a) {
+  if (a < it.begin || a >= it.end) return false;
+  return !EXT || a < it.sure || row_first(p, it.first + (a - it.shift)) <= a;
+}
 
 constexpr int kFineTokens = 1024;          // (see is_fine)
 
@@ -137,6 +147,7 @@ struct Walk {
       const int last = row_first(p, it.first + hi - it.shift);
       it.begin = min(max(it.begin, row_first(p, it.first + lo - it.shift)), it.end);
       const int span = it.end - last;
+      it.sure = p.first_pos ? min(seen_end(p, it.len, lo, it.prefix), it.end) : it.end;
       it.fine = (p.window > 0 ? min(p.window, span) : span) <= kFineTokens;
     }
     it.t0 = it.begin / TILE;

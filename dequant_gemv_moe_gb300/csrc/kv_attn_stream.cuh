@@ -349,18 +349,20 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
       const int prefix = EXT ? it.prefix : 0;
       hi_all = seen_end(p, it.len, lo_pos, prefix);
       lo_all = first_seen(p, hi_pos);
-      if (EXT) lo_all = max(lo_all, row_first(p, it.first + hi_pos - it.shift));
       if (lane < C::ROWS) {
         const int row = EXT ? min(it.row0 + lane, it.row0 + it.rows - 1) : it.row0 + lane;
         const int tokq = row_token(p, row), pos = it.shift + tokq;
         S.hi[lane] = seen_end(p, it.len, pos, prefix);
         S.lo[lane] = first_seen(p, pos);
         if (EXT) {
-          S.lo[lane] = max(S.lo[lane], row_first(p, it.first + tokq));
+          const int lo = max(S.lo[lane], row_first(p, it.first + tokq));
+          S.lo[lane] = lo;
+          lo_all = max(lo_all, lo);
           S.pos[lane] = pos;
           S.slope[lane] = BIAS && p.slopes ? __ldg(p.slopes + it.h * p.group + row - tokq * p.group) * kLog2e : 0.f;
         }
       }
+      if (EXT) lo_all = __reduce_max_sync(0xffffffffu, lo_all);
       __syncwarp();
     }
 
@@ -449,8 +451,11 @@ kv_stream_kernel(const __grid_constant__ AttnParams p) {
         }
         // tokens 2t + 8j of block k, and the one behind: those that no row sees may hold anything, their V scales
         // become 0
+        uint32_t seen = 0;
+        if (EXT && !inner) seen = __ballot_sync(0xffffffffu, token_seen<EXT>(p, S.at[0].it, tok0 + lane));
         auto kept = [&](int k, int j) -> uint32_t {
           const int a = tok0 + k * 16 + 8 * j + 2 * lt;
+          if (EXT) return (seen >> (a - tok0) & 1 ? 0x0000FFFFu : 0u) | (seen >> (a + 1 - tok0) & 1 ? 0xFFFF0000u : 0u);
           const int from = S.at[0].it.begin, to = S.at[0].it.end;
           return ((a >= from && a < to) ? 0x0000FFFFu : 0u) | ((a + 1 >= from && a + 1 < to) ? 0xFFFF0000u : 0u);
         };

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
   using C = TcCfg<D, MODE>;
   using B = KvBlk<D>;
   constexpr bool EXT = MODE != kPlain, ANY = MODE == kAnyScores, BIAS = MODE == kBias || ANY;
-  // Masks as bits, and by the warp's rows (docs_prompts below 130 -> 115 us, cap_chunk 1400 -> 1378; without masks and
+  // Masks as bits (docs_prompts below 130 -> 115 us, cap_chunk 1400 -> 1378; without masks and
   // with a bias comparisons by the row tile's take less: 880 and 1052 us for the chunk so, 908 and 1086 with bits)
   constexpr bool BITS = MODE != kPlain && MODE != kBias;
   // A bias falls with the distance: from the last tile to the first one, M hardly has to follow.
@@ -412,15 +412,15 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
       const int hi = seen_end(p, it.len, pos, prefix);
       int lo = first_seen(p, pos);
       if (EXT) lo = max(lo, row_first(p, (int)q_at));
-      int lo_all, hi_all;
-      {
-        // (the warp's rows, or the row tile's)
-        const int wr = tile * 128 + (BITS ? 32 * (warp & 3) : 0);
-        const int pa = it.shift + row_token(p, it.row0 + min(it.rows - 1, wr));
-        const int pb = it.shift + row_token(p, it.row0 + min(it.rows - 1, wr + (BITS ? 31 : 127)));
-        hi_all = seen_end(p, it.len, pa, prefix);
+      int lo_all, hi_all;                  // what all of the row tile's rows see, or of the warp's
+      if (EXT) {
+        hi_all = __reduce_min_sync(0xffffffffu, hi);
+        lo_all = __reduce_max_sync(0xffffffffu, lo);
+      } else {
+        const int pa = it.shift + row_token(p, it.row0 + min(it.rows - 1, tile * 128));
+        const int pb = it.shift + row_token(p, it.row0 + min(it.rows, tile * 128 + 128) - 1);
+        hi_all = seen_end(p, it.len, pa);
         lo_all = first_seen(p, pb);
-        if (EXT) lo_all = max(lo_all, row_first(p, it.first + pb - it.shift));
       }
       const float cfs = ANY ? 1.f : cf;    // of the scores that the softmax reads
       const float slope = BIAS && p.slopes ? __ldg(p.slopes + head) * -kLog2e : 0.f;
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
       const bool fine = is_fine_of<EXT>(p, it);
       for (int j = ta; j < tb && ok; ++j) {
         const int tok0 = (it.t0 + (BACK ? ta + tb - 1 - j : j)) * TT;
-        const bool inner = tok0 >= it.begin && tok0 <= it.end - TT;
+        const bool inner = tok0 >= it.begin && tok0 <= (EXT ? it.sure : it.end) - TT;
         const int buf = gt % C::KVS, buf2 = (gt + 1) % C::KVS;
         if (gt >= C::KVS) ok = mbar_wait(&kv_empty[buf], (gt / C::KVS - 1) & 1);
         if (fine && ok && gt + 1 >= C::KVS) ok = mbar_wait(&kv_empty[buf2], ((gt + 1) / C::KVS - 1) & 1);
@@ -799,8 +799,9 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
         const uint32_t rb = raw0 + st * C::PIECE_B;
         // a token that no row sees may hold anything: its V scale becomes 0
         const int at0 = tok0 + pc * kPiece + vrow;
-        const uint32_t keep = (at0 >= it.begin && at0 < it.end ? 0x0000FFFFu : 0u) |
-                              (at0 + 1 >= it.begin && at0 + 1 < it.end ? 0xFFFF0000u : 0u);
+        uint32_t keep = 0;
+        if (!inner)
+          keep = (token_seen<EXT>(p, it, at0) ? 0x0000FFFFu : 0u) | (token_seen<EXT>(p, it, at0 + 1) ? 0xFFFF0000u : 0u);
         const uint32_t row_b = pc * kPiece * 128;          // 32 rows of 128 bytes
         auto decode = [&](auto fine_c) {
           constexpr bool FINE = decltype(fine_c)::value;

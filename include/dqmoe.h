@@ -610,7 +610,7 @@ typedef struct {
   int32_t T;                /* rows, >= 1 */
   const int64_t* slots;     /* device [T], as dq_kv_append's */
   const int32_t* positions; /* device [T] */
-  const float* inv_freq;    /* device fp32 [rotary_dim / 2], radians per position */
+  const float* inv_freq;    /* device fp32 [rotary_dim / 2], radians per position, of magnitude at most 1 */
   int32_t rotary_dim;       /* a multiple of 16 (others: DQ_ERR_UNSUPPORTED), <= head_dim */
   int32_t interleaved;      /* 0 or 1 */
   float factor;             /* of cos and sin: 1, or a long-context scheme's; in (0, 1e4] */
@@ -697,7 +697,7 @@ typedef struct {
   const float* slopes;        /* device fp32 [n_q_heads], finite, or NULL */
   const int32_t* prefix_len;  /* device [B], or NULL; above kv_len it reads as that, below 0 as 0 */
   const int32_t* first_pos;   /* device [T], not descending within a request (else rows may miss positions that
-                                 they should see), or NULL; below 0 reads as 0 */
+                                 they should see; none sees more), or NULL; below 0 reads as 0 */
 } dq_kv_scores;
 
 /* Errors: as dq_kv_attention; DQ_ERR_ARG for another softcap. */

@@ -11,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv_ref
 import scores_ref
 from test_gpu_kv import U, Case, _i32, dq  # noqa: F401  (dq is the fixture)
 
@@ -222,3 +223,71 @@ def test_one_graph_serves_other_masks(dq):  # noqa: F811
         torch.cuda.synchronize()
         want, wl = c.call(softcap=30.0, slopes=steep(8), first_pos=a)
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+GAPS = [([4, 9, 1], [50, 40, 7], 8, 2, 128), ([6], [700], 3, 3, 64), ([5, 8], [30, 600], 8, 1, 256),
+        ([200, 90], [260, 400], 4, 2, 64), ([300], [1900], 2, 2, 128), ([150, 40], [900, 40], 4, 1, 256)]
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(softcap=300.0), dict(slopes=True),
+                                dict(softcap=20.0, slopes=True), dict(prefix=True), dict(window=25)])
+@pytest.mark.parametrize("new,kv,H,n_kv,D", GAPS)
+def test_what_no_row_sees_may_hold_anything(dq, new, kv, H, n_kv, D, kw):  # noqa: F811
+    # documents with rows between and behind them that see nothing, as padding does: their tokens hold NaN scales
+    c = Scored(dq, 15, new, kv, H, n_kv, D, 16, "bf16")
+    kw = dict(kw)
+    if kw.pop("slopes", False):
+        kw["slopes"] = steep(H)
+    prefix = [k // 4 for k in kv] if kw.pop("prefix", False) else None
+    first = []
+    for n, L in zip(new, kv):
+        at, far = max(L - n - 5, 0), 2 ** 31 - 1
+        for i in range(n):
+            third = i * 3 // n
+            # the first third sees its document, the second one nothing up to the next one, the last rows nothing at all
+            first.append(at if third == 0 else max(at, L - n + n * 2 // 3) if i < n - n // 5 else far)
+    first = np.array(first)
+    nan = np.frombuffer(np.float16(np.nan).tobytes(), dtype=np.uint8)
+    lost = 0
+    for r, (n, L) in enumerate(zip(new, kv)):
+        f = first[int(c.start[r]):int(c.start[r + 1])]
+        see = scores_ref.rows_see(n, L, True, kw.get("window", 0), 0 if prefix is None else prefix[r], f).any(0)
+        for j in np.nonzero(~see)[0]:
+            page, off = c.table[r, j // 16], j % 16
+            for at in [kv_ref.k_scale(D, off, g) for g in range(D // 32)] + [kv_ref.v_scale(D, off, g) for g in range(D // 32)]:
+                c.host[page, :, 0, at:at + 2] = nan
+            lost += j >= L - n
+    assert lost > 0
+    c.cache.pages.copy_(torch.from_numpy(c.host).cuda().reshape(c.cache.pages.shape))
+    if prefix is not None:
+        kw["prefix_len"] = prefix
+    c.call(exact=False, first_pos=first, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(softcap=300.0), dict(slopes=True), dict(softcap=2.0, slopes=True)])
+@pytest.mark.parametrize("new,kv,H,n_kv,D", [([8], [500], 8, 2, 128), ([64, 70], [300, 900], 2, 2, 64), ([250], [1500], 4, 2, 128)])
+def test_first_positions_that_descend_show_no_row_more(dq, new, kv, H, n_kv, D, kw):  # noqa: F811
+    # out of contract, but a row still sees no position below its own: all V there is 100 times as large
+    c = Scored(dq, 16, new, kv, H, n_kv, D, 16, "fp16")
+    kw = dict(kw)
+    if kw.pop("slopes", False):
+        kw["slopes"] = [0.0] * H
+    c.q.zero_()
+    T, rng = sum(new), np.random.default_rng(3)
+    for low in (200, 420):
+        first = np.full(T, low)
+        first[rng.permutation(T)[:T // 2]] = 5              # rows that may see what others may not
+        first[int(c.start[-1]) - 1] = 5                     # (the last row among them)
+        host = c.host.copy()
+        for r, L in enumerate(kv):
+            for j in range(L):
+                for g in range(D // 32):
+                    at = kv_ref.v_scale(D, j % 16, g)
+                    host[c.table[r, j // 16], :, 0, at:at + 2] = np.frombuffer(
+                        np.float16(64.0 if j < low else 2.0 ** -6).tobytes(), dtype=np.uint8)
+        c.cache.pages.copy_(torch.from_numpy(host).cuda().reshape(c.cache.pages.shape))
+        out, _ = c.run(max_q_len=max(new), first_pos=_i32(first), softcap=kw.get("softcap", 0.0),
+                       slopes=None if "slopes" not in kw else torch.zeros(H, device="cuda"))
+        torch.cuda.synchronize()
+        assert dq.device_status() == 0
+        assert out.float().abs().amax((1, 2)).cpu().numpy()[first == low].max() <= 8 * 2.0 ** -6
