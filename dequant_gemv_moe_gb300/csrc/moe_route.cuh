@@ -23,7 +23,7 @@
 //
 // What bounds it: instructions, 760 a token (the rounds 170, keys and sort 100, scores and groups 180), with issue in
 // 0.6 of the cycles; a warp of its own for every token, so that the GPU evens out what the doubts cost.
-// 16384 tokens of 256 experts, 8 of 4 in 8 groups: 17.9 us (bytes alone: 2.7); 8 tokens 3.1 us, a
+// 16384 tokens of 256 experts, 8 of 4 in 8 groups: 16.3 us (bytes alone: 2.7); 8 tokens 2.9 us, a
 // launch and one token's chain.  Eight tokens to a warp, four lanes each, took 560 instructions a token but 21 us:
 // too few warps to hide their chains.
 #pragma once
@@ -70,6 +70,12 @@ __device__ __forceinline__ uint32_t route_key(float f) {
 }
 __device__ __forceinline__ float route_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// (no intermediate leaves fp32's range before the score itself does)
+__device__ __forceinline__ float sigmoid_of(float x) {
+  const float e = expf(-fabsf(x));
+  return (x >= 0.f ? 1.f : e) / (1.f + e);
 }
 
 // The expert at place j of a lane.
@@ -126,6 +132,11 @@ static __device__ __noinline__ Pair score_pair(int sigmoid, float x, float top) 
   const Pair q = divide(e, add({1.f, 0.f}, e));
   return x >= 0.f ? add({1.f, 0.f}, {-q.h, -q.l}) : q;
 }
+// Below 2^-80, where a pair's second part leaves fp32's range, a score is formed in 64 bits: z as in e^(x - top) / z.
+constexpr float kLeastPair = 0x1p-80f;
+static __device__ __noinline__ double score_tiny(int sigmoid, float x, float top, Pair z) {
+  return sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / ((double)z.h + (double)z.l);
+}
 __device__ __forceinline__ Pair shfl_xor_pair(Pair a, int o) {
   return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
 }
@@ -137,7 +148,14 @@ __device__ __forceinline__ Key64 key64(double x) {
   return b ^ ((b >> 63) & 0x7fffffffffffffffLL);
 }
 __device__ __forceinline__ double value64(Key64 k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL)); }
-__device__ __forceinline__ Key64 key64(Pair a, float bias) { return key64((double)a.h + (double)a.l + (double)bias); }
+// The value of logit x, whose score is e.
+__device__ __forceinline__ Key64 key64(Pair e, float bias, int sigmoid, float x, float top, Pair z) {
+  const double s = e.h < kLeastPair ? score_tiny(sigmoid, x, top, z) : (double)e.h + (double)e.l;
+  return key64(s + (double)bias);
+}
+__device__ __forceinline__ Key64 sigmoid_key(float x, float bias) {
+  return key64(score_pair(1, x, 0.f), bias, 1, x, 0.f, {1.f, 0.f});
+}
 
 // The token's selection in 64 bits: lane i < k gets pick i and its score.
 // `row`: the token's logits, or `summed`.
@@ -171,8 +189,8 @@ static __device__ __noinline__ void route_exact(const RouteParams& p, const floa
     if (!p.sigmoid && z.h > 0.f) e[j] = divide(e[j], z);
     // (without a bias logits are compared, which differ where scores of 1 or 0 do not; only sums take scores)
     if (!(l[j] > -INFINITY)) v[j] = kNoKey;
-    else if (p.bias) v[j] = key64(e[j], __ldg(p.bias + e0 + j));
-    else v[j] = p.top2 ? key64(e[j], 0.f) : key64((double)l[j]);
+    else if (p.bias || p.top2) v[j] = key64(e[j], p.bias ? __ldg(p.bias + e0 + j) : 0.f, p.sigmoid, l[j], top, z);
+    else v[j] = key64((double)(l[j] + 0.f));
     g2 = max(g2, min(g1, v[j]));
     g1 = max(g1, v[j]);
   }
@@ -198,7 +216,7 @@ static __device__ __noinline__ void route_exact(const RouteParams& p, const floa
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (!p.bias) v[j] = key64((double)l[j]);
+    if (!p.bias) v[j] = key64((double)(l[j] + 0.f));
     if (!(l[j] > -INFINITY)) v[j] = kNoKey;
   }
   uint32_t left = (1u << n) - 1;           // places that are not taken yet
@@ -379,9 +397,14 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
       for (int j = 0; j < 8; ++j)
         if (j < n) v[j] += __ldg(p.bias + e0 + j);
     }
-  } else if (!group_sums) {
+  } else {
+    // (-0 is 0; a sum is never -0)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = l[j];
+    for (int j = 0; j < 8; ++j) l[j] += 0.f;
+    if (!group_sums) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = l[j];
+    }
   }
   if (ODD || !FULL) {
 #pragma unroll
@@ -436,7 +459,7 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
           list_experts(list, at, e0, may);
           const int e = list[min(lane, all - 1)];
           const float x = usable(summed ? summed[e] : logit_at<DT>(p, row + e));
-          const Key64 y = key64(score_pair(1, x, 0.f), p.bias ? __ldg(p.bias + e) : 0.f);
+          const Key64 y = sigmoid_key(x, p.bias ? __ldg(p.bias + e) : 0.f);
           Key64 k1 = kNoKey, k2 = kNoKey;
 #pragma unroll 1
           for (int i = 0; i < all; ++i) {
@@ -505,7 +528,7 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
   float s = 0.f;
   if (lane < p.k && mine >= 16u) {
     const float x = usable(summed ? summed[pick] : logit_at<DT>(p, row + pick));
-    s = p.sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) / z;
+    s = p.sigmoid ? sigmoid_of(x) : expf(x - top) / z;
   }
   if (__any_sync(0xffffffffu, doubtful || close)) {
     // The experts that may be among the picks, a lane each, where they are so few that they find room and a value
@@ -523,7 +546,7 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
       list_experts(list, at, e0, may);
       const int e = list[min(lane, all - 1)];
       const float x = usable(summed ? summed[e] : logit_at<DT>(p, row + e));
-      const Key64 y = by_logit ? key64((double)x) : key64(score_pair(1, x, 0.f), __ldg(p.bias + e));
+      const Key64 y = by_logit ? key64((double)(x + 0.f)) : sigmoid_key(x, __ldg(p.bias + e));
       int rank = 0;
 #pragma unroll 1
       for (int i = 0; i < all; ++i) {
@@ -536,7 +559,7 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
       if (lane < p.k) {
         pick = list[lane];
         const float x = usable(summed ? summed[pick] : logit_at<DT>(p, row + pick));
-        s = p.sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) / z;
+        s = p.sigmoid ? sigmoid_of(x) : expf(x - top) / z;
       }
       __syncwarp();
     } else {

@@ -24,7 +24,7 @@ def dq():
     return m
 
 
-def check(dq, logits, top_k, **kw):
+def check(dq, logits, top_k, small=1e-37, **kw):
     bias = kw.get("bias")
     r = dq.MoeRouting(**{**kw, "bias": None if bias is None else torch.tensor(bias, dtype=torch.float32).cuda()})
     idx, gate = dq.moe_route(logits, top_k, r)
@@ -40,7 +40,7 @@ def check(dq, logits, top_k, **kw):
         x = np.where(np.isfinite(host), host, 0.0).astype(np.float64)
         far = np.abs(np.take_along_axis(x, want_i, 1) - x.max(1, keepdims=True))
         tol = tol + np.minimum(far, 100.0).max(1, keepdims=True) * 2.0 ** -24
-    assert (np.abs(got - want_g) <= tol * np.abs(want_g) + 1e-37).all(), np.abs(got / want_g - 1).max()
+    assert (np.abs(got - want_g) <= tol * np.abs(want_g) + small).all(), np.abs(got / want_g - 1).max()
     return idx, gate
 
 
@@ -84,6 +84,38 @@ def test_values_that_fp32_cannot_tell_apart(dq):
     # a bias that cancels the score
     s = 1.0 / (1.0 + np.exp(-l[0].astype(np.float64)))
     check(dq, torch.tensor(l[:1]).cuda(), 8, scores="sigmoid", bias=-s)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("E,groups,top", [(256, 1, 1), (256, 8, 4), (60, 4, 2)])
+def test_zeros_of_both_signs_are_equal(dq, dtype, E, groups, top):
+    g = torch.Generator().manual_seed(E)
+    l = torch.where(torch.rand(30, E, generator=g) < 0.5, -0.0, 0.0)
+    l[10:] = torch.where(torch.rand(20, E, generator=g) < 0.9, l[10:], -1.0)
+    l[20:, 3] = 1.0
+    for scores in ("softmax", "sigmoid"):
+        for group_score in ("max", "top2"):
+            for bias in (None, np.zeros(E)):
+                check(dq, l.to(NP[dtype]).cuda(), 6, scores=scores, n_groups=groups, top_groups=top, group_score=group_score,
+                      bias=bias)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top,group_score", [(1, 1, "max"), (4, 2, "top2"), (4, 2, "max")])
+@pytest.mark.parametrize("bias", [True, False])
+def test_scores_that_fp32_has_not(dq, scores, groups, top, group_score, bias):
+    # e^-60 to e^-800: beside a bias of 0 64 bits tell them apart (below e^-745, or 1 / e^710, they are 0 there too)
+    E = 32
+    g = torch.Generator().manual_seed(5)
+    l = -60 - 740 * torch.rand(40, E, generator=g)
+    l[:20, 8:16] = l[:20, :8].round()                       # some groups near one another
+    l[:20, :8] = l[:20, :8].round() + torch.randint(-1, 2, (20, 8), generator=g) * 2.0 ** -14
+    l[::3, 5] = 1.0
+    b = np.zeros(E)
+    b[::7] = 1e-40
+    # an fp32 score below 2^-126 is off by 2^-149, and its gate, a share of a sum of 1e-20 and more, by 2^-149 / 1e-20
+    check(dq, l.cuda(), 8, small=2.0 ** -149 * 1e20, scores=scores, bias=b if bias else None, n_groups=groups, top_groups=top,
+          group_score=group_score)
 
 
 def test_experts_that_are_out(dq):
