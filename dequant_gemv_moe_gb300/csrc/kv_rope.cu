@@ -49,6 +49,7 @@ struct RopeParams {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMostTile = 8;             // tokens of a CTA in a long call
+constexpr int kTileCtas = 300;
 constexpr int kLongCall = 1024;
 // of |a| + |b|: cos and sin 2.3e-7 with the factor's product, a product and a sum of 2^-24 each
 constexpr float kErr = 4.5e-7f;
@@ -480,8 +481,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kv_rope_kernel(const __grid_c
 template <int D>
 int launch_rope(RopeParams p, int dtype, cudaStream_t s) {
   constexpr int HL = 32 / (D / 16);
-  // long calls spread an angle's price over more heads, short ones the work over more warps
-  p.q_each = HL * (p.T >= kLongCall ? 8 : 2);
+  // long calls spread an angle's price over more heads, short ones and rows of twice the bytes the work over more warps
+  // (32 heads of 128 and 8: 4096 bf16 tokens 21.7 us with two turns, 20.9 with eight; 1023 7.7 and 8.1; 2047 fp32 tokens
+  // 16.6, 16.4, 25.4 with one, two, eight, 1023 with 15 heads of 64 and 5 6.2, 7.4, 7.5)
+  p.q_each = HL * (dtype == DQ_F32 ? 1 : p.T >= kLongCall ? 8 : 2);
   p.q_splits = (p.q_heads + p.q_each - 1) / p.q_each;
   const int64_t ctas = 2 * (((int64_t)p.T + p.tile - 1) / p.tile) + ((int64_t)p.T * p.q_splits + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 2147483647 || (int64_t)p.T * p.q_splits > 2147483647) return DQ_ERR_UNSUPPORTED;
@@ -546,7 +549,10 @@ extern "C" int dq_kv_append_rope(const dq_kv_cache* cache, const dq_kv_rope* a, 
   p.out = a->q_out;
   p.out_stride = a->out_stride;
   p.out_dtype = a->out_dtype;
-  p.tile = a->T >= kLongCall ? kMostTile : 1;
+  // about kTileCtas CTAs of K, of two tokens at least (64 tokens: 5.0 us with one, 4.3, 6.7, 8.5 with two, four, eight;
+  // 1023: 11.4, 8.1, 7.6, 9.7; 4096: 40.0, 25.9, 22.6, 21.0)
+  p.tile = 2;
+  while (p.tile < kMostTile && p.tile * kTileCtas < a->T) p.tile *= 2;
   return by_dim(cache->head_dim,
                 [&](auto d) { return launch_rope<decltype(d)::value>(p, a->dtype, (cudaStream_t)stream); });
 }

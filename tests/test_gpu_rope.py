@@ -92,7 +92,8 @@ def check_q(got, q, pn, freq, interleaved=False, factor=1.0, name=None):
 
 CASES = [(1, 1, 1, 64, 64, False), (1, 32, 8, 128, 128, False), (3, 5, 5, 64, 32, True), (5, 4, 1, 256, 256, False),
          (37, 6, 2, 128, 64, False), (37, 6, 3, 128, 96, True), (64, 8, 8, 256, 64, True), (200, 7, 1, 128, 16, False),
-         (33, 16, 2, 64, 48, False), (1025, 3, 1, 128, 128, False), (1026, 2, 2, 64, 64, True), (1030, 4, 2, 256, 112, False)]
+         (33, 16, 2, 64, 48, False), (601, 3, 1, 256, 64, False), (1203, 2, 3, 64, 48, True), (2402, 1, 1, 128, 128, False),
+         (1025, 3, 1, 128, 128, False), (1026, 2, 2, 64, 64, True), (1030, 4, 2, 256, 112, False)]
 
 
 @pytest.mark.parametrize("T,H,HK,D,R,inter", CASES)
