@@ -250,13 +250,8 @@ __device__ __forceinline__ bool larger(Pair a, Pair b) {
   const float la = a.h < 0.f ? -a.l : a.l, lb = b.h < 0.f ? -b.l : b.l;
   return fabsf(a.h) > fabsf(b.h) || (fabsf(a.h) == fabsf(b.h) && la > lb);
 }
-// The fp16 nearest to -x / 8: the last bit of x.h stands for what lies behind it (rounded to odd), so that one rounding
-// is all there is.
-__device__ __forceinline__ __half scale_of(Pair x) {
-  uint32_t b = __float_as_uint(x.h);
-  if (x.l != 0.f) b = (b - ((x.l < 0.f) != (x.h < 0.f) ? 1u : 0u)) | 1u;
-  return __float2half_rn(__uint_as_float(b) * -0.125f);
-}
+// The scale: the fp16 nearest to -1/8 of the fp32 nearest to x (rows of dq_kv_append are fp32 at most).
+__device__ __forceinline__ __half scale_of(Pair x) { return __float2half_rn(x.h * -0.125f); }
 __device__ __forceinline__ Pair within_fp16(Pair x) {
   return fabsf(x.h) > 65504.f || (fabsf(x.h) == 65504.f && (x.l < 0.f) == (x.h < 0.f)) ? Pair{copysignf(65504.f, x.h), 0.f} : x;
 }

@@ -24,3 +24,13 @@ def rotate(x, pos, inv_freq, interleaved=False, factor=1.0):
 
 def frequencies(R, base=10000.0):
     return (base ** (-np.arange(0, R, 2) / R)).astype(np.float32)
+
+
+def quantise(x):
+    """x [..., D] in 64 bits -> (codes, scales [..., D / 32]) of Q4_0 blocks: exact arithmetic, but that the scale is
+    the fp16 nearest to -1/8 of the largest value's fp32."""
+    g = np.clip(np.asarray(x, dtype=np.float64), -65504.0, 65504.0).reshape(*x.shape[:-1], -1, 32)
+    m = np.take_along_axis(g, np.argmax(np.abs(g), axis=-1)[..., None], -1)
+    d = (m.astype(np.float32) / np.float32(-8)).astype(np.float16).astype(np.float64)
+    c = np.clip(np.floor(g / np.where(d == 0, 1.0, d) + 8.5), 0, 15)
+    return np.where(d == 0, 8, c).astype(np.int64).reshape(x.shape), d[..., 0]

@@ -61,7 +61,7 @@ def run(dq, q, k, v, pos, freq, page=16, interleaved=False, factor=1.0, slots=No
     kr, _ = rope_ref.rotate(kf, np.maximum(pn, 0), freq, interleaved, factor)
     pages = cache.pages.cpu().numpy().reshape(n_pages, hk, page // 16, 18 * D)
     want_cache = before.cpu().numpy().reshape(pages.shape)
-    kc, kd = kv_ref.quantise(kr)
+    kc, kd = rope_ref.quantise(kr)
     vc, vd = quantise32(vf)
     wk = (kd[..., None] * (kc.reshape(T, hk, -1, 32) - 8)).reshape(T, hk, D)
     wv = (vd[..., None] * (vc.reshape(T, hk, -1, 32) - 8)).reshape(T, hk, D)
@@ -222,6 +222,6 @@ def test_captured(dq):
         torch.cuda.synchronize()
         check_q(out, q, np.full(T, at), freq, name="bf16")
         kr, _ = rope_ref.rotate(k.float().cpu().numpy(), np.full(T, at), freq)
-        c, d = kv_ref.quantise(kr)
+        c, d = rope_ref.quantise(kr)
         want = (d[..., None] * (c.reshape(T, 2, -1, 32) - 8)).reshape(T, 2, D)
         np.testing.assert_array_equal(dq.kv_read(cache, slots)[0].cpu().numpy(), want)

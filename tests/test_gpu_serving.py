@@ -74,7 +74,7 @@ def test_serving_loop(example, monkeypatch, rope, softcap, alibi, groups):  # no
         # check_q's bars are of the output's type: bf16's half step here, of fp32 rows
         check_q(got, q_in, pos, freq.cpu().numpy(), name="bf16")
         kr, _ = rope_ref.rotate(k.cpu().numpy(), pos, freq.cpu().numpy())
-        kc, kd = kv_ref.quantise(kr)
+        kc, kd = rope_ref.quantise(kr)
         vc, vd = quantise32(v.cpu().numpy())
         host = cache.pages.cpu().numpy().reshape(cache.n_pages, layer.kv_heads, server.page_size // 16, 18 * layer.head_dim)
         for h in range(layer.kv_heads):
