@@ -110,7 +110,7 @@ struct Item {
   int shift;                   // position of its first token
   int begin, end;              // tokens that some row sees
   int t0, tiles;               // first tile, tiles (at least one)
-  int prefix, fine;            // EXT: the request's prefix; whether its last row sees few tokens (is_fine)
+  int prefix;                  // EXT: the request's
   int sure;                    // EXT: the tokens from begin up to here are seen by its first row
 };
 
@@ -122,8 +122,6 @@ DQ_HD bool token_seen(const AttnParams& p, const Item& it, int a) {
   if (a < it.begin || a >= it.end) return false;
   return !EXT || a < it.sure || row_first(p, it.first + (a - it.shift)) <= a;
 }
-
-constexpr int kFineTokens = 1024;          // (see is_fine)
 
 // A call's work as one line of units: (request, row tile, K/V head, tile of
 // TILE tokens), the tokens fastest.  An item (all of them but the tokens) takes
@@ -143,12 +141,9 @@ struct Walk {
     it.end = seen_end(p, it.len, hi, EXT ? it.prefix : 0);
     it.begin = first_seen(p, lo);
     if (EXT) {
-      // first positions ascend within a request: the first row's is the least, the last row's the largest
-      const int last = row_first(p, it.first + hi - it.shift);
+      // first positions ascend within a request: the first row's is the least
       it.begin = min(max(it.begin, row_first(p, it.first + lo - it.shift)), it.end);
-      const int span = it.end - last;
       it.sure = p.first_pos ? min(seen_end(p, it.len, lo, it.prefix), it.end) : it.end;
-      it.fine = (p.window > 0 ? min(p.window, span) : span) <= kFineTokens;
     }
     it.t0 = it.begin / TILE;
     it.tiles = it.end > it.begin ? (it.end - 1) / TILE + 1 - it.t0 : 1;
@@ -371,32 +366,26 @@ using StreamWalk = StreamWalkOf<false>;
 // second one takes the K half of a second decoded buffer.
 // (7 prompts up to 3001 tokens, 12 heads of 64: 142 us so, 136 with one product everywhere, 180 with two.
 // The long chunk, none of whose rows sees that few: 935 us so, 1856 with two products.)
+constexpr int kFineTokens = 1024;
 DQ_HD bool is_fine(const AttnParams& p, const Item& it) {
   return (p.window > 0 ? min(p.window, it.end) : it.end) <= kFineTokens;
 }
 
-// With first positions it is the last row's tokens that count (a document that begins among the rows has
-// rows that see few).
-template <bool EXT>
-DQ_HD bool is_fine_of(const AttnParams& p, const Item& it) {
-  return EXT ? it.fine != 0 : is_fine(p, it);
-}
-
-// Two sums for a score, and half the decoded buffers: such a tile takes about twice as long.
+// Two sums for a score, and half the decoded buffers: such a tile takes about twice as long.  (EXT: all tiles are such.)
 template <bool EXT>
 struct TcWeightOf {
-  DQ_HD static int of(const AttnParams& p, const Item& it) { return is_fine_of<EXT>(p, it) ? 2 : 1; }
+  DQ_HD static int of(const AttnParams& p, const Item& it) { return !EXT && is_fine(p, it) ? 2 : 1; }
 };
 
 // Many rows: row tiles of 128 rows, two a CTA (one for head_dim 256), and tiles of 64 tokens; starting and
-// ending an item takes as long as four of them, or ten where scores are masked, capped or biased (7 prompts of
-// documents up to 3001 tokens, 12 heads of 64: 115 us with four, 108 with ten; 32 heads of 128 on 8: 347 and 290, with
-// a bias and no masks 546 and 425; one of 9000 tokens 108 and 111).
+// ending an item takes as long as four of them, or eight where scores are masked, capped or biased (7 prompts of
+// documents up to 3001 tokens, 12 heads of 64: 93 us with four, 90 with six, 87 with eight; 32 heads of 128 on 8: 275,
+// 246, 238, with a bias and no masks 576, 508, 458, capped at 50 336, 320, 329).
 constexpr int kTcTile = 64;
 template <int D>
 constexpr int kTcRowTiles = D == 256 ? 1 : 2;
 template <int D, bool EXT = false>
-using TcWalk = Walk<128 * kTcRowTiles<D>, kTcTile, EXT ? 10 : 4, TcWeightOf<EXT>, EXT>;
+using TcWalk = Walk<128 * kTcRowTiles<D>, kTcTile, EXT ? 8 : 4, TcWeightOf<EXT>, EXT>;
 // a line of U units is cut into this many shares, of two units at least: none inside an item is without a tile
 DQ_HD int tc_shares(int ctas, int64_t U) { return (int)min((int64_t)ctas, U / 2); }
 

@@ -40,8 +40,8 @@
 // Modes other than kPlain: prefixes and first positions, capped scores, a distance bias (dq_kv_scores), an instance each:
 // the softmax's loop misses the instruction cache where it holds more than it needs (7 prompts of documents with
 // prefixes up to 3001 tokens, 12 heads of 64, docs_prompts below: 137 us with masks alone, 159 in an instance that can
-// cap as well; 107 since masks are bits).  cap_chunk below: the chunks of above with scores capped at 30, 1372 us;
-// with a bias 1052.  A cap takes an ex2 and half an inverse a score beside the softmax's own ex2: its pipe is
+// cap as well; 87 since masks are bits and K and V are released apart).  cap_chunk below: the chunks of above with scores
+// capped at 30, 1435 us; with a bias 1188.  A cap takes an ex2 and half an inverse a score beside the softmax's own ex2: its pipe is
 // busy in 0.35 of the cycles, issue in 0.46, the tensor pipe in 0.23, and two softmax warps to a scheduler do not hide the
 // chain from a score to its weight.
 #pragma once
@@ -71,7 +71,7 @@ template <int D, int MODE = kPlain>
 struct TcCfg {
   static constexpr int NQ = kTcRowTiles<D>;          // 128-row tiles
   static constexpr int TT = kTcTile;                 // tokens per tile
-  static constexpr int KVS = D == 256 ? 2 : 4;   // decoded tiles
+  static constexpr int KVS = D == 256 ? 2 : 4;   // decoded tiles of K and of V
   static constexpr int ROWS = 128 * NQ;
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int KV_BUF = TT * D * 2;
@@ -94,7 +94,7 @@ struct TcCfg {
   static constexpr int COL_S = NQ * D;
   static_assert(COL_S + NQ * 2 * TT <= 512, "tensor memory");
   static_assert(TT == 2 * kPiece && RS >= 3, "a tile is two pieces");
-  static_assert((2 * RS + 2 * KVS + 16) * 8 + 4 <= OFF_SHARE && (NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE &&
+  static_assert((2 * RS + 3 * KVS + 16) * 8 + 4 <= OFF_SHARE && (NTH + 1 + NTH / 32) * 8 <= OFF_Q - OFF_PRE &&
                     SMEM <= 232448, "shared memory");
 };
 
@@ -268,6 +268,11 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
   constexpr bool BITS = MODE != kPlain && MODE != kBias;
   // A bias falls with the distance: from the last tile to the first one, M hardly has to follow.
   constexpr bool BACK = BIAS;
+  // Where scores are masked, capped or biased they are exact, from two K's a tile, whatever a row sees: a few tokens may
+  // carry its sum (lse 1e-5 to 4e-5 off with K rounded, 1e-7 so).  K and V are then released apart, K once its scores are
+  // there: two tiles' K's and four tiles' V's are in turn (cap_chunk 2263 -> 1452 us with exact scores, 1372 with rounded
+  // ones; docs_prompts 107 -> 92.  Without masks, where few tiles need it, the chunk takes 903 us so, 878 as it is.)
+  constexpr bool SPLIT = EXT;
   constexpr bool VALUES = MODE == kCaps || MODE == kBias;     // scores are changed as they are read
   using Wk = TcWalk<D, EXT>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
@@ -280,8 +285,9 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
   uint64_t* raw_full = (uint64_t*)smem;
   uint64_t* raw_empty = raw_full + C::RS;
   uint64_t* kv_full = raw_empty + C::RS;
-  uint64_t* kv_empty = kv_full + C::KVS;
-  uint64_t* s_full = kv_empty + C::KVS;    // [row tile][tile parity], as the next two
+  uint64_t* k_empty = kv_full + C::KVS;
+  uint64_t* v_empty = k_empty + C::KVS;
+  uint64_t* s_full = v_empty + C::KVS;     // [row tile][tile parity], as the next two
   uint64_t* p_full = s_full + 4;
   uint64_t* pv_done = p_full + 4;
   uint64_t* q_full = pv_done + 4;
@@ -310,7 +316,8 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
     }
     for (int i = 0; i < C::KVS; ++i) {
       mbar_init(&kv_full[i], 32 * C::DW);
-      mbar_init(&kv_empty[i], NQ);
+      mbar_init(&k_empty[i], NQ);
+      mbar_init(&v_empty[i], NQ);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
@@ -778,19 +785,23 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
     const uint32_t k_sel[2] = {odd ? 0x3232u : 0x1010u, odd ? 0x1010u : 0x3232u};
     const uint32_t v_at[2] = {sw128_offset(vrow, r4), sw128_offset(vrow + 1, r4)};
     const uint32_t raw0 = smem_u32(smem + C::OFF_RAW) + blk * B::BYTES;
-    int gt = 0, st = pc0, st_phase = 0;    // every other stage is this warp's, or all are
+    int gt = 0;                            // decoded V's so far
+    int st = pc0, st_phase = 0;            // every other stage is this warp's, or all are
     for (bool more = Wk::here(p, it, iu, share[0], share[1], ta, tb); more && ok;
          more = Wk::after(p, it, iu, share[0], share[1], ta, tb)) {
-      const bool fine = is_fine_of<EXT>(p, it);
+      const bool fine = EXT || is_fine(p, it);
       for (int j = ta; j < tb && ok; ++j) {
         const int tok0 = (it.t0 + (BACK ? ta + tb - 1 - j : j)) * TT;
         const bool inner = tok0 >= it.begin && tok0 <= (EXT ? it.sure : it.end) - TT;
-        const int buf = gt % C::KVS, buf2 = (gt + 1) % C::KVS;
-        if (gt >= C::KVS) ok = mbar_wait(&kv_empty[buf], (gt / C::KVS - 1) & 1);
-        if (fine && ok && gt + 1 >= C::KVS) ok = mbar_wait(&kv_empty[buf2], ((gt + 1) / C::KVS - 1) & 1);
+        const int kr = SPLIT ? 2 * gt : gt;
+        const int buf = gt % C::KVS, kb1 = kr % C::KVS, k2 = (kr + 1) % C::KVS;
+        if (gt >= C::KVS) ok = mbar_wait(&v_empty[buf], (gt / C::KVS - 1) & 1);
+        uint64_t* const k_free = SPLIT ? k_empty : v_empty;
+        if (SPLIT && ok && kr >= C::KVS) ok = mbar_wait(&k_free[kb1], (kr / C::KVS - 1) & 1);
+        if (fine && ok && kr + 1 >= C::KVS) ok = mbar_wait(&k_free[k2], ((kr + 1) / C::KVS - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t kb = ks + buf * C::KV_BUF, kb2 = ks + buf2 * C::KV_BUF, vb = vs + buf * C::KV_BUF;
+        const uint32_t kb = ks + kb1 * C::KV_BUF, kb2 = ks + k2 * C::KV_BUF, vb = vs + buf * C::KV_BUF;
 #pragma unroll 1
         for (int pc = pc0; pc < pc0 + PIECES; ++pc) {
         ok = mbar_wait(&raw_full[st], st_phase);
@@ -858,7 +869,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
             }
           }
         };
-        if (fine) decode(std::true_type());
+        if (EXT || fine) decode(std::true_type());
         else decode(std::false_type());
         __syncwarp();
         if (lane == 0) mbar_arrive(&raw_empty[st]);
@@ -871,8 +882,8 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
         if (!ok) break;
         fence_proxy_async_smem();
         mbar_arrive(&kv_full[buf]);
-        if (fine) mbar_arrive(&kv_full[buf2]);
-        gt += fine ? 2 : 1;
+        if (!SPLIT && fine) mbar_arrive(&kv_full[k2]);
+        gt += !SPLIT && fine ? 2 : 1;
       }
     }
   } else {
@@ -939,31 +950,36 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
       const int i = warp - C::MMA;
       const uint32_t q_i = q_lo + (uint32_t)(i * (C::Q_TILE >> 4)), o_i = tm + (uint32_t)(i * D);
       const uint32_t s_i = tm + (uint32_t)(C::COL_S + i * 2 * TT);
-      int gt = 0, ring = 0, seg = 0;         // tiles of this row tile, of the CTA; items
-      // S of this row tile's tile g, which is the CTA's tile r; its buffer's last weights must have been used
-      auto scores = [&](int g, int r, auto fine_c) {
+      int gt = 0, ring = 0, seg = 0;         // tiles of this row tile, decoded V's of the CTA; items
+      // S of this row tile's tile g, whose V is the decoded one r and its K the one kr (and the next); its buffer's last
+      // weights must have been used
+      auto scores = [&](int g, int r, int kr, auto fine_c) {
         constexpr bool FINE = decltype(fine_c)::value;
-        const int par = g & 1, buf = r % C::KVS, buf2 = (r + 1) % C::KVS;
+        const int par = g & 1, k1 = kr % C::KVS, k2 = (kr + 1) % C::KVS;
         bool good = g < 2 || mbar_wait(&pv_done[i * 2 + par], ((g - 2) >> 1) & 1);
-        good = good && mbar_wait(&kv_full[buf], (r / C::KVS) & 1);
-        if (FINE) good = good && mbar_wait(&kv_full[buf2], ((r + 1) / C::KVS) & 1);
+        good = good && mbar_wait(&kv_full[r % C::KVS], (r / C::KVS) & 1);
+        if (!SPLIT && FINE) good = good && mbar_wait(&kv_full[k2], ((kr + 1) / C::KVS) & 1);
         if (!__all_sync(0xffffffffu, good)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t b = k_lo + (uint32_t)(buf * (C::KV_BUF >> 4));
+          const uint32_t b = k_lo + (uint32_t)(k1 * (C::KV_BUF >> 4));
           const uint32_t d = s_i + (uint32_t)(par * TT);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             mma_ss(d, q_i + (k >> 2) * (16384 >> 4) + 2 * (k & 3), b + (k >> 2) * (TT * 128 >> 4) + 2 * (k & 3),
                    hi, id_s, k ? 1u : 0u);
           if (FINE) {
-            const uint32_t b2 = k_lo + (uint32_t)(buf2 * (C::KV_BUF >> 4));
+            const uint32_t b2 = k_lo + (uint32_t)(k2 * (C::KV_BUF >> 4));
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
               mma_ss(d, q_i + (k >> 2) * (16384 >> 4) + 2 * (k & 3), b2 + (k >> 2) * (TT * 128 >> 4) + 2 * (k & 3),
                      hi, id_s, 1u);
           }
           tc_commit(&s_full[i * 2 + par]);
+          if (SPLIT) {
+            tc_commit(&k_empty[k1]);
+            tc_commit(&k_empty[k2]);
+          }
         }
         __syncwarp();
         return true;
@@ -980,17 +996,23 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
           for (int k = 0; k < TT / 16; ++k)
             mma_ts(o_i, a + 8 * k, b + k * (2048 >> 4), hi, id_o, (first && k == 0) ? 0u : 1u);
           tc_commit(&pv_done[i * 2 + par]);
-          tc_commit(&kv_empty[buf]);
-          if (FINE) tc_commit(&kv_empty[(r + 1) % C::KVS]);
+          tc_commit(&v_empty[buf]);
+          if (!SPLIT && FINE) tc_commit(&v_empty[(r + 1) % C::KVS]);
         }
         __syncwarp();
         return true;
       };
-      // a tile that this row tile has no part in
+      // a decoded V that this row tile has no part in, and its K's
       auto pass = [&](int r) {
         const int buf = r % C::KVS;
         if (!__all_sync(0xffffffffu, mbar_wait(&kv_full[buf], (r / C::KVS) & 1))) return false;
-        if (lane == 0) mbar_arrive(&kv_empty[buf]);
+        if (lane == 0) {
+          mbar_arrive(&v_empty[buf]);
+          if (SPLIT) {
+            mbar_arrive(&k_empty[2 * r % C::KVS]);
+            mbar_arrive(&k_empty[(2 * r + 1) % C::KVS]);
+          }
+        }
         return true;
       };
       for (bool more = Wk::here(p, it, iu, share[0], share[1], ta, tb); more && ok;
@@ -998,29 +1020,33 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
         int ra, rb;
         row_tile_range<EXT>(p, it, i, ta, tb, ra, rb);
         auto item = [&](auto fine_c) {
-          constexpr int STEP = decltype(fine_c)::value ? 2 : 1;     // decoded buffers a tile takes
+          constexpr int KSTEP = decltype(fine_c)::value ? 2 : 1;    // decoded K's a tile takes
+          constexpr int STEP = SPLIT ? 1 : KSTEP;                   // decoded V's
           // scores run two tiles ahead of the weights, or one where two tiles' buffers are not there
           constexpr int AHEAD = C::KVS >= 2 * STEP ? 2 : 1;
           const int before = uniform(BACK ? tb - rb : ra - ta) * STEP, nt = uniform(rb - ra),
                     behind = uniform(BACK ? ra - ta : tb - rb) * STEP;
+          // (every tile of an instance that splits them takes two K's)
+          auto k_of = [&](int r) { return SPLIT ? 2 * r : r; };
           for (int k = 0; k < before && ok; ++k) ok = pass(ring++);
           if (nt > 0 && ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(&q_full[i], seg & 1));
             ++seg;
-            ok = ok && scores(gt, ring, fine_c);
-            if (nt > 1 && AHEAD == 2) ok = ok && scores(gt + 1, ring + STEP, fine_c);
+            ok = ok && scores(gt, ring, k_of(ring), fine_c);
+            if (nt > 1 && AHEAD == 2) ok = ok && scores(gt + 1, ring + STEP, k_of(ring + STEP), fine_c);
             for (int k = 0; k < nt && ok; ++k, ++gt, ring += STEP) {
               ok = weighted(gt, ring, k == 0, fine_c);
-              if (k + AHEAD < nt) ok = ok && scores(gt + AHEAD, ring + AHEAD * STEP, fine_c);
+              if (k + AHEAD < nt)
+                ok = ok && scores(gt + AHEAD, ring + AHEAD * STEP, k_of(ring + AHEAD * STEP), fine_c);
             }
           }
           for (int k = 0; k < behind && ok; ++k) ok = pass(ring++);
         };
-        if (is_fine_of<EXT>(p, it)) item(std::true_type());
+        if (EXT || is_fine(p, it)) item(std::true_type());
         else item(std::false_type());
       }
       // no arrival and no product is under way when the CTA ends, whichever wait ran out
-      if (ok && ring > 0) mbar_wait(&kv_empty[(ring - 1) % C::KVS], ((ring - 1) / C::KVS) & 1);
+      if (ok && ring > 0) mbar_wait(&v_empty[(ring - 1) % C::KVS], ((ring - 1) / C::KVS) & 1);
       if (elect_one()) tc_commit(&drained[i]);
       __syncwarp();
       mbar_drain(&drained[i], 0);

@@ -272,7 +272,7 @@ def kv_attention(cache, q, q_start, kv_len, block_table, scale=None, causal=True
     Sums are fp32, operands fp16: weights are rounded to it, and where a request has
     many rows V and K as decoded too.  Whatever out_dtype is, out carries 1.5e-4 to
     4e-4 of its size from that; lse 1e-7, or up to 6e-6 for many rows that see more
-    than 1024 tokens.
+    than 1024 tokens, or up to 1e-6 where scores are capped, biased or masked.
     """
     T, H, D = q.shape
     qs, qh, qd = q.stride()

@@ -594,7 +594,8 @@ int dq_kv_append(const dq_kv_cache* cache, const void* k, int64_t k_stride, cons
  *   a' = factor * (a cos - b sin),  b' = factor * (b cos + a sin),  angle = position * inv_freq[i];
  * the others stay.  q' is rounded once to out_dtype (rotations are fp32: off by 5e-7 of |a| + |b|; angles are
  * exact to 2e-7 at positions below 2^24, to 1e-6 above).  k' is not rounded before it becomes blocks: codes and
- * scales are those of k' in 64 bits, with dq_kv_append's formula in exact arithmetic.  v is written as dq_kv_append
+ * scales are those of k' in 64 bits, with dq_kv_append's formula in exact arithmetic and the scale that of the
+ * largest value rounded to fp32.  v is written as dq_kv_append
  * writes it.  Infinite and NaN values are out of contract.
  * A row with a position below 0 (dq_kv_plan's rows behind the last token) is left out: neither its q row nor
  * the cache is written.  A row whose slot lies outside the cache has its q row alone. */
@@ -691,7 +692,8 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* args, void* ws, 
  * So a prefix is read both ways (its rows see all of it), and rows of a request that holds several documents
  * see their own one.  Rows that see nothing, garbage in unseen places, types, limits, the workspace: as
  * dq_kv_attention.  Capped scores are off by 2.5e-7 of themselves, or, up to
- * 100 and where a request has more rows per K/V head than stream, by 4e-7 of the cap; a bias is fp32 of fp32 slopes. */
+ * 100 and where a request has more rows per K/V head than stream, by 4e-7 of the cap; a bias is fp32 of fp32 slopes.
+ * q . k_j is exact to fp32 sums whatever the number of rows: a few tokens may carry a row. */
 typedef struct {
   float softcap;              /* 0: none; else 0.01 to 1e6 */
   const float* slopes;        /* device fp32 [n_q_heads], finite, or NULL */

@@ -151,7 +151,7 @@ void check(const Call& c, const AttnParams& p, int tile, int shares_of, F part) 
     size_t i = i0;
     for (bool more = Wk::here(p, x, iu, u0, u1, a, b); more; more = Wk::after(p, x, iu, u0, u1, a, b)) {
       while (at[i] < iu) ++i;
-      CHECK(at[i] == iu && items[i].r == x.r && items[i].h == x.h && items[i].row0 == x.row0 && items[i].fine == x.fine &&
+      CHECK(at[i] == iu && items[i].r == x.r && items[i].h == x.h && items[i].row0 == x.row0 && items[i].sure == x.sure &&
                 items[i].prefix == x.prefix && items[i].tiles == x.tiles, "share %d: item %zu", w, i);
       CHECK(a == done[i] && a < b && b <= x.tiles, "share %d, item %zu: [%d, %d) after %d", w, i, a, b, done[i]);
       done[i] = b;
@@ -179,11 +179,6 @@ void many(const Call& c) {
       const int64_t a = std::max<int64_t>(lo / kTcTile - it.t0, ta), b = std::min<int64_t>((hi - 1) / kTcTile + 1 - it.t0, tb);
       CHECK(a >= b || (ra <= a && b <= rb), "row tile %d takes [%d, %d), needs [%lld, %lld)", i, ra, rb, (long long)a,
             (long long)b);
-      // a row that sees few tokens has exact scores
-      int64_t l, h;
-      seen(c, it.r, (it.row0 + last) / c.group, &l, &h);
-      if (l < h && h - l <= kFineTokens && it.row0 + last == it.row0 + it.rows - 1)
-        CHECK(it.fine, "row %d sees %lld", it.row0 + last, (long long)(h - l));
     }
   });
 }
