@@ -436,8 +436,8 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 }
 
 // Capped scores in units of log 2 from u = score / cap.  tanh(u) / u is a polynomial in u^2 of degree 6 where
-// |u| <= 1 (its Chebyshev interpolation: 2.5e-7 of itself, fp32's roundings included); beyond, tanh(|u|) = 1 - 2 / (1 + e^2|u|), whose
-// terms do not cancel there.
+// |u| <= 1 (its Chebyshev interpolation: 2.5e-7 of itself, fp32's roundings included); beyond,
+// tanh(|u|) = 1 - 2 / (1 + e^2|u|), whose terms do not cancel there.
 //
 // Eight scores at a time: chains of packed steps keep the pipe busy, and a coefficient is fetched once.
 template <int N>

@@ -18,7 +18,7 @@
 //   16-bit operands; S, M, the sum of p and O are fp32.  (Against 64 bits, norm over norm: fp32 outputs
 //   2.8e-4 for 7 prompts of heads of 64, 4.0e-4 for the long chunk below, of which fp16 and bf16 outputs
 //   round off 2.1e-4 and 1.7e-3; lse 6.0e-6 and 2.6e-6.  The streaming kernel, which takes K exactly:
-//   1.6e-4 to 2.1e-4, lse 1.2e-7.)
+//   1.6e-4 to 2.1e-4, lse 1.2e-7.  K exactly here, where scores are masked, capped or biased: lse 2e-7 to 8e-7.)
 //
 // Roles.  Warp groups of the row tiles do the softmax (a thread per row); eight
 // warps decode; one warp copies the pages' blocks (bulk copies, 32 tokens at a
@@ -38,12 +38,12 @@
 // the time, the exponentials none, three quarters of the products 6 %.  Four warps decoding and 64
 // scores a thread at a time took 966 us, two warps to a row 1088 (registers).
 // Modes other than kPlain: prefixes and first positions, capped scores, a distance bias (dq_kv_scores), an instance each:
-// the softmax's loop misses the instruction cache where it holds more than it needs (7 prompts of documents with
-// prefixes up to 3001 tokens, 12 heads of 64, docs_prompts below: 137 us with masks alone, 159 in an instance that can
-// cap as well; 87 since masks are bits and K and V are released apart).  cap_chunk below: the chunks of above with scores
-// capped at 30, 1435 us; with a bias 1188.  A cap takes an ex2 and half an inverse a score beside the softmax's own ex2: its pipe is
-// busy in 0.35 of the cycles, issue in 0.46, the tensor pipe in 0.23, and two softmax warps to a scheduler do not hide the
-// chain from a score to its weight.
+// the softmax's loop misses the instruction cache where it holds more than it needs.  Two cases stand for them in what
+// follows: docs_prompts, 7 prompts of documents with prefixes up to 3001 tokens, 12 heads of 64 (159 us in an instance
+// that can cap as well, 137 with masks alone, 87 since masks are bits and K and V are released apart), and cap_chunk,
+// the chunks of above with scores capped at 30 (1435 us; with a bias instead 1188).  A cap takes an ex2 and half an
+// inverse a score beside the softmax's own ex2: their pipe is busy in 0.36 of the cycles, issue in 0.49, the tensor pipe
+// in 0.36, and two softmax warps to a scheduler do not hide the chain from a score to its weight.
 #pragma once
 
 #include <algorithm>
@@ -86,7 +86,7 @@ struct TcCfg {
   static constexpr int SMEM = OFF_RAW + RS * PIECE_B;
   static constexpr int DEC0 = 4 * NQ;                // first decoding warp
   // decoding warps: capped scores keep the softmax so long that four are enough, and the registers of the others
-  // let its threads hold 64 scores (cap_chunk below 1625 -> 1571 us; a bias 1046 -> 1090)
+  // let its threads hold 64 scores (cap_chunk 1432 us, 1680 with eight; a bias 1235, 1190 with eight)
   static constexpr int DW = MODE == kCaps ? 4 : 8;
   static constexpr int PROD = DEC0 + DW, MMA = PROD + 1;  // one warp of products per row tile
   static constexpr int NTH = 32 * (MMA + NQ);
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
   using C = TcCfg<D, MODE>;
   using B = KvBlk<D>;
   constexpr bool EXT = MODE != kPlain, ANY = MODE == kAnyScores, BIAS = MODE == kBias || ANY;
-  // Masks as bits (docs_prompts below 130 -> 115 us, cap_chunk 1400 -> 1378; without masks and
+  // Masks as bits (docs_prompts 130 -> 115 us, cap_chunk 1400 -> 1378; without masks and
   // with a bias comparisons by the row tile's take less: 880 and 1052 us for the chunk so, 908 and 1086 with bits)
   constexpr bool BITS = MODE != kPlain && MODE != kBias;
   // A bias falls with the distance: from the last tile to the first one, M hardly has to follow.
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
         const uint32_t s_addr = tmem + lane_base + (uint32_t)(C::COL_S + sl * TT);
         const bool inner = tok0 >= lo_all && tok0 <= hi_all - TT;
         // Any cap, any bias: the scores, in units of log 2, capped and biased, take their own place in a pass in front of
-        // the softmax's.  (1050 -> 1870 us for cap_chunk below, in its warps or in others: tensor memory's
+        // the softmax's.  (1050 -> 1870 us for cap_chunk, in its warps or in others: tensor memory's
         // bandwidth.  The polynomial in the softmax's passes misses the instruction cache: 3970.)
         if (ANY) {
           // a bias is linear in the position on either side of the row's own

@@ -481,7 +481,8 @@ int launch_rope(RopeParams p, int dtype, cudaStream_t s) {
   // 16.6, 16.4, 25.4 with one, two, eight, 1023 with 15 heads of 64 and 5 6.2, 7.4, 7.5)
   p.q_each = HL * (dtype == DQ_F32 ? 1 : p.T >= kLongCall ? 8 : 2);
   p.q_splits = (p.q_heads + p.q_each - 1) / p.q_each;
-  const int64_t ctas = 2 * (((int64_t)p.T + p.tile - 1) / p.tile) + ((int64_t)p.T * p.q_splits + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  const int64_t ctas = 2 * (((int64_t)p.T + p.tile - 1) / p.tile) +
+                       ((int64_t)p.T * p.q_splits + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 2147483647 || (int64_t)p.T * p.q_splits > 2147483647) return DQ_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)ctas), block(kRopeThreads);
 #define DQ_KV_ROPE(DT) \

@@ -1424,8 +1424,8 @@ int launch_moe_forward(const dq_moe_desc& d, const void* x, int xdt, int T, floa
     rp.idx = idx;
     rp.gate = gate;
   }
-  launch_pdl(routing && fuse_topk ? permute_kernel<true> : permute_kernel<false>, dim3(1), dim3(1024), 0, s, 0, idx, T, d.top_k, d.E, d.n_shared,
-             pl.GW, offsets, sorted, inv, tok, groups, ngroups, pl.wide ? units : nullptr, nunits,
+  launch_pdl(routing && fuse_topk ? permute_kernel<true> : permute_kernel<false>, dim3(1), dim3(1024), 0, s, 0,
+             idx, T, d.top_k, d.E, d.n_shared, pl.GW, offsets, sorted, inv, tok, groups, ngroups, pl.wide ? units : nullptr, nunits,
              fuse_x16 ? x : nullptr, xdt, d.hidden, fuse_x16 ? x16t : nullptr,
              fuse_x16 ? xinvt : nullptr,
              fuse_topk ? TopkIn{part, pl.KS, lg, gate} : TopkIn{nullptr, 0, nullptr, nullptr},
