@@ -1047,6 +1047,8 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
       }
       // no arrival and no product is under way when the CTA ends, whichever wait ran out
       if (ok && ring > 0) mbar_wait(&v_empty[(ring - 1) % C::KVS], ((ring - 1) / C::KVS) & 1);
+      if (SPLIT && ok)
+        for (int k = max(2 * ring - 2, 0); k < 2 * ring; ++k) mbar_wait(&k_empty[k % C::KVS], (k / C::KVS) & 1);
       if (elect_one()) tc_commit(&drained[i]);
       __syncwarp();
       mbar_drain(&drained[i], 0);
