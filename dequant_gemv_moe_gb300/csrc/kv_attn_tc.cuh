@@ -86,8 +86,10 @@ struct TcCfg {
   static constexpr int SMEM = OFF_RAW + RS * PIECE_B;
   static constexpr int DEC0 = 4 * NQ;                // first decoding warp
   // decoding warps: capped scores keep the softmax so long that four are enough, and the registers of the others
-  // let its threads hold 64 scores (cap_chunk 1432 us, 1680 with eight; a bias 1235, 1190 with eight)
-  static constexpr int DW = MODE == kCaps ? 4 : 8;
+  // let its threads hold 64 scores, but not with one row tile to twice the values a token (chunks of 2048 over 16384 with four
+  // and eight: capped, 32 heads of 128 1432 and 1680 us, of 64 1330 and 1541, 16 of 256 2625 and 2380; capped and biased
+  // 2106 and 2195, 2040 and 2105, 2755 and 2466; biased 1213 and 1178, 972 and 974, 2609 and 2361)
+  static constexpr int DW = (MODE == kCaps || MODE == kAnyScores) && D != 256 ? 4 : 8;
   static constexpr int PROD = DEC0 + DW, MMA = PROD + 1;  // one warp of products per row tile
   static constexpr int NTH = 32 * (MMA + NQ);
   // tensor memory columns: O of every row tile, then two score buffers of each
