@@ -449,7 +449,9 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
         // The two largest values of the groups at the border, and what may be one of them, a lane each: the
         // groups are ranked by their sums.
         const bool near = sc >= best_out - tol && sc <= worst_in + tol;
-        const float least = (p.top2 && g2 > -INFINITY ? g2 : g1) - (0.5f * tol + 1e-6f * fabsf(g2 > -INFINITY ? g2 : g1));
+        const float low = p.top2 && g2 > -INFINITY ? g2 : g1;
+        // (finite: an expert that is out is below a bias of fp32's lowest value)
+        const float least = fmaxf(low - (0.5f * tol + 1e-6f * fabsf(g2 > -INFINITY ? g2 : g1)), -kMostLogit);
         uint32_t may = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) may |= j < n && near && v[j] >= least ? 1u << j : 0u;
@@ -534,7 +536,8 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
     // The experts that may be among the picks, a lane each, where they are so few that they find room and a value
     // can be had of a logit alone: they are ranked.
     const float last = __shfl_sync(0xffffffffu, mine_v, p.k - 1);
-    const float least = last - fmaxf(tolerance(last), 0.f);
+    // (finite, as above)
+    const float least = fmaxf(last - fmaxf(tolerance(last), 0.f), -kMostLogit);
     uint32_t may = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) may |= j < n && in && (by_logit ? l[j] : v[j]) >= least ? 1u << j : 0u;
