@@ -414,7 +414,7 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
 
   // ---- groups.  A sigmoid is known to 3e-7 (ex2's and the product's error enter times s (1 - s) |l|, at most
   // 0.28 |l| 2^-23), a softmax to 1.2e-6 (of which most is the common sum's), each plus the rounding of the
-  // bias' sum.
+  // bias' sum; a group's score adds the roundings of both values, which may be far larger than their sum, and its own.
   bool doubtful = false, in = true;
   if (p.top_groups < p.groups) {
     float g1 = v[0], g2 = -INFINITY;
@@ -429,7 +429,8 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
       g2 = fmaxf(fminf(g1, a1), fmaxf(g2, a2));
       g1 = fmaxf(g1, a1);
     }
-    const float sc = p.top2 && g2 > -INFINITY ? g1 + g2 : g1;
+    const bool two = p.top2 && g2 > -INFINITY;
+    const float sc = two ? g1 + g2 : g1;
     // the groups that beat this lane's: its lanes take one other group each
     const int g = lane >> p.lane_shift;
     int better = 0;
@@ -441,17 +442,20 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
     }
     in = better < p.top_groups;
     if (!by_logit || group_sums) {
-      const uint32_t key = route_key(sc);
-      const float worst_in = route_value(__reduce_min_sync(0xffffffffu, in ? key : 0xffffffffu));
-      const float best_out = route_value(__reduce_max_sync(0xffffffffu, in ? 0u : key));
-      const float tol = (p.sigmoid ? 1.6e-6f : 5e-6f) + 6e-7f * (fabsf(worst_in) + fabsf(best_out));
-      if (worst_in > -INFINITY && best_out > -INFINITY && worst_in - best_out <= tol) {
+      // Half of what two scores apart by less may be mistaken for.  (A group without experts is known: its score is
+      // -inf.  A sum beyond fp32's range is not: then a bound below is NaN, and the comparisons say so.)
+      const float err = g1 > -INFINITY
+                            ? (p.sigmoid ? 8e-7f : 2.5e-6f) + 3e-7f * (fabsf(g1) + (two ? fabsf(g2) : 0.f))
+                            : 0.f;
+      const float worst_in = route_value(__reduce_min_sync(0xffffffffu, in ? route_key(sc - err) : 0xffffffffu));
+      const float best_out = route_value(__reduce_max_sync(0xffffffffu, in ? 0u : route_key(sc + err)));
+      if (best_out != -INFINITY && !(worst_in > best_out)) {
         // The two largest values of the groups at the border, and what may be one of them, a lane each: the
         // groups are ranked by their sums.
-        const bool near = sc >= best_out - tol && sc <= worst_in + tol;
-        const float low = p.top2 && g2 > -INFINITY ? g2 : g1;
+        const bool near = in ? !(sc - err > best_out) : !(sc + err < worst_in);
         // (finite: an expert that is out is below a bias of fp32's lowest value)
-        const float least = fmaxf(low - (0.5f * tol + 1e-6f * fabsf(g2 > -INFINITY ? g2 : g1)), -kMostLogit);
+        const float low = two ? g2 : g1;
+        const float least = fmaxf(low - (8e-7f + 1e-6f * fabsf(low)), -kMostLogit);
         uint32_t may = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) may |= j < n && near && v[j] >= least ? 1u << j : 0u;

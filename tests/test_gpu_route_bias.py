@@ -1,9 +1,10 @@
-"""dq_moe_route with biases of any size and sign: picks and groups are those of 64 bits (tests/route_ref.py)."""
+"""dq_moe_route with biases of any size and sign: picks and groups are those of 64 bits (tests/route_ref.py), where the
+biases of a group's two best cancel too."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_route import check, dq  # noqa: F401  (dq is the fixture)
+from test_gpu_route import check, dq, normal  # noqa: F401  (dq is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,36 @@ def test_biases_of_the_lowest_and_the_largest_value(dq, E, groups, top, k, score
     l, biases = far_biases(E, groups)
     for b in biases:
         check(dq, l, k, scores=scores, bias=b, n_groups=groups, top_groups=top, group_score="max")
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(16, 8, 5, 8), (24, 8, 3, 4), (64, 32, 20, 8), (256, 8, 4, 8), (256, 32, 16, 8)])
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_sums_that_fp32_has_not(dq, E, groups, top, k, scores):  # noqa: F811
+    l, biases = far_biases(E, groups)
+    for b in biases:
+        check(dq, l, k, scores=scores, bias=b, n_groups=groups, top_groups=top, group_score="top2")
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(64, 32, 8, 8), (96, 32, 9, 6), (128, 32, 8, 8), (256, 32, 8, 8)])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e5, 1e6])
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_two_best_that_cancel(dq, E, groups, top, k, size, scores):  # noqa: F811
+    # a group's score is s + s' while its values are s + size and s' - size, which fp32 rounds to size * 2^-24
+    T, per = 3000, E // groups
+    b = np.where(np.arange(E) % per == 0, size, -size)
+    b[np.arange(E) % per > 1] = -2 * size
+    check(dq, normal(T, E, seed=E + int(np.log10(size))), k, scores=scores, bias=b, n_groups=groups, top_groups=top,
+          group_score="top2")
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(64, 16, 5, 8), (256, 32, 8, 8)])
+def test_groups_of_other_sizes_than_the_border(dq, E, groups, top, k):  # noqa: F811
+    # biases of every size: what decides is small beside what most groups are
+    rng = np.random.default_rng(E)
+    b = rng.choice([-1.0, 1.0], E) * 10.0 ** rng.uniform(-3, 6, E)
+    per = E // groups
+    for g in range(groups):
+        b[g * per + 1] = -b[g * per] * (1 + 1e-7 * rng.normal())
+        b[g * per + 2:(g + 1) * per] = -1e7
+    for scores in ("sigmoid", "softmax"):
+        check(dq, normal(1500, E, seed=7), k, scores=scores, bias=b, n_groups=groups, top_groups=top, group_score="top2")
