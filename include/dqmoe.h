@@ -691,8 +691,9 @@ int dq_kv_attention(const dq_kv_cache* cache, const dq_kv_attn* args, void* ws, 
  *   j >= first_pos[row].
  * So a prefix is read both ways (its rows see all of it), and rows of a request that holds several documents
  * see their own one.  Rows that see nothing, garbage in unseen places, types, limits, the workspace: as
- * dq_kv_attention.  Capped scores are off by 2.5e-7 of themselves, or, up to
- * 100 and where a request has more rows per K/V head than stream, by 4e-7 of the cap; a bias is fp32 of fp32 slopes.
+ * dq_kv_attention.  A cap's own error in a score is 2.5e-7 of the capped score where a request has no more rows per K/V head
+ * than stream (64, or 32 beside requests with more), where the cap is above 100 or where there are slopes, and else at
+ * most 7e-7 of the cap (3.6e-7 measured); the lse carries it.  A bias is fp32 of fp32 slopes.
  * q . k_j is exact to fp32 sums whatever the number of rows: a few tokens may carry a row. */
 typedef struct {
   float softcap;              /* 0: none; else 0.01 to 1e6 */
