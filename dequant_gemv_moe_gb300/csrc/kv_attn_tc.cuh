@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
   // there: two tiles' K's and four tiles' V's are in turn (cap_chunk 2263 -> 1452 us with exact scores, 1372 with rounded
   // ones; docs_prompts 107 -> 92.  Without masks, where few tiles need it, the chunk takes 903 us so, 878 as it is.)
   constexpr bool SPLIT = EXT;
-  constexpr bool VALUES = MODE == kCaps || MODE == kBias;     // scores are changed as they are read
   using Wk = TcWalk<D, EXT>;
   constexpr int G = B::G, W = B::W, GH = G / W, NQ = C::NQ, TT = C::TT;
   constexpr int LPR = D / 8, RPI = 32 / LPR, QB = D == 64 ? 8 : 4;   // rows to and from the warps
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
             for (int i = 0; i < 32; ++i) r[i] = (BITS ? see >> i & 1 : i < n && i >= f) ? r[i] : 0xFF800000u;
           }
         };
-        // 32 scores of this thread's row, those that it does not see as -inf
+        // 32 scores of this thread's row, those that it does not see as -inf (not with a bias: `values`)
         auto load = [&](int c, uint32_t (&r)[32]) {
           tmem_ld32(s_addr + c, r);
           tmem_wait_ld();
@@ -566,7 +565,7 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
             const int n = hi - tok0 - c;
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = i < n ? r[i] : 0xFF800000u;
-            if (EXT || p.window > 0) {
+            if (p.window > 0) {
               const int f = lo - tok0 - c;
 #pragma unroll
               for (int i = 0; i < 32; ++i) r[i] = i >= f ? r[i] : 0xFF800000u;
