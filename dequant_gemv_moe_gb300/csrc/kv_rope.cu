@@ -7,9 +7,10 @@
 //   With inv_freq / 2 pi as two floats the turns are a product and its exact error (FMA) and the low part's;
 //   the whole turns are taken off exactly, and what the last addition rounds off comes back as a first-order
 //   term: cos and sin within 2.3e-7, for positions below 2^24.  Beyond, the turns are formed in 64 bits.
-// * K's codes are those of the rotated row in 64 bits, not of its rounding: a code or a scale next to a
-//   border would otherwise depend on how the rotation was rounded, and an equal pair of largest magnitudes
-//   decides the sign of a scale.  The fp32 rotation knows its error (kErr of |a| + |b|), and where a group has
+// * A group's scale is the fp16 nearest to -1/8 of its largest value's fp32, as of rows that come in fp32: the rotation in
+//   64 bits, rounded to fp32 and then to fp16 (rounded to fp16 at once, one scale in 25000 is its neighbour).  K's codes are
+//   those of the rotated row in 64 bits for that scale.  Neither may depend on how a kernel rounds its rotation next to a
+//   border, and of an equal pair of largest magnitudes the first decides the sign of the scale.  The fp32 rotation knows its error (kErr of |a| + |b|), and where a group has
 //   a value that close to a border, that value is formed again, to 2^-44 (pair.cuh).  (bf16 rows, heads of 128: a
 //   warp's 256 values in about 250.)
 //
@@ -17,7 +18,7 @@
 // TB/s: K and V by themselves 23.4 us, which are instructions (a K value's range, bounds, quotient, clamp and
 // packing; issue in 0.58 of the cycles), q the rest, which waits for its loads (two heads' worth a lane in flight).
 // With an angle per head and thread from shared memory, and K's doubts in 64 bits, it was 96 us.  64 tokens
-// 4.7 us, of which K's doubts, one warp's or two's, are 1.6.
+// 4.1 us (left out for a measurement, K's doubts, one warp's or two's, were 1.6 of 4.7).
 #include "kv_rows.cuh"
 #include "pair.cuh"
 
@@ -545,8 +546,8 @@ extern "C" int dq_kv_append_rope(const dq_kv_cache* cache, const dq_kv_rope* a, 
   p.out = a->q_out;
   p.out_stride = a->out_stride;
   p.out_dtype = a->out_dtype;
-  // about kTileCtas CTAs of K, of two tokens at least (64 tokens: 5.0 us with one, 4.3, 6.7, 8.5 with two, four, eight;
-  // 1023: 11.4, 8.1, 7.6, 9.7; 4096: 40.0, 25.9, 22.6, 21.0)
+  // about kTileCtas CTAs of K, of two tokens at least (64 tokens: 4.1 us with one, 4.1, 4.8, 6.7 with two, four, eight;
+  // 1023: 11.2, 7.8, 7.4, 9.4; 4096: 39.9, 25.8, 22.3, 20.7)
   p.tile = 2;
   while (p.tile < kMostTile && p.tile * kTileCtas < a->T) p.tile *= 2;
   return by_dim(cache->head_dim,

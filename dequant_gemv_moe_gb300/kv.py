@@ -181,7 +181,7 @@ def kv_append_rope(cache, q, k, v, slots, positions, inv_freq, interleaved=False
     rows below 0 are left out; slots int64 [T] as kv_append's.  inv_freq fp32 [rotary_dim / 2]: the first
     rotary_dim values of a head turn, in pairs half of them apart or, interleaved, next to one another;
     factor: of cos and sin.  out: fp32/fp16/bf16 rows (out_dtype, q's unless given); q itself may be given.
-    K's codes are those of the rotated values before any rounding.
+    K's codes are those of the rotated values in 64 bits, its scales those of a group's largest value as fp32.
     """
     shape, D, dev = k.shape, cache.head_dim, cache.dev
     T, dt = shape[0], k.dtype

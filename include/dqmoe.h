@@ -593,10 +593,9 @@ int dq_kv_append(const dq_kv_cache* cache, const void* k, int64_t k_stride, cons
  * (x[2i], x[2i + 1]) if interleaved, become
  *   a' = factor * (a cos - b sin),  b' = factor * (b cos + a sin),  angle = position * inv_freq[i];
  * the others stay.  q' is rounded once to out_dtype (rotations are fp32: off by 5e-7 of |a| + |b|; angles are
- * exact to 2e-7 at positions below 2^24, to 1e-6 above).  k' is not rounded before it becomes blocks: codes and
- * scales are those of k' in 64 bits, with dq_kv_append's formula in exact arithmetic and the scale that of the
- * largest value rounded to fp32.  v is written as dq_kv_append
- * writes it.  Infinite and NaN values are out of contract.
+ * exact to 2e-7 at positions below 2^24, to 1e-6 above).  k' is that of 64 bits, whatever `dtype`: a group's
+ * scale is the fp16 nearest to -1/8 of the fp32 nearest to its largest value (the scale that dq_kv_append gives k' in fp32), and
+ * codes are dq_kv_append's formula in exact arithmetic on k' and that scale.  v is written as dq_kv_append writes it.  Infinite and NaN values are out of contract.
  * A row with a position below 0 (dq_kv_plan's rows behind the last token) is left out: neither its q row nor
  * the cache is written.  A row whose slot lies outside the cache has its q row alone. */
 typedef struct {
