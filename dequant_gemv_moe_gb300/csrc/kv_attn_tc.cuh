@@ -41,7 +41,7 @@
 // the softmax's loop misses the instruction cache where it holds more than it needs.  Two cases stand for them in what
 // follows: docs_prompts, 7 prompts of documents with prefixes up to 3001 tokens, 12 heads of 64 (159 us in an instance
 // that can cap as well, 137 with masks alone, 87 since masks are bits and K and V are released apart), and cap_chunk,
-// the chunks of above with scores capped at 30 (1435 us; with a bias instead 1188).  A cap takes an ex2 and half an
+// the chunks of above with scores capped at 30 (1435 us; with a bias instead 1205).  A cap takes an ex2 and half an
 // inverse a score beside the softmax's own ex2: their pipe is busy in 0.36 of the cycles, issue in 0.49, the tensor pipe
 // in 0.36, and two softmax warps to a scheduler do not hide the chain from a score to its weight.
 #pragma once
@@ -88,7 +88,7 @@ struct TcCfg {
   // decoding warps: capped scores keep the softmax so long that four are enough, and the registers of the others
   // let its threads hold 64 scores, but not with one row tile to twice the values a token (chunks of 2048 over 16384 with four
   // and eight: capped, 32 heads of 128 1432 and 1680 us, of 64 1330 and 1541, 16 of 256 2625 and 2380; capped and biased
-  // 2106 and 2195, 2040 and 2105, 2755 and 2466; biased 1213 and 1178, 972 and 974, 2609 and 2361)
+  // 2106 and 2195, 2040 and 2105, 2755 and 2466; biased, 2 % faster then, 1213 and 1178, 972 and 974, 2609 and 2361)
   static constexpr int DW = (MODE == kCaps || MODE == kAnyScores) && D != 256 ? 4 : 8;
   static constexpr int PROD = DEC0 + DW, MMA = PROD + 1;  // one warp of products per row tile
   static constexpr int NTH = 32 * (MMA + NQ);
@@ -531,11 +531,15 @@ __global__ void __launch_bounds__(TcCfg<D, MODE>::NTH, 1) kv_tc_kernel(const __g
             // a bias is linear in the position on either side of the row's own
             const float d = (float)(pos - tok0 - c);
             if ((p.causal && !p.prefix) || __all_sync(0xffffffffu, pos >= tok0 + TT)) {
-              float2 z = make_float2(fmaf(d, slope, -less), fmaf(d - 1.f, slope, -less));
+              // (distances are exact; running sums of the slope drift by a rounding each: 1185 us for the chunk instead of 1205,
+              // but 1e-4 off for a slope of 30, 5e-6 for small ones)
+              float2 at = make_float2(d, d - 1.f);
+              const float2 s2 = make_float2(slope, slope), l2 = make_float2(-less, -less);
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
-                const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(cf, cf), z);
-                z = fadd2(z, make_float2(-2.f * slope, -2.f * slope));
+                const float2 t = ffma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), make_float2(cf, cf),
+                                       ffma2(at, s2, l2));
+                at = fadd2(at, make_float2(-2.f, -2.f));
                 r[k] = __float_as_uint(t.x);
                 r[k + 1] = __float_as_uint(t.y);
               }
