@@ -157,11 +157,10 @@ __device__ __forceinline__ Key64 sigmoid_key(float x, float bias) {
   return key64(score_pair(1, x, 0.f), bias, 1, x, 0.f, {1.f, 0.f});
 }
 
-// The token's selection in 64 bits: lane i < k gets pick i and its score.
+// The token's selection in 64 bits: lane i < k returns pick i, and in `live` whether it is a candidate.
 // `row`: the token's logits, or `summed`.
 template <int DT>
-static __device__ __noinline__ void route_exact(const RouteParams& p, const float* summed, int64_t row, int lane, int& pick,
-                                         float& score) {
+static __device__ __noinline__ int route_exact(const RouteParams& p, const float* summed, int64_t row, int lane, bool& live) {
   const int n = lane_experts(p, lane), e0 = expert_of(p, lane, 0);
   float l[8], top = -INFINITY;
 #pragma unroll
@@ -220,38 +219,35 @@ static __device__ __noinline__ void route_exact(const RouteParams& p, const floa
     if (!(l[j] > -INFINITY)) v[j] = kNoKey;
   }
   uint32_t left = (1u << n) - 1;           // places that are not taken yet
-  pick = 0;
-  score = 0.f;
+  int pick = 0;
+  live = false;
 #pragma unroll 1
   for (int r = 0; r < p.k; ++r) {
     Key64 best = kNoKey;
-    float bs = 0.f;
     int at = 0x7fffffff;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if ((left >> j & 1) && (at == 0x7fffffff || v[j] > best)) {
         best = v[j];
-        bs = v[j] > kNoKey ? e[j].h : 0.f;
         at = e0 + j;
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const Key64 b = __shfl_xor_sync(0xffffffffu, best, o);
-      const float c = __shfl_xor_sync(0xffffffffu, bs, o);
       const int a = __shfl_xor_sync(0xffffffffu, at, o);
       if (a != 0x7fffffff && (at == 0x7fffffff || b > best || (b == best && a < at))) {
         best = b;
-        bs = c;
         at = a;
       }
     }
     if (lane == r) {
       pick = at;
-      score = bs;
+      live = best > kNoKey;
     }
     if (at >= e0 && at < e0 + n) left &= ~(1u << (at - e0));
   }
+  return pick;
 }
 
 __device__ __forceinline__ void cas_keys(uint32_t& a, uint32_t& b) {
@@ -531,11 +527,13 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
     close = lane < p.k && next >= 16u && mine_v - route_value(next & ~7u) <= tolerance(mine_v);
   }
   int pick = expert_of(p, from, 7 - (int)(mine & 7u));
-  float s = 0.f;
-  if (lane < p.k && mine >= 16u) {
+  // the pick's score, down to what fp32 holds at least
+  auto score = [&]() {
     const float x = usable(summed ? summed[pick] : logit_at<DT>(p, row + pick));
-    s = p.sigmoid ? sigmoid_of(x) : expf(x - top) / z;
-  }
+    return p.sigmoid ? sigmoid_of(x) : expf(x - top) / z;
+  };
+  float s = 0.f;
+  if (lane < p.k && mine >= 16u) s = score();
   if (__any_sync(0xffffffffu, doubtful || close)) {
     // The experts that may be among the picks, a lane each, where they are so few that they find room and a value
     // can be had of a logit alone: they are ranked.
@@ -565,14 +563,13 @@ __device__ __forceinline__ int route_logits(const RouteParams& p, int t, int lan
       __syncwarp();
       if (lane < p.k) {
         pick = list[lane];
-        const float x = usable(summed ? summed[pick] : logit_at<DT>(p, row + pick));
-        s = p.sigmoid ? sigmoid_of(x) : expf(x - top) / z;
+        s = score();
       }
       __syncwarp();
     } else {
-      int exact_pick;
-      route_exact<DT>(p, summed, row, lane, exact_pick, s);
-      pick = exact_pick;
+      bool live;
+      pick = route_exact<DT>(p, summed, row, lane, live);
+      s = lane < p.k && live ? score() : 0.f;
     }
   }
   float sum = lane < p.k ? s : 0.f;

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_route import check, dq, normal  # noqa: F401  (dq is the fixture)
+from test_gpu_route import NP, check, dq, normal  # noqa: F401  (dq is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,19 @@ def test_groups_of_other_sizes_than_the_border(dq, E, groups, top, k):  # noqa: 
         b[g * per + 2:(g + 1) * per] = -1e7
     for scores in ("sigmoid", "softmax"):
         check(dq, normal(1500, E, seed=7), k, scores=scores, bias=b, n_groups=groups, top_groups=top, group_score="top2")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_gates_of_the_least_scores(dq, scores, dtype, renorm):  # noqa: F811
+    # scores of e^-88 to e^-100, where fp32 has no full precision left, equal ones among them: the bias takes the picks there
+    E, top = 64, 100.0 if scores == "softmax" else 0.0
+    g = torch.Generator().manual_seed(3)
+    l = top - 88.0 - torch.randint(0, 13, (60, E), generator=g).float()
+    l[:, 0] = top
+    b = np.zeros(E)
+    b[0] = -5.0
+    # off by 2^-149 at most before the scale of 2.5, and a gate, a share of a sum of 1e-20 and more, by that over 1e-20
+    small = 2.5 * 2.0 ** -148 * (1e20 if renorm else 1.0)
+    check(dq, l.to(NP[dtype]).cuda(), 8, small=small, scores=scores, bias=b, renormalize=renorm, scale=2.5)
