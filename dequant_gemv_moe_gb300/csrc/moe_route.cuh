@@ -137,6 +137,15 @@ constexpr float kLeastPair = 0x1p-80f;
 static __device__ __noinline__ double score_tiny(int sigmoid, float x, float top, Pair z) {
   return sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / ((double)z.h + (double)z.l);
 }
+// A score next to 1 is 1 / t for t = 1 + e^-x, or the sum of a softmax's e^(x - top) for the largest itself.  64 bits round t to
+// a multiple of 2^-52: scores above 1 - 2^-28 are few values that many logits share, which a pair, rounded once, would tell
+// apart.  So t is rounded as it is there, and 1 / t = 1 - d + d^2 - d^3 + d^4 for d = t - 1 < 2^-12 once more.
+constexpr float kNearOne = 8.5f;
+static __device__ __noinline__ double score_near_one(int sigmoid, float x, Pair z) {
+  const Pair e = sigmoid ? exp_pair({-x, 0.f}) : z;
+  const double t = (double)e.h + (double)e.l, d = sigmoid ? (1.0 + t) - 1.0 : t - 1.0;
+  return (1.0 - d) + d * d * (1.0 - d * (1.0 - d));
+}
 __device__ __forceinline__ Pair shfl_xor_pair(Pair a, int o) {
   return {__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
 }
@@ -150,7 +159,9 @@ __device__ __forceinline__ Key64 key64(double x) {
 __device__ __forceinline__ double value64(Key64 k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL)); }
 // The value of logit x, whose score is e.
 __device__ __forceinline__ Key64 key64(Pair e, float bias, int sigmoid, float x, float top, Pair z) {
-  const double s = e.h < kLeastPair ? score_tiny(sigmoid, x, top, z) : (double)e.h + (double)e.l;
+  const bool near = sigmoid ? x > kNearOne : x == top && z.h < 1.f + 0x1p-12f;
+  const double s = near ? score_near_one(sigmoid, x, z)
+                   : e.h < kLeastPair ? score_tiny(sigmoid, x, top, z) : (double)e.h + (double)e.l;
   return key64(s + (double)bias);
 }
 __device__ __forceinline__ Key64 sigmoid_key(float x, float bias) {

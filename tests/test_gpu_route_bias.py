@@ -81,3 +81,16 @@ def test_gates_of_the_least_scores(dq, scores, dtype, renorm):  # noqa: F811
     # off by 2^-149 at most before the scale of 2.5, and a gate, a share of a sum of 1e-20 and more, by that over 1e-20
     small = 2.5 * 2.0 ** -148 * (1e20 if renorm else 1.0)
     check(dq, l.to(NP[dtype]).cuda(), 8, small=small, scores=scores, bias=b, renormalize=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("E,groups,top", [(30, 1, 1), (256, 1, 1), (64, 8, 3), (256, 32, 9)])
+@pytest.mark.parametrize("bias", [0.0, -1.0, 3.0])
+def test_sigmoids_that_64_bits_do_not_tell_apart(dq, E, groups, top, bias):  # noqa: F811
+    # above 19 neighbouring logits begin to share 1 / (1 + e^-l), from 37 on it is 1: equal ones go to the lowest index
+    g = torch.Generator().manual_seed(E)
+    l = 16.0 + 28.0 * torch.rand(150, E, generator=g)
+    l[50:100] = 30.0 + 8.0 * torch.rand(50, E, generator=g)
+    for x in range(20):                                     # steps of one float
+        l[100 + x] = (18.0 + x) * (1 + torch.randint(0, 40, (E,), generator=g) * 2.0 ** -23)
+    for gs in ("max", "top2"):
+        check(dq, l.cuda(), 6, scores="sigmoid", bias=np.full(E, bias), n_groups=groups, top_groups=top, group_score=gs)
