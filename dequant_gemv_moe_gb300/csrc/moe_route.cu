@@ -45,7 +45,9 @@ int launch_route(const void* logits, int dtype, int64_t stride, int KS, int T, i
   p.idx = idx;
   p.gate = gate;
   const int ctas = (int)(((int64_t)T + kRouteWarps - 1) / kRouteWarps);
-  // rows and bias that the lanes take in 16-byte words
+  // Rows and bias that the lanes take in 16-byte words, eight experts each and none without: 256 experts on a boundary (16384
+  // tokens, fp32 16.5 us, one logit at a time 20.0; bf16 20.8 and 24.1; 8 tokens 3.0 and 3.3).  Fewer experts leave lanes that have
+  // fewer than eight and are loaded one at a time: 64, 128 or 160 take 18.1 to 18.3.
   const int el = dtype == DQ_F32 ? 4 : 2;
   const bool full = E == 256 && (uintptr_t)logits % 16 == 0 && stride * el % 16 == 0 && (uintptr_t)r.bias % 16 == 0;
   cudaError_t e = cudaSuccess;

@@ -21,9 +21,9 @@
 // place in the lane, then k + 1 rounds take the best head (one warp reduction
 // and a vote) and advance that lane's list.
 //
-// What bounds it: instructions, 760 a token (the rounds 170, keys and sort 100, scores and groups 180), with issue in
+// What bounds it: instructions, 773 a token (the rounds 170, keys and sort 100, scores and groups 180), with issue in
 // 0.6 of the cycles; a warp of its own for every token, so that the GPU evens out what the doubts cost.
-// 16384 tokens of 256 experts, 8 of 4 in 8 groups: 16.3 us (bytes alone: 2.7); 8 tokens 2.9 us, a
+// 16384 tokens of 256 experts, 8 of 4 in 8 groups: 16.5 us (bytes alone: 2.7); 8 tokens 3.0 us, a
 // launch and one token's chain.  Eight tokens to a warp, four lanes each, took 560 instructions a token but 21 us:
 // too few warps to hide their chains.
 #pragma once

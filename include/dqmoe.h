@@ -358,11 +358,14 @@ int dq_moe_forward_noalloc(const dq_moe_desc* desc, const void* x, int x_dtype, 
 /*   sel   = the top_k largest v of the kept groups, in descending order, the */
 /*           lowest index first among equal ones                             */
 /*   gate  = scale * s_e / (sum over sel of s + 1e-20), or scale * s_e        */
-/* The selection is that of 64-bit arithmetic on the given logits (without a  */
-/* bias experts are compared by their logits); gates are fp32.  A logit       */
-/* that is -inf or NaN takes its expert out: it is chosen only where nothing  */
-/* else is left (the lowest index first), with gate 0; +inf counts as the     */
-/* largest float.  A bias is finite.                                         */
+/* The selection is that of 64-bit arithmetic on the given logits, with       */
+/* sigmoid(l) = 1 / (1 + e^-l); without a bias experts are compared by their  */
+/* logits.  (Equal values that only the rounding of its exponential can tell  */
+/* apart, as the sums s(l) + s(-l) of two groups, may fall either way.)       */
+/* Gates are fp32.  A logit that is -inf or NaN takes its expert out, as a     */
+/* group that is not kept takes out its experts: one is chosen only where     */
+/* nothing else is left (the lowest index first), with gate 0; +inf counts as */
+/* the largest float.  A bias is finite.                                     */
 /* ------------------------------------------------------------------------ */
 #define DQ_ROUTE_SOFTMAX 0
 #define DQ_ROUTE_SIGMOID 1
